@@ -443,6 +443,93 @@ int pasa_kprep_fp8_blocks(const void* k, void* k8, void* means, float* kscale, i
                           int mode, int first_block, void* stream);
 
 /*
+ * 4-bit key/value cache. (The paper has no counterpart: it keeps its Abstract's idea, that a
+ * shift of the keys along the sequence leaves attention unchanged, and spends it on the
+ * bits of the cache.) Keys and values are held as 4-bit codes with one scale per row and group
+ * of 32 channels; every row stands for itself, so rows are appended, moved and dropped
+ * without touching others. With x = fp16_rn(K - shift) for keys and x = V for values (a NaN
+ * counts as 0, an infinity as the largest finite value):
+ *     s = max|x| / 7 over the group, rounded to 8 significant bits and then to fp16,
+ *     c = x / s rounded to the nearest integer (ties to even), within -7 .. 7; 0 where s = 0.
+ * Tensors (device, contiguous, 16-byte aligned; Sk_cap allocated rows per head):
+ *     k4, v4         uint8 [B, Hkv, Sk_cap, D / 2]: byte i holds c + 8 of channel 2i in its low
+ *                    nibble and of channel 2i + 1 in its high nibble
+ *     kscale, vscale fp16 [B, Hkv, Sk_cap, D / 32]
+ *     shift          fp16 [B, Hkv, D], or NULL for none: subtracted from every key row of its
+ *                    head. Any values give the same attention up to the rounding of the codes;
+ *                    an average of the first keys (a block's means from pasa_kshift) takes
+ *                    a bias along the sequence out of the scales. It has to stay the same for a
+ *                    cache's whole life.
+ * A row takes 9 D / 16 bytes where fp16 takes 2 D; s has 8 bits so that s * c is exact in fp16.
+ *
+ * pasa_kv4_append stores rows 0 .. n - 1 of k and v (fp16 [B, Hkv, n, D]) as cache rows
+ * starts[b] + i of sequence b, and pasa_kv4_read writes what those rows stand for, fp16_rn(s c
+ * + shift) and s c, to k and v (fp16 [B, Hkv, n, D]; for a prefill on the cache through
+ * pasa_attn_fwd, or to look at it).
+ *   starts  int32 [B], device, or NULL: `start` for every sequence (0 <= start, start + n <=
+ *           Sk_cap, else PASA_ERR_SHAPE)
+ *   counts  int32 [B], device, or NULL for n: only rows i < counts[b] are stored or read (a
+ *           padded batch; the padding is not read)
+ * Rows that fall outside 0 .. Sk_cap - 1 (from starts on the device) are skipped, and what
+ * is not stored or read is left as it was. starts and counts need 4-byte alignment.
+ */
+int pasa_kv4_append(const void* k, const void* v, const void* shift, void* k4, void* kscale, void* v4, void* vscale,
+                    const int* starts, int start, const int* counts, int B, int Hkv, int n, int Sk_cap, int D,
+                    void* stream);
+int pasa_kv4_read(const void* k4, const void* kscale, const void* v4, const void* vscale, const void* shift, void* k,
+                  void* v, const int* starts, int start, const int* counts, int B, int Hkv, int n, int Sk_cap, int D,
+                  void* stream);
+
+/*
+ * Decode attention on a 4-bit cache: a few query rows per head (Hq / Hkv * Sq <= 128, else
+ * PASA_ERR_UNSUPPORTED), q and o fp16 [B, Hq, Sq, D], lse fp32 [B, Hq, Sq] or NULL:
+ *     O = softmax(scale * q K'^T) V,  LSE = ln sum_j exp(scale * q . (K'_j + shift))
+ * over the values K' = s c and V = s c of the cache (the shift of a head is the same for all
+ * its keys and cancels in the softmax).
+ *   lengths  int32 [B], device, 4-byte aligned: rows of each sequence, taken as 0 below 0 and as
+ *            Sk above Sk; NULL: Sk in every sequence. Rows past a sequence's last are
+ *            not read. The causal mask is bottom-right aligned in each sequence: query row i of
+ *            sequence b sees keys j <= i + lengths[b] - Sq. A row that sees no key gets O = 0
+ *            and LSE = -inf.
+ *   weights  fp32 [B, Hkv, Sk_cap] or NULL: the softmax weight of cache row j, summed over the
+ *            kv head's Hq / Hkv * Sq query rows, is added to weights[b, h, j] (j < lengths[b]),
+ *            in the same order at every call.
+ *   workspace  device, 256-byte aligned, at least pasa_attn_fwd_decode_kv4_workspace_bytes(...)
+ *            bytes (`weights` nonzero where the call passes weights; may be NULL where that is
+ *            0), written before it is read, used on `stream` only.
+ */
+size_t pasa_attn_fwd_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int weights);
+int pasa_attn_fwd_decode_kv4(const void* q, const void* k4, const void* kscale, const void* v4, const void* vscale,
+                             const void* shift, const int* lengths, void* o, float* lse, float* weights, int B, int Hq,
+                             int Hkv, int Sq, int Sk, int Sk_cap, int D, int causal, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Eviction from a cache by accumulated attention weight. (No counterpart in the paper.) Of
+ * each sequence with more than `budget` rows, every kv head keeps budget rows: its last
+ * `recent` ones (0 <= recent <= budget) and, of the others, those with the largest
+ * weights (equal ones: the lowest row first; a NaN counts as -inf). The kept rows move to rows
+ * 0 .. budget - 1 in their old order. Shorter sequences keep everything.
+ *   planes, out_planes, row_bytes  host arrays of n_planes (1 .. 8) entries: the tensors of the
+ *            cache, [B, Hkv, Sk_cap, row_bytes[i] bytes] each (a multiple of 4, at most 65536),
+ *            e.g. k4, kscale, v4, vscale, or fp16 k and v, and where their rows go:
+ *            [B, Hkv, out_cap, row_bytes[i]], out_cap >= budget. Rows past the kept ones are
+ *            left as they were there.
+ *   weights, out_weights  fp32 [B, Hkv, Sk_cap] and [B, Hkv, out_cap]: the weights move with
+ *            their rows; those past the new length become 0.
+ *   In place: out_planes[i] == planes[i] for every i and out_weights == weights, with
+ *            out_cap == Sk_cap; a mixture is PASA_ERR_SHAPE. Else no output may overlap an input.
+ *   lengths  int32 [B], device, or NULL for Sk: rows of each sequence, within 0 .. Sk.
+ *   index    int32 [B, Hkv, budget], out: the old row of each kept one, -1 past the last.
+ *   new_lengths  int32 [B], out, or NULL: min(length, budget); may be `lengths` itself.
+ * A shifted or e4m3 copy of the keys (pasa_kshift, pasa_kprep_fp8) depends on whole key
+ * blocks: make it again from the moved keys.
+ */
+int pasa_cache_evict(const void* const* planes, void* const* out_planes, const int* row_bytes, int n_planes,
+                     const float* weights, float* out_weights, const int* lengths, int* index, int* new_lengths, int B,
+                     int Hkv, int Sk, int Sk_cap, int out_cap, int budget, int recent, void* stream);
+
+/*
  * Synchronise `stream` and read the device error word. Returns PASA_OK, PASA_ERR_TIMEOUT
  * (a pipeline wait gave up; `info`, if not NULL, receives the CTA index << 32 | wait site)
  * or PASA_ERR_CUDA. Reading the word clears it.

@@ -19,6 +19,7 @@ import torch
 __all__ = [
     "MODE_SHIFT_F16ACC", "MODE_SHIFT_F32ACC", "MODE_NAIVE_F16ACC", "MODE_NOSHIFT_F32ACC", "MODE_SHIFT_F16ALL", "MODE_SHIFT_FP8", "MODE_NAIVE_FP8", "kprep_fp8", "attn_fwd_fp8",
     "PasaError", "attn_fwd", "attn_fwd_alloc", "attn_fwd_fused", "attn_fwd_shifted", "attn_fwd_stats", "kshift", "workspace_bytes", "check_device_error", "block_rows",
+    "kv4_append", "kv4_read", "attn_fwd_decode_kv4", "cache_evict",
     "library", "library_path",
 ]
 
@@ -64,6 +65,11 @@ SIGNATURES = {
     "pasa_attn_fwd_host_device_bytes": ([_I] * 9, _SZ),
     "pasa_attn_fwd_host_plan": ([_I] * 9 + [_P, _I], _I),
     "pasa_release_host_streams": ([], _I),
+    "pasa_kv4_append": ([_P] * 7 + [_P, _I, _P] + [_I] * 5 + [_P], _I),
+    "pasa_kv4_read": ([_P] * 7 + [_P, _I, _P] + [_I] * 5 + [_P], _I),
+    "pasa_attn_fwd_decode_kv4_workspace_bytes": ([_I] * 7, _SZ),
+    "pasa_attn_fwd_decode_kv4": ([_P] * 10 + [_I] * 8 + [_F, _P, _SZ, _P], _I),
+    "pasa_cache_evict": ([_P, _P, _P, _I] + [_P] * 5 + [_I] * 7 + [_P], _I),
     "pasa_check_device_error": ([_P, ctypes.POINTER(ctypes.c_ulonglong)], _I),
     "pasa_selftest_wait_timeout": ([_P], _I),
     "pasa_selftest_exp2": ([_P, _P, _P, _I, _P], _I),
@@ -502,6 +508,168 @@ def attn_fwd_decode_fp8(q, k8, means, kscale, v, causal: bool = False, scale: fl
     if rc != 0:
         raise PasaError(rc, "pasa_attn_fwd_decode_fp8")
     return out, lse
+
+
+def _check_cuda(x, name: str, dtype, shape=None, device=None):
+    """A contiguous CUDA tensor of `dtype` (and shape) on the current device."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != dtype or not x.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if x.get_device() != device:
+        raise ValueError(f"{name} is on device {x.get_device()}, the current device is {device}")
+    return x.data_ptr()
+
+
+def _check_kv4(k4, kscale, v4, vscale, shift, device):
+    """The cache tensors' pointers, and (B, Hkv, cap, D)."""
+    if not isinstance(k4, torch.Tensor) or k4.dim() != 4:
+        raise ValueError("expected k4 [B,Hkv,cap,D/2]")
+    B, Hkv, cap, half = k4.shape
+    codes, scales = (B, Hkv, cap, half), (B, Hkv, cap, half // 16)
+    ptrs = (_check_cuda(k4, "k4", torch.uint8, codes, device),
+            _check_cuda(kscale, "kscale", torch.float16, scales, device),
+            _check_cuda(v4, "v4", torch.uint8, codes, device),
+            _check_cuda(vscale, "vscale", torch.float16, scales, device))
+    sp = None if shift is None else _check_cuda(shift, "shift", torch.float16, (B, Hkv, 2 * half), device)
+    return ptrs, sp, (B, Hkv, cap, 2 * half)
+
+
+def _int32(x, name: str) -> int:
+    """A size or position that the C ABI takes as an int."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} = {x} does not fit an int")
+    return x
+
+
+def _per_sequence(x, name, B, device):
+    """(pointer, value) of an argument that is one int or an int32 tensor [B]."""
+    if isinstance(x, torch.Tensor):
+        return _check_cuda(x, name, torch.int32, (B,), device), 0
+    return None, _int32(x, name)
+
+
+def kv4_append(k, v, k4, kscale, v4, vscale, start=0, counts=None, shift=None):
+    """Store rows of k, v [B,Hkv,n,D] (fp16) in the 4-bit cache (k4, v4 uint8 [B,Hkv,cap,D/2];
+    kscale, vscale fp16 [B,Hkv,cap,D/32]) from row `start` on (an int, or an int32 tensor [B]);
+    with counts (int32 [B]) only the first counts[b] rows of each sequence. shift (fp16
+    [B,Hkv,D]) is subtracted from every key row and stays the same for the cache's life."""
+    dev = torch.cuda.current_device()
+    ptrs, sp, (B, Hkv, cap, D) = _check_kv4(k4, kscale, v4, vscale, shift, dev)
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("expected k, v [B,Hkv,n,D]")
+    n = k.shape[2]
+    kp = _check_cuda(k, "k", torch.float16, (B, Hkv, n, D), dev)
+    vp = _check_cuda(v, "v", torch.float16, (B, Hkv, n, D), dev)
+    starts, first = _per_sequence(start, "start", B, dev)
+    cp = None if counts is None else _check_cuda(counts, "counts", torch.int32, (B,), dev)
+    rc = library().pasa_kv4_append(kp, vp, sp, *ptrs, starts, first, cp, B, Hkv, n, cap, D, _stream())
+    if rc != 0:
+        raise PasaError(rc, "pasa_kv4_append")
+
+
+def kv4_read(k4, kscale, v4, vscale, n: int, start=0, counts=None, shift=None, out_k=None, out_v=None):
+    """What cache rows start .. start + n - 1 stand for: (k, v) fp16 [B,Hkv,n,D]. start, counts
+    and shift as in :func:`kv4_append`; rows at counts[b] and later are left as they are in out_k
+    and out_v (0 in new tensors)."""
+    dev = torch.cuda.current_device()
+    ptrs, sp, (B, Hkv, cap, D) = _check_kv4(k4, kscale, v4, vscale, shift, dev)
+    new = torch.empty if counts is None and not isinstance(start, torch.Tensor) else torch.zeros
+    if out_k is None:
+        out_k = new((B, Hkv, n, D), device=k4.device, dtype=torch.float16)
+    if out_v is None:
+        out_v = new((B, Hkv, n, D), device=k4.device, dtype=torch.float16)
+    kp = _check_cuda(out_k, "out_k", torch.float16, (B, Hkv, n, D), dev)
+    vp = _check_cuda(out_v, "out_v", torch.float16, (B, Hkv, n, D), dev)
+    starts, first = _per_sequence(start, "start", B, dev)
+    cp = None if counts is None else _check_cuda(counts, "counts", torch.int32, (B,), dev)
+    rc = library().pasa_kv4_read(*ptrs, sp, kp, vp, starts, first, cp, B, Hkv, n, cap, D, _stream())
+    if rc != 0:
+        raise PasaError(rc, "pasa_kv4_read")
+    return out_k, out_v
+
+
+def decode_kv4_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: int, weights: bool = False) -> int:
+    return library().pasa_attn_fwd_decode_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, int(bool(weights)))
+
+
+def attn_fwd_decode_kv4(q, k4, kscale, v4, vscale, causal: bool = False, scale: float | None = None, shift=None,
+                        length: int | None = None, lengths=None, weights=None, out=None, lse=None, workspace=None):
+    """Decode attention on a 4-bit cache (see :func:`kv4_append`): q fp16 [B,Hq,Sq,D] with
+    Hq / Hkv * Sq <= 128. The sequences hold `length` rows (default: all of the cache's) or
+    lengths[b] (int32 tensor [B]; `length` is then an upper bound). With weights (fp32
+    [B,Hkv,cap]) each cache row's softmax weight, summed over the kv head's query rows, is added
+    there. Returns (o, lse)."""
+    dev = torch.cuda.current_device()
+    ptrs, sp, (B, Hkv, cap, D) = _check_kv4(k4, kscale, v4, vscale, shift, dev)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("expected q [B,Hq,Sq,D]")
+    _, Hq, Sq, _ = q.shape
+    Sk = cap if length is None else _int32(length, "length")
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, Hq, Sq), device=q.device, dtype=torch.float32) if lse is None else lse
+    qp = _check_cuda(q, "q", torch.float16, (B, Hq, Sq, D), dev)
+    op = _check_cuda(out, "out", torch.float16, (B, Hq, Sq, D), dev)
+    lp = _check_cuda(lse, "lse", torch.float32, (B, Hq, Sq), dev)
+    np_ = None if lengths is None else _check_cuda(lengths, "lengths", torch.int32, (B,), dev)
+    wp = None if weights is None else _check_cuda(weights, "weights", torch.float32, (B, Hkv, cap), dev)
+    lib = library()
+    nbytes = lib.pasa_attn_fwd_decode_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, 0 if wp is None else 1)
+    if nbytes and (workspace is None or workspace.numel() * workspace.element_size() < nbytes):
+        workspace = torch.empty(nbytes, device=q.device, dtype=torch.uint8)
+    elif nbytes:
+        _check_cuda(workspace, "workspace", workspace.dtype, None, dev)
+    rc = lib.pasa_attn_fwd_decode_kv4(qp, *ptrs, sp, np_, op, lp, wp, B, Hq, Hkv, Sq, Sk, cap, D, int(bool(causal)),
+                                      float(scale) if scale is not None else 0.0,
+                                      workspace.data_ptr() if nbytes else None, nbytes, _stream())
+    if rc != 0:
+        raise PasaError(rc, "pasa_attn_fwd_decode_kv4")
+    return out, lse
+
+
+def cache_evict(planes, weights, budget: int, recent: int = 0, length: int | None = None, lengths=None, out=None,
+                out_weights=None, index=None, new_lengths=None):
+    """Keep `budget` rows of every sequence that has more: per kv head the last `recent` and the
+    heaviest of the others, in their old order (pasa_cache_evict). planes: the cache's tensors
+    [B,Hkv,cap,*], e.g. (k4, kscale, v4, vscale) or fp16 (k, v); weights fp32 [B,Hkv,cap]. The
+    sequences hold `length` rows (default cap) or lengths[b] (int32 [B]). In place, or into out (tensors
+    [B,Hkv,out_cap,*]) and out_weights (fp32 [B,Hkv,out_cap]). Returns (index int32 [B,Hkv,budget]:
+    the old rows, -1 past the last; new_lengths int32 [B])."""
+    dev = torch.cuda.current_device()
+    planes, budget, recent = list(planes), _int32(budget, "budget"), _int32(recent, "recent")
+    if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
+        raise ValueError("expected weights [B,Hkv,cap]")
+    if (out is None) != (out_weights is None):
+        raise ValueError("out and out_weights go together")
+    out, out_weights = (planes, weights) if out is None else (list(out), out_weights)
+    if not isinstance(out_weights, torch.Tensor) or out_weights.dim() != 3 or len(out) != len(planes):
+        raise ValueError("expected out_weights [B,Hkv,out_cap] and as many out tensors as planes")
+    B, Hkv, cap = weights.shape
+    out_cap = out_weights.shape[2]
+    Sk = cap if length is None else _int32(length, "length")
+    wp = _check_cuda(weights, "weights", torch.float32, (B, Hkv, cap), dev)
+    owp = _check_cuda(out_weights, "out_weights", torch.float32, (B, Hkv, out_cap), dev)
+    src, dst, nbytes = [], [], []
+    for i, (a, b) in enumerate(zip(planes, out)):
+        if not isinstance(a, torch.Tensor) or a.dim() != 4:
+            raise ValueError("expected planes [B,Hkv,cap,*]")
+        src.append(_check_cuda(a, f"planes[{i}]", a.dtype, (B, Hkv, cap, a.shape[3]), dev))
+        dst.append(_check_cuda(b, f"out[{i}]", a.dtype, (B, Hkv, out_cap, a.shape[3]), dev))
+        nbytes.append(a.shape[3] * a.element_size())
+    np_ = None if lengths is None else _check_cuda(lengths, "lengths", torch.int32, (B,), dev)
+    if index is None:
+        index = torch.empty((B, Hkv, max(budget, 0)), device=weights.device, dtype=torch.int32)
+    if new_lengths is None:
+        new_lengths = torch.empty((B,), device=weights.device, dtype=torch.int32)
+    ip = _check_cuda(index, "index", torch.int32, (B, Hkv, max(budget, 0)), dev)
+    nlp = _check_cuda(new_lengths, "new_lengths", torch.int32, (B,), dev)
+    count = len(planes)
+    rc = library().pasa_cache_evict((_P * count)(*src), (_P * count)(*dst), (_I * count)(*nbytes), count, wp, owp, np_,
+                                    ip, nlp, B, Hkv, Sk, cap, out_cap, budget, recent, _stream())
+    if rc != 0:
+        raise PasaError(rc, "pasa_cache_evict")
+    return index, new_lengths
 
 
 def selftest_wait_timeout():

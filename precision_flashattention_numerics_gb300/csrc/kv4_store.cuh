@@ -1,0 +1,186 @@
+// The 4-bit key/value cache: its format, storing rows in it (kv4_append_kernel) and reading
+// them back (kv4_read_kernel).
+//
+// Format. A row of D channels is held as D / 2 bytes of codes (byte i: channel 2i in the low
+// nibble, 2i + 1 in the high one) and D / 32 fp16 scales, one per group of 32 channels. With
+// x = fp16_rn(K - shift) for keys (one shift per kv head and channel) and x = V for values,
+// NaN counting as 0 and +-inf as +-65504:
+//     s = fp16_rn(rn_8bits(max|x| / 7)),   c = clamp(rint_even(x / s), -7, 7) (0 where s = 0),
+// stored as the nibble c + 8. s has 8 significant bits, so s * c (8 + 3 bits) is exactly an
+// fp16 number and a reader that multiplies in fp16 rounds nothing.
+#pragma once
+
+#include <cstdint>
+#include <cuda_fp16.h>
+
+#include "ptx.cuh"
+
+namespace pasa {
+
+constexpr int kKv4Group = 32;          // channels that share a scale
+constexpr int kKv4StoreThreads = 256;
+
+// Where a call's rows go: row i of sequence b (i < counts[b], or n) is cache row
+// start[b] + i (or start + i); rows outside [0, cap) are skipped.
+struct Kv4Window {
+  const int* starts;   // device, or nullptr: `start` for every sequence
+  const int* counts;   // device, or nullptr: n for every sequence
+  int start, n, cap;
+  // The cache row of row i of sequence b, or -1 where there is none.
+  __device__ __forceinline__ long long row(int b, int i) const {
+    const long long at = static_cast<long long>(starts ? starts[b] : start) + i;
+    if (counts && i >= counts[b]) return -1;
+    return at >= 0 && at < cap ? at : -1;
+  }
+};
+
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+
+// x rounded (ties to even) to 8 significant bits; x >= 0 and finite.
+__device__ __forceinline__ float round_8bits(float x) {
+  uint32_t u = __float_as_uint(x);
+  u += 0x7FFFu + ((u >> 16) & 1u);
+  return __uint_as_float(u & 0xFFFF0000u);
+}
+
+// The codes of 8 channels, one nibble each (bits 4i .. 4i + 3: channel i), and the group's
+// scale; x: 8 fp16 in 4 registers. Called by the 4 lanes of a group together (aligned groups
+// of 4 lanes hold the 32 channels).
+//
+// x / s is needed only to the nearest integer. Where it is no tie (a multiple of 1/2), it is at
+// least 2.4e-4 away from one: x has 11 significant bits, s 8, and both are multiples of a power
+// of two no smaller than s * 2^-12. So x * (1 / s), off by at most 7 * 2^-24, is first rounded
+// to a multiple of 2^-14 (by adding 768), which puts true ties exactly on the tie and
+// moves no other value across one, and then to an integer (by adding 1.5 * 2^23 - 768), ties to
+// even. No division per channel.
+__device__ __forceinline__ uint32_t kv4_codes(const uint32_t (&xin)[4], __half& scale) {
+  uint32_t x[4] = {xin[0], xin[1], xin[2], xin[3]};
+  __half2 m2 = __hmax2_nan(__hmax2_nan(__habs2(bits_h2(x[0])), __habs2(bits_h2(x[1]))),
+                           __hmax2_nan(__habs2(bits_h2(x[2])), __habs2(bits_h2(x[3]))));
+  __half m = __hmax_nan(__low2half(m2), __high2half(m2));
+  m = __hmax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = __hmax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  float a = __half2float(m);
+  const bool odd = !(a <= 65504.0f);   // an infinity or NaN in the group: the same in its 4 lanes
+  if (__any_sync(0xFFFFFFFFu, odd)) {
+    float b = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 f = __half22float2(bits_h2(x[i]));
+      f.x = f.x == f.x ? fminf(fmaxf(f.x, -65504.0f), 65504.0f) : 0.0f;
+      f.y = f.y == f.y ? fminf(fmaxf(f.y, -65504.0f), 65504.0f) : 0.0f;
+      b = fmaxf(b, fmaxf(fabsf(f.x), fabsf(f.y)));
+      x[i] = h2_bits(__float22half2_rn(f));
+    }
+    b = fmaxf(b, __shfl_xor_sync(0xFFFFFFFFu, b, 1));
+    a = fmaxf(b, __shfl_xor_sync(0xFFFFFFFFu, b, 2));
+  }
+  scale = __float2half_rn(round_8bits(a / 7.0f));
+  const float s = __half2float(scale);
+  const float r = s > 0.0f ? 1.0f / s : 0.0f;
+  uint32_t y[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(bits_h2(x[i]));
+    // |x / s| passes 7 by more than rounding only where s itself is an fp16 subnormal
+    const float lo = fminf(fmaxf(fmaf(f.x, r, 768.0f), 761.0f), 775.0f);
+    const float hi = fminf(fmaxf(fmaf(f.y, r, 768.0f), 761.0f), 775.0f);
+    // 12582912 = 1.5 * 2^23: the integer code + 8 lands in the low bits of the float
+    y[2 * i] = __float_as_uint(lo + (12582912.0f + 8.0f - 768.0f));
+    y[2 * i + 1] = __float_as_uint(hi + (12582912.0f + 8.0f - 768.0f));
+  }
+  uint32_t b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = y[2 * i + 1] * 16u + y[2 * i];   // low byte: two codes (1 .. 15 each)
+  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+
+// Store rows of k and v [B, H, n, D] in the cache. One thread per 8 channels of a row (16
+// bytes in, 4 bytes of codes out), blockIdx.y picking keys or values. HBM-bound: 4 D bytes in
+// and 9 D / 8 out per row of K and V.
+template <int D>
+__global__ void __launch_bounds__(kKv4StoreThreads) kv4_append_kernel(
+    const __half* __restrict__ k, const __half* __restrict__ v, const __half* __restrict__ shift,
+    uint8_t* __restrict__ k4, __half* __restrict__ kscale, uint8_t* __restrict__ v4, __half* __restrict__ vscale,
+    int B, int H, Kv4Window win) {
+  griddep_launch_dependents();
+  constexpr int kPer = D / 8;   // threads per row
+  const long long idx = static_cast<long long>(blockIdx.x) * kKv4StoreThreads + threadIdx.x;
+  const long long r = idx / kPer;
+  const int u = static_cast<int>(idx % kPer);
+  const long long plane = r / win.n;   // b * H + h
+  const bool in = plane < static_cast<long long>(B) * H;
+  const int b = in ? static_cast<int>(plane / H) : 0;
+  const long long row = in ? win.row(b, static_cast<int>(r % win.n)) : -1;
+  const bool keys = blockIdx.y == 0;
+  uint32_t x[4] = {0u, 0u, 0u, 0u};
+  if (row >= 0) {
+    const uint4 raw = *reinterpret_cast<const uint4*>((keys ? k : v) + r * D + u * 8);
+    x[0] = raw.x, x[1] = raw.y, x[2] = raw.z, x[3] = raw.w;
+    if (keys && shift) {
+      const uint4 sh = *reinterpret_cast<const uint4*>(shift + plane * D + u * 8);
+      x[0] = h2_bits(__hsub2_rn(bits_h2(x[0]), bits_h2(sh.x)));
+      x[1] = h2_bits(__hsub2_rn(bits_h2(x[1]), bits_h2(sh.y)));
+      x[2] = h2_bits(__hsub2_rn(bits_h2(x[2]), bits_h2(sh.z)));
+      x[3] = h2_bits(__hsub2_rn(bits_h2(x[3]), bits_h2(sh.w)));
+    }
+  }
+  __half s;
+  const uint32_t codes = kv4_codes(x, s);
+  if (row >= 0) {
+    const long long at = plane * win.cap + row;
+    *reinterpret_cast<uint32_t*>((keys ? k4 : v4) + at * (D / 2) + u * 4) = codes;
+    if ((u & 3) == 0) (keys ? kscale : vscale)[at * (D / kKv4Group) + u / 4] = s;
+  }
+}
+
+// 8 codes (nibble i: channel i) times the scale, exactly, as 4 pairs (0, 4), (1, 5), (2, 6),
+// (3, 7): a nibble masked into the mantissa of 1024 is 1024 + n, or 1024 + 16 n one place up.
+__device__ __forceinline__ void kv4_expand(uint32_t w, __half2 s2, __half2 (&out)[4]) {
+  const __half2 off0 = __float2half2_rn(-1032.0f), off1 = __float2half2_rn(-72.0f), sixteenth = __float2half2_rn(0.0625f);
+  const uint32_t w8 = w >> 8;
+  const uint32_t magic = 0x64006400u;
+  out[0] = __hmul2(__hadd2(bits_h2((w & 0x000F000Fu) | magic), off0), s2);
+  out[1] = __hmul2(__hfma2(bits_h2((w & 0x00F000F0u) | magic), sixteenth, off1), s2);
+  out[2] = __hmul2(__hadd2(bits_h2((w8 & 0x000F000Fu) | magic), off0), s2);
+  out[3] = __hmul2(__hfma2(bits_h2((w8 & 0x00F000F0u) | magic), sixteenth, off1), s2);
+}
+
+// Read cache rows back as fp16: fp16_rn(s * c + shift) for keys, s * c for values, into
+// k, v [B, H, n, D]; output rows without a cache row are left as they are.
+template <int D>
+__global__ void __launch_bounds__(kKv4StoreThreads) kv4_read_kernel(
+    const uint8_t* __restrict__ k4, const __half* __restrict__ kscale, const uint8_t* __restrict__ v4,
+    const __half* __restrict__ vscale, const __half* __restrict__ shift, __half* __restrict__ k,
+    __half* __restrict__ v, int B, int H, Kv4Window win) {
+  constexpr int kPer = D / 8;
+  const long long idx = static_cast<long long>(blockIdx.x) * kKv4StoreThreads + threadIdx.x;
+  const long long r = idx / kPer;
+  const int u = static_cast<int>(idx % kPer);
+  const long long plane = r / win.n;
+  if (plane >= static_cast<long long>(B) * H) return;
+  const long long row = win.row(static_cast<int>(plane / H), static_cast<int>(r % win.n));
+  if (row < 0) return;
+  const bool keys = blockIdx.y == 0;
+  const long long at = plane * win.cap + row;
+  const uint32_t w = *reinterpret_cast<const uint32_t*>((keys ? k4 : v4) + at * (D / 2) + u * 4);
+  const __half s = (keys ? kscale : vscale)[at * (D / kKv4Group) + u / 4];
+  __half2 p[4];
+  kv4_expand(w, __half2half2(s), p);
+  uint4 o;
+  o.x = h2_bits(__lows2half2(p[0], p[1]));
+  o.y = h2_bits(__lows2half2(p[2], p[3]));
+  o.z = h2_bits(__highs2half2(p[0], p[1]));
+  o.w = h2_bits(__highs2half2(p[2], p[3]));
+  if (keys && shift) {
+    const uint4 sh = *reinterpret_cast<const uint4*>(shift + plane * D + u * 8);
+    o.x = h2_bits(__hadd2_rn(bits_h2(o.x), bits_h2(sh.x)));
+    o.y = h2_bits(__hadd2_rn(bits_h2(o.y), bits_h2(sh.y)));
+    o.z = h2_bits(__hadd2_rn(bits_h2(o.z), bits_h2(sh.z)));
+    o.w = h2_bits(__hadd2_rn(bits_h2(o.w), bits_h2(sh.w)));
+  }
+  *reinterpret_cast<uint4*>((keys ? k : v) + r * D + u * 8) = o;
+}
+
+}  // namespace pasa

@@ -15,6 +15,9 @@
 #include "attn_fwd.cuh"
 #include "attn_fwd2s.cuh"
 #include "decode_fwd.cuh"
+#include "evict.cuh"
+#include "kv4_decode.cuh"
+#include "kv4_store.cuh"
 #include "kshift.cuh"
 #include "ptx.cuh"
 
@@ -1406,3 +1409,252 @@ extern "C" int pasa_attn_fwd_host(const void* q, const void* k, const void* v, v
   if (rc != PASA_OK) return rc;
   return e == cudaSuccess ? PASA_OK : cuda_fail(e);
 }
+
+// ---------------------------------------------------------------------------------------
+// 4-bit key/value cache
+// ---------------------------------------------------------------------------------------
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The cache tensors and sizes that every kv4 entry point takes.
+int kv4_validate(const void* k4, const void* kscale, const void* v4, const void* vscale, const void* shift, int B,
+                 int Hkv, int Sk_cap, int D) {
+  if (!k4 || !kscale || !v4 || !vscale) return PASA_ERR_NULLPTR;
+  if (B <= 0 || Hkv <= 0 || Sk_cap <= 0) return PASA_ERR_SHAPE;
+  if (static_cast<long long>(B) * Hkv > INT_MAX) return PASA_ERR_SHAPE;
+  if (D != 64 && D != 128) return PASA_ERR_UNSUPPORTED;
+  if (!aligned16(k4) || !aligned16(kscale) || !aligned16(v4) || !aligned16(vscale) || !aligned16(shift))
+    return PASA_ERR_ALIGN;
+  return PASA_OK;
+}
+
+// kv4_append and kv4_read share their arguments: n rows of k and v from cache row `start` on.
+int kv4_window(const void* k, const void* v, const int* starts, int start, const int* counts, int n, int B, int Hkv,
+               int Sk_cap, int D, pasa::Kv4Window* win, unsigned* blocks) {
+  if (!k || !v) return PASA_ERR_NULLPTR;
+  if (n <= 0) return PASA_ERR_SHAPE;
+  if (!starts && (start < 0 || static_cast<long long>(start) + n > Sk_cap)) return PASA_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(starts) || !aligned4(counts)) return PASA_ERR_ALIGN;
+  const unsigned long long rows = static_cast<unsigned long long>(B) * Hkv * static_cast<unsigned long long>(n);
+  const unsigned long long grid = (rows * (D / 8) + pasa::kKv4StoreThreads - 1) / pasa::kKv4StoreThreads;
+  if (rows > (1ull << 50) || grid > INT_MAX) return PASA_ERR_SHAPE;
+  *win = pasa::Kv4Window{starts, counts, start, n, Sk_cap};
+  *blocks = static_cast<unsigned>(grid);
+  return PASA_OK;
+}
+
+int launch_status() {
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? PASA_OK : cuda_fail(e);
+}
+
+// How a decode call is laid out: query rows in tiles of 8 (NT = 1) or 16, and either one CTA per
+// (sequence, kv head, row tile), or a fixed number of CTAs sharing all their keys evenly with
+// partial results in the workspace.
+struct Kv4Plan {
+  int nt, row_tiles, ctas;
+  bool stream_k;
+  long long segments;
+  size_t part_o, part_ml, lse2, total;   // workspace: byte offsets and size
+};
+
+constexpr int kKv4WholeKeys = 512;   // up to this many keys a CTA takes a segment whole
+
+Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
+  Kv4Plan pl = {};
+  const int rows = Hq / Hkv * Sq;
+  pl.nt = rows <= 8 ? 1 : 2;
+  pl.row_tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
+  pl.segments = static_cast<long long>(B) * Hkv * pl.row_tiles;
+  pl.stream_k = Sk > kKv4WholeKeys;
+  pl.ctas = 152 * (pl.nt == 1 ? 2 : 1);
+  const size_t tile = static_cast<size_t>(8 * pl.nt);
+  const size_t slots = pl.stream_k ? static_cast<size_t>(pl.ctas + pl.segments) : 0;
+  pl.part_o = 0;
+  pl.part_ml = align_up(slots * tile * D * 4, 256);
+  pl.lse2 = pl.part_ml + align_up(slots * tile * 8, 256);
+  pl.total = pl.lse2 + (weights ? align_up(static_cast<size_t>(pl.segments) * tile * 4, 256) : 0);
+  return pl;
+}
+
+template <int D, int NT, bool STREAM_K>
+cudaError_t kv4_launch(const pasa::Kv4Params& p, unsigned grid, cudaStream_t st, bool pdl) {
+  auto kern = pasa::kv4_decode_kernel<D, NT, STREAM_K>;
+  const int smem = static_cast<int>(sizeof(pasa::Kv4Smem<D, NT>));
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(grid), dim3(pasa::kKv4Warps * 32), smem, st, pdl, p);
+}
+
+template <int D>
+cudaError_t kv4_decode_launch(const pasa::Kv4Params& p, const Kv4Plan& pl, cudaStream_t st, bool pdl) {
+  const unsigned grid = pl.stream_k ? static_cast<unsigned>(pl.ctas) : static_cast<unsigned>(pl.segments);
+  const int tile = 8 * pl.nt;
+  cudaError_t e = pl.nt == 1 ? (pl.stream_k ? kv4_launch<D, 1, true>(p, grid, st, pdl) : kv4_launch<D, 1, false>(p, grid, st, pdl))
+                             : (pl.stream_k ? kv4_launch<D, 2, true>(p, grid, st, pdl) : kv4_launch<D, 2, false>(p, grid, st, pdl));
+  if (e == cudaSuccess && pl.stream_k)
+    e = launch_kernel(pasa::kv4_merge_kernel<D>, dim3(static_cast<unsigned>(pl.segments), tile), dim3(256), 0, st, true,
+                      p, tile);
+  if (e == cudaSuccess && p.weights) {
+    const long long planes = static_cast<long long>(p.B) * p.Hkv;
+    const unsigned gy = static_cast<unsigned>(std::min<long long>(planes, 65535));
+    const unsigned gz = static_cast<unsigned>((planes + gy - 1) / gy);
+    const int units = (p.Sk + pasa::kKv4Unit - 1) / pasa::kKv4Unit;
+    const unsigned gx = static_cast<unsigned>((units + pasa::kKv4Warps - 1) / pasa::kKv4Warps);
+    e = launch_kernel(pasa::kv4_weights_kernel<D>, dim3(gx, gy, gz), dim3(pasa::kKv4Warps * 32), 0, st, true, p, tile);
+  }
+  return e;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pasa_kv4_append(const void* k, const void* v, const void* shift, void* k4, void* kscale, void* v4, void* vscale,
+                    const int* starts, int start, const int* counts, int B, int Hkv, int n, int Sk_cap, int D,
+                    void* stream) {
+  int rc = kv4_validate(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
+  if (rc != PASA_OK) return rc;
+  pasa::Kv4Window win;
+  unsigned blocks = 0;
+  rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, &win, &blocks);
+  if (rc != PASA_OK) return rc;
+  rc = check_device();
+  if (rc != PASA_OK) return rc;
+  auto kern = D == 64 ? pasa::kv4_append_kernel<64> : pasa::kv4_append_kernel<128>;
+  kern<<<dim3(blocks, 2), pasa::kKv4StoreThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      static_cast<const __half*>(k), static_cast<const __half*>(v), static_cast<const __half*>(shift),
+      static_cast<uint8_t*>(k4), static_cast<__half*>(kscale), static_cast<uint8_t*>(v4), static_cast<__half*>(vscale),
+      B, Hkv, win);
+  return launch_status();
+}
+
+int pasa_kv4_read(const void* k4, const void* kscale, const void* v4, const void* vscale, const void* shift, void* k,
+                  void* v, const int* starts, int start, const int* counts, int B, int Hkv, int n, int Sk_cap, int D,
+                  void* stream) {
+  int rc = kv4_validate(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
+  if (rc != PASA_OK) return rc;
+  pasa::Kv4Window win;
+  unsigned blocks = 0;
+  rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, &win, &blocks);
+  if (rc != PASA_OK) return rc;
+  rc = check_device();
+  if (rc != PASA_OK) return rc;
+  auto kern = D == 64 ? pasa::kv4_read_kernel<64> : pasa::kv4_read_kernel<128>;
+  kern<<<dim3(blocks, 2), pasa::kKv4StoreThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      static_cast<const uint8_t*>(k4), static_cast<const __half*>(kscale), static_cast<const uint8_t*>(v4),
+      static_cast<const __half*>(vscale), static_cast<const __half*>(shift), static_cast<__half*>(k),
+      static_cast<__half*>(v), B, Hkv, win);
+  return launch_status();
+}
+
+size_t pasa_attn_fwd_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int weights) {
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Sq <= 0 || Sk <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
+  if (static_cast<long long>(Hq / Hkv) * Sq > pasa::kTileRows) return 0;
+  return kv4_plan(B, Hq, Hkv, Sq, Sk, D, weights != 0).total;
+}
+
+int pasa_attn_fwd_decode_kv4(const void* q, const void* k4, const void* kscale, const void* v4, const void* vscale,
+                             const void* shift, const int* lengths, void* o, float* lse, float* weights, int B, int Hq,
+                             int Hkv, int Sq, int Sk, int Sk_cap, int D, int causal, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!q || !o) return PASA_ERR_NULLPTR;
+  int rc = kv4_validate(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
+  if (rc != PASA_OK) return rc;
+  if (Hq <= 0 || Sq <= 0 || Sk <= 0 || Hq % Hkv != 0 || Sk_cap < Sk) return PASA_ERR_SHAPE;
+  if (static_cast<long long>(Hq / Hkv) * Sq > pasa::kTileRows) return PASA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(weights) || !aligned4(lengths))
+    return PASA_ERR_ALIGN;
+  const Kv4Plan pl = kv4_plan(B, Hq, Hkv, Sq, Sk, D, weights != nullptr);
+  if (pl.segments > INT_MAX) return PASA_ERR_SHAPE;
+  if (pl.total > 0) {
+    if (!workspace || workspace_bytes < pl.total) return PASA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PASA_ERR_ALIGN;
+  }
+  rc = check_device();
+  if (rc != PASA_OK) return rc;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt(static_cast<float>(D));
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  pasa::Kv4Params p = {};
+  p.q = static_cast<const __half*>(q);
+  p.k4 = static_cast<const uint8_t*>(k4);
+  p.v4 = static_cast<const uint8_t*>(v4);
+  p.kscale = static_cast<const __half*>(kscale);
+  p.vscale = static_cast<const __half*>(vscale);
+  p.shift = static_cast<const __half*>(shift);
+  p.lengths = lengths;
+  p.o = static_cast<__half*>(o);
+  p.lse = lse;
+  p.weights = weights;
+  p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + pl.part_ml);
+  p.lse2 = reinterpret_cast<float*>(ws + pl.lse2);
+  p.B = B;
+  p.Hkv = Hkv;
+  p.g = Hq / Hkv;
+  p.Sq = Sq;
+  p.rows = p.g * Sq;
+  p.row_tiles = pl.row_tiles;
+  p.Sk = Sk;
+  p.cap = Sk_cap;
+  p.causal = causal ? 1 : 0;
+  p.ctas = pl.ctas;
+  p.scale = scale;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = D == 64 ? kv4_decode_launch<64>(p, pl, st, false) : kv4_decode_launch<128>(p, pl, st, false);
+  return e == cudaSuccess ? launch_status() : cuda_fail(e);
+}
+
+int pasa_cache_evict(const void* const* planes, void* const* out_planes, const int* row_bytes, int n_planes,
+                     const float* weights, float* out_weights, const int* lengths, int* index, int* new_lengths, int B,
+                     int Hkv, int Sk, int Sk_cap, int out_cap, int budget, int recent, void* stream) {
+  if (!planes || !out_planes || !row_bytes || !weights || !out_weights || !index) return PASA_ERR_NULLPTR;
+  if (B <= 0 || Hkv <= 0 || Sk <= 0 || Sk_cap < Sk) return PASA_ERR_SHAPE;
+  if (static_cast<long long>(B) * Hkv > INT_MAX) return PASA_ERR_SHAPE;
+  if (budget <= 0 || recent < 0 || recent > budget || out_cap < budget) return PASA_ERR_SHAPE;
+  if (n_planes < 1 || n_planes > pasa::kEvictPlanes) return PASA_ERR_UNSUPPORTED;
+  if (!aligned16(weights) || !aligned16(out_weights) || !aligned16(index) || !aligned4(lengths) || !aligned4(new_lengths))
+    return PASA_ERR_ALIGN;
+  pasa::EvictPlanes pl = {};
+  bool in_place = false, moved = false;
+  pl.n = n_planes;
+  for (int i = 0; i < n_planes; ++i) {
+    if (!planes[i] || !out_planes[i]) return PASA_ERR_NULLPTR;
+    if (row_bytes[i] <= 0 || row_bytes[i] > 65536) return PASA_ERR_SHAPE;
+    if (row_bytes[i] % 4 != 0) return PASA_ERR_UNSUPPORTED;
+    if (!aligned16(planes[i]) || !aligned16(out_planes[i])) return PASA_ERR_ALIGN;
+    pl.src[i] = static_cast<const unsigned char*>(planes[i]);
+    pl.dst[i] = static_cast<unsigned char*>(out_planes[i]);
+    pl.row_bytes[i] = row_bytes[i];
+    // the widest power of two up to a 32-byte sector that a row is made of (and that keeps rows aligned)
+    int w = 32;
+    while (row_bytes[i] % w != 0) w /= 2;
+    pl.width[i] = w;
+    pl.first_column[i + 1] = pl.first_column[i] + row_bytes[i] / w;
+    in_place |= planes[i] == out_planes[i];
+    moved |= planes[i] != out_planes[i];
+  }
+  // a cache moves in place as a whole, in a cache of the same size
+  in_place |= weights == out_weights;
+  moved |= weights != out_weights;
+  if (in_place && (moved || out_cap != Sk_cap)) return PASA_ERR_SHAPE;
+  if (pl.first_column[n_planes] > 65535) return PASA_ERR_SHAPE;
+  int rc = check_device();
+  if (rc != PASA_OK) return rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const unsigned planes_bh = static_cast<unsigned>(B) * static_cast<unsigned>(Hkv);
+  pasa::evict_select_kernel<<<planes_bh, pasa::kEvictThreads, 0, st>>>(weights, out_weights, lengths, index, Hkv, Sk,
+                                                                       Sk_cap, out_cap, budget, recent);
+  rc = launch_status();
+  if (rc != PASA_OK) return rc;
+  const int rows_per_cta = in_place ? budget : std::max(4 * pasa::kMoveThreads, (budget + 65534) / 65535);
+  const dim3 grid(planes_bh, pl.first_column[n_planes], (budget + rows_per_cta - 1) / rows_per_cta);
+  const cudaError_t e = launch_kernel(pasa::evict_move_kernel, grid, dim3(pasa::kMoveThreads), 0, st, true, pl, index,
+                                      new_lengths, Hkv, static_cast<long long>(Sk_cap), static_cast<long long>(out_cap),
+                                      budget, rows_per_cta);
+  return e == cudaSuccess ? launch_status() : cuda_fail(e);
+}
+
+}  // extern "C"

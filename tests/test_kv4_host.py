@@ -1,0 +1,173 @@
+"""The 4-bit cache without a GPU: the oracle's pins, and the refusals of the C ABI (every call
+below is rejected by host-side checks, so no pointer is dereferenced) and of the binding."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv4
+
+P = ctypes.c_void_p
+FAKE = 1 << 20
+MIS4, MIS16, MIS256 = FAKE + 2, FAKE + 8, FAKE + 16
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from precision_flashattention_numerics_gb300 import build
+
+    build.build()
+    import precision_flashattention_numerics_gb300 as pasa
+
+    return pasa.library()
+
+
+# ---- the oracle ----
+
+def test_hand_worked_group():
+    """max|x| = 7: scale 1, so codes are the rounded values; ties go to the even code."""
+    x = np.zeros((1, 1, 1, 32), np.float16)
+    x[0, 0, 0, :8] = [7, -7, 0.5, 1.5, 2.5, -0.5, -1.5, 3.25]
+    codes, s = kv4.quantise(x)
+    assert s.tolist() == [[[[1.0]]]]
+    want = [7, -7, 0, 2, 2, 0, -2, 3] + [0] * 24
+    assert kv4.values(codes, s)[0, 0, 0].tolist() == want
+    assert codes[0, 0, 0, 0] == (7 + 8) | ((-7 + 8) << 4)
+
+
+def test_scale_has_eight_bits_and_products_are_exact_in_fp16():
+    rng = np.random.default_rng(1)
+    x = (rng.standard_normal((1, 1, 4000, 64)) * 10.0 ** rng.uniform(-7, 4, (1, 1, 4000, 1))).astype(np.float16)
+    codes, s = kv4.quantise(x)
+    assert np.array_equal(kv4.round_bits(s, 8), s.astype(np.float64))
+    v = kv4.values(codes, s)
+    assert np.array_equal(kv4.to_fp16(v), v)
+    # within half a step of the input, where the scale is not an fp16 subnormal
+    step = np.repeat(s.astype(np.float64), 32, -1)
+    fine = step >= 2.0 ** -14
+    assert (np.abs(v - x.astype(np.float64)) <= 0.5 * step * (1 + 1e-12))[fine].all()
+
+
+def test_what_is_not_finite_or_zero():
+    x = np.zeros((1, 1, 1, 64), np.float16)
+    x[0, 0, 0, :4] = [np.nan, np.inf, -np.inf, 65504]
+    codes, s = kv4.quantise(x)
+    v = kv4.values(codes, s)[0, 0, 0]
+    assert v[0] == 0 and v[1] == v[3] == -v[2] == 7 * 9344.0 and np.isfinite(v).all()
+    assert (v[32:] == 0).all() and s[0, 0, 0, 1] == 0
+
+
+def test_fp32_route_gives_the_same_codes():
+    """The kernel multiplies by 1 / s in fp32, rounds to a multiple of 2^-14 and then to an
+    integer. Every fp16 value against every 8-bit scale of one binade (other binades are the
+    same numbers times a power of two): equal to the rounding of the exact quotient."""
+    s = (np.arange(128, 256) * 2.0 ** -7).astype(np.float32)          # 1 .. 2
+    x = np.arange(0, 0x4C01, dtype=np.uint16).view(np.float16).astype(np.float64)   # 0 .. 16
+    r = np.float32(1) / s
+    for sv, rv in zip(s, r):
+        xs = x[x <= 7.04 * float(sv)]
+        fma = np.rint((xs * float(rv) + 768.0) * 2.0 ** 14) * 2.0 ** -14   # one rounding, as an fma at 768
+        got = np.rint(fma - 768.0)
+        assert np.array_equal(got, np.rint(xs / float(sv)))
+
+
+def test_select_order_and_ties():
+    w = np.array([3, 1, 3, np.nan, 2, -0.0, 0.0, 9], np.float32)
+    assert kv4.select(w, 8, 3, 1) == [0, 2, 7]
+    assert kv4.select(w, 8, 2, 1) == [0, 7]
+    assert kv4.select(w, 7, 6, 0) == [0, 1, 2, 4, 5, 6]
+    assert kv4.select(w, 4, 3, 0) == [0, 1, 2] and kv4.select(w, 3, 3, 0) == [0, 1, 2] and kv4.select(w, 0, 3, 0) == []
+
+
+# ---- the C ABI ----
+
+def test_store_refusals(lib):
+    def store(fn, k=FAKE, v=FAKE, shift=FAKE, k4=FAKE, ks=FAKE, v4=FAKE, vs=FAKE, starts=0, start=0, counts=0, B=1, H=2,
+              n=5, cap=16, D=128):
+        p = lambda x: P(x) if x else None   # noqa: E731
+        if fn is lib.pasa_kv4_append:
+            t = [p(k), p(v), p(shift), p(k4), p(ks), p(v4), p(vs)]
+        else:
+            t = [p(k4), p(ks), p(v4), p(vs), p(shift), p(k), p(v)]
+        return fn(*t, p(starts), start, p(counts), B, H, n, cap, D, None)
+
+    for fn in (lib.pasa_kv4_append, lib.pasa_kv4_read):
+        for name in ("k", "v", "k4", "ks", "v4", "vs"):
+            assert store(fn, **{name: 0}) == -1
+            assert store(fn, **{name: MIS16}) == -4
+        assert store(fn, shift=MIS16) == -4
+        assert store(fn, starts=MIS4) == -4 and store(fn, counts=MIS4) == -4
+        for bad in ({"B": 0}, {"H": -1}, {"n": 0}, {"cap": 0}, {"start": -1}, {"start": 12}, {"n": 17}):
+            assert store(fn, **bad) == -2, bad
+        assert store(fn, start=2 ** 31 - 1, n=2 ** 31 - 1) == -2
+        assert store(fn, B=65536, H=65536) == -2                      # B * Hkv overflows
+        assert store(fn, B=2 ** 20, H=2 ** 10, n=2 ** 20, cap=2 ** 20) == -2   # grid overflows
+        assert store(fn, D=96) == -3 and store(fn, D=32) == -3
+
+
+def test_decode_refusals(lib):
+    def dec(q=FAKE, k4=FAKE, ks=FAKE, v4=FAKE, vs=FAKE, shift=0, lengths=0, o=FAKE, lse=FAKE, weights=0, B=1, Hq=8,
+            Hkv=2, Sq=1, Sk=5000, cap=5000, D=128, ws=FAKE, nbytes=None):
+        p = lambda x: P(x) if x else None   # noqa: E731
+        if nbytes is None:
+            nbytes = lib.pasa_attn_fwd_decode_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, int(bool(weights)))
+        return lib.pasa_attn_fwd_decode_kv4(p(q), p(k4), p(ks), p(v4), p(vs), p(shift), p(lengths), p(o), p(lse),
+                                            p(weights), B, Hq, Hkv, Sq, Sk, cap, D, 1, 0.0, p(ws), nbytes, None)
+
+    for name in ("q", "k4", "ks", "v4", "vs", "o"):
+        assert dec(**{name: 0}) == -1
+    for name in ("q", "k4", "ks", "v4", "vs", "o", "lse", "shift", "weights"):
+        assert dec(**{name: MIS16}) == -4
+    assert dec(lengths=MIS4) == -4
+    for bad in ({"B": 0}, {"Hq": 0}, {"Hkv": 0}, {"Hq": 7}, {"Sq": 0}, {"Sk": 0}, {"cap": 4999}):
+        assert dec(**bad, nbytes=1 << 30) == -2, bad
+    assert dec(D=96, nbytes=1 << 30) == -3
+    assert dec(Sq=33, nbytes=1 << 30) == -3                           # 4 heads x 33 rows
+    assert dec(ws=0) == -7 and dec(ws=MIS256) == -4
+    need = lib.pasa_attn_fwd_decode_kv4_workspace_bytes(1, 8, 2, 1, 5000, 128, 0)
+    assert need > 0 and dec(nbytes=need - 1) == -7
+    more = lib.pasa_attn_fwd_decode_kv4_workspace_bytes(1, 8, 2, 1, 5000, 128, 1)
+    assert more > need and dec(weights=FAKE, nbytes=need) == -7
+    assert lib.pasa_attn_fwd_decode_kv4_workspace_bytes(1, 8, 2, 1, 100, 128, 0) == 0   # a CTA per kv head
+    assert lib.pasa_attn_fwd_decode_kv4_workspace_bytes(1, 7, 2, 1, 100, 128, 0) == 0
+    assert lib.pasa_attn_fwd_decode_kv4_workspace_bytes(1, 8, 2, 33, 5000, 128, 0) == 0
+
+
+def test_evict_refusals(lib):
+    def evict(planes=(FAKE, FAKE), out=(FAKE * 2, FAKE * 2), rb=(64, 8), n=None, w=FAKE, ow=FAKE * 2, lengths=0,
+              index=FAKE, new=0, B=1, H=2, Sk=64, cap=64, out_cap=32, budget=32, recent=4):
+        p = lambda x: P(x) if x else None   # noqa: E731
+        k = max(len(planes), len(out))
+        arr = lambda t, x: (t * k)(*x)      # noqa: E731
+        return lib.pasa_cache_evict(arr(P, planes) if planes else None, arr(P, out), arr(ctypes.c_int, rb),
+                                    len(planes) if n is None else n, p(w), p(ow), p(lengths), p(index), p(new), B, H, Sk,
+                                    cap, out_cap, budget, recent, None)
+
+    assert evict(planes=()) == -1 and evict(w=0) == -1 and evict(ow=0) == -1 and evict(index=0) == -1
+    assert evict(planes=(FAKE, 0)) == -1 and evict(out=(FAKE * 2, 0)) == -1
+    for bad in ({"B": 0}, {"H": 0}, {"Sk": 0}, {"cap": 63}, {"budget": 0}, {"recent": -1}, {"recent": 33},
+                {"out_cap": 31}, {"rb": (64, 0)}, {"rb": (64, 65540)}):
+        assert evict(**bad) == -2, bad
+    assert evict(n=0) == -3 and evict(n=9) == -3 and evict(rb=(64, 6)) == -3
+    for bad in ({"planes": (FAKE, MIS16)}, {"out": (FAKE * 2, MIS16)}, {"w": MIS16}, {"ow": MIS16}, {"index": MIS16},
+                {"lengths": MIS4}, {"new": MIS4}):
+        assert evict(**bad) == -4, bad
+    # in place: everything, and in a cache of the same size
+    same = {"out": (FAKE, FAKE), "ow": FAKE, "out_cap": 64}
+    assert evict(**{**same, "out_cap": 32}) == -2
+    assert evict(**{**same, "ow": FAKE * 2}) == -2
+    assert evict(**{**same, "out": (FAKE, FAKE * 2)}) == -2
+    if not torch.cuda.is_available():
+        assert evict(**same) in (-3, -5) and evict() in (-3, -5)   # nothing wrong but the device
+
+
+# ---- the binding ----
+
+def test_binding_refuses_host_tensors_and_large_ints():
+    import precision_flashattention_numerics_gb300 as pasa
+
+    with pytest.raises(ValueError):
+        pasa._int32(2 ** 31, "start")
+    with pytest.raises(TypeError):
+        pasa._check_cuda(torch.zeros(4), "x", torch.float32, (4,), 0)
