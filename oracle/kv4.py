@@ -52,7 +52,8 @@ def values(codes, scales):
 def decode(q, kv, vv, lengths, causal, scale, shift=None):
     """O, LSE and row weights of q [B, Hq, Sq, D] on cache values kv, vv [B, Hkv, S, D]: a dict with
     o [B, Hq, Sq, D], lse, weights [B, Hkv, S], and for error bounds pv = sum_j p_j |v_j| (like o),
-    n (keys seen), sabs = max_j scale * sum_d |q_d k_jd| and vabs = sum_j |v_j|."""
+    n (keys seen), vabs = sum_j |v_j| and sabs = max_j scale * sum_groups max|k_j in group| sum |q in group|
+    (at least the sum of the magnitudes of a score's products)."""
     q = np.asarray(q, np.float64)
     B, Hq, Sq, D = q.shape
     H, S = kv.shape[1:3]
@@ -79,7 +80,8 @@ def decode(q, kv, vv, lengths, causal, scale, shift=None):
                 out["vabs"][b, h, i] = np.abs(v).sum(0)
                 out["weights"][b, h // g, :see] += p
                 out["n"][b, h, i] = see
-                out["sabs"][b, h, i] = scale * (np.abs(k) @ np.abs(q[b, h, i])).max()
+                kg = np.abs(k).reshape(see, -1, GROUP).max(-1)
+                out["sabs"][b, h, i] = scale * (kg @ np.abs(q[b, h, i]).reshape(-1, GROUP).sum(-1)).max()
     return out
 
 

@@ -616,10 +616,10 @@ def attn_fwd_decode_kv4(q, k4, kscale, v4, vscale, causal: bool = False, scale: 
     wp = None if weights is None else _check_cuda(weights, "weights", torch.float32, (B, Hkv, cap), dev)
     lib = library()
     nbytes = lib.pasa_attn_fwd_decode_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, 0 if wp is None else 1)
-    if nbytes and (workspace is None or workspace.numel() * workspace.element_size() < nbytes):
+    if workspace is not None:
+        _check_cuda(workspace, "workspace", torch.uint8, None, dev)
+    if nbytes and (workspace is None or workspace.numel() < nbytes):
         workspace = torch.empty(nbytes, device=q.device, dtype=torch.uint8)
-    elif nbytes:
-        _check_cuda(workspace, "workspace", workspace.dtype, None, dev)
     rc = lib.pasa_attn_fwd_decode_kv4(qp, *ptrs, sp, np_, op, lp, wp, B, Hq, Hkv, Sq, Sk, cap, D, int(bool(causal)),
                                       float(scale) if scale is not None else 0.0,
                                       workspace.data_ptr() if nbytes else None, nbytes, _stream())

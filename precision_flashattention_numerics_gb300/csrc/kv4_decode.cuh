@@ -37,6 +37,7 @@ namespace pasa {
 
 constexpr int kKv4Warps = 8;
 constexpr int kKv4Unit = 32;    // keys a warp takes at a time
+constexpr int kKv4SegmentStart = 16;   // units that the start and end of a segment cost a CTA
 
 struct Kv4Params {
   const __half* q;
@@ -52,7 +53,8 @@ struct Kv4Params {
   int B, Hkv, g, Sq, rows, row_tiles;      // rows = g * Sq query rows of a kv head
   int Sk, cap, causal;
   int len_add;       // added to lengths[] (a step call appends that many rows first)
-  int ctas;          // gridDim.x of the decode kernel
+  int ctas;          // gridDim.x of the stream-K decode
+  int cluster;       // CTAs that share a segment (1 with stream-K)
   float scale, scale_log2;
 
   __device__ __forceinline__ int length(int b) const {
@@ -70,16 +72,41 @@ struct Kv4Params {
 
 __device__ __forceinline__ int kv4_units(int len) { return (len + kKv4Unit - 1) / kKv4Unit; }
 
-// Units of all sequences (per kv head and row tile), summed by a whole warp.
-__device__ __forceinline__ long long kv4_sum_units(const Kv4Params& p, int b_end) {
-  if (!p.lengths) return static_cast<long long>(b_end) * kv4_units(p.Sk);
-  long long n = 0;
-  for (int b = threadIdx.x & 31; b < b_end; b += 32) n += kv4_units(p.length(b));
+// A segment's weight when segments are shared out: its units, and `start` for what every segment
+// costs a CTA (query, joining the warps, partial results).
+__device__ __forceinline__ int kv4_weight(int units, int start) { return units == 0 ? 0 : units + start; }
+
+// Weight of the first b_end sequences (per kv head and row tile), summed by a whole warp. All
+// weights of a call fit an int (checked on the host).
+__device__ __forceinline__ int kv4_sum_weight(const Kv4Params& p, int b_end, int start) {
+  if (!p.lengths) return b_end * kv4_weight(kv4_units(p.Sk), start);
+  int n = 0;
+  for (int b = threadIdx.x & 31; b < b_end; b += 32) n += kv4_weight(kv4_units(p.length(b)), start);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
   return n;
 }
 
+// The units [first(c), first(c + 1)) of CTA c of `ctas`, total >= ctas >= 1: as equal as can be.
+struct Kv4Share {
+  unsigned base, more;   // units of a CTA, and how many CTAs have one more
+  __device__ __forceinline__ Kv4Share(int total, int ctas)
+      : base(static_cast<unsigned>(total) / ctas), more(static_cast<unsigned>(total) - base * ctas) {}
+  __device__ __forceinline__ int first(unsigned c) const { return c * base + min(c, more); }
+  __device__ __forceinline__ int cta_of(unsigned u) const {
+    const unsigned split = more * (base + 1);
+    return u < split ? u / (base + 1) : more + (u - split) / base;
+  }
+};
+
+// d = A B + (c0, c1) of every output row pair: m16n8k16, fp16 in, fp32 out.
+__device__ __forceinline__ void mma_f16_init(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1, float c0, float c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
@@ -94,107 +121,209 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   return d;
 }
 
-// Codes and scales stream past once: no L1 line is kept for them.
-template <int N>
-__device__ __forceinline__ void ldg_words(uint32_t (&d)[N], const void* p) {
-  if constexpr (N == 4)
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "l"(p));
-  else if constexpr (N == 2)
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(d[0]), "=r"(d[1]) : "l"(p));
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&d)[4], uint32_t saddr) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(saddr) : "memory");
   else
-    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(d[0]) : "l"(p));
-}
-__device__ __forceinline__ uint32_t ldg_half(const __half* p) {
-  uint16_t d;
-  asm volatile("ld.global.u16 %0, [%1];" : "=h"(d) : "l"(p));
-  return d;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(saddr) : "memory");
 }
 
-// A warp's codes and scales of 32 keys of one head. Keys past the sequence's last are not
-// read: their scale is 0, and so are their values, whatever the memory holds.
+// 16 bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void cp_async16(uint32_t saddr, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr), "l"(g) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// A warp's stage of 32 rows of codes: 16-byte chunk c (channels 32 c .. 32 c + 31) of row r at
+// r * D/2 + 16 (c ^ swizzle(r)), so that the 8 rows of an 8 x 8 ldmatrix block lie in 8 different
+// bank groups.
 template <int D>
-struct Kv4Keys {
-  static constexpr int W = D / 32;   // 32-bit words of a lane's channels
-  uint32_t k[4][W], ks[4];           // keys g + 8 i
-  __device__ __forceinline__ void load(const uint8_t* k4, const __half* kscale, long long key0, int left, int lane) {
+__device__ __forceinline__ uint32_t kv4_chunk(int row, int c) {
+  return static_cast<uint32_t>(D == 128 ? row * 64 + ((c ^ ((row >> 1) & 3)) << 4) : row * 32 + ((c ^ ((row >> 2) & 1)) << 4));
+}
+
+// Start copying the codes of 32 rows to a stage; rows from `left` on are filled with zeros, not
+// read. rows: this lane's first 16 bytes (16 lane past the unit's first row); stage: likewise its
+// swizzled place, the same for all its chunks but for multiples of 512 bytes.
+template <int D>
+__device__ __forceinline__ uint32_t kv4_lane_place(int lane) { return kv4_chunk<D>(lane / (D / 32), lane % (D / 32)); }
+template <int D>
+__device__ __forceinline__ void kv4_fetch(uint32_t stage, const uint8_t* rows, int left, int lane) {
+  constexpr int kChunks = D / 32;   // per row
+  if (left >= kKv4Unit) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) cp_async16(stage + 512 * i, rows + 512 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      if ((i * 32 + lane) / kChunks < left)
+        cp_async16(stage + 512 * i, rows + 512 * i);
+      else
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(stage + 512 * i), "r"(0) : "memory");
+    }
+  }
+}
+
+// The scales of one row (D / 32 fp16), lane l holding row l's; 0 past the last row.
+template <int D>
+__device__ __forceinline__ uint2 kv4_row_scales(const __half* rows, int left, int lane) {
+  uint2 s = make_uint2(0u, 0u);
+  if (lane < left) {
+    if constexpr (D == 128)
+      s = *reinterpret_cast<const uint2*>(rows + lane * 4);
+    else
+      s.x = *reinterpret_cast<const uint32_t*>(rows + lane * 2);
+  }
+  return s;
+}
+
+// 8 query rows as S needs them, in the lanes of a warp. The scores of a group of 32 channels
+// are the MMA of raw codes: a code masked out of its byte is a subnormal fp16 number, n 2^-24 or
+// (the high nibble) n 2^-20, n = c + 8, so the query entries it meets are q' 2^4 or q', and the
+// -8 of every code is the accumulator's start, -8 2^-20 sum q'. No instruction per value but
+// the mask; the group's scale multiplies the fp32 sum. q' = q 2^e with the row's largest |q'|
+// in [2^10, 2^11): exact but for entries 2^-34 below the largest.
+template <int D>
+struct Kv4Query {
+  uint4 b[D / 32];       // per group: channels (0, 4) and (2, 6) times 16, (1, 5), (3, 7) of the lane's 8
+  float2 init[D / 32];   // columns 2t, 2t + 1
+  float2 factor;         // scores to log2 units: scale log2(e) 2^(20 - e)
+  __device__ __forceinline__ void load(const __half* rows, int n, float scale_log2, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const uint8_t* kp = k4 + (key0 + g) * (D / 2) + t * (D / 8);
-    const __half* sp = kscale + (key0 + g) * (D / 32) + t * (D / 32) / 4;
+    uint4 x[D / 32];
+    __half2 m2 = __float2half2_rn(0.0f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (g + 8 * i < left) {
-        ldg_words(k[i], kp + i * 8 * (D / 2));
-        ks[i] = ldg_half(sp + i * 8 * (D / 32));
-      } else {
+    for (int w = 0; w < D / 32; ++w) {
+      x[w] = make_uint4(0u, 0u, 0u, 0u);
+      if (g < n) x[w] = *reinterpret_cast<const uint4*>(rows + g * D + 32 * w + 8 * t);
+      m2 = __hmax2_nan(m2, __hmax2_nan(__hmax2_nan(__habs2(bits_h2(x[w].x)), __habs2(bits_h2(x[w].y))),
+                                       __hmax2_nan(__habs2(bits_h2(x[w].z)), __habs2(bits_h2(x[w].w)))));
+    }
+    __half m1 = __hmax_nan(__low2half(m2), __high2half(m2));
+    m1 = __hmax_nan(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 1));
+    m1 = __hmax_nan(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 2));
+    const float m = __half2float(m1);
+    // a row that is all 0, or not finite, is left as it is
+    const int e = m > 0.0f && m <= 65504.0f ? 137 - static_cast<int>(__float_as_uint(m) >> 23) : 0;
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    const float f = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 20 - e) << 23);
+    factor = make_float2(__shfl_sync(0xFFFFFFFFu, f, 8 * t), __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4));
+    const __half2 sixteen = __float2half2_rn(16.0f);
 #pragma unroll
-        for (int w = 0; w < W; ++w) k[i][w] = 0;
-        ks[i] = 0;
+    for (int w = 0; w < D / 32; ++w) {
+      const uint32_t in[4] = {x[w].x, x[w].y, x[w].z, x[w].w};
+      uint32_t h[4];
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 v = __half22float2(bits_h2(in[i]));
+        v.x *= up, v.y *= up;
+        const __half2 r = __float22half2_rn(v);
+        v = __half22float2(r);
+        sum += v.x + v.y;
+        h[i] = h2_bits(r);
       }
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+      sum *= -8.0f / 1048576.0f;
+      init[w] = make_float2(__shfl_sync(0xFFFFFFFFu, sum, 8 * t), __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4));
+      b[w].x = h2_bits(__hmul2(bits_h2(__byte_perm(h[0], h[2], 0x5410)), sixteen));
+      b[w].y = h2_bits(__hmul2(bits_h2(__byte_perm(h[1], h[3], 0x5410)), sixteen));
+      b[w].z = __byte_perm(h[0], h[2], 0x7632);
+      b[w].w = __byte_perm(h[1], h[3], 0x7632);
     }
   }
 };
 
+// The same in shared memory, for the warps of a CTA to share.
 template <int D>
-struct Kv4Values {
-  static constexpr int W = D / 64;
-  uint32_t v[8][W], vs[8];           // keys 16 (j / 4) + 2t + j % 2 + 8 (j / 2 % 2)
-  __device__ __forceinline__ void load(const uint8_t* v4, const __half* vscale, long long key0, int left, int lane) {
-    const int g = lane >> 2, t = lane & 3;
-    const uint8_t* vp = v4 + (key0 + 2 * t) * (D / 2) + g * (D / 16);
-    const __half* sp = vscale + (key0 + 2 * t) * (D / 32) + g * (D / 32) / 8;
+struct Kv4QueryShared {
+  uint4 b[D / 32][32];
+  float2 init[D / 32][32];
+  float2 factor[32];
+  __device__ __forceinline__ void put(const Kv4Query<D>& q, int lane) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int key = 16 * (j / 4) + (j & 1) + 8 * ((j >> 1) & 1);
-      if (2 * t + key < left) {
-        ldg_words(v[j], vp + key * (D / 2));
-        vs[j] = ldg_half(sp + key * (D / 32));
-      } else {
-#pragma unroll
-        for (int w = 0; w < W; ++w) v[j][w] = 0;
-        vs[j] = 0;
-      }
-    }
+    for (int w = 0; w < D / 32; ++w) b[w][lane] = q.b[w], init[w][lane] = q.init[w];
+    factor[lane] = q.factor;
   }
 };
 
-// The B operands of S for 8 query rows: lane (g, t) holds channels t * D/4 .. of row g in the
-// order the expanded codes have.
-template <int D>
-__device__ __forceinline__ void kv4_query(uint32_t (&q)[D / 16][2], const __half* rows, int n, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int w = 0; w < D / 32; ++w) {
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (g < n) x = *reinterpret_cast<const uint4*>(rows + g * D + t * (D / 4) + 8 * w);
-    q[2 * w][0] = __byte_perm(x.x, x.z, 0x5410);       // channels 0, 4
-    q[2 * w][1] = __byte_perm(x.x, x.z, 0x7632);       // 1, 5
-    q[2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);   // 2, 6
-    q[2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);   // 3, 7
+// S^T (unscaled) of 16 keys and 8 rows, group w's part added to acc (set where w is 0). ka, kb:
+// the lane's 8 codes of keys g and g + 8 in the group; sa, sb: their scales.
+__device__ __forceinline__ void kv4_score_group(float (&acc)[4], int w, uint32_t ka, uint32_t kb, float sa, float sb,
+                                                const uint4& qb, const float2& init) {
+  const uint32_t lo = 0x000F000Fu, hi = 0x00F000F0u;
+  const uint32_t a8 = ka >> 8, b8 = kb >> 8;
+  float d[4];
+  mma_f16_init(d, ka & lo, kb & lo, a8 & lo, b8 & lo, qb.x, qb.y, init.x, init.y);
+  mma_f16(d, ka & hi, kb & hi, a8 & hi, b8 & hi, qb.z, qb.w);
+  acc[0] = w == 0 ? sa * d[0] : fmaf(sa, d[0], acc[0]);
+  acc[1] = w == 0 ? sa * d[1] : fmaf(sa, d[1], acc[1]);
+  acc[2] = w == 0 ? sb * d[2] : fmaf(sb, d[2], acc[2]);
+  acc[3] = w == 0 ? sb * d[3] : fmaf(sb, d[3], acc[3]);
+}
+
+// One stage of a warp: 32 rows of key and value codes and their scales, the keys' as fp32
+// rows, the values' as fp16 [group][8 t + 2 blk + key % 2] for key 8 blk + 2 t + ..: the four
+// key pairs of a lane side by side.
+template <int D, bool VALUES>
+struct __align__(128) Kv4Stage {
+  uint8_t k[kKv4Unit * D / 2];
+  uint8_t v[VALUES ? kKv4Unit * D / 2 : 16];
+  float ks[kKv4Unit][D / 32];
+  __half vs[D / 32][kKv4Unit];
+};
+
+template <int D, bool VALUES>
+__device__ __forceinline__ void kv4_put_scales(Kv4Stage<D, VALUES>& st, uint2 ks, uint2 vs, int lane) {
+  const float2 a = __half22float2(bits_h2(ks.x));
+  if constexpr (D == 128) {
+    const float2 b = __half22float2(bits_h2(ks.y));
+    *reinterpret_cast<float4*>(st.ks[lane]) = make_float4(a.x, a.y, b.x, b.y);
+  } else {
+    *reinterpret_cast<float2*>(st.ks[lane]) = a;
+  }
+  if constexpr (VALUES) {
+    const int at = (lane >> 1 & 3) * 8 + (lane >> 3) * 2 + (lane & 1);
+    st.vs[0][at] = __low2half(bits_h2(vs.x));
+    st.vs[1][at] = __high2half(bits_h2(vs.x));
+    if constexpr (D == 128) {
+      st.vs[2][at] = __low2half(bits_h2(vs.y));
+      st.vs[3][at] = __high2half(bits_h2(vs.y));
+    }
   }
 }
 
-// S^T of 16 keys (half s of the unit) and NT * 8 rows.
-template <int D, int NT>
-__device__ __forceinline__ void kv4_scores(float (&acc)[NT][4], const Kv4Keys<D>& kk, int s,
-                                           const uint32_t (&q)[NT][D / 16][2]) {
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[nt][e] = 0.0f;
-  const __half2 sa = bits_h2(__byte_perm(kk.ks[2 * s], 0, 0x1010));
-  const __half2 sb = bits_h2(__byte_perm(kk.ks[2 * s + 1], 0, 0x1010));
-#pragma unroll
-  for (int w = 0; w < D / 32; ++w) {
-    __half2 a[4], b[4];
-    kv4_expand(kk.k[2 * s][w], sa, a);
-    kv4_expand(kk.k[2 * s + 1][w], sb, b);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      mma_f16(acc[nt], h2_bits(a[0]), h2_bits(b[0]), h2_bits(a[1]), h2_bits(b[1]), q[nt][2 * w][0], q[nt][2 * w][1]);
-      mma_f16(acc[nt], h2_bits(a[2]), h2_bits(b[2]), h2_bits(a[3]), h2_bits(b[3]), q[nt][2 * w + 1][0],
-              q[nt][2 * w + 1][1]);
-    }
+// The codes of keys 16 h + g (ka) and 16 h + 8 + g (kb) from a stage: word w the lane's 8
+// channels 32 w + 8 t ... `base`: the stage's key codes + kv4_key_place.
+template <int D>
+__device__ __forceinline__ uint32_t kv4_key_place(int lane) {
+  return D == 128 ? kv4_chunk<D>(lane & 7, lane >> 3) : kv4_chunk<D>(8 * (lane >> 4) + (lane & 7), (lane >> 3) & 1);
+}
+template <int D>
+__device__ __forceinline__ void kv4_take_keys(uint32_t (&ka)[D / 32], uint32_t (&kb)[D / 32], uint32_t base, int h) {
+  if constexpr (D == 128) {   // matrix j: chunk j of 8 rows
+    ldmatrix_x4<false>(ka, base + 1024 * h);
+    ldmatrix_x4<false>(kb, base + 1024 * h + 512);
+  } else {                    // matrix j: chunk j % 2 of rows 8 (j / 2) ..
+    uint32_t x[4];
+    ldmatrix_x4<false>(x, base + 512 * h);
+    ka[0] = x[0], ka[1] = x[1], kb[0] = x[2], kb[1] = x[3];
+  }
+}
+template <int D>
+__device__ __forceinline__ void kv4_take_scales(float (&s)[D / 32], const float (&row)[D / 32]) {
+  if constexpr (D == 128) {
+    const float4 x = *reinterpret_cast<const float4*>(row);
+    s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w;
+  } else {
+    const float2 x = *reinterpret_cast<const float2*>(row);
+    s[0] = x.x, s[1] = x.y;
   }
 }
 
@@ -203,12 +332,20 @@ __device__ __forceinline__ float kv4_lse(float m, float l, float offset) {
   return l == 0.0f ? -INFINITY : 0.69314718055994531f * (m + log2f(l)) + offset;
 }
 
+constexpr float kKv4NoKey = -3.0e38f;   // a running maximum before the first key: below every score
+
 template <int D, int NT>
 struct Kv4Smem {
-  float o[kKv4Warps][NT * 8][D + 4];
+  union {
+    Kv4Stage<D, true> stage[2][kKv4Warps];
+    float o[kKv4Warps][NT * 8][D + 4];   // when the stages are empty
+  };
+  Kv4QueryShared<D> q[NT];
+  float sum[NT * 8][D];                  // the CTA's O, read by the others of its cluster
   float m[kKv4Warps][NT * 8], l[kKv4Warps][NT * 8];
   float factor[kKv4Warps][NT * 8];
   float row_m[NT * 8], row_l[NT * 8], offset[NT * 8];
+  int limit[NT * 8];                     // keys a row sees
 };
 
 // scale * q . shift of a row (natural-log units), by a whole warp.
@@ -226,54 +363,89 @@ __device__ __forceinline__ float kv4_offset(const Kv4Params& p, long long bh, in
 }
 
 template <int D, int NT, bool STREAM_K>
-__global__ void __launch_bounds__(kKv4Warps * 32, NT == 1 ? 2 : 1) kv4_decode_kernel(Kv4Params p) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
+__global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params p) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
   Kv4Smem<D, NT>& sm = *reinterpret_cast<Kv4Smem<D, NT>*>(smem_raw);
   constexpr int kRows = NT * 8;
+  constexpr int kThreads = kKv4Warps * 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
+  const int rank = STREAM_K ? 0 : static_cast<int>(blockIdx.x % p.cluster);
   griddep_launch_dependents();
   griddep_wait();   // rows that the call's append kernel stores
 
   // this CTA's segments: (b, h, row tile) in order, and the units [u0, u1) of the first
-  long long u_begin = 0, u_end = 0;
-  int b = 0, u0 = 0, n_units = 0, len = 0;
-  long long in_b = 0;   // segment inside sequence b: h * row_tiles + row tile
-  const long long per_b = static_cast<long long>(p.Hkv) * p.row_tiles;
+  int todo = 0, b = 0, u0 = 0, n_units = 0, len = 0;
+  int in_b = 0;   // segment inside sequence b: h * row_tiles + row tile
+  const int per_b = p.Hkv * p.row_tiles;
   if (STREAM_K) {
-    const long long total = kv4_sum_units(p, p.B) * per_b;
-    const long long ctas = total < gridDim.x ? total : gridDim.x;
-    if (blockIdx.x >= ctas) return;
-    u_begin = static_cast<long long>(blockIdx.x) * total / ctas;
-    u_end = (static_cast<long long>(blockIdx.x) + 1) * total / ctas;
-    long long before = 0;
+    const int total = kv4_sum_weight(p, p.B, kKv4SegmentStart) * per_b;
+    const int ctas = min(total, static_cast<int>(gridDim.x));
+    if (static_cast<int>(blockIdx.x) >= ctas) return;
+    const Kv4Share share(total, ctas);
+    int before = share.first(blockIdx.x);
+    todo = share.first(blockIdx.x + 1) - before;   // weight: a segment's first kKv4SegmentStart are no units
     for (;; ++b) {
       len = p.length(b);
       n_units = kv4_units(len);
-      if (before + n_units * per_b > u_begin) break;
-      before += n_units * per_b;
+      const int weight = kv4_weight(n_units, kKv4SegmentStart);
+      if (before < weight * per_b) {
+        in_b = before / weight;
+        u0 = before - in_b * weight - kKv4SegmentStart;
+        break;
+      }
+      before -= weight * per_b;
     }
-    in_b = (u_begin - before) / n_units;
-    u0 = static_cast<int>((u_begin - before) % n_units);
   } else {
-    b = static_cast<int>(blockIdx.x / per_b);
-    in_b = blockIdx.x % per_b;
+    const int seg = blockIdx.x / p.cluster;
+    b = seg / per_b;
+    in_b = seg - b * per_b;
     len = p.length(b);
-    n_units = kv4_units(len);
-    u_end = n_units;
+    todo = n_units = kv4_units(len);
   }
 
   while (true) {
     const long long bh = static_cast<long long>(b) * p.Hkv + in_b / p.row_tiles;
-    const int row0 = static_cast<int>(in_b % p.row_tiles) * kRows;
+    const int row0 = in_b % p.row_tiles * kRows;
     const int n_rows = min(kRows, p.rows - row0);
-    const int u1 = static_cast<int>(min(static_cast<long long>(n_units), u0 + (u_end - u_begin)));
+    const int u1 = min(n_units, u0 + todo);
+    todo -= u1 - u0;
+    u0 = max(0, u0);
+    if (STREAM_K && u0 >= u1) return;   // the range ends in what a segment's start weighs
+    const int u_step = STREAM_K ? kKv4Warps : kKv4Warps * p.cluster;
 
     // ---- the warp's share of units u0 .. u1 ----
-    uint32_t q[NT][D / 16][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-      kv4_query<D>(q[nt], p.q + (bh * p.rows + row0 + nt * 8) * D, n_rows - nt * 8, lane);
+    int u = u0 + rank * kKv4Warps + warp;
+    const uint32_t stage0 = smem_u32(&sm.stage[0][warp]);
+    constexpr uint32_t kStageBytes = sizeof(Kv4Stage<D, true>) * kKv4Warps, kValues = kKv4Unit * D / 2;
+    uint2 ks = make_uint2(0u, 0u), vs = make_uint2(0u, 0u);   // row scales of the unit last fetched
+    auto fetch = [&](int unit, uint32_t stage) {
+      if (unit < u1) {
+        const long long row = bh * p.cap + static_cast<long long>(unit) * kKv4Unit;
+        const int left = len - unit * kKv4Unit;
+        const uint32_t place = stage + kv4_lane_place<D>(lane);
+        kv4_fetch<D>(place, p.k4 + row * (D / 2) + lane * 16, left, lane);
+        kv4_fetch<D>(place + kValues, p.v4 + row * (D / 2) + lane * 16, left, lane);
+        ks = kv4_row_scales<D>(p.kscale + row * (D / 32), left, lane);
+        vs = kv4_row_scales<D>(p.vscale + row * (D / 32), left, lane);
+      }
+      cp_async_commit();
+    };
+    fetch(u, stage0);
+    Kv4Query<D> q;   // NT = 1: in registers; else in shared memory, a tile per warp
+    if constexpr (NT == 1) {
+      q.load(p.q + (bh * p.rows + row0) * D, n_rows, p.scale_log2, lane);
+    } else if (warp < NT) {
+      q.load(p.q + (bh * p.rows + row0 + warp * 8) * D, n_rows - warp * 8, p.scale_log2, lane);
+      sm.q[warp].put(q, lane);
+    }
+    if (threadIdx.x < kRows) sm.limit[threadIdx.x] = p.limit(row0 + threadIdx.x, len);
+    if (rank == 0 && p.lse)
+      for (int r = warp; r < n_rows; r += kKv4Warps) {
+        const float off = kv4_offset<D>(p, bh, row0 + r, lane);
+        if (lane == 0) sm.offset[r] = off;
+      }
+    __syncthreads();
     float o[NT][D / 16][4];
     float m[NT][2], l[NT][2];
 #pragma unroll
@@ -282,36 +454,45 @@ __global__ void __launch_bounds__(kKv4Warps * 32, NT == 1 ? 2 : 1) kv4_decode_ke
       for (int i = 0; i < D / 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kKv4NoKey;
       l[nt][0] = l[nt][1] = 0.0f;
     }
-    const uint8_t* k4 = p.k4 + bh * p.cap * (D / 2);
-    const uint8_t* v4 = p.v4 + bh * p.cap * (D / 2);
-    const __half* kscale = p.kscale + bh * p.cap * (D / 32);
-    const __half* vscale = p.vscale + bh * p.cap * (D / 32);
     const int all_see = p.causal ? max(0, len - p.Sq + 1) : len;   // keys that every row sees
 
-    Kv4Keys<D> kk;
-    Kv4Values<D> vv;
-    int u = u0 + warp;
-    if (u < u1) {
-      kk.load(k4, kscale, static_cast<long long>(u) * kKv4Unit, len - u * kKv4Unit, lane);
-      vv.load(v4, vscale, static_cast<long long>(u) * kKv4Unit, len - u * kKv4Unit, lane);
-    }
-    for (; u < u1; u += kKv4Warps) {
+    uint32_t odd = 0;   // the stage at hand
+    for (; u < u1; u += u_step) {
       const int key0 = u * kKv4Unit;
-      const int next = u + kKv4Warps;
+      auto& st = sm.stage[odd][warp];
+      const uint32_t here = stage0 + odd * kStageBytes;
+      cp_async_wait<0>();
+      kv4_put_scales(st, ks, vs, lane);
+      __syncwarp();   // the stage is there, and every lane is done with the other one
+      odd ^= 1;
+      fetch(u + u_step, stage0 + odd * kStageBytes);
       float s[2][NT][4];
-      kv4_scores<D, NT>(s[0], kk, 0, q);
-      kv4_scores<D, NT>(s[1], kk, 1, q);
-      if (next < u1)
-        kk.load(k4, kscale, static_cast<long long>(next) * kKv4Unit, len - next * kKv4Unit, lane);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t ka[D / 32], kb[D / 32];
+        kv4_take_keys<D>(ka, kb, here + kv4_key_place<D>(lane), h);
+        float sa[D / 32], sb[D / 32];
+        kv4_take_scales<D>(sa, st.ks[16 * h + g]);
+        kv4_take_scales<D>(sb, st.ks[16 * h + 8 + g]);
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (NT == 1)
+              kv4_score_group(s[h][nt], w, ka[w], kb[w], sa[w], sb[w], q.b[w], q.init[w]);
+            else
+              kv4_score_group(s[h][nt], w, ka[w], kb[w], sa[w], sb[w], sm.q[nt].b[w][lane], sm.q[nt].init[w][lane]);
+          }
+      }
       if (key0 + kKv4Unit > all_see) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int lim = p.limit(row0 + nt * 8 + 2 * t + c, len) - key0 - g;
+            const int lim = sm.limit[nt * 8 + 2 * t + c] - key0 - g;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               if (16 * h >= lim) s[h][nt][c] = -INFINITY;
@@ -321,15 +502,18 @@ __global__ void __launch_bounds__(kKv4Warps * 32, NT == 1 ? 2 : 1) kv4_decode_ke
       }
       // the reference a row's exponentials are taken against moves only when a score passes it
       // by more than 8 (log2 units): P stays below 2^8, and most units need no reduction
+      uint32_t pb[2][NT][2];
       bool grow = false;
       float mx[NT][2];
+      float2 factor[NT];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          mx[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][2 + c]), fmaxf(s[1][nt][c], s[1][nt][2 + c])) * p.scale_log2;
-          grow |= mx[nt][c] > m[nt][c] + 8.0f;
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+        factor[nt] = NT == 1 ? q.factor : sm.q[nt].factor[lane];
+        mx[nt][0] = fmaxf(fmaxf(s[0][nt][0], s[0][nt][2]), fmaxf(s[1][nt][0], s[1][nt][2])) * factor[nt].x;
+        mx[nt][1] = fmaxf(fmaxf(s[0][nt][1], s[0][nt][3]), fmaxf(s[1][nt][1], s[1][nt][3])) * factor[nt].y;
+        grow |= mx[nt][0] > m[nt][0] + 8.0f;
+        grow |= mx[nt][1] > m[nt][1] + 8.0f;
+      }
       if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -340,7 +524,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, NT == 1 ? 2 : 1) kv4_decode_ke
             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
             x = fmaxf(x, m[nt][c]);
-            const float f = m[nt][c] == x ? 1.0f : ex2_approx(m[nt][c] - x);
+            const float f = ex2_approx(m[nt][c] - x);
             m[nt][c] = x;
             l[nt][c] *= f;
 #pragma unroll
@@ -350,47 +534,42 @@ __global__ void __launch_bounds__(kKv4Warps * 32, NT == 1 ? 2 : 1) kv4_decode_ke
             }
           }
       }
-      uint32_t pb[2][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float r0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
-        const float r1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float e[4];
+          const float e0 = ex2_approx(fmaf(s[h][nt][0], factor[nt].x, -m[nt][0]));
+          const float e1 = ex2_approx(fmaf(s[h][nt][1], factor[nt].y, -m[nt][1]));
+          const float e2 = ex2_approx(fmaf(s[h][nt][2], factor[nt].x, -m[nt][0]));
+          const float e3 = ex2_approx(fmaf(s[h][nt][3], factor[nt].y, -m[nt][1]));
+          l[nt][0] += e0 + e2;
+          l[nt][1] += e1 + e3;
+          pb[h][nt][0] = movmatrix(h2_bits(__floats2half2_rn(e0, e1)));
+          pb[h][nt][1] = movmatrix(h2_bits(__floats2half2_rn(e2, e3)));
+        }
+      // O^T += V^T P^T, a group of 32 channels at a time: a transposed 8 x 8 block of 16-bit words
+      // is 4 channels (4 g ..) of the two keys 8 blk + 2 t, + 1
 #pragma unroll
-          for (int c = 0; c < 4; ++c) e[c] = ex2_approx(fmaf(s[h][nt][c], p.scale_log2, -((c & 1) ? r1 : r0)));
-          l[nt][0] += e[0] + e[2];
-          l[nt][1] += e[1] + e[3];
-          pb[h][nt][0] = movmatrix(h2_bits(__floats2half2_rn(e[0], e[1])));
-          pb[h][nt][1] = movmatrix(h2_bits(__floats2half2_rn(e[2], e[3])));
+      for (int j = 0; j < D / 32; ++j) {
+        uint32_t v[4];
+        ldmatrix_x4<true>(v, (here + kValues + kv4_chunk<D>(lane, 0)) ^ (j << 4));   // chunk j: stages are 128-byte aligned
+        const uint4 sv = *reinterpret_cast<const uint4*>(&st.vs[j][8 * t]);
+        const uint32_t s2[4] = {sv.x, sv.y, sv.z, sv.w};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          __half2 a[4], c[4];
+          kv4_expand(v[2 * h], bits_h2(s2[2 * h]), a);
+          kv4_expand(v[2 * h + 1], bits_h2(s2[2 * h + 1]), c);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16(o[nt][2 * j], h2_bits(a[0]), h2_bits(a[1]), h2_bits(c[0]), h2_bits(c[1]), pb[h][nt][0], pb[h][nt][1]);
+            mma_f16(o[nt][2 * j + 1], h2_bits(a[2]), h2_bits(a[3]), h2_bits(c[2]), h2_bits(c[3]), pb[h][nt][0],
+                    pb[h][nt][1]);
+          }
         }
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const __half2 sa = bits_h2(__byte_perm(vv.vs[4 * h], vv.vs[4 * h + 1], 0x5410));
-        const __half2 sb = bits_h2(__byte_perm(vv.vs[4 * h + 2], vv.vs[4 * h + 3], 0x5410));
-#pragma unroll
-        for (int w = 0; w < D / 64; ++w)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            // nibbles 4 half .. 4 half + 3 of two keys side by side, then expanded in key pairs
-            const uint32_t sel = half ? 0x7632 : 0x5410;
-            __half2 a[4], c[4];
-            kv4_expand(__byte_perm(vv.v[4 * h][w], vv.v[4 * h + 1][w], sel), sa, a);
-            kv4_expand(__byte_perm(vv.v[4 * h + 2][w], vv.v[4 * h + 3][w], sel), sb, c);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const int i = 4 * w + 2 * half;
-              mma_f16(o[nt][i], h2_bits(a[0]), h2_bits(a[1]), h2_bits(c[0]), h2_bits(c[1]), pb[h][nt][0], pb[h][nt][1]);
-              mma_f16(o[nt][i + 1], h2_bits(a[2]), h2_bits(a[3]), h2_bits(c[2]), h2_bits(c[3]), pb[h][nt][0],
-                      pb[h][nt][1]);
-            }
-          }
-      }
-      if (next < u1)
-        vv.load(v4, vscale, static_cast<long long>(next) * kKv4Unit, len - next * kKv4Unit, lane);
     }
+    __syncthreads();   // no stage is read or written any more: their space is free
 
     // ---- join the warps ----
 #pragma unroll
@@ -408,65 +587,90 @@ __global__ void __launch_bounds__(kKv4Warps * 32, NT == 1 ? 2 : 1) kv4_decode_ke
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          *reinterpret_cast<float2*>(&sm.o[warp][r][g * (D / 8) + 2 * i]) = make_float2(o[nt][i][c], o[nt][i][2 + c]);
+          *reinterpret_cast<float2*>(&sm.o[warp][r][32 * (i / 2) + 4 * g + 2 * (i % 2)]) =
+              make_float2(o[nt][i][c], o[nt][i][2 + c]);
       }
     __syncthreads();
     const long long seg = static_cast<long long>(b) * per_b + in_b;
-    const bool whole = u0 == 0 && u1 == n_units;
-    for (int r = threadIdx.x; r < n_rows; r += kKv4Warps * 32) {
+    const bool whole = u0 == 0 && u1 == n_units;   // the CTA, or its cluster, has all of the segment
+    if (threadIdx.x < n_rows) {
+      const int r = threadIdx.x;
       float mm = sm.m[0][r];
 #pragma unroll
       for (int w = 1; w < kKv4Warps; ++w) mm = fmaxf(mm, sm.m[w][r]);
       float ll = 0.0f;
 #pragma unroll
       for (int w = 0; w < kKv4Warps; ++w) {
-        // a warp that saw no key of this row has max -inf and sum 0
-        const float f = sm.m[w][r] == -INFINITY ? 0.0f : ex2_approx(sm.m[w][r] - mm);
+        const float f = ex2_approx(sm.m[w][r] - mm);   // a warp without a key of this row has sum 0
         sm.factor[w][r] = f;
         ll = fmaf(f, sm.l[w][r], ll);
       }
       sm.row_m[r] = mm;
       sm.row_l[r] = ll;
     }
-    if (whole)
-      for (int r = warp; r < n_rows; r += kKv4Warps) {
-        const float off = kv4_offset<D>(p, bh, row0 + r, lane);
-        if (lane == 0) sm.offset[r] = off;
-      }
     __syncthreads();
     const long long out0 = bh * p.rows + row0;
-    const long long slot = (blockIdx.x + seg) * kRows;
-    for (int idx = threadIdx.x; idx < n_rows * (D / 2); idx += kKv4Warps * 32) {
-      const int r = idx / (D / 2), ch = idx % (D / 2) * 2;
-      float x = 0.0f, y = 0.0f;
+    const bool alone = STREAM_K || p.cluster == 1;
+    if (!alone || !whole) {
+      // the CTA's own sums: to its cluster, or to the workspace
+      const long long slot = (blockIdx.x + seg) * kRows;
+      for (int idx = threadIdx.x; idx < n_rows * (D / 2); idx += kThreads) {
+        const int r = idx / (D / 2), ch = idx % (D / 2) * 2;
+        float2 x = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < kKv4Warps; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(&sm.o[w][r][ch]);
-        x = fmaf(sm.factor[w][r], v.x, x);
-        y = fmaf(sm.factor[w][r], v.y, y);
+        for (int w = 0; w < kKv4Warps; ++w) {
+          const float2 v = *reinterpret_cast<const float2*>(&sm.o[w][r][ch]);
+          x.x = fmaf(sm.factor[w][r], v.x, x.x);
+          x.y = fmaf(sm.factor[w][r], v.y, x.y);
+        }
+        *reinterpret_cast<float2*>(alone ? p.part_o + (slot + r) * D + ch : &sm.sum[r][ch]) = x;
       }
-      if (whole) {
-        const float ll = sm.row_l[r];
+      if (alone && threadIdx.x < n_rows) p.part_ml[slot + threadIdx.x] = make_float2(sm.row_m[threadIdx.x], sm.row_l[threadIdx.x]);
+    }
+    if (!alone) cluster_sync_all();
+    if (whole) {
+      const int parts = alone ? kKv4Warps : p.cluster;
+      for (int idx = threadIdx.x + rank * kThreads; idx < n_rows * (D / 2); idx += kThreads * p.cluster) {
+        const int r = idx / (D / 2), ch = idx % (D / 2) * 2;
+        float mm = sm.row_m[r], ll = sm.row_l[r];
+        float2 x = make_float2(0.0f, 0.0f);
+        if (alone) {
+#pragma unroll
+          for (int w = 0; w < kKv4Warps; ++w) {
+            const float2 v = *reinterpret_cast<const float2*>(&sm.o[w][r][ch]);
+            x.x = fmaf(sm.factor[w][r], v.x, x.x);
+            x.y = fmaf(sm.factor[w][r], v.y, x.y);
+          }
+        } else {
+          mm = kKv4NoKey, ll = 0.0f;
+          for (int w = 0; w < parts; ++w) mm = fmaxf(mm, ld_shared_cluster_f32(mapa_shared(smem_u32(&sm.row_m[r]), w)));
+          for (int w = 0; w < parts; ++w) {
+            const float f = ex2_approx(ld_shared_cluster_f32(mapa_shared(smem_u32(&sm.row_m[r]), w)) - mm);
+            const uint32_t at = mapa_shared(smem_u32(&sm.sum[r][ch]), w);
+            ll = fmaf(f, ld_shared_cluster_f32(mapa_shared(smem_u32(&sm.row_l[r]), w)), ll);
+            x.x = fmaf(f, ld_shared_cluster_f32(at), x.x);
+            x.y = fmaf(f, ld_shared_cluster_f32(at + 4), x.y);
+          }
+        }
         const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-        *reinterpret_cast<__half2*>(p.o + (out0 + r) * D + ch) = __floats2half2_rn(x * inv, y * inv);
-      } else {
-        *reinterpret_cast<float2*>(p.part_o + (slot + r) * D + ch) = make_float2(x, y);
+        *reinterpret_cast<__half2*>(p.o + (out0 + r) * D + ch) = __floats2half2_rn(x.x * inv, x.y * inv);
+        if (ch == 0) {
+          if (p.lse) {
+            float off = 0.0f;
+            if (alone) off = sm.offset[r]; else off = ld_shared_cluster_f32(mapa_shared(smem_u32(&sm.offset[r]), 0));
+            p.lse[out0 + r] = kv4_lse(mm, ll, off);
+          }
+          if (p.weights) p.lse2[seg * kRows + r] = ll == 0.0f ? INFINITY : mm + log2f(ll);
+        }
       }
     }
-    for (int r = threadIdx.x; r < n_rows; r += kKv4Warps * 32) {
-      const float mm = sm.row_m[r], ll = sm.row_l[r];
-      if (whole) {
-        if (p.lse) p.lse[out0 + r] = kv4_lse(mm, ll, sm.offset[r]);
-        if (p.weights) p.lse2[seg * kRows + r] = ll == 0.0f ? INFINITY : mm + log2f(ll);
-      } else {
-        p.part_ml[slot + r] = make_float2(mm, ll);
-      }
+    if (!STREAM_K) {
+      if (!alone) cluster_sync_all();   // the others have read this CTA's sums
+      return;
     }
-    if (!STREAM_K) return;
     // ---- next segment ----
-    u_begin += u1 - u0;
-    if (u_begin >= u_end) return;
-    u0 = 0;
+    if (todo <= 0) return;
+    u0 = -kKv4SegmentStart;
     if (++in_b == per_b) {
       in_b = 0;
       do {
@@ -486,7 +690,6 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
   __shared__ float sl[8];
   __shared__ float s_m, s_off;
   griddep_launch_dependents();
-  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long seg = blockIdx.x;
   const long long per_b = static_cast<long long>(p.Hkv) * p.row_tiles;
@@ -505,13 +708,18 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
     }
     return;
   }
-  const long long total = kv4_sum_units(p, p.B) * per_b;
-  const long long ctas = total < p.ctas ? total : p.ctas;
-  const long long t0 = kv4_sum_units(p, b) * per_b + in_b * n_units;
-  // the CTA of unit u takes the range with u in [c total / ctas, (c + 1) total / ctas)
-  const long long c0 = ((t0 + 1) * ctas - 1) / total, c1 = ((t0 + n_units) * ctas - 1) / total;
+  const int weight = kv4_weight(n_units, kKv4SegmentStart);
+  const int total = kv4_sum_weight(p, p.B, kKv4SegmentStart) * static_cast<int>(per_b);
+  const Kv4Share share(total, min(total, p.ctas));
+  const int t0 = kv4_sum_weight(p, b, kKv4SegmentStart) * static_cast<int>(per_b) + static_cast<int>(in_b) * weight;
+  const int c0 = share.cta_of(t0 + kKv4SegmentStart), c1 = share.cta_of(t0 + weight - 1);
   if (c0 == c1) return;   // finished where it was computed
-  float mm = -INFINITY;
+  if (warp == 0) {
+    const float off = kv4_offset<D>(p, bh, row, lane);
+    if (lane == 0) s_off = off;
+  }
+  griddep_wait();   // the partials
+  float mm = kKv4NoKey;
   for (long long c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, p.part_ml[(c + seg) * tile_rows + r].x);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, d));
@@ -521,7 +729,7 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
   for (long long c = c0 + warp; c <= c1; c += 8) {
     const long long at = (c + seg) * tile_rows + r;
     const float2 ml = p.part_ml[at];
-    const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mm);
+    const float f = ex2_approx(ml.x - mm);
     ll = fmaf(f, ml.y, ll);
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(f, p.part_o[at * D + e * 32 + lane], acc[e]);
@@ -529,10 +737,7 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) so[warp][e * 32 + lane] = acc[e];
   if (lane == 0) sl[warp] = ll;
-  if (warp == 0) {
-    const float off = kv4_offset<D>(p, bh, row, lane);
-    if (lane == 0) s_m = mm, s_off = off;
-  }
+  if (threadIdx.x == 0) s_m = mm;
   __syncthreads();
   ll = 0.0f;
 #pragma unroll
@@ -554,48 +759,125 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
 // key codes (half of the cache's bytes), which needs no buffer of rows x keys scores. One warp
 // per 32-key unit, each weight summed and stored by one lane: the same order every time.
 template <int D>
-__global__ void __launch_bounds__(kKv4Warps * 32) kv4_weights_kernel(Kv4Params p, int tile_rows) {
-  griddep_wait();
+struct Kv4WeightsSmem {
+  Kv4Stage<D, false> stage[2][kKv4Warps];
+  float ref[128];            // a row's log2-sum-exp2
+  int limit[128];
+  Kv4QueryShared<D> q[16];   // as many as the rows have tiles of 8
+};
+
+template <int D>
+__global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Params p, int tile_rows) {
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  Kv4WeightsSmem<D>& sm = *reinterpret_cast<Kv4WeightsSmem<D>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const long long bh = blockIdx.y + static_cast<long long>(blockIdx.z) * gridDim.y;
-  if (bh >= static_cast<long long>(p.B) * p.Hkv) return;
-  const int len = p.length(static_cast<int>(bh / p.Hkv));
-  const int all_see = p.causal ? max(0, len - p.Sq + 1) : len;
-  const uint8_t* k4 = p.k4 + bh * p.cap * (D / 2);
-  const __half* kscale = p.kscale + bh * p.cap * (D / 32);
-  const int n_units = kv4_units(len);
-  for (int u = blockIdx.x * kKv4Warps + warp; u < n_units; u += gridDim.x * kKv4Warps) {
-    const int key0 = u * kKv4Unit;
-    Kv4Keys<D> kk;
-    kk.load(k4, kscale, key0, len - key0, lane);
-    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // keys g + 8 i
-    for (int r0 = 0; r0 < p.rows; r0 += 8) {
-      uint32_t q[1][D / 16][2];
-      kv4_query<D>(q[0], p.q + (bh * p.rows + r0) * D, p.rows - r0, lane);
-      float s[2][1][4];
-      kv4_scores<D, 1>(s[0], kk, 0, q);
-      kv4_scores<D, 1>(s[1], kk, 1, q);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = r0 + 2 * t + c;
-        if (r >= p.rows) continue;
-        const long long seg = bh * p.row_tiles + r / tile_rows;
-        const float ref = p.lse2[seg * tile_rows + r % tile_rows];
-        const int lim = (key0 + kKv4Unit > all_see ? p.limit(r, len) : len) - key0 - g;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (8 * i < lim) sum[i] += ex2_approx(fmaf(s[i / 2][0][2 * (i % 2) + c], p.scale_log2, -ref));
+  const int total = kv4_sum_weight(p, p.B, 0) * p.Hkv;
+  const int ctas = min(total, static_cast<int>(gridDim.x));
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const Kv4Share share(total, ctas);
+  int u0 = share.first(blockIdx.x), todo = share.first(blockIdx.x + 1) - u0;
+  int b = 0, len, n_units;
+  for (;; ++b) {
+    len = p.length(b);
+    n_units = kv4_units(len);
+    if (u0 < n_units * p.Hkv) break;
+    u0 -= n_units * p.Hkv;
+  }
+  int h = u0 / n_units;
+  u0 -= h * n_units;
+  griddep_wait();   // lse2
+  while (true) {
+    const long long bh = static_cast<long long>(b) * p.Hkv + h;
+    const int u1 = min(n_units, u0 + todo);
+    const uint8_t* k4 = p.k4 + bh * p.cap * (D / 2);
+    const __half* kscale = p.kscale + bh * p.cap * (D / 32);
+    const uint32_t stage0 = smem_u32(&sm.stage[0][warp]);
+    constexpr uint32_t kStageBytes = sizeof(Kv4Stage<D, false>) * kKv4Warps;
+    uint2 ks = make_uint2(0u, 0u);
+    auto fetch = [&](int unit, uint32_t stage) {
+      if (unit < u1) {
+        const long long key = static_cast<long long>(unit) * kKv4Unit;
+        const int left = len - unit * kKv4Unit;
+        kv4_fetch<D>(stage + kv4_lane_place<D>(lane), k4 + key * (D / 2) + lane * 16, left, lane);
+        ks = kv4_row_scales<D>(kscale + key * (D / 32), left, lane);
       }
+      cp_async_commit();
+    };
+    int u = u0 + warp;
+    fetch(u, stage0);
+    for (int i = warp; i * 8 < p.rows; i += kKv4Warps) {
+      Kv4Query<D> q;
+      q.load(p.q + (bh * p.rows + i * 8) * D, p.rows - i * 8, p.scale_log2, lane);
+      sm.q[i].put(q, lane);
     }
+    for (int r = threadIdx.x; r < (p.rows + 7) / 8 * 8; r += kKv4Warps * 32) {
+      // a row past the last, or without a key, weighs nothing
+      sm.ref[r] = r < p.rows ? p.lse2[(bh * p.row_tiles + r / tile_rows) * tile_rows + r % tile_rows] : INFINITY;
+      sm.limit[r] = p.limit(r, len);
+    }
+    __syncthreads();
+    const int all_see = p.causal ? max(0, len - p.Sq + 1) : len;
+    uint32_t odd = 0;
+    for (; u < u1; u += kKv4Warps) {
+      const int key0 = u * kKv4Unit;
+      auto& st = sm.stage[odd][warp];
+      const uint32_t here = stage0 + odd * kStageBytes;
+      cp_async_wait<0>();
+      kv4_put_scales(st, ks, ks, lane);
+      __syncwarp();
+      odd ^= 1;
+      fetch(u + kKv4Warps, stage0 + odd * kStageBytes);
+      const bool masked = key0 + kKv4Unit > all_see;
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // keys g + 8 i
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
-      sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
+      for (int half = 0; half < 2; ++half) {
+        uint32_t ka[D / 32], kb[D / 32];
+        kv4_take_keys<D>(ka, kb, here + kv4_key_place<D>(lane), half);
+        float sa[D / 32], sb[D / 32];
+        kv4_take_scales<D>(sa, st.ks[16 * half + g]);
+        kv4_take_scales<D>(sb, st.ks[16 * half + 8 + g]);
+        for (int r0 = 0; r0 < p.rows; r0 += 8) {
+          const auto& q = sm.q[r0 / 8];
+          float s[4];
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w)
+            kv4_score_group(s, w, ka[w], kb[w], sa[w], sb[w], q.b[w][lane], q.init[w][lane]);
+          const float2 factor = q.factor[lane], ref = *reinterpret_cast<const float2*>(&sm.ref[r0 + 2 * t]);
+          float e[4] = {ex2_approx(fmaf(s[0], factor.x, -ref.x)), ex2_approx(fmaf(s[1], factor.y, -ref.y)),
+                        ex2_approx(fmaf(s[2], factor.x, -ref.x)), ex2_approx(fmaf(s[3], factor.y, -ref.y))};
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int lim = sm.limit[r0 + 2 * t + c] - key0 - 16 * half - g;
+              if (lim <= 0) e[c] = 0.0f;
+              if (lim <= 8) e[2 + c] = 0.0f;
+            }
+          }
+          sum[2 * half] += e[0] + e[1];
+          sum[2 * half + 1] += e[2] + e[3];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
+        sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
+      }
+      const float mine = t == 0 ? sum[0] : t == 1 ? sum[1] : t == 2 ? sum[2] : sum[3];
+      const int key = key0 + g + 8 * t;
+      if (key < len) p.weights[bh * p.cap + key] += mine;
     }
-    const float mine = t == 0 ? sum[0] : t == 1 ? sum[1] : t == 2 ? sum[2] : sum[3];
-    const int key = key0 + g + 8 * t;
-    if (key < len) p.weights[bh * p.cap + key] += mine;
+    todo -= u1 - u0;
+    if (todo <= 0) return;
+    u0 = 0;
+    if (++h == p.Hkv) {
+      h = 0;
+      do {
+        len = p.length(++b);
+        n_units = kv4_units(len);
+      } while (n_units == 0);
+    }
+    __syncthreads();   // queries, references and limits are the next head's
   }
 }
 

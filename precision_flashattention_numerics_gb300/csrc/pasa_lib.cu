@@ -2,6 +2,7 @@
 // descriptor encoding, workspace layout and kernel dispatch. Compiled as one translation
 // unit for sm_103a.
 #include <climits>
+#include <cstddef>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -1453,13 +1454,16 @@ int launch_status() {
 // (sequence, kv head, row tile), or a fixed number of CTAs sharing all their keys evenly with
 // partial results in the workspace.
 struct Kv4Plan {
-  int nt, row_tiles, ctas;
+  int nt, row_tiles, ctas, cluster;
   bool stream_k;
   long long segments;
   size_t part_o, part_ml, lse2, total;   // workspace: byte offsets and size
 };
 
-constexpr int kKv4WholeKeys = 512;   // up to this many keys a CTA takes a segment whole
+#ifndef CU
+#define CU 4
+#endif
+constexpr int kKv4ClusterUnits = CU;
 
 Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   Kv4Plan pl = {};
@@ -1467,8 +1471,12 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   pl.nt = rows <= 8 ? 1 : 2;
   pl.row_tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
   pl.segments = static_cast<long long>(B) * Hkv * pl.row_tiles;
-  pl.stream_k = Sk > kKv4WholeKeys;
-  pl.ctas = 152 * (pl.nt == 1 ? 2 : 1);
+  pl.ctas = 152 * 2;
+  const int units = (Sk + pasa::kKv4Unit - 1) / pasa::kKv4Unit;
+  pl.cluster = 1;
+  while (pl.cluster < 8 && pl.segments * pl.cluster * 2 <= pl.ctas && units > pasa::kKv4Warps * pl.cluster) pl.cluster *= 2;
+  pl.stream_k = units > pasa::kKv4Warps * pl.cluster * kKv4ClusterUnits;
+  if (pl.stream_k) pl.cluster = 1;
   const size_t tile = static_cast<size_t>(8 * pl.nt);
   const size_t slots = pl.stream_k ? static_cast<size_t>(pl.ctas + pl.segments) : 0;
   pl.part_o = 0;
@@ -1478,18 +1486,41 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   return pl;
 }
 
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kern)(Params...), unsigned grid, int block, int smem, cudaStream_t st, bool pdl,
+                            int cluster, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  if (pdl) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = cluster;
+    attr[cfg.numAttrs].val.clusterDim.y = 1;
+    attr[cfg.numAttrs++].val.clusterDim.z = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
 template <int D, int NT, bool STREAM_K>
 cudaError_t kv4_launch(const pasa::Kv4Params& p, unsigned grid, cudaStream_t st, bool pdl) {
   auto kern = pasa::kv4_decode_kernel<D, NT, STREAM_K>;
   const int smem = static_cast<int>(sizeof(pasa::Kv4Smem<D, NT>));
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(grid), dim3(pasa::kKv4Warps * 32), smem, st, pdl, p);
+  return launch_clusters(kern, grid, pasa::kKv4Warps * 32, smem, st, pdl, p.cluster, p);
 }
 
 template <int D>
 cudaError_t kv4_decode_launch(const pasa::Kv4Params& p, const Kv4Plan& pl, cudaStream_t st, bool pdl) {
-  const unsigned grid = pl.stream_k ? static_cast<unsigned>(pl.ctas) : static_cast<unsigned>(pl.segments);
+  const unsigned grid = static_cast<unsigned>(pl.stream_k ? pl.ctas : pl.segments * pl.cluster);
   const int tile = 8 * pl.nt;
   cudaError_t e = pl.nt == 1 ? (pl.stream_k ? kv4_launch<D, 1, true>(p, grid, st, pdl) : kv4_launch<D, 1, false>(p, grid, st, pdl))
                              : (pl.stream_k ? kv4_launch<D, 2, true>(p, grid, st, pdl) : kv4_launch<D, 2, false>(p, grid, st, pdl));
@@ -1497,12 +1528,10 @@ cudaError_t kv4_decode_launch(const pasa::Kv4Params& p, const Kv4Plan& pl, cudaS
     e = launch_kernel(pasa::kv4_merge_kernel<D>, dim3(static_cast<unsigned>(pl.segments), tile), dim3(256), 0, st, true,
                       p, tile);
   if (e == cudaSuccess && p.weights) {
-    const long long planes = static_cast<long long>(p.B) * p.Hkv;
-    const unsigned gy = static_cast<unsigned>(std::min<long long>(planes, 65535));
-    const unsigned gz = static_cast<unsigned>((planes + gy - 1) / gy);
-    const int units = (p.Sk + pasa::kKv4Unit - 1) / pasa::kKv4Unit;
-    const unsigned gx = static_cast<unsigned>((units + pasa::kKv4Warps - 1) / pasa::kKv4Warps);
-    e = launch_kernel(pasa::kv4_weights_kernel<D>, dim3(gx, gy, gz), dim3(pasa::kKv4Warps * 32), 0, st, true, p, tile);
+    const int smem = static_cast<int>(offsetof(pasa::Kv4WeightsSmem<D>, q) + sizeof(pasa::Kv4QueryShared<D>) * ((p.rows + 7) / 8));
+    e = cudaFuncSetAttribute(pasa::kv4_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+      e = launch_kernel(pasa::kv4_weights_kernel<D>, dim3(static_cast<unsigned>(pl.ctas)), dim3(pasa::kKv4Warps * 32), smem, st, true, p, tile);
   }
   return e;
 }
@@ -1567,7 +1596,8 @@ int pasa_attn_fwd_decode_kv4(const void* q, const void* k4, const void* kscale, 
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(weights) || !aligned4(lengths))
     return PASA_ERR_ALIGN;
   const Kv4Plan pl = kv4_plan(B, Hq, Hkv, Sq, Sk, D, weights != nullptr);
-  if (pl.segments > INT_MAX) return PASA_ERR_SHAPE;
+  // grids and weights fit an int
+  if (pl.segments * ((Sk + pasa::kKv4Unit - 1) / pasa::kKv4Unit + pasa::kKv4SegmentStart) > INT_MAX) return PASA_ERR_SHAPE;
   if (pl.total > 0) {
     if (!workspace || workspace_bytes < pl.total) return PASA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PASA_ERR_ALIGN;
@@ -1600,6 +1630,7 @@ int pasa_attn_fwd_decode_kv4(const void* q, const void* k4, const void* kscale, 
   p.cap = Sk_cap;
   p.causal = causal ? 1 : 0;
   p.ctas = pl.ctas;
+  p.cluster = pl.cluster;
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);

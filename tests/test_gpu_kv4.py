@@ -119,10 +119,12 @@ def test_uneven_starts_and_counts(D):
 def decode_bounds(ref, scale, D, g, Sq, q, shift):
     """Bounds on |o - ref|, |lse - ref| and |weights - ref| (of values starting at 0).
 
-    ds: a score's absolute error. The fp32 sum of D products errs by at most D 2^-23 of the sum
-        of their magnitudes (an adder that truncates), its product with scale log2(e) and the
-        difference from the running reference by 2^-22 of |x| <= sabs, plus 2^-20 for numbers
-        below the reference (within 8 + |x|) and for ex2.approx (2^-22 relative).
+    ds: a score's absolute error. A group of 32 channels is the fp32 sum, in two MMAs, of 32
+        products n q (n = code + 8, up to 15) and of -8 sum q: 17 terms at a time, each cut at
+        2^-24 of at most 23 sum|q|, together 2 * 17 * 23 2^-24 sum|q| s, and max|k| of a group is
+        7 s: at most 56 2^-23 sum|q| max|k|, within D 2^-23 of sabs. Joining the groups, the product
+        with scale log2(e) and the difference from the running reference add 2^-21 of
+        |x| <= sabs, and 2^-19 numbers within 8 of it and ex2.approx (2^-22 relative).
     o:  each p moves by a factor within e^(2 ds) (its own error and the sum's), P is rounded to
         fp16 (2^-11 relative, or 2^-25 absolute against a sum of at least 1), the sum of n terms
         in fp32 errs by (n / 16 + 2) 2^-23, and the output is rounded (2^-11, or 2^-25)."""
@@ -170,6 +172,8 @@ DECODE = [
     (2, 14, 2, 18, 777, 780, 128, True, [777, 100], True),   # 126 rows: 8 row tiles
     (1, 2, 1, 64, 70, 70, 64, True, None, False),            # 128 rows
     (1, 4, 4, 1, 40000, 40000, 64, False, None, False),
+    (1, 7, 1, 1, 90001, 90001, 64, True, None, True),        # shared through the workspace, 7 rows
+    (2, 12, 1, 1, 40001, 40001, 64, True, [40001, 33], True),  # and 12
     (3, 5, 5, 3, 4000, 4100, 64, False, [4100, -5, 2222], True),  # lengths past Sk and below 0
     (70, 2, 1, 1, 600, 600, 64, True, [(37 * i) % 601 for i in range(70)], True),   # many short sequences
 ]

@@ -108,7 +108,7 @@ def test_store_refusals(lib):
 
 def test_decode_refusals(lib):
     def dec(q=FAKE, k4=FAKE, ks=FAKE, v4=FAKE, vs=FAKE, shift=0, lengths=0, o=FAKE, lse=FAKE, weights=0, B=1, Hq=8,
-            Hkv=2, Sq=1, Sk=5000, cap=5000, D=128, ws=FAKE, nbytes=None):
+            Hkv=2, Sq=1, Sk=50000, cap=50000, D=128, ws=FAKE, nbytes=None):
         p = lambda x: P(x) if x else None   # noqa: E731
         if nbytes is None:
             nbytes = lib.pasa_attn_fwd_decode_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, int(bool(weights)))
@@ -120,14 +120,14 @@ def test_decode_refusals(lib):
     for name in ("q", "k4", "ks", "v4", "vs", "o", "lse", "shift", "weights"):
         assert dec(**{name: MIS16}) == -4
     assert dec(lengths=MIS4) == -4
-    for bad in ({"B": 0}, {"Hq": 0}, {"Hkv": 0}, {"Hq": 7}, {"Sq": 0}, {"Sk": 0}, {"cap": 4999}):
+    for bad in ({"B": 0}, {"Hq": 0}, {"Hkv": 0}, {"Hq": 7}, {"Sq": 0}, {"Sk": 0}, {"cap": 49999}):
         assert dec(**bad, nbytes=1 << 30) == -2, bad
     assert dec(D=96, nbytes=1 << 30) == -3
     assert dec(Sq=33, nbytes=1 << 30) == -3                           # 4 heads x 33 rows
     assert dec(ws=0) == -7 and dec(ws=MIS256) == -4
-    need = lib.pasa_attn_fwd_decode_kv4_workspace_bytes(1, 8, 2, 1, 5000, 128, 0)
+    need = lib.pasa_attn_fwd_decode_kv4_workspace_bytes(1, 8, 2, 1, 50000, 128, 0)
     assert need > 0 and dec(nbytes=need - 1) == -7
-    more = lib.pasa_attn_fwd_decode_kv4_workspace_bytes(1, 8, 2, 1, 5000, 128, 1)
+    more = lib.pasa_attn_fwd_decode_kv4_workspace_bytes(1, 8, 2, 1, 50000, 128, 1)
     assert more > need and dec(weights=FAKE, nbytes=need) == -7
     assert lib.pasa_attn_fwd_decode_kv4_workspace_bytes(1, 8, 2, 1, 100, 128, 0) == 0   # a CTA per kv head
     assert lib.pasa_attn_fwd_decode_kv4_workspace_bytes(1, 7, 2, 1, 100, 128, 0) == 0
