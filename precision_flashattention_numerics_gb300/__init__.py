@@ -11,6 +11,7 @@ Inference" (arXiv 2503.01873), Abstract.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -92,6 +93,8 @@ class PasaError(RuntimeError):
 def library():
     """Load libpasa.so (built by __graft_entry__.build()); raises if it is not there."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(library_path):
@@ -510,15 +513,25 @@ def attn_fwd_decode_fp8(q, k8, means, kscale, v, causal: bool = False, scale: fl
     return out, lse
 
 
-def _check_cuda(x, name: str, dtype, shape=None, device=None):
-    """A contiguous CUDA tensor of `dtype` (and shape) on the current device."""
+def _here():
+    """The current device and its current stream. (The raw stream: torch.cuda.current_stream()
+    builds a Stream object, which takes longer than a launch.)"""
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _check_cuda(x, name: str, dtype, shape, device):
+    """The pointer of a contiguous tensor of `dtype` and shape on `device`, the current one."""
+    try:
+        if x.dtype is dtype and x.get_device() == device and x.is_contiguous() and (shape is None or x.shape == shape):
+            return x.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != dtype or not x.is_contiguous():
         raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor")
-    if shape is not None and tuple(x.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
     if x.get_device() != device:
         raise ValueError(f"{name} is on device {x.get_device()}, the current device is {device}")
-    return x.data_ptr()
+    raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
 
 
 def _check_kv4(k4, kscale, v4, vscale, shift, device):
@@ -555,7 +568,7 @@ def kv4_append(k, v, k4, kscale, v4, vscale, start=0, counts=None, shift=None):
     kscale, vscale fp16 [B,Hkv,cap,D/32]) from row `start` on (an int, or an int32 tensor [B]);
     with counts (int32 [B]) only the first counts[b] rows of each sequence. shift (fp16
     [B,Hkv,D]) is subtracted from every key row and stays the same for the cache's life."""
-    dev = torch.cuda.current_device()
+    dev, stream = _here()
     ptrs, sp, (B, Hkv, cap, D) = _check_kv4(k4, kscale, v4, vscale, shift, dev)
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("expected k, v [B,Hkv,n,D]")
@@ -564,7 +577,7 @@ def kv4_append(k, v, k4, kscale, v4, vscale, start=0, counts=None, shift=None):
     vp = _check_cuda(v, "v", torch.float16, (B, Hkv, n, D), dev)
     starts, first = _per_sequence(start, "start", B, dev)
     cp = None if counts is None else _check_cuda(counts, "counts", torch.int32, (B,), dev)
-    rc = library().pasa_kv4_append(kp, vp, sp, *ptrs, starts, first, cp, B, Hkv, n, cap, D, _stream())
+    rc = library().pasa_kv4_append(kp, vp, sp, *ptrs, starts, first, cp, B, Hkv, n, cap, D, stream)
     if rc != 0:
         raise PasaError(rc, "pasa_kv4_append")
 
@@ -573,7 +586,7 @@ def kv4_read(k4, kscale, v4, vscale, n: int, start=0, counts=None, shift=None, o
     """What cache rows start .. start + n - 1 stand for: (k, v) fp16 [B,Hkv,n,D]. start, counts
     and shift as in :func:`kv4_append`; rows at counts[b] and later are left as they are in out_k
     and out_v (0 in new tensors)."""
-    dev = torch.cuda.current_device()
+    dev, stream = _here()
     ptrs, sp, (B, Hkv, cap, D) = _check_kv4(k4, kscale, v4, vscale, shift, dev)
     new = torch.empty if counts is None and not isinstance(start, torch.Tensor) else torch.zeros
     if out_k is None:
@@ -584,12 +597,13 @@ def kv4_read(k4, kscale, v4, vscale, n: int, start=0, counts=None, shift=None, o
     vp = _check_cuda(out_v, "out_v", torch.float16, (B, Hkv, n, D), dev)
     starts, first = _per_sequence(start, "start", B, dev)
     cp = None if counts is None else _check_cuda(counts, "counts", torch.int32, (B,), dev)
-    rc = library().pasa_kv4_read(*ptrs, sp, kp, vp, starts, first, cp, B, Hkv, n, cap, D, _stream())
+    rc = library().pasa_kv4_read(*ptrs, sp, kp, vp, starts, first, cp, B, Hkv, n, cap, D, stream)
     if rc != 0:
         raise PasaError(rc, "pasa_kv4_read")
     return out_k, out_v
 
 
+@functools.lru_cache(maxsize=None)
 def decode_kv4_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: int, weights: bool = False) -> int:
     return library().pasa_attn_fwd_decode_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, int(bool(weights)))
 
@@ -601,7 +615,7 @@ def attn_fwd_decode_kv4(q, k4, kscale, v4, vscale, causal: bool = False, scale: 
     lengths[b] (int32 tensor [B]; `length` is then an upper bound). With weights (fp32
     [B,Hkv,cap]) each cache row's softmax weight, summed over the kv head's query rows, is added
     there. Returns (o, lse)."""
-    dev = torch.cuda.current_device()
+    dev, stream = _here()
     ptrs, sp, (B, Hkv, cap, D) = _check_kv4(k4, kscale, v4, vscale, shift, dev)
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("expected q [B,Hq,Sq,D]")
@@ -614,15 +628,14 @@ def attn_fwd_decode_kv4(q, k4, kscale, v4, vscale, causal: bool = False, scale: 
     lp = _check_cuda(lse, "lse", torch.float32, (B, Hq, Sq), dev)
     np_ = None if lengths is None else _check_cuda(lengths, "lengths", torch.int32, (B,), dev)
     wp = None if weights is None else _check_cuda(weights, "weights", torch.float32, (B, Hkv, cap), dev)
-    lib = library()
-    nbytes = lib.pasa_attn_fwd_decode_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, 0 if wp is None else 1)
+    nbytes = decode_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, weights is not None)
     if workspace is not None:
         _check_cuda(workspace, "workspace", torch.uint8, None, dev)
     if nbytes and (workspace is None or workspace.numel() < nbytes):
         workspace = torch.empty(nbytes, device=q.device, dtype=torch.uint8)
-    rc = lib.pasa_attn_fwd_decode_kv4(qp, *ptrs, sp, np_, op, lp, wp, B, Hq, Hkv, Sq, Sk, cap, D, int(bool(causal)),
+    rc = library().pasa_attn_fwd_decode_kv4(qp, *ptrs, sp, np_, op, lp, wp, B, Hq, Hkv, Sq, Sk, cap, D, int(bool(causal)),
                                       float(scale) if scale is not None else 0.0,
-                                      workspace.data_ptr() if nbytes else None, nbytes, _stream())
+                                      workspace.data_ptr() if nbytes else None, nbytes, stream)
     if rc != 0:
         raise PasaError(rc, "pasa_attn_fwd_decode_kv4")
     return out, lse
@@ -636,7 +649,7 @@ def cache_evict(planes, weights, budget: int, recent: int = 0, length: int | Non
     sequences hold `length` rows (default cap) or lengths[b] (int32 [B]). In place, or into out (tensors
     [B,Hkv,out_cap,*]) and out_weights (fp32 [B,Hkv,out_cap]). Returns (index int32 [B,Hkv,budget]:
     the old rows, -1 past the last; new_lengths int32 [B])."""
-    dev = torch.cuda.current_device()
+    dev, stream = _here()
     planes, budget, recent = list(planes), _int32(budget, "budget"), _int32(recent, "recent")
     if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
         raise ValueError("expected weights [B,Hkv,cap]")
@@ -666,7 +679,7 @@ def cache_evict(planes, weights, budget: int, recent: int = 0, length: int | Non
     nlp = _check_cuda(new_lengths, "new_lengths", torch.int32, (B,), dev)
     count = len(planes)
     rc = library().pasa_cache_evict((_P * count)(*src), (_P * count)(*dst), (_I * count)(*nbytes), count, wp, owp, np_,
-                                    ip, nlp, B, Hkv, Sk, cap, out_cap, budget, recent, _stream())
+                                    ip, nlp, B, Hkv, Sk, cap, out_cap, budget, recent, stream)
     if rc != 0:
         raise PasaError(rc, "pasa_cache_evict")
     return index, new_lengths

@@ -37,6 +37,7 @@ namespace pasa {
 
 constexpr int kKv4Warps = 8;
 constexpr int kKv4Unit = 32;    // keys a warp takes at a time
+constexpr int kKv4MaxCtas = 304;       // two CTAs on each of 152 SMs
 constexpr int kKv4SegmentStart = 16;   // units that the start and end of a segment cost a CTA
 
 struct Kv4Params {
@@ -85,6 +86,11 @@ __device__ __forceinline__ int kv4_sum_weight(const Kv4Params& p, int b_end, int
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
   return n;
+}
+
+// How many of the launched CTAs share the work: each has a unit for every warp at least.
+__device__ __forceinline__ int kv4_ctas(int total, int launched) {
+  return max(1, min((total + kKv4Warps - 1) / kKv4Warps, launched));
 }
 
 // The units [first(c), first(c + 1)) of CTA c of `ctas`, total >= ctas >= 1: as equal as can be.
@@ -380,8 +386,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
   const int per_b = p.Hkv * p.row_tiles;
   if (STREAM_K) {
     const int total = kv4_sum_weight(p, p.B, kKv4SegmentStart) * per_b;
-    const int ctas = min(total, static_cast<int>(gridDim.x));
-    if (static_cast<int>(blockIdx.x) >= ctas) return;
+    const int ctas = kv4_ctas(total, gridDim.x);
+    if (total == 0 || static_cast<int>(blockIdx.x) >= ctas) return;
     const Kv4Share share(total, ctas);
     int before = share.first(blockIdx.x);
     todo = share.first(blockIdx.x + 1) - before;   // weight: a segment's first kKv4SegmentStart are no units
@@ -686,9 +692,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
 // the rows of sequences without a key. One CTA per (segment, row).
 template <int D>
 __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_rows) {
-  __shared__ float so[8][D];
-  __shared__ float sl[8];
-  __shared__ float s_m, s_off;
+  __shared__ float so[8][D], factor[kKv4MaxCtas];
+  __shared__ float s_m[8], s_l[8], s_off;
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long seg = blockIdx.x;
@@ -697,10 +702,16 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
   const long long in_b = seg % per_b;
   const long long bh = static_cast<long long>(b) * p.Hkv + in_b / p.row_tiles;
   const int r = blockIdx.y, row = static_cast<int>(in_b % p.row_tiles) * tile_rows + r;
-  if (row >= p.rows) return;
+  // every CTA waits for the decode, also those without work: a kernel behind this one waits for
+  // this one only
+  if (row >= p.rows) {
+    griddep_wait();
+    return;
+  }
   const long long out = bh * p.rows + row;
   const int n_units = kv4_units(p.length(b));
   if (n_units == 0) {
+    griddep_wait();
     if (threadIdx.x < D) p.o[out * D + threadIdx.x] = __float2half_rn(0.0f);
     if (threadIdx.x == 0) {
       if (p.lse) p.lse[out] = -INFINITY;
@@ -710,38 +721,69 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
   }
   const int weight = kv4_weight(n_units, kKv4SegmentStart);
   const int total = kv4_sum_weight(p, p.B, kKv4SegmentStart) * static_cast<int>(per_b);
-  const Kv4Share share(total, min(total, p.ctas));
+  const Kv4Share share(total, kv4_ctas(total, p.ctas));
   const int t0 = kv4_sum_weight(p, b, kKv4SegmentStart) * static_cast<int>(per_b) + static_cast<int>(in_b) * weight;
-  const int c0 = share.cta_of(t0 + kKv4SegmentStart), c1 = share.cta_of(t0 + weight - 1);
-  if (c0 == c1) return;   // finished where it was computed
+  const int c0 = share.cta_of(t0 + kKv4SegmentStart), n = share.cta_of(t0 + weight - 1) - c0 + 1;
+  if (n == 1) {   // finished where it was computed
+    griddep_wait();
+    return;
+  }
   if (warp == 0) {
     const float off = kv4_offset<D>(p, bh, row, lane);
     if (lane == 0) s_off = off;
   }
   griddep_wait();   // the partials
+  // every partial's max and sum at once, then its factor
+  constexpr int kMine = (kKv4MaxCtas + 255) / 256;
+  const long long first = (c0 + seg) * tile_rows + r;   // partial c0 + i of the row: + i * tile_rows
+  float2 ml[kMine];
   float mm = kKv4NoKey;
-  for (long long c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, p.part_ml[(c + seg) * tile_rows + r].x);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, d));
-  float acc[D / 32], ll = 0.0f;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
-  for (long long c = c0 + warp; c <= c1; c += 8) {
-    const long long at = (c + seg) * tile_rows + r;
-    const float2 ml = p.part_ml[at];
-    const float f = ex2_approx(ml.x - mm);
-    ll = fmaf(f, ml.y, ll);
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(f, p.part_o[at * D + e * 32 + lane], acc[e]);
+  for (int i = 0; i < kMine; ++i) {
+    const int c = i * 256 + threadIdx.x;
+    ml[i] = c < n ? p.part_ml[first + static_cast<long long>(c) * tile_rows] : make_float2(kKv4NoKey, 0.0f);
+    mm = fmaxf(mm, ml[i].x);
   }
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) so[warp][e * 32 + lane] = acc[e];
-  if (lane == 0) sl[warp] = ll;
-  if (threadIdx.x == 0) s_m = mm;
+  for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, d));
+  if (lane == 0) s_m[warp] = mm;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) mm = fmaxf(mm, s_m[w]);
+  float ll = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int c = i * 256 + threadIdx.x;
+    const float f = ex2_approx(ml[i].x - mm);
+    if (c < n) factor[c] = f;
+    ll = fmaf(f, ml[i].y, ll);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) ll += __shfl_xor_sync(0xFFFFFFFFu, ll, d);
+  if (lane == 0) s_l[warp] = ll;
+  __syncthreads();
+  float acc[D / 32];
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
+  const float* part = p.part_o + first * D + lane * (D / 32);
+#pragma unroll 4
+  for (int c = warp; c < n; c += 8) {
+    const float f = factor[c];
+    if constexpr (D == 128) {
+      const float4 x = *reinterpret_cast<const float4*>(part + static_cast<long long>(c) * tile_rows * D);
+      acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]);
+      acc[2] = fmaf(f, x.z, acc[2]), acc[3] = fmaf(f, x.w, acc[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(part + static_cast<long long>(c) * tile_rows * D);
+      acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e) so[warp][lane * (D / 32) + e] = acc[e];
   __syncthreads();
   ll = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) ll += sl[w];
+  for (int w = 0; w < 8; ++w) ll += s_l[w];
   if (threadIdx.x < D) {
     float x = 0.0f;
 #pragma unroll
@@ -749,8 +791,8 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
     p.o[out * D + threadIdx.x] = __float2half_rn(ll == 0.0f ? 0.0f : x / ll);
   }
   if (threadIdx.x == 0) {
-    if (p.lse) p.lse[out] = kv4_lse(s_m, ll, s_off);
-    if (p.weights) p.lse2[seg * tile_rows + r] = ll == 0.0f ? INFINITY : s_m + log2f(ll);
+    if (p.lse) p.lse[out] = kv4_lse(mm, ll, s_off);
+    if (p.weights) p.lse2[seg * tile_rows + r] = ll == 0.0f ? INFINITY : mm + log2f(ll);
   }
 }
 
@@ -772,24 +814,33 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
   Kv4WeightsSmem<D>& sm = *reinterpret_cast<Kv4WeightsSmem<D>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int total = kv4_sum_weight(p, p.B, 0) * p.Hkv;
-  const int ctas = min(total, static_cast<int>(gridDim.x));
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const int total = kv4_sum_weight(p, p.B, kKv4SegmentStart) * p.Hkv;
+  const int ctas = kv4_ctas(total, gridDim.x);
+  if (total == 0 || static_cast<int>(blockIdx.x) >= ctas) {
+    griddep_wait();
+    return;
+  }
   const Kv4Share share(total, ctas);
-  int u0 = share.first(blockIdx.x), todo = share.first(blockIdx.x + 1) - u0;
-  int b = 0, len, n_units;
+  int before = share.first(blockIdx.x), todo = share.first(blockIdx.x + 1) - before;
+  int b = 0, h = 0, u0 = 0, len, n_units;
   for (;; ++b) {
     len = p.length(b);
     n_units = kv4_units(len);
-    if (u0 < n_units * p.Hkv) break;
-    u0 -= n_units * p.Hkv;
+    const int weight = kv4_weight(n_units, kKv4SegmentStart);
+    if (before < weight * p.Hkv) {
+      h = before / weight;
+      u0 = before - h * weight - kKv4SegmentStart;
+      break;
+    }
+    before -= weight * p.Hkv;
   }
-  int h = u0 / n_units;
-  u0 -= h * n_units;
   griddep_wait();   // lse2
   while (true) {
     const long long bh = static_cast<long long>(b) * p.Hkv + h;
     const int u1 = min(n_units, u0 + todo);
+    todo -= u1 - u0;
+    u0 = max(0, u0);
+    if (u0 >= u1) return;
     const uint8_t* k4 = p.k4 + bh * p.cap * (D / 2);
     const __half* kscale = p.kscale + bh * p.cap * (D / 32);
     const uint32_t stage0 = smem_u32(&sm.stage[0][warp]);
@@ -829,6 +880,9 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
       odd ^= 1;
       fetch(u + kKv4Warps, stage0 + odd * kStageBytes);
       const bool masked = key0 + kKv4Unit > all_see;
+      const int key = key0 + g + 8 * t;   // the lane's weight
+      float* weight = p.weights + bh * p.cap + key;
+      const float old = key < len ? *weight : 0.0f;
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // keys g + 8 i
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -864,12 +918,10 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
         sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
       }
       const float mine = t == 0 ? sum[0] : t == 1 ? sum[1] : t == 2 ? sum[2] : sum[3];
-      const int key = key0 + g + 8 * t;
-      if (key < len) p.weights[bh * p.cap + key] += mine;
+      if (key < len) *weight = old + mine;
     }
-    todo -= u1 - u0;
     if (todo <= 0) return;
-    u0 = 0;
+    u0 = -kKv4SegmentStart;
     if (++h == p.Hkv) {
       h = 0;
       do {

@@ -96,42 +96,59 @@ __device__ __forceinline__ uint32_t kv4_codes(const uint32_t (&xin)[4], __half& 
   return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
 }
 
-// Store rows of k and v [B, H, n, D] in the cache. One thread per 8 channels of a row (16
-// bytes in, 4 bytes of codes out), blockIdx.y picking keys or values. HBM-bound: 4 D bytes in
-// and 9 D / 8 out per row of K and V.
+// Rows a thread of the store kernels handles, kv4_block_rows apart.
+constexpr int kKv4StoreRows = 2;
+template <int D>
+__host__ __device__ constexpr int kv4_block_rows() { return kKv4StoreThreads / (D / 8); }
+
+// Store rows of k and v [B, H, n, D] in the cache. A thread takes the same 8 channels (16 bytes
+// in, 4 bytes of codes out) of a few rows of K and V; blockIdx.y: (sequence, kv head). HBM-bound:
+// 4 D bytes in and 9 D / 8 out per row.
 template <int D>
 __global__ void __launch_bounds__(kKv4StoreThreads) kv4_append_kernel(
     const __half* __restrict__ k, const __half* __restrict__ v, const __half* __restrict__ shift,
     uint8_t* __restrict__ k4, __half* __restrict__ kscale, uint8_t* __restrict__ v4, __half* __restrict__ vscale,
-    int B, int H, Kv4Window win) {
+    int planes, int H, Kv4Window win) {
   griddep_launch_dependents();
   constexpr int kPer = D / 8;   // threads per row
-  const long long idx = static_cast<long long>(blockIdx.x) * kKv4StoreThreads + threadIdx.x;
-  const long long r = idx / kPer;
-  const int u = static_cast<int>(idx % kPer);
-  const long long plane = r / win.n;   // b * H + h
-  const bool in = plane < static_cast<long long>(B) * H;
-  const int b = in ? static_cast<int>(plane / H) : 0;
-  const long long row = in ? win.row(b, static_cast<int>(r % win.n)) : -1;
-  const bool keys = blockIdx.y == 0;
-  uint32_t x[4] = {0u, 0u, 0u, 0u};
-  if (row >= 0) {
-    const uint4 raw = *reinterpret_cast<const uint4*>((keys ? k : v) + r * D + u * 8);
-    x[0] = raw.x, x[1] = raw.y, x[2] = raw.z, x[3] = raw.w;
-    if (keys && shift) {
-      const uint4 sh = *reinterpret_cast<const uint4*>(shift + plane * D + u * 8);
-      x[0] = h2_bits(__hsub2_rn(bits_h2(x[0]), bits_h2(sh.x)));
-      x[1] = h2_bits(__hsub2_rn(bits_h2(x[1]), bits_h2(sh.y)));
-      x[2] = h2_bits(__hsub2_rn(bits_h2(x[2]), bits_h2(sh.z)));
-      x[3] = h2_bits(__hsub2_rn(bits_h2(x[3]), bits_h2(sh.w)));
+  const int u = threadIdx.x % kPer;
+  const int i0 = blockIdx.x * (kKv4StoreRows * kv4_block_rows<D>()) + threadIdx.x / kPer;
+  for (int plane = blockIdx.y; plane < planes; plane += gridDim.y) {
+    const int b = plane / H;
+    long long row[kKv4StoreRows];
+    uint4 xk[kKv4StoreRows], xv[kKv4StoreRows];
+#pragma unroll
+    for (int j = 0; j < kKv4StoreRows; ++j) {
+      const int i = i0 + j * kv4_block_rows<D>();
+      row[j] = i < win.n ? win.row(b, i) : -1;
+      xk[j] = xv[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (row[j] >= 0) {
+        const long long from = (static_cast<long long>(plane) * win.n + i) * D + u * 8;
+        xk[j] = __ldcs(reinterpret_cast<const uint4*>(k + from));
+        xv[j] = __ldcs(reinterpret_cast<const uint4*>(v + from));
+      }
     }
-  }
-  __half s;
-  const uint32_t codes = kv4_codes(x, s);
-  if (row >= 0) {
-    const long long at = plane * win.cap + row;
-    *reinterpret_cast<uint32_t*>((keys ? k4 : v4) + at * (D / 2) + u * 4) = codes;
-    if ((u & 3) == 0) (keys ? kscale : vscale)[at * (D / kKv4Group) + u / 4] = s;
+    uint4 sh = make_uint4(0u, 0u, 0u, 0u);   // x - 0 = x
+    if (shift) sh = *reinterpret_cast<const uint4*>(shift + static_cast<long long>(plane) * D + u * 8);
+#pragma unroll
+    for (int j = 0; j < kKv4StoreRows; ++j) {
+      const uint32_t x[4] = {h2_bits(__hsub2_rn(bits_h2(xk[j].x), bits_h2(sh.x))),
+                             h2_bits(__hsub2_rn(bits_h2(xk[j].y), bits_h2(sh.y))),
+                             h2_bits(__hsub2_rn(bits_h2(xk[j].z), bits_h2(sh.z))),
+                             h2_bits(__hsub2_rn(bits_h2(xk[j].w), bits_h2(sh.w)))};
+      const uint32_t y[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
+      __half sk, sv;
+      const uint32_t ck = kv4_codes(x, sk), cv = kv4_codes(y, sv);
+      if (row[j] >= 0) {
+        const long long at = static_cast<long long>(plane) * win.cap + row[j];
+        *reinterpret_cast<uint32_t*>(k4 + at * (D / 2) + u * 4) = ck;
+        *reinterpret_cast<uint32_t*>(v4 + at * (D / 2) + u * 4) = cv;
+        if ((u & 3) == 0) {
+          kscale[at * (D / kKv4Group) + u / 4] = sk;
+          vscale[at * (D / kKv4Group) + u / 4] = sv;
+        }
+      }
+    }
   }
 }
 
@@ -147,40 +164,59 @@ __device__ __forceinline__ void kv4_expand(uint32_t w, __half2 s2, __half2 (&out
   out[3] = __hmul2(__hfma2(bits_h2((w8 & 0x00F000F0u) | magic), sixteenth, off1), s2);
 }
 
+// 8 codes times the scale, exactly, in channel order.
+__device__ __forceinline__ uint4 kv4_values8(uint32_t w, __half s) {
+  __half2 p[4];
+  kv4_expand(w, __half2half2(s), p);
+  return make_uint4(h2_bits(__lows2half2(p[0], p[1])), h2_bits(__lows2half2(p[2], p[3])),
+                    h2_bits(__highs2half2(p[0], p[1])), h2_bits(__highs2half2(p[2], p[3])));
+}
+
 // Read cache rows back as fp16: fp16_rn(s * c + shift) for keys, s * c for values, into
-// k, v [B, H, n, D]; output rows without a cache row are left as they are.
+// k, v [B, H, n, D]; output rows without a cache row are left as they are. Laid out as
+// kv4_append_kernel.
 template <int D>
 __global__ void __launch_bounds__(kKv4StoreThreads) kv4_read_kernel(
     const uint8_t* __restrict__ k4, const __half* __restrict__ kscale, const uint8_t* __restrict__ v4,
     const __half* __restrict__ vscale, const __half* __restrict__ shift, __half* __restrict__ k,
-    __half* __restrict__ v, int B, int H, Kv4Window win) {
+    __half* __restrict__ v, int planes, int H, Kv4Window win) {
   constexpr int kPer = D / 8;
-  const long long idx = static_cast<long long>(blockIdx.x) * kKv4StoreThreads + threadIdx.x;
-  const long long r = idx / kPer;
-  const int u = static_cast<int>(idx % kPer);
-  const long long plane = r / win.n;
-  if (plane >= static_cast<long long>(B) * H) return;
-  const long long row = win.row(static_cast<int>(plane / H), static_cast<int>(r % win.n));
-  if (row < 0) return;
-  const bool keys = blockIdx.y == 0;
-  const long long at = plane * win.cap + row;
-  const uint32_t w = *reinterpret_cast<const uint32_t*>((keys ? k4 : v4) + at * (D / 2) + u * 4);
-  const __half s = (keys ? kscale : vscale)[at * (D / kKv4Group) + u / 4];
-  __half2 p[4];
-  kv4_expand(w, __half2half2(s), p);
-  uint4 o;
-  o.x = h2_bits(__lows2half2(p[0], p[1]));
-  o.y = h2_bits(__lows2half2(p[2], p[3]));
-  o.z = h2_bits(__highs2half2(p[0], p[1]));
-  o.w = h2_bits(__highs2half2(p[2], p[3]));
-  if (keys && shift) {
-    const uint4 sh = *reinterpret_cast<const uint4*>(shift + plane * D + u * 8);
-    o.x = h2_bits(__hadd2_rn(bits_h2(o.x), bits_h2(sh.x)));
-    o.y = h2_bits(__hadd2_rn(bits_h2(o.y), bits_h2(sh.y)));
-    o.z = h2_bits(__hadd2_rn(bits_h2(o.z), bits_h2(sh.z)));
-    o.w = h2_bits(__hadd2_rn(bits_h2(o.w), bits_h2(sh.w)));
+  const int u = threadIdx.x % kPer;
+  const int i0 = blockIdx.x * (kKv4StoreRows * kv4_block_rows<D>()) + threadIdx.x / kPer;
+  for (int plane = blockIdx.y; plane < planes; plane += gridDim.y) {
+    const int b = plane / H;
+    long long row[kKv4StoreRows];
+    uint32_t ck[kKv4StoreRows], cv[kKv4StoreRows];
+    __half sk[kKv4StoreRows], sv[kKv4StoreRows];
+#pragma unroll
+    for (int j = 0; j < kKv4StoreRows; ++j) {
+      const int i = i0 + j * kv4_block_rows<D>();
+      row[j] = i < win.n ? win.row(b, i) : -1;
+      ck[j] = cv[j] = 0u;
+      sk[j] = sv[j] = __ushort_as_half(0);
+      if (row[j] >= 0) {
+        const long long at = static_cast<long long>(plane) * win.cap + row[j];
+        ck[j] = *reinterpret_cast<const uint32_t*>(k4 + at * (D / 2) + u * 4);
+        cv[j] = *reinterpret_cast<const uint32_t*>(v4 + at * (D / 2) + u * 4);
+        sk[j] = kscale[at * (D / kKv4Group) + u / 4];
+        sv[j] = vscale[at * (D / kKv4Group) + u / 4];
+      }
+    }
+    uint4 sh = make_uint4(0u, 0u, 0u, 0u);
+    if (shift) sh = *reinterpret_cast<const uint4*>(shift + static_cast<long long>(plane) * D + u * 8);
+#pragma unroll
+    for (int j = 0; j < kKv4StoreRows; ++j) {
+      if (row[j] < 0) continue;
+      const long long to = (static_cast<long long>(plane) * win.n + i0 + j * kv4_block_rows<D>()) * D + u * 8;
+      uint4 x = kv4_values8(ck[j], sk[j]);
+      x.x = h2_bits(__hadd2_rn(bits_h2(x.x), bits_h2(sh.x)));
+      x.y = h2_bits(__hadd2_rn(bits_h2(x.y), bits_h2(sh.y)));
+      x.z = h2_bits(__hadd2_rn(bits_h2(x.z), bits_h2(sh.z)));
+      x.w = h2_bits(__hadd2_rn(bits_h2(x.w), bits_h2(sh.w)));
+      *reinterpret_cast<uint4*>(k + to) = x;
+      *reinterpret_cast<uint4*>(v + to) = kv4_values8(cv[j], sv[j]);
+    }
   }
-  *reinterpret_cast<uint4*>((keys ? k : v) + r * D + u * 8) = o;
 }
 
 }  // namespace pasa

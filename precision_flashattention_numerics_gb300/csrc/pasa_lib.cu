@@ -1,6 +1,7 @@
 // libpasa.so: the C ABI declared in include/pasa.h. Host-side argument validation, TMA
 // descriptor encoding, workspace layout and kernel dispatch. Compiled as one translation
 // unit for sm_103a.
+#include <atomic>
 #include <climits>
 #include <cstddef>
 #include <cmath>
@@ -1432,16 +1433,15 @@ int kv4_validate(const void* k4, const void* kscale, const void* v4, const void*
 
 // kv4_append and kv4_read share their arguments: n rows of k and v from cache row `start` on.
 int kv4_window(const void* k, const void* v, const int* starts, int start, const int* counts, int n, int B, int Hkv,
-               int Sk_cap, int D, pasa::Kv4Window* win, unsigned* blocks) {
+               int Sk_cap, int D, pasa::Kv4Window* win, dim3* grid) {
   if (!k || !v) return PASA_ERR_NULLPTR;
   if (n <= 0) return PASA_ERR_SHAPE;
   if (!starts && (start < 0 || static_cast<long long>(start) + n > Sk_cap)) return PASA_ERR_SHAPE;
   if (!aligned16(k) || !aligned16(v) || !aligned4(starts) || !aligned4(counts)) return PASA_ERR_ALIGN;
-  const unsigned long long rows = static_cast<unsigned long long>(B) * Hkv * static_cast<unsigned long long>(n);
-  const unsigned long long grid = (rows * (D / 8) + pasa::kKv4StoreThreads - 1) / pasa::kKv4StoreThreads;
-  if (rows > (1ull << 50) || grid > INT_MAX) return PASA_ERR_SHAPE;
+  if (n > INT_MAX - 256) return PASA_ERR_SHAPE;   // row numbers of a block's last threads
+  const int per_block = pasa::kKv4StoreRows * (D == 64 ? pasa::kv4_block_rows<64>() : pasa::kv4_block_rows<128>());
   *win = pasa::Kv4Window{starts, counts, start, n, Sk_cap};
-  *blocks = static_cast<unsigned>(grid);
+  *grid = dim3(static_cast<unsigned>((n + per_block - 1) / per_block), static_cast<unsigned>(std::min(B * Hkv, 65535)));
   return PASA_OK;
 }
 
@@ -1471,7 +1471,7 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   pl.nt = rows <= 8 ? 1 : 2;
   pl.row_tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
   pl.segments = static_cast<long long>(B) * Hkv * pl.row_tiles;
-  pl.ctas = 152 * 2;
+  pl.ctas = pasa::kKv4MaxCtas;
   const int units = (Sk + pasa::kKv4Unit - 1) / pasa::kKv4Unit;
   pl.cluster = 1;
   while (pl.cluster < 8 && pl.segments * pl.cluster * 2 <= pl.ctas && units > pasa::kKv4Warps * pl.cluster) pl.cluster *= 2;
@@ -1486,9 +1486,12 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   return pl;
 }
 
-template <typename... Params, typename... Args>
-cudaError_t launch_clusters(void (*kern)(Params...), unsigned grid, int block, int smem, cudaStream_t st, bool pdl,
-                            int cluster, Args&&... args) {
+// Launch `kern` in clusters of `cluster` CTAs with `smem` bytes of dynamic shared memory, `max_smem`
+// at most in any call. The limit on those is raised at the first launch on a device (bit of
+// `raised`), and again if a launch fails (the device was reset).
+template <typename... Params>
+cudaError_t launch_clusters(void (*kern)(Params...), unsigned grid, int block, int smem, int max_smem,
+                            cudaStream_t st, bool pdl, int cluster, std::atomic<unsigned long long>& raised, Params... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
@@ -1506,16 +1509,28 @@ cudaError_t launch_clusters(void (*kern)(Params...), unsigned grid, int block, i
     attr[cfg.numAttrs].val.clusterDim.y = 1;
     attr[cfg.numAttrs++].val.clusterDim.z = 1;
   }
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (raised.load(std::memory_order_relaxed) & bit) != 0) {
+    e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e == cudaSuccess) return e;
+    (void)cudaGetLastError();
+  }
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
+  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e == cudaSuccess) raised.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 template <int D, int NT, bool STREAM_K>
 cudaError_t kv4_launch(const pasa::Kv4Params& p, unsigned grid, cudaStream_t st, bool pdl) {
-  auto kern = pasa::kv4_decode_kernel<D, NT, STREAM_K>;
-  const int smem = static_cast<int>(sizeof(pasa::Kv4Smem<D, NT>));
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return launch_clusters(kern, grid, pasa::kKv4Warps * 32, smem, st, pdl, p.cluster, p);
+  static std::atomic<unsigned long long> raised{0};
+  constexpr int smem = static_cast<int>(sizeof(pasa::Kv4Smem<D, NT>));
+  return launch_clusters(pasa::kv4_decode_kernel<D, NT, STREAM_K>, grid, pasa::kKv4Warps * 32, smem, smem, st, pdl,
+                         p.cluster, raised, p);
 }
 
 template <int D>
@@ -1529,9 +1544,9 @@ cudaError_t kv4_decode_launch(const pasa::Kv4Params& p, const Kv4Plan& pl, cudaS
                       p, tile);
   if (e == cudaSuccess && p.weights) {
     const int smem = static_cast<int>(offsetof(pasa::Kv4WeightsSmem<D>, q) + sizeof(pasa::Kv4QueryShared<D>) * ((p.rows + 7) / 8));
-    e = cudaFuncSetAttribute(pasa::kv4_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess)
-      e = launch_kernel(pasa::kv4_weights_kernel<D>, dim3(static_cast<unsigned>(pl.ctas)), dim3(pasa::kKv4Warps * 32), smem, st, true, p, tile);
+    static std::atomic<unsigned long long> raised{0};
+    e = launch_clusters(pasa::kv4_weights_kernel<D>, static_cast<unsigned>(pl.ctas), pasa::kKv4Warps * 32, smem,
+                        static_cast<int>(sizeof(pasa::Kv4WeightsSmem<D>)), st, true, 1, raised, p, tile);
   }
   return e;
 }
@@ -1546,16 +1561,16 @@ int pasa_kv4_append(const void* k, const void* v, const void* shift, void* k4, v
   int rc = kv4_validate(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
   if (rc != PASA_OK) return rc;
   pasa::Kv4Window win;
-  unsigned blocks = 0;
-  rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, &win, &blocks);
+  dim3 grid;
+  rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, &win, &grid);
   if (rc != PASA_OK) return rc;
   rc = check_device();
   if (rc != PASA_OK) return rc;
   auto kern = D == 64 ? pasa::kv4_append_kernel<64> : pasa::kv4_append_kernel<128>;
-  kern<<<dim3(blocks, 2), pasa::kKv4StoreThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+  kern<<<grid, pasa::kKv4StoreThreads, 0, static_cast<cudaStream_t>(stream)>>>(
       static_cast<const __half*>(k), static_cast<const __half*>(v), static_cast<const __half*>(shift),
       static_cast<uint8_t*>(k4), static_cast<__half*>(kscale), static_cast<uint8_t*>(v4), static_cast<__half*>(vscale),
-      B, Hkv, win);
+      B * Hkv, Hkv, win);
   return launch_status();
 }
 
@@ -1565,16 +1580,16 @@ int pasa_kv4_read(const void* k4, const void* kscale, const void* v4, const void
   int rc = kv4_validate(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
   if (rc != PASA_OK) return rc;
   pasa::Kv4Window win;
-  unsigned blocks = 0;
-  rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, &win, &blocks);
+  dim3 grid;
+  rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, &win, &grid);
   if (rc != PASA_OK) return rc;
   rc = check_device();
   if (rc != PASA_OK) return rc;
   auto kern = D == 64 ? pasa::kv4_read_kernel<64> : pasa::kv4_read_kernel<128>;
-  kern<<<dim3(blocks, 2), pasa::kKv4StoreThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+  kern<<<grid, pasa::kKv4StoreThreads, 0, static_cast<cudaStream_t>(stream)>>>(
       static_cast<const uint8_t*>(k4), static_cast<const __half*>(kscale), static_cast<const uint8_t*>(v4),
       static_cast<const __half*>(vscale), static_cast<const __half*>(shift), static_cast<__half*>(k),
-      static_cast<__half*>(v), B, Hkv, win);
+      static_cast<__half*>(v), B * Hkv, Hkv, win);
   return launch_status();
 }
 
@@ -1648,40 +1663,38 @@ int pasa_cache_evict(const void* const* planes, void* const* out_planes, const i
   if (n_planes < 1 || n_planes > pasa::kEvictPlanes) return PASA_ERR_UNSUPPORTED;
   if (!aligned16(weights) || !aligned16(out_weights) || !aligned16(index) || !aligned4(lengths) || !aligned4(new_lengths))
     return PASA_ERR_ALIGN;
-  pasa::EvictPlanes pl = {};
-  bool in_place = false, moved = false;
-  pl.n = n_planes;
+  bool in_place = weights == out_weights, apart = !in_place;
   for (int i = 0; i < n_planes; ++i) {
     if (!planes[i] || !out_planes[i]) return PASA_ERR_NULLPTR;
     if (row_bytes[i] <= 0 || row_bytes[i] > 65536) return PASA_ERR_SHAPE;
     if (row_bytes[i] % 4 != 0) return PASA_ERR_UNSUPPORTED;
     if (!aligned16(planes[i]) || !aligned16(out_planes[i])) return PASA_ERR_ALIGN;
-    pl.src[i] = static_cast<const unsigned char*>(planes[i]);
-    pl.dst[i] = static_cast<unsigned char*>(out_planes[i]);
-    pl.row_bytes[i] = row_bytes[i];
-    // the widest power of two up to a 32-byte sector that a row is made of (and that keeps rows aligned)
-    int w = 32;
-    while (row_bytes[i] % w != 0) w /= 2;
-    pl.width[i] = w;
-    pl.first_column[i + 1] = pl.first_column[i] + row_bytes[i] / w;
     in_place |= planes[i] == out_planes[i];
-    moved |= planes[i] != out_planes[i];
+    apart |= planes[i] != out_planes[i];
   }
   // a cache moves in place as a whole, in a cache of the same size
-  in_place |= weights == out_weights;
-  moved |= weights != out_weights;
-  if (in_place && (moved || out_cap != Sk_cap)) return PASA_ERR_SHAPE;
-  if (pl.first_column[n_planes] > 65535) return PASA_ERR_SHAPE;
+  if (in_place && (apart || out_cap != Sk_cap)) return PASA_ERR_SHAPE;
+  pasa::EvictPlanes pl = {};
+  pl.n = n_planes + 1;
+  for (int i = 0; i <= n_planes; ++i) {
+    const bool w = i == n_planes;
+    pl.src[i] = static_cast<const unsigned char*>(w ? static_cast<const void*>(weights) : planes[i]);
+    pl.dst[i] = static_cast<unsigned char*>(w ? static_cast<void*>(out_weights) : out_planes[i]);
+    pl.row_bytes[i] = w ? 4 : row_bytes[i];
+    pl.width[i] = in_place ? 32 : 128;
+    pl.first_column[i + 1] = pl.first_column[i] + (pl.row_bytes[i] + pl.width[i] - 1) / pl.width[i];
+  }
+  if (pl.first_column[pl.n] > 65535) return PASA_ERR_SHAPE;
   int rc = check_device();
   if (rc != PASA_OK) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned planes_bh = static_cast<unsigned>(B) * static_cast<unsigned>(Hkv);
-  pasa::evict_select_kernel<<<planes_bh, pasa::kEvictThreads, 0, st>>>(weights, out_weights, lengths, index, Hkv, Sk,
-                                                                       Sk_cap, out_cap, budget, recent);
+  pasa::evict_select_kernel<<<planes_bh, pasa::kEvictThreads, 0, st>>>(weights, lengths, index, Hkv, Sk, Sk_cap, budget,
+                                                                       recent);
   rc = launch_status();
   if (rc != PASA_OK) return rc;
-  const int rows_per_cta = in_place ? budget : std::max(4 * pasa::kMoveThreads, (budget + 65534) / 65535);
-  const dim3 grid(planes_bh, pl.first_column[n_planes], (budget + rows_per_cta - 1) / rows_per_cta);
+  const int rows_per_cta = in_place ? budget : std::max(256, (budget + 65534) / 65535);
+  const dim3 grid(planes_bh, pl.first_column[pl.n], (budget + rows_per_cta - 1) / rows_per_cta);
   const cudaError_t e = launch_kernel(pasa::evict_move_kernel, grid, dim3(pasa::kMoveThreads), 0, st, true, pl, index,
                                       new_lengths, Hkv, static_cast<long long>(Sk_cap), static_cast<long long>(out_cap),
                                       budget, rows_per_cta);

@@ -102,7 +102,7 @@ def test_store_refusals(lib):
             assert store(fn, **bad) == -2, bad
         assert store(fn, start=2 ** 31 - 1, n=2 ** 31 - 1) == -2
         assert store(fn, B=65536, H=65536) == -2                      # B * Hkv overflows
-        assert store(fn, B=2 ** 20, H=2 ** 10, n=2 ** 20, cap=2 ** 20) == -2   # grid overflows
+        assert store(fn, n=2 ** 31 - 1, cap=2 ** 31 - 1) == -2        # so do a block's last row numbers
         assert store(fn, D=96) == -3 and store(fn, D=32) == -3
 
 
