@@ -38,7 +38,7 @@ namespace pasa {
 constexpr int kKv4Warps = 8;
 constexpr int kKv4Unit = 32;    // keys a warp takes at a time
 constexpr int kKv4MaxCtas = 304;       // two CTAs on each of 152 SMs
-constexpr int kKv4SegmentStart = 16;   // units that the start and end of a segment cost a CTA
+constexpr int kKv4SegmentStart = 2;    // rounds that the start and end of a segment cost a CTA
 
 struct Kv4Params {
   const __half* q;
@@ -73,29 +73,26 @@ struct Kv4Params {
 
 __device__ __forceinline__ int kv4_units(int len) { return (len + kKv4Unit - 1) / kKv4Unit; }
 
-// A segment's weight when segments are shared out: its units, and `start` for what every segment
-// costs a CTA (query, joining the warps, partial results).
-__device__ __forceinline__ int kv4_weight(int units, int start) { return units == 0 ? 0 : units + start; }
+// A segment's weight when segments are shared out: its rounds (a unit for each warp of a CTA: what
+// is shared is whole rounds, so that no warp idles in the middle), and kKv4SegmentStart.
+__device__ __forceinline__ int kv4_weight(int units) {
+  return units == 0 ? 0 : (units + kKv4Warps - 1) / kKv4Warps + kKv4SegmentStart;
+}
 
 // Weight of the first b_end sequences (per kv head and row tile), summed by a whole warp. All
 // weights of a call fit an int (checked on the host).
-__device__ __forceinline__ int kv4_sum_weight(const Kv4Params& p, int b_end, int start) {
-  if (!p.lengths) return b_end * kv4_weight(kv4_units(p.Sk), start);
+__device__ __forceinline__ int kv4_sum_weight(const Kv4Params& p, int b_end) {
+  if (!p.lengths) return b_end * kv4_weight(kv4_units(p.Sk));
   int n = 0;
-  for (int b = threadIdx.x & 31; b < b_end; b += 32) n += kv4_weight(kv4_units(p.length(b)), start);
+  for (int b = threadIdx.x & 31; b < b_end; b += 32) n += kv4_weight(kv4_units(p.length(b)));
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
   return n;
 }
 
-// How many of the launched CTAs share the work: each has a unit for every warp at least.
-__device__ __forceinline__ int kv4_ctas(int total, int launched) {
-  return max(1, min((total + kKv4Warps - 1) / kKv4Warps, launched));
-}
-
-// The units [first(c), first(c + 1)) of CTA c of `ctas`, total >= ctas >= 1: as equal as can be.
+// The rounds [first(c), first(c + 1)) of CTA c of `ctas`, total >= ctas >= 1: as equal as can be.
 struct Kv4Share {
-  unsigned base, more;   // units of a CTA, and how many CTAs have one more
+  unsigned base, more;   // rounds of a CTA, and how many CTAs have one more
   __device__ __forceinline__ Kv4Share(int total, int ctas)
       : base(static_cast<unsigned>(total) / ctas), more(static_cast<unsigned>(total) - base * ctas) {}
   __device__ __forceinline__ int first(unsigned c) const { return c * base + min(c, more); }
@@ -380,24 +377,24 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
   griddep_launch_dependents();
   griddep_wait();   // rows that the call's append kernel stores
 
-  // this CTA's segments: (b, h, row tile) in order, and the units [u0, u1) of the first
-  int todo = 0, b = 0, u0 = 0, n_units = 0, len = 0;
+  // this CTA's segments: (b, h, row tile) in order, its rounds in all, and the first one's number
+  int todo = 0, b = 0, r0 = 0, n_units = 0, len = 0;
   int in_b = 0;   // segment inside sequence b: h * row_tiles + row tile
   const int per_b = p.Hkv * p.row_tiles;
   if (STREAM_K) {
-    const int total = kv4_sum_weight(p, p.B, kKv4SegmentStart) * per_b;
-    const int ctas = kv4_ctas(total, gridDim.x);
-    if (total == 0 || static_cast<int>(blockIdx.x) >= ctas) return;
+    const int total = kv4_sum_weight(p, p.B) * per_b;
+    const int ctas = min(total, static_cast<int>(gridDim.x));
+    if (static_cast<int>(blockIdx.x) >= ctas) return;
     const Kv4Share share(total, ctas);
     int before = share.first(blockIdx.x);
-    todo = share.first(blockIdx.x + 1) - before;   // weight: a segment's first kKv4SegmentStart are no units
+    todo = share.first(blockIdx.x + 1) - before;
     for (;; ++b) {
       len = p.length(b);
       n_units = kv4_units(len);
-      const int weight = kv4_weight(n_units, kKv4SegmentStart);
+      const int weight = kv4_weight(n_units);
       if (before < weight * per_b) {
         in_b = before / weight;
-        u0 = before - in_b * weight - kKv4SegmentStart;
+        r0 = before - in_b * weight - kKv4SegmentStart;   // its first rounds stand for its start
         break;
       }
       before -= weight * per_b;
@@ -407,17 +404,22 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
     b = seg / per_b;
     in_b = seg - b * per_b;
     len = p.length(b);
-    todo = n_units = kv4_units(len);
+    n_units = kv4_units(len);
+    todo = n_units;
   }
 
   while (true) {
     const long long bh = static_cast<long long>(b) * p.Hkv + in_b / p.row_tiles;
     const int row0 = in_b % p.row_tiles * kRows;
     const int n_rows = min(kRows, p.rows - row0);
-    const int u1 = min(n_units, u0 + todo);
-    todo -= u1 - u0;
-    u0 = max(0, u0);
-    if (STREAM_K && u0 >= u1) return;   // the range ends in what a segment's start weighs
+    int u0 = 0, u1 = n_units;
+    if (STREAM_K) {
+      const int r1 = min((n_units + kKv4Warps - 1) / kKv4Warps, r0 + todo);
+      todo -= r1 - r0;
+      u0 = max(0, r0) * kKv4Warps;
+      u1 = min(n_units, r1 * kKv4Warps);
+      if (u0 >= u1) return;   // the range ends in what a segment's start weighs
+    }
     const int u_step = STREAM_K ? kKv4Warps : kKv4Warps * p.cluster;
 
     // ---- the warp's share of units u0 .. u1 ----
@@ -676,7 +678,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
     }
     // ---- next segment ----
     if (todo <= 0) return;
-    u0 = -kKv4SegmentStart;
+    r0 = -kKv4SegmentStart;
     if (++in_b == per_b) {
       in_b = 0;
       do {
@@ -719,10 +721,10 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
     }
     return;
   }
-  const int weight = kv4_weight(n_units, kKv4SegmentStart);
-  const int total = kv4_sum_weight(p, p.B, kKv4SegmentStart) * static_cast<int>(per_b);
-  const Kv4Share share(total, kv4_ctas(total, p.ctas));
-  const int t0 = kv4_sum_weight(p, b, kKv4SegmentStart) * static_cast<int>(per_b) + static_cast<int>(in_b) * weight;
+  const int weight = kv4_weight(n_units);
+  const int total = kv4_sum_weight(p, p.B) * static_cast<int>(per_b);
+  const Kv4Share share(total, min(total, p.ctas));
+  const int t0 = kv4_sum_weight(p, b) * static_cast<int>(per_b) + static_cast<int>(in_b) * weight;
   const int c0 = share.cta_of(t0 + kKv4SegmentStart), n = share.cta_of(t0 + weight - 1) - c0 + 1;
   if (n == 1) {   // finished where it was computed
     griddep_wait();
@@ -814,22 +816,22 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
   Kv4WeightsSmem<D>& sm = *reinterpret_cast<Kv4WeightsSmem<D>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int total = kv4_sum_weight(p, p.B, kKv4SegmentStart) * p.Hkv;
-  const int ctas = kv4_ctas(total, gridDim.x);
-  if (total == 0 || static_cast<int>(blockIdx.x) >= ctas) {
+  const int total = kv4_sum_weight(p, p.B) * p.Hkv;
+  const int ctas = min(total, static_cast<int>(gridDim.x));
+  if (static_cast<int>(blockIdx.x) >= ctas) {
     griddep_wait();
     return;
   }
   const Kv4Share share(total, ctas);
   int before = share.first(blockIdx.x), todo = share.first(blockIdx.x + 1) - before;
-  int b = 0, h = 0, u0 = 0, len, n_units;
+  int b = 0, h = 0, r0 = 0, len, n_units;
   for (;; ++b) {
     len = p.length(b);
     n_units = kv4_units(len);
-    const int weight = kv4_weight(n_units, kKv4SegmentStart);
+    const int weight = kv4_weight(n_units);
     if (before < weight * p.Hkv) {
       h = before / weight;
-      u0 = before - h * weight - kKv4SegmentStart;
+      r0 = before - h * weight - kKv4SegmentStart;
       break;
     }
     before -= weight * p.Hkv;
@@ -837,9 +839,9 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
   griddep_wait();   // lse2
   while (true) {
     const long long bh = static_cast<long long>(b) * p.Hkv + h;
-    const int u1 = min(n_units, u0 + todo);
-    todo -= u1 - u0;
-    u0 = max(0, u0);
+    const int r1 = min((n_units + kKv4Warps - 1) / kKv4Warps, r0 + todo);
+    todo -= r1 - r0;
+    const int u0 = max(0, r0) * kKv4Warps, u1 = min(n_units, r1 * kKv4Warps);
     if (u0 >= u1) return;
     const uint8_t* k4 = p.k4 + bh * p.cap * (D / 2);
     const __half* kscale = p.kscale + bh * p.cap * (D / 32);
@@ -891,19 +893,19 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
         float sa[D / 32], sb[D / 32];
         kv4_take_scales<D>(sa, st.ks[16 * half + g]);
         kv4_take_scales<D>(sb, st.ks[16 * half + 8 + g]);
-        for (int r0 = 0; r0 < p.rows; r0 += 8) {
-          const auto& q = sm.q[r0 / 8];
+        for (int i = 0; i < p.rows; i += 8) {
+          const auto& q = sm.q[i / 8];
           float s[4];
 #pragma unroll
           for (int w = 0; w < D / 32; ++w)
             kv4_score_group(s, w, ka[w], kb[w], sa[w], sb[w], q.b[w][lane], q.init[w][lane]);
-          const float2 factor = q.factor[lane], ref = *reinterpret_cast<const float2*>(&sm.ref[r0 + 2 * t]);
+          const float2 factor = q.factor[lane], ref = *reinterpret_cast<const float2*>(&sm.ref[i + 2 * t]);
           float e[4] = {ex2_approx(fmaf(s[0], factor.x, -ref.x)), ex2_approx(fmaf(s[1], factor.y, -ref.y)),
                         ex2_approx(fmaf(s[2], factor.x, -ref.x)), ex2_approx(fmaf(s[3], factor.y, -ref.y))};
           if (masked) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const int lim = sm.limit[r0 + 2 * t + c] - key0 - 16 * half - g;
+              const int lim = sm.limit[i + 2 * t + c] - key0 - 16 * half - g;
               if (lim <= 0) e[c] = 0.0f;
               if (lim <= 8) e[2 + c] = 0.0f;
             }
@@ -921,7 +923,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
       if (key < len) *weight = old + mine;
     }
     if (todo <= 0) return;
-    u0 = -kKv4SegmentStart;
+    r0 = -kKv4SegmentStart;
     if (++h == p.Hkv) {
       h = 0;
       do {

@@ -37,6 +37,12 @@ struct Kv4Window {
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
+__device__ __forceinline__ float rcp_approx(float x) {   // within 2^-23
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // x rounded (ties to even) to 8 significant bits; x >= 0 and finite.
 __device__ __forceinline__ float round_8bits(float x) {
   uint32_t u = __float_as_uint(x);
@@ -48,21 +54,25 @@ __device__ __forceinline__ float round_8bits(float x) {
 // scale; x: 8 fp16 in 4 registers. Called by the 4 lanes of a group together (aligned groups
 // of 4 lanes hold the 32 channels).
 //
-// x / s is needed only to the nearest integer. Where it is no tie (a multiple of 1/2), it is at
-// least 2.4e-4 away from one: x has 11 significant bits, s 8, and both are multiples of a power
-// of two no smaller than s * 2^-12. So x * (1 / s), off by at most 7 * 2^-24, is first rounded
-// to a multiple of 2^-14 (by adding 768), which puts true ties exactly on the tie and
-// moves no other value across one, and then to an integer (by adding 1.5 * 2^23 - 768), ties to
-// even. No division per channel.
+// Both quotients are only needed rounded, so products with reciprocals do. max|x| / 7 to 8 bits: a
+// tie is a 9-bit number t with max|x| = 7 t; any other quotient of an 11-bit number is at least
+// 2^-10 / 7 of t away from one. The product with 1 / 7, off by 2^-23, is first rounded to 16 bits:
+// a true tie is then exact, and nothing else has moved onto or across one. x / s to an integer: where
+// it is no tie (a multiple of 1/2), it is at least 2.4e-4 away from one: x has 11 significant bits,
+// s 8, and both are multiples of a power of two no smaller than s * 2^-12. So x * (1 / s), off by
+// at most 7 * 2^-22, is first rounded to a multiple of 2^-14 (by adding 768), and then to an integer
+// (by adding 1.5 * 2^23 - 768), ties to even.
 __device__ __forceinline__ uint32_t kv4_codes(const uint32_t (&xin)[4], __half& scale) {
   uint32_t x[4] = {xin[0], xin[1], xin[2], xin[3]};
   __half2 m2 = __hmax2_nan(__hmax2_nan(__habs2(bits_h2(x[0])), __habs2(bits_h2(x[1]))),
                            __hmax2_nan(__habs2(bits_h2(x[2])), __habs2(bits_h2(x[3]))));
-  __half m = __hmax_nan(__low2half(m2), __high2half(m2));
-  m = __hmax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  m = __hmax_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  m2 = __hmax2_nan(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 1));
+  m2 = __hmax2_nan(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 2));
+  const __half m = __hmax_nan(__low2half(m2), __high2half(m2));
   float a = __half2float(m);
-  const bool odd = !(a <= 65504.0f);   // an infinity or NaN in the group: the same in its 4 lanes
+  // a group that is not finite, or so small that its scale has fewer than 8 bits and |x / s| may
+  // pass 7 by more than rounding: the same in its 4 lanes
+  const bool odd = !(a <= 65504.0f) || a < 7.0f * 0x1p-14f;
   if (__any_sync(0xFFFFFFFFu, odd)) {
     float b = 0.0f;
 #pragma unroll
@@ -76,19 +86,22 @@ __device__ __forceinline__ uint32_t kv4_codes(const uint32_t (&xin)[4], __half& 
     b = fmaxf(b, __shfl_xor_sync(0xFFFFFFFFu, b, 1));
     a = fmaxf(b, __shfl_xor_sync(0xFFFFFFFFu, b, 2));
   }
-  scale = __float2half_rn(round_8bits(a / 7.0f));
+  const float sixteen_bits = __uint_as_float((__float_as_uint(a * (1.0f / 7.0f)) + 0x80u) & 0xFFFFFF00u);
+  scale = __float2half_rn(round_8bits(sixteen_bits));
+  if (__any_sync(0xFFFFFFFFu, odd)) {
+    const __half2 top = __hmul2(__half2half2(scale), __float2half2_rn(7.0f));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = h2_bits(__hmax2(__hmin2(bits_h2(x[i]), top), __hneg2(top)));
+  }
   const float s = __half2float(scale);
-  const float r = s > 0.0f ? 1.0f / s : 0.0f;
+  const float r = s > 0.0f ? rcp_approx(s) : 0.0f;
   uint32_t y[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(bits_h2(x[i]));
-    // |x / s| passes 7 by more than rounding only where s itself is an fp16 subnormal
-    const float lo = fminf(fmaxf(fmaf(f.x, r, 768.0f), 761.0f), 775.0f);
-    const float hi = fminf(fmaxf(fmaf(f.y, r, 768.0f), 761.0f), 775.0f);
     // 12582912 = 1.5 * 2^23: the integer code + 8 lands in the low bits of the float
-    y[2 * i] = __float_as_uint(lo + (12582912.0f + 8.0f - 768.0f));
-    y[2 * i + 1] = __float_as_uint(hi + (12582912.0f + 8.0f - 768.0f));
+    y[2 * i] = __float_as_uint(fmaf(f.x, r, 768.0f) + (12582912.0f + 8.0f - 768.0f));
+    y[2 * i + 1] = __float_as_uint(fmaf(f.y, r, 768.0f) + (12582912.0f + 8.0f - 768.0f));
   }
   uint32_t b[4];
 #pragma unroll
@@ -97,7 +110,7 @@ __device__ __forceinline__ uint32_t kv4_codes(const uint32_t (&xin)[4], __half& 
 }
 
 // Rows a thread of the store kernels handles, kv4_block_rows apart.
-constexpr int kKv4StoreRows = 2;
+constexpr int kKv4StoreRows = 4;
 template <int D>
 __host__ __device__ constexpr int kv4_block_rows() { return kKv4StoreThreads / (D / 8); }
 

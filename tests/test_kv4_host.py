@@ -58,18 +58,23 @@ def test_what_is_not_finite_or_zero():
     assert (v[32:] == 0).all() and s[0, 0, 0, 1] == 0
 
 
-def test_fp32_route_gives_the_same_codes():
-    """The kernel multiplies by 1 / s in fp32, rounds to a multiple of 2^-14 and then to an
-    integer. Every fp16 value against every 8-bit scale of one binade (other binades are the
-    same numbers times a power of two): equal to the rounding of the exact quotient."""
-    s = (np.arange(128, 256) * 2.0 ** -7).astype(np.float32)          # 1 .. 2
+def test_fp32_route_gives_the_same_scales_and_codes():
+    """The kernel takes both quotients as products with reciprocals in fp32. Scales: max|x| * (1 / 7),
+    rounded to 16 bits and then to 8, for every fp16 value. Codes: x * (1 / s) (the reciprocal off by
+    up to 2^-22), rounded to a multiple of 2^-14 by adding 768 in one fma and then to an
+    integer, for every fp16 value against every 8-bit scale of one binade (other binades are the
+    same numbers times a power of two). Both equal the rounding of the exact quotient."""
+    a = np.arange(1, 0x7C00, dtype=np.uint16).view(np.float16).astype(np.float32)
+    bits = (a * np.float32(1 / 7)).view(np.uint32)
+    s16 = ((bits + np.uint32(0x80)) & np.uint32(0xFFFFFF00)).view(np.float32)
+    assert np.array_equal(kv4.round_bits(s16, 8), kv4.round_bits(a.astype(np.float64) / 7, 8))
     x = np.arange(0, 0x4C01, dtype=np.uint16).view(np.float16).astype(np.float64)   # 0 .. 16
-    r = np.float32(1) / s
-    for sv, rv in zip(s, r):
-        xs = x[x <= 7.04 * float(sv)]
-        fma = np.rint((xs * float(rv) + 768.0) * 2.0 ** 14) * 2.0 ** -14   # one rounding, as an fma at 768
-        got = np.rint(fma - 768.0)
-        assert np.array_equal(got, np.rint(xs / float(sv)))
+    for sv in np.arange(128, 256) * 2.0 ** -7:          # 1 .. 2
+        xs = x[x <= 7.04 * sv]
+        for off in (-2.0 ** -22, 0.0, 2.0 ** -22):
+            r = float(np.float32((1 + off) / sv))
+            snapped = np.rint((xs * r + 768.0) * 2.0 ** 14) * 2.0 ** -14
+            assert np.array_equal(np.rint(snapped - 768.0), np.rint(xs / sv))
 
 
 def test_select_order_and_ties():
