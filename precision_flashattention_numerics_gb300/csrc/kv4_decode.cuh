@@ -79,16 +79,46 @@ __device__ __forceinline__ int kv4_weight(int units) {
   return units == 0 ? 0 : (units + kKv4Warps - 1) / kKv4Warps + kKv4SegmentStart;
 }
 
-// Weight of the first b_end sequences (per kv head and row tile), summed by a whole warp. All
-// weights of a call fit an int (checked on the host).
-__device__ __forceinline__ int kv4_sum_weight(const Kv4Params& p, int b_end) {
-  if (!p.lengths) return b_end * kv4_weight(kv4_units(p.Sk));
-  int n = 0;
-  for (int b = threadIdx.x & 31; b < b_end; b += 32) n += kv4_weight(kv4_units(p.length(b)));
+// The weights of all sequences (per kv head and row tile), looked at by a whole warp: their sum, the
+// sum of the first b, and the sequence that a place falls in. Lane l holds length l of the first
+// 32, so that a batch that small is read once. All weights of a call fit an int (checked on the host).
+struct Kv4Lengths {
+  const Kv4Params& p;
+  int mine;   // lane l: length l, or 0
+  __device__ __forceinline__ explicit Kv4Lengths(const Kv4Params& params) : p(params), mine(at(threadIdx.x & 31)) {}
+  __device__ __forceinline__ int at(int b) const { return b < p.B ? p.length(b) : 0; }
+  __device__ __forceinline__ int block(int b0) const { return b0 == 0 ? mine : at(b0 + (threadIdx.x & 31)); }
+  __device__ __forceinline__ int sum(int b_end) const {
+    int n = 0;
+    for (int b0 = 0; b0 < b_end; b0 += 32) {
+      const int w = kv4_weight(kv4_units(block(b0)));
+      n += b0 + static_cast<int>(threadIdx.x & 31) < b_end ? w : 0;
+    }
+    return __reduce_add_sync(0xFFFFFFFFu, n);
+  }
+  // The sequence b that `place` falls in, each sequence's weight counted per_b times; `place` becomes
+  // the place inside b. place is less than the sum.
+  __device__ __forceinline__ int find(int& place, int per_b, int& len) const {
+    for (int b0 = 0;; b0 += 32) {
+      const int l = block(b0);
+      const int w = kv4_weight(kv4_units(l)) * per_b;
+      int upto = w;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
-  return n;
-}
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (static_cast<int>(threadIdx.x & 31) >= d) upto += x;
+      }
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > place);
+      if (past != 0) {
+        const int lane = __ffs(past) - 1;
+        place -= __shfl_sync(0xFFFFFFFFu, upto - w, lane);
+        len = __shfl_sync(0xFFFFFFFFu, l, lane);
+        return b0 + lane;
+      }
+      place -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+  }
+};
 
 // The rounds [first(c), first(c + 1)) of CTA c of `ctas`, total >= ctas >= 1: as equal as can be.
 struct Kv4Share {
@@ -344,10 +374,10 @@ struct Kv4Smem {
     float o[kKv4Warps][NT * 8][D + 4];   // when the stages are empty
   };
   Kv4QueryShared<D> q[NT];
-  float sum[NT * 8][D];                  // the CTA's O, read by the others of its cluster
-  float m[kKv4Warps][NT * 8], l[kKv4Warps][NT * 8];
-  float factor[kKv4Warps][NT * 8];
-  float row_m[NT * 8], row_l[NT * 8], offset[NT * 8];
+  float sum[NT * 8][D];                  // the CTA's O, maxima and sums, read by its cluster
+  float2 sum_ml[NT * 8];
+  float2 ml[kKv4Warps][NT * 8];
+  float offset[NT * 8];
   int limit[NT * 8];                     // keys a row sees
 };
 
@@ -363,6 +393,31 @@ __device__ __forceinline__ float kv4_offset(const Kv4Params& p, long long bh, in
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
   return s * p.scale;
+}
+
+__device__ __forceinline__ float2 ld_cluster_float2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_float4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// Write channels ch .. ch + 3 of a row, and with channel 0 its log-sum-exps.
+template <int D>
+__device__ __forceinline__ void kv4_finish(const Kv4Params& p, long long out, long long lse2_at, int ch, float4 x, float mm,
+                                           float ll, float offset) {
+  const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+  const __half2 a = __floats2half2_rn(x.x * inv, x.y * inv), b = __floats2half2_rn(x.z * inv, x.w * inv);
+  *reinterpret_cast<uint2*>(p.o + out * D + ch) = make_uint2(h2_bits(a), h2_bits(b));
+  if (ch == 0) {
+    if (p.lse) p.lse[out] = kv4_lse(mm, ll, offset);
+    if (p.weights) p.lse2[lse2_at] = ll == 0.0f ? INFINITY : mm + log2f(ll);
+  }
 }
 
 template <int D, int NT, bool STREAM_K>
@@ -382,23 +437,18 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
   int in_b = 0;   // segment inside sequence b: h * row_tiles + row tile
   const int per_b = p.Hkv * p.row_tiles;
   if (STREAM_K) {
-    const int total = kv4_sum_weight(p, p.B) * per_b;
+    const Kv4Lengths lengths(p);
+    const int total = lengths.sum(p.B) * per_b;
     const int ctas = min(total, static_cast<int>(gridDim.x));
     if (static_cast<int>(blockIdx.x) >= ctas) return;
     const Kv4Share share(total, ctas);
-    int before = share.first(blockIdx.x);
-    todo = share.first(blockIdx.x + 1) - before;
-    for (;; ++b) {
-      len = p.length(b);
-      n_units = kv4_units(len);
-      const int weight = kv4_weight(n_units);
-      if (before < weight * per_b) {
-        in_b = before / weight;
-        r0 = before - in_b * weight - kKv4SegmentStart;   // its first rounds stand for its start
-        break;
-      }
-      before -= weight * per_b;
-    }
+    int place = share.first(blockIdx.x);
+    todo = share.first(blockIdx.x + 1) - place;
+    b = lengths.find(place, per_b, len);
+    n_units = kv4_units(len);
+    const int weight = kv4_weight(n_units);
+    in_b = place / weight;
+    r0 = place - in_b * weight - kKv4SegmentStart;   // its first rounds stand for its start
   } else {
     const int seg = blockIdx.x / p.cluster;
     b = seg / per_b;
@@ -448,7 +498,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
       sm.q[warp].put(q, lane);
     }
     if (threadIdx.x < kRows) sm.limit[threadIdx.x] = p.limit(row0 + threadIdx.x, len);
-    if (rank == 0 && p.lse)
+    const bool whole = u0 == 0 && u1 == n_units;   // the CTA, or its cluster, has all of the segment
+    if (whole && rank == 0 && p.lse)
       for (int r = warp; r < n_rows; r += kKv4Warps) {
         const float off = kv4_offset<D>(p, bh, row0 + r, lane);
         if (lane == 0) sm.offset[r] = off;
@@ -589,87 +640,73 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
         x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
         x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
         const int r = nt * 8 + 2 * t + c;
-        if (g == 0) {
-          sm.m[warp][r] = m[nt][c];
-          sm.l[warp][r] = x;
-        }
+        if (g == 0) sm.ml[warp][r] = make_float2(m[nt][c], x);
+        // channels 32 j + 4 g ..: a row stride of 4 floats past a multiple of 32 spreads the
+        // quarter warps' rows over the banks
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          *reinterpret_cast<float2*>(&sm.o[warp][r][32 * (i / 2) + 4 * g + 2 * (i % 2)]) =
-              make_float2(o[nt][i][c], o[nt][i][2 + c]);
+        for (int j = 0; j < D / 32; ++j)
+          *reinterpret_cast<float4*>(&sm.o[warp][r][32 * j + 4 * g]) =
+              make_float4(o[nt][2 * j][c], o[nt][2 * j][2 + c], o[nt][2 * j + 1][c], o[nt][2 * j + 1][2 + c]);
       }
     __syncthreads();
     const long long seg = static_cast<long long>(b) * per_b + in_b;
-    const bool whole = u0 == 0 && u1 == n_units;   // the CTA, or its cluster, has all of the segment
-    if (threadIdx.x < n_rows) {
-      const int r = threadIdx.x;
-      float mm = sm.m[0][r];
-#pragma unroll
-      for (int w = 1; w < kKv4Warps; ++w) mm = fmaxf(mm, sm.m[w][r]);
-      float ll = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kKv4Warps; ++w) {
-        const float f = ex2_approx(sm.m[w][r] - mm);   // a warp without a key of this row has sum 0
-        sm.factor[w][r] = f;
-        ll = fmaf(f, sm.l[w][r], ll);
-      }
-      sm.row_m[r] = mm;
-      sm.row_l[r] = ll;
-    }
-    __syncthreads();
     const long long out0 = bh * p.rows + row0;
     const bool alone = STREAM_K || p.cluster == 1;
-    if (!alone || !whole) {
-      // the CTA's own sums: to its cluster, or to the workspace
-      const long long slot = (blockIdx.x + seg) * kRows;
-      for (int idx = threadIdx.x; idx < n_rows * (D / 2); idx += kThreads) {
-        const int r = idx / (D / 2), ch = idx % (D / 2) * 2;
-        float2 x = make_float2(0.0f, 0.0f);
+    // a thread: 4 channels of a row, the row's maximum and sum with them
+    for (int idx = threadIdx.x; idx < n_rows * (D / 4); idx += kThreads) {
+      const int r = idx / (D / 4), ch = idx % (D / 4) * 4;
+      float2 ml[kKv4Warps];
+      float mm = kKv4NoKey, ll = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kKv4Warps; ++w) {
-          const float2 v = *reinterpret_cast<const float2*>(&sm.o[w][r][ch]);
-          x.x = fmaf(sm.factor[w][r], v.x, x.x);
-          x.y = fmaf(sm.factor[w][r], v.y, x.y);
-        }
-        *reinterpret_cast<float2*>(alone ? p.part_o + (slot + r) * D + ch : &sm.sum[r][ch]) = x;
+      for (int w = 0; w < kKv4Warps; ++w) {
+        ml[w] = sm.ml[w][r];
+        mm = fmaxf(mm, ml[w].x);
       }
-      if (alone && threadIdx.x < n_rows) p.part_ml[slot + threadIdx.x] = make_float2(sm.row_m[threadIdx.x], sm.row_l[threadIdx.x]);
-    }
-    if (!alone) cluster_sync_all();
-    if (whole) {
-      const int parts = alone ? kKv4Warps : p.cluster;
-      for (int idx = threadIdx.x + rank * kThreads; idx < n_rows * (D / 2); idx += kThreads * p.cluster) {
-        const int r = idx / (D / 2), ch = idx % (D / 2) * 2;
-        float mm = sm.row_m[r], ll = sm.row_l[r];
-        float2 x = make_float2(0.0f, 0.0f);
-        if (alone) {
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-          for (int w = 0; w < kKv4Warps; ++w) {
-            const float2 v = *reinterpret_cast<const float2*>(&sm.o[w][r][ch]);
-            x.x = fmaf(sm.factor[w][r], v.x, x.x);
-            x.y = fmaf(sm.factor[w][r], v.y, x.y);
-          }
-        } else {
-          mm = kKv4NoKey, ll = 0.0f;
-          for (int w = 0; w < parts; ++w) mm = fmaxf(mm, ld_shared_cluster_f32(mapa_shared(smem_u32(&sm.row_m[r]), w)));
-          for (int w = 0; w < parts; ++w) {
-            const float f = ex2_approx(ld_shared_cluster_f32(mapa_shared(smem_u32(&sm.row_m[r]), w)) - mm);
-            const uint32_t at = mapa_shared(smem_u32(&sm.sum[r][ch]), w);
-            ll = fmaf(f, ld_shared_cluster_f32(mapa_shared(smem_u32(&sm.row_l[r]), w)), ll);
-            x.x = fmaf(f, ld_shared_cluster_f32(at), x.x);
-            x.y = fmaf(f, ld_shared_cluster_f32(at + 4), x.y);
+      for (int w = 0; w < kKv4Warps; ++w) {
+        const float f = ex2_approx(ml[w].x - mm);   // a warp without a key of this row has sum 0
+        const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][r][ch]);
+        ll = fmaf(f, ml[w].y, ll);
+        x.x = fmaf(f, v.x, x.x), x.y = fmaf(f, v.y, x.y), x.z = fmaf(f, v.z, x.z), x.w = fmaf(f, v.w, x.w);
+      }
+      if (!alone) {
+        *reinterpret_cast<float4*>(&sm.sum[r][ch]) = x;
+        if (ch == 0) sm.sum_ml[r] = make_float2(mm, ll);
+      } else if (whole) {
+        kv4_finish<D>(p, out0 + r, seg * kRows + r, ch, x, mm, ll, sm.offset[r]);
+      } else {
+        const long long slot = (blockIdx.x + seg) * kRows + r;
+        *reinterpret_cast<float4*>(p.part_o + slot * D + ch) = x;
+        if (ch == 0) p.part_ml[slot] = make_float2(mm, ll);
+      }
+    }
+    if (!alone) {
+      cluster_sync_all();
+      for (int idx = threadIdx.x * p.cluster + rank; idx < n_rows * (D / 4); idx += kThreads * p.cluster) {
+        const int r = idx / (D / 4), ch = idx % (D / 4) * 4;
+        float2 ml[8];
+        float4 v[8];
+        float mm = kKv4NoKey, ll = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {   // clusters are of 8 at most
+          ml[w] = make_float2(kKv4NoKey, 0.0f), v[w] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (w < p.cluster) {
+            ml[w] = ld_cluster_float2(mapa_shared(smem_u32(&sm.sum_ml[r]), w));
+            v[w] = ld_cluster_float4(mapa_shared(smem_u32(&sm.sum[r][ch]), w));
           }
         }
-        const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-        *reinterpret_cast<__half2*>(p.o + (out0 + r) * D + ch) = __floats2half2_rn(x.x * inv, x.y * inv);
-        if (ch == 0) {
-          if (p.lse) {
-            float off = 0.0f;
-            if (alone) off = sm.offset[r]; else off = ld_shared_cluster_f32(mapa_shared(smem_u32(&sm.offset[r]), 0));
-            p.lse[out0 + r] = kv4_lse(mm, ll, off);
-          }
-          if (p.weights) p.lse2[seg * kRows + r] = ll == 0.0f ? INFINITY : mm + log2f(ll);
+        const float off = ch == 0 ? ld_shared_cluster_f32(mapa_shared(smem_u32(&sm.offset[r]), 0)) : 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) mm = fmaxf(mm, ml[w].x);
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          const float f = ex2_approx(ml[w].x - mm);
+          ll = fmaf(f, ml[w].y, ll);
+          x.x = fmaf(f, v[w].x, x.x), x.y = fmaf(f, v[w].y, x.y), x.z = fmaf(f, v[w].z, x.z), x.w = fmaf(f, v[w].w, x.w);
         }
+        kv4_finish<D>(p, out0 + r, seg * kRows + r, ch, x, mm, ll, off);
       }
     }
     if (!STREAM_K) {
@@ -704,6 +741,7 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
   const long long in_b = seg % per_b;
   const long long bh = static_cast<long long>(b) * p.Hkv + in_b / p.row_tiles;
   const int r = blockIdx.y, row = static_cast<int>(in_b % p.row_tiles) * tile_rows + r;
+  const Kv4Lengths lengths(p);
   // every CTA waits for the decode, also those without work: a kernel behind this one waits for
   // this one only
   if (row >= p.rows) {
@@ -722,9 +760,9 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
     return;
   }
   const int weight = kv4_weight(n_units);
-  const int total = kv4_sum_weight(p, p.B) * static_cast<int>(per_b);
+  const int total = lengths.sum(p.B) * static_cast<int>(per_b);
   const Kv4Share share(total, min(total, p.ctas));
-  const int t0 = kv4_sum_weight(p, b) * static_cast<int>(per_b) + static_cast<int>(in_b) * weight;
+  const int t0 = lengths.sum(b) * static_cast<int>(per_b) + static_cast<int>(in_b) * weight;
   const int c0 = share.cta_of(t0 + kKv4SegmentStart), n = share.cta_of(t0 + weight - 1) - c0 + 1;
   if (n == 1) {   // finished where it was computed
     griddep_wait();
@@ -816,26 +854,19 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
   Kv4WeightsSmem<D>& sm = *reinterpret_cast<Kv4WeightsSmem<D>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int total = kv4_sum_weight(p, p.B) * p.Hkv;
+  const Kv4Lengths lengths(p);
+  const int total = lengths.sum(p.B) * p.Hkv;
   const int ctas = min(total, static_cast<int>(gridDim.x));
   if (static_cast<int>(blockIdx.x) >= ctas) {
     griddep_wait();
     return;
   }
   const Kv4Share share(total, ctas);
-  int before = share.first(blockIdx.x), todo = share.first(blockIdx.x + 1) - before;
-  int b = 0, h = 0, r0 = 0, len, n_units;
-  for (;; ++b) {
-    len = p.length(b);
-    n_units = kv4_units(len);
-    const int weight = kv4_weight(n_units);
-    if (before < weight * p.Hkv) {
-      h = before / weight;
-      r0 = before - h * weight - kKv4SegmentStart;
-      break;
-    }
-    before -= weight * p.Hkv;
-  }
+  int place = share.first(blockIdx.x), todo = share.first(blockIdx.x + 1) - place, len;
+  int b = lengths.find(place, p.Hkv, len);
+  int n_units = kv4_units(len);
+  int h = place / kv4_weight(n_units);
+  int r0 = place - h * kv4_weight(n_units) - kKv4SegmentStart;
   griddep_wait();   // lse2
   while (true) {
     const long long bh = static_cast<long long>(b) * p.Hkv + h;
