@@ -80,42 +80,45 @@ __device__ __forceinline__ int kv4_weight(int units) {
 }
 
 // The weights of all sequences (per kv head and row tile), looked at by a whole warp: their sum, the
-// sum of the first b, and the sequence that a place falls in. Lane l holds length l of the first
-// 32, so that a batch that small is read once. All weights of a call fit an int (checked on the host).
+// sum of the first b, and the sequence that a place falls in. The lanes hold the first 32
+// lengths and their running sums, so that a batch that small is read and scanned once. All
+// weights of a call fit an int (checked on the host).
 struct Kv4Lengths {
   const Kv4Params& p;
-  int mine;   // lane l: length l, or 0
-  __device__ __forceinline__ explicit Kv4Lengths(const Kv4Params& params) : p(params), mine(at(threadIdx.x & 31)) {}
-  __device__ __forceinline__ int at(int b) const { return b < p.B ? p.length(b) : 0; }
-  __device__ __forceinline__ int block(int b0) const { return b0 == 0 ? mine : at(b0 + (threadIdx.x & 31)); }
-  __device__ __forceinline__ int sum(int b_end) const {
-    int n = 0;
-    for (int b0 = 0; b0 < b_end; b0 += 32) {
-      const int w = kv4_weight(kv4_units(block(b0)));
-      n += b0 + static_cast<int>(threadIdx.x & 31) < b_end ? w : 0;
+  int len, upto;   // lane l: length l of the first 32, and their weights up to it
+  __device__ __forceinline__ explicit Kv4Lengths(const Kv4Params& params) : p(params) { block(0, len, upto); }
+  __device__ __forceinline__ void block(int b0, int& l, int& sum) const {
+    const int lane = threadIdx.x & 31;
+    l = b0 + lane < p.B ? p.length(b0 + lane) : 0;
+    sum = kv4_weight(kv4_units(l));
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += x;
     }
-    return __reduce_add_sync(0xFFFFFFFFu, n);
+  }
+  __device__ __forceinline__ int sum(int b_end) const {
+    int n = 0, l, s = upto;
+    for (int b0 = 0; b0 < b_end; b0 += 32) {
+      if (b0 > 0) block(b0, l, s);
+      n += __shfl_sync(0xFFFFFFFFu, s, min(b_end - b0, 32) - 1);
+    }
+    return n;
   }
   // The sequence b that `place` falls in, each sequence's weight counted per_b times; `place` becomes
   // the place inside b. place is less than the sum.
-  __device__ __forceinline__ int find(int& place, int per_b, int& len) const {
+  __device__ __forceinline__ int find(int& place, int per_b, int& length) const {
+    int l = len, s = upto;
     for (int b0 = 0;; b0 += 32) {
-      const int l = block(b0);
-      const int w = kv4_weight(kv4_units(l)) * per_b;
-      int upto = w;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-        if (static_cast<int>(threadIdx.x & 31) >= d) upto += x;
-      }
-      const uint32_t past = __ballot_sync(0xFFFFFFFFu, upto > place);
+      if (b0 > 0) block(b0, l, s);
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, s * per_b > place);
       if (past != 0) {
         const int lane = __ffs(past) - 1;
-        place -= __shfl_sync(0xFFFFFFFFu, upto - w, lane);
-        len = __shfl_sync(0xFFFFFFFFu, l, lane);
+        length = __shfl_sync(0xFFFFFFFFu, l, lane);
+        place -= (__shfl_sync(0xFFFFFFFFu, s, lane) - kv4_weight(kv4_units(length))) * per_b;
         return b0 + lane;
       }
-      place -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+      place -= __shfl_sync(0xFFFFFFFFu, s, 31) * per_b;
     }
   }
 };
@@ -164,9 +167,16 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t (&d)[4], uint32_t saddr) {
                  : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(saddr) : "memory");
 }
 
-// 16 bytes from global to shared memory, asynchronously.
-__device__ __forceinline__ void cp_async16(uint32_t saddr, const void* g) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr), "l"(g) : "memory");
+// 16 bytes from global to shared memory, asynchronously. `policy`: what L2 does with the line.
+__device__ __forceinline__ void cp_async16(uint32_t saddr, const void* g, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(saddr), "l"(g), "l"(policy)
+               : "memory");
+}
+// Codes stream past once: they leave L2 first, so that queries, lengths and partial results stay.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -186,16 +196,16 @@ __device__ __forceinline__ uint32_t kv4_chunk(int row, int c) {
 template <int D>
 __device__ __forceinline__ uint32_t kv4_lane_place(int lane) { return kv4_chunk<D>(lane / (D / 32), lane % (D / 32)); }
 template <int D>
-__device__ __forceinline__ void kv4_fetch(uint32_t stage, const uint8_t* rows, int left, int lane) {
+__device__ __forceinline__ void kv4_fetch(uint32_t stage, const uint8_t* rows, int left, int lane, uint64_t policy) {
   constexpr int kChunks = D / 32;   // per row
   if (left >= kKv4Unit) {
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) cp_async16(stage + 512 * i, rows + 512 * i);
+    for (int i = 0; i < kChunks; ++i) cp_async16(stage + 512 * i, rows + 512 * i, policy);
   } else {
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       if ((i * 32 + lane) / kChunks < left)
-        cp_async16(stage + 512 * i, rows + 512 * i);
+        cp_async16(stage + 512 * i, rows + 512 * i, policy);
       else
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(stage + 512 * i), "r"(0) : "memory");
     }
@@ -226,14 +236,20 @@ struct Kv4Query {
   uint4 b[D / 32];       // per group: channels (0, 4) and (2, 6) times 16, (1, 5), (3, 7) of the lane's 8
   float2 init[D / 32];   // columns 2t, 2t + 1
   float2 factor;         // scores to log2 units: scale log2(e) 2^(20 - e)
-  __device__ __forceinline__ void load(const __half* rows, int n, float scale_log2, int lane) {
+  // The raw rows, n of 8: to be asked for ahead of the codes, whose first burst fills the memory system.
+  static __device__ __forceinline__ void raw(uint4 (&x)[D / 32], const __half* rows, int n, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    uint4 x[D / 32];
-    __half2 m2 = __float2half2_rn(0.0f);
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
       x[w] = make_uint4(0u, 0u, 0u, 0u);
       if (g < n) x[w] = *reinterpret_cast<const uint4*>(rows + g * D + 32 * w + 8 * t);
+    }
+  }
+  __device__ __forceinline__ void prepare(const uint4 (&x)[D / 32], float scale_log2, int lane) {
+    const int t = lane & 3;
+    __half2 m2 = __float2half2_rn(0.0f);
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
       m2 = __hmax2_nan(m2, __hmax2_nan(__hmax2_nan(__habs2(bits_h2(x[w].x)), __habs2(bits_h2(x[w].y))),
                                        __hmax2_nan(__habs2(bits_h2(x[w].z)), __habs2(bits_h2(x[w].w)))));
     }
@@ -431,6 +447,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
   const int rank = STREAM_K ? 0 : static_cast<int>(blockIdx.x % p.cluster);
   griddep_launch_dependents();
   griddep_wait();   // rows that the call's append kernel stores
+  const uint64_t policy = evict_first_policy();
 
   // this CTA's segments: (b, h, row tile) in order, its rounds in all, and the first one's number
   int todo = 0, b = 0, r0 = 0, n_units = 0, len = 0;
@@ -482,20 +499,22 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
         const long long row = bh * p.cap + static_cast<long long>(unit) * kKv4Unit;
         const int left = len - unit * kKv4Unit;
         const uint32_t place = stage + kv4_lane_place<D>(lane);
-        kv4_fetch<D>(place, p.k4 + row * (D / 2) + lane * 16, left, lane);
-        kv4_fetch<D>(place + kValues, p.v4 + row * (D / 2) + lane * 16, left, lane);
+        kv4_fetch<D>(place, p.k4 + row * (D / 2) + lane * 16, left, lane, policy);
+        kv4_fetch<D>(place + kValues, p.v4 + row * (D / 2) + lane * 16, left, lane, policy);
         ks = kv4_row_scales<D>(p.kscale + row * (D / 32), left, lane);
         vs = kv4_row_scales<D>(p.vscale + row * (D / 32), left, lane);
       }
       cp_async_commit();
     };
-    fetch(u, stage0);
-    Kv4Query<D> q;   // NT = 1: in registers; else in shared memory, a tile per warp
-    if constexpr (NT == 1) {
-      q.load(p.q + (bh * p.rows + row0) * D, n_rows, p.scale_log2, lane);
-    } else if (warp < NT) {
-      q.load(p.q + (bh * p.rows + row0 + warp * 8) * D, n_rows - warp * 8, p.scale_log2, lane);
-      sm.q[warp].put(q, lane);
+    // the queries: NT = 1 in registers, else in shared memory, a tile per warp
+    Kv4Query<D> q;
+    {
+      uint4 raw[D / 32];
+      const int tile = NT == 1 ? 0 : warp;
+      if (tile < NT) Kv4Query<D>::raw(raw, p.q + (bh * p.rows + row0 + tile * 8) * D, n_rows - tile * 8, lane);
+      fetch(u, stage0);
+      if (tile < NT) q.prepare(raw, p.scale_log2, lane);
+      if (NT > 1 && tile < NT) sm.q[tile].put(q, lane);
     }
     if (threadIdx.x < kRows) sm.limit[threadIdx.x] = p.limit(row0 + threadIdx.x, len);
     const bool whole = u0 == 0 && u1 == n_units;   // the CTA, or its cluster, has all of the segment
@@ -868,6 +887,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
   int h = place / kv4_weight(n_units);
   int r0 = place - h * kv4_weight(n_units) - kKv4SegmentStart;
   griddep_wait();   // lse2
+  const uint64_t policy = evict_first_policy();
   while (true) {
     const long long bh = static_cast<long long>(b) * p.Hkv + h;
     const int r1 = min((n_units + kKv4Warps - 1) / kKv4Warps, r0 + todo);
@@ -883,18 +903,21 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
       if (unit < u1) {
         const long long key = static_cast<long long>(unit) * kKv4Unit;
         const int left = len - unit * kKv4Unit;
-        kv4_fetch<D>(stage + kv4_lane_place<D>(lane), k4 + key * (D / 2) + lane * 16, left, lane);
+        kv4_fetch<D>(stage + kv4_lane_place<D>(lane), k4 + key * (D / 2) + lane * 16, left, lane, policy);
         ks = kv4_row_scales<D>(kscale + key * (D / 32), left, lane);
       }
       cp_async_commit();
     };
     int u = u0 + warp;
-    fetch(u, stage0);
     for (int i = warp; i * 8 < p.rows; i += kKv4Warps) {
       Kv4Query<D> q;
-      q.load(p.q + (bh * p.rows + i * 8) * D, p.rows - i * 8, p.scale_log2, lane);
+      uint4 raw[D / 32];
+      Kv4Query<D>::raw(raw, p.q + (bh * p.rows + i * 8) * D, p.rows - i * 8, lane);
+      if (i == warp) fetch(u, stage0);
+      q.prepare(raw, p.scale_log2, lane);
       sm.q[i].put(q, lane);
     }
+    if (warp * 8 >= p.rows) fetch(u, stage0);
     for (int r = threadIdx.x; r < (p.rows + 7) / 8 * 8; r += kKv4Warps * 32) {
       // a row past the last, or without a key, weighs nothing
       sm.ref[r] = r < p.rows ? p.lse2[(bh * p.row_tiles + r / tile_rows) * tile_rows + r % tile_rows] : INFINITY;
