@@ -233,9 +233,9 @@ __device__ __forceinline__ uint2 kv4_row_scales(const __half* rows, int left, in
 // in [2^10, 2^11): exact but for entries 2^-34 below the largest.
 template <int D>
 struct Kv4Query {
-  uint4 b[D / 32];       // per group: channels (0, 4) and (2, 6) times 16, (1, 5), (3, 7) of the lane's 8
-  float2 init[D / 32];   // columns 2t, 2t + 1
-  float2 factor;         // scores to log2 units: scale log2(e) 2^(20 - e)
+  uint4 b[D / 32];      // per group: channels (0, 4) and (2, 6) times 16, (1, 5), (3, 7) of the lane's 8
+  float start[D / 32];  // of row g: -8 2^-20 sum q'
+  float factor;         // of row g: scores to log2 units: scale log2(e) 2^(20 - e)
   // The raw rows, n of 8: to be asked for ahead of the codes, whose first burst fills the memory system.
   static __device__ __forceinline__ void raw(uint4 (&x)[D / 32], const __half* rows, int n, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -245,14 +245,12 @@ struct Kv4Query {
       if (g < n) x[w] = *reinterpret_cast<const uint4*>(rows + g * D + 32 * w + 8 * t);
     }
   }
-  __device__ __forceinline__ void prepare(const uint4 (&x)[D / 32], float scale_log2, int lane) {
-    const int t = lane & 3;
+  __device__ __forceinline__ void prepare(const uint4 (&x)[D / 32], float scale_log2) {
     __half2 m2 = __float2half2_rn(0.0f);
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
+    for (int w = 0; w < D / 32; ++w)
       m2 = __hmax2_nan(m2, __hmax2_nan(__hmax2_nan(__habs2(bits_h2(x[w].x)), __habs2(bits_h2(x[w].y))),
                                        __hmax2_nan(__habs2(bits_h2(x[w].z)), __habs2(bits_h2(x[w].w)))));
-    }
     __half m1 = __hmax_nan(__low2half(m2), __high2half(m2));
     m1 = __hmax_nan(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 1));
     m1 = __hmax_nan(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, 2));
@@ -260,8 +258,7 @@ struct Kv4Query {
     // a row that is all 0, or not finite, is left as it is
     const int e = m > 0.0f && m <= 65504.0f ? 137 - static_cast<int>(__float_as_uint(m) >> 23) : 0;
     const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    const float f = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 20 - e) << 23);
-    factor = make_float2(__shfl_sync(0xFFFFFFFFu, f, 8 * t), __shfl_sync(0xFFFFFFFFu, f, 8 * t + 4));
+    factor = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + 20 - e) << 23);
     const __half2 sixteen = __float2half2_rn(16.0f);
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
@@ -279,26 +276,46 @@ struct Kv4Query {
       }
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-      sum *= -8.0f / 1048576.0f;
-      init[w] = make_float2(__shfl_sync(0xFFFFFFFFu, sum, 8 * t), __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4));
+      start[w] = sum * (-8.0f / 1048576.0f);
       b[w].x = h2_bits(__hmul2(bits_h2(__byte_perm(h[0], h[2], 0x5410)), sixteen));
       b[w].y = h2_bits(__hmul2(bits_h2(__byte_perm(h[1], h[3], 0x5410)), sixteen));
       b[w].z = __byte_perm(h[0], h[2], 0x7632);
       b[w].w = __byte_perm(h[1], h[3], 0x7632);
     }
   }
+  // A value of row g as the values of rows 2t and 2t + 1, the columns of an output fragment.
+  static __device__ __forceinline__ float2 columns(float x, int lane) {
+    return make_float2(__shfl_sync(0xFFFFFFFFu, x, 8 * (lane & 3)), __shfl_sync(0xFFFFFFFFu, x, 8 * (lane & 3) + 4));
+  }
 };
 
-// The same in shared memory, for the warps of a CTA to share.
+// 8 rows in shared memory as S^T needs them, for the warps of a CTA to share.
 template <int D>
-struct Kv4QueryShared {
+struct __align__(16) Kv4QueryShared {
   uint4 b[D / 32][32];
   float2 init[D / 32][32];
   float2 factor[32];
   __device__ __forceinline__ void put(const Kv4Query<D>& q, int lane) {
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) b[w][lane] = q.b[w], init[w][lane] = q.init[w];
-    factor[lane] = q.factor;
+    for (int w = 0; w < D / 32; ++w) b[w][lane] = q.b[w], init[w][lane] = Kv4Query<D>::columns(q.start[w], lane);
+    factor[lane] = Kv4Query<D>::columns(q.factor, lane);
+  }
+};
+
+// 16 rows in shared memory as S = Q K'^T needs them: the A operands of a group's two MMAs.
+template <int D>
+struct __align__(16) Kv4Query16 {
+  uint32_t a[D / 32][2][32][4];
+  float start[D / 32][32][2];    // rows g, g + 8
+  float factor[32][2];
+  __device__ __forceinline__ void put(const Kv4Query<D>& q, int tile, int lane) {
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      a[w][0][lane][tile] = q.b[w].x, a[w][0][lane][2 + tile] = q.b[w].y;
+      a[w][1][lane][tile] = q.b[w].z, a[w][1][lane][2 + tile] = q.b[w].w;
+      start[w][lane][tile] = q.start[w];
+    }
+    factor[lane][tile] = q.factor;
   }
 };
 
@@ -317,28 +334,48 @@ __device__ __forceinline__ void kv4_score_group(float (&acc)[4], int w, uint32_t
   acc[3] = w == 0 ? sb * d[3] : fmaf(sb, d[3], acc[3]);
 }
 
-// One stage of a warp: 32 rows of key and value codes and their scales, the keys' as fp32
-// rows, the values' as fp16 [group][8 t + 2 blk + key % 2] for key 8 blk + 2 t + ..: the four
-// key pairs of a lane side by side.
+// S (unscaled) of 16 rows (g and g + 8) and the keys 2t and 2t + 1 of 8, group w's part; k: the
+// lane's 8 codes of key g, s0, s1: the scales of the two keys.
+__device__ __forceinline__ void kv4_score_group16(float (&acc)[4], int w, uint32_t k, float s0, float s1, const uint4& qa,
+                                                  const uint4& qb, const float2& start) {
+  const uint32_t lo = 0x000F000Fu, hi = 0x00F000F0u;
+  const uint32_t k8 = k >> 8;
+  float d[4];
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%11,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(qa.x), "r"(qa.y), "r"(qa.z), "r"(qa.w), "r"(k & lo), "r"(k8 & lo), "f"(start.x), "f"(start.y));
+  mma_f16(d, qb.x, qb.y, qb.z, qb.w, k & hi, k8 & hi);
+  acc[0] = w == 0 ? s0 * d[0] : fmaf(s0, d[0], acc[0]);
+  acc[1] = w == 0 ? s1 * d[1] : fmaf(s1, d[1], acc[1]);
+  acc[2] = w == 0 ? s0 * d[2] : fmaf(s0, d[2], acc[2]);
+  acc[3] = w == 0 ? s1 * d[3] : fmaf(s1, d[3], acc[3]);
+}
+
+// One stage of a warp: 32 rows of key and value codes and their scales. Where a lane needs keys by
+// pairs (8 blk + 2 t, + 1 for blk = 0 .. 3), the scales are [group][8 t + 2 blk + key % 2]: the
+// values' as fp16, and with 16 query rows (PAIRS) the keys' as fp32; else those are rows.
 template <int D, bool VALUES>
 struct __align__(128) Kv4Stage {
   uint8_t k[kKv4Unit * D / 2];
   uint8_t v[VALUES ? kKv4Unit * D / 2 : 16];
-  float ks[kKv4Unit][D / 32];
+  float ks[kKv4Unit * D / 32];
   __half vs[D / 32][kKv4Unit];
 };
 
-template <int D, bool VALUES>
+template <int D, bool VALUES, bool PAIRS>
 __device__ __forceinline__ void kv4_put_scales(Kv4Stage<D, VALUES>& st, uint2 ks, uint2 vs, int lane) {
-  const float2 a = __half22float2(bits_h2(ks.x));
-  if constexpr (D == 128) {
-    const float2 b = __half22float2(bits_h2(ks.y));
-    *reinterpret_cast<float4*>(st.ks[lane]) = make_float4(a.x, a.y, b.x, b.y);
+  const int at = (lane >> 1 & 3) * 8 + (lane >> 3) * 2 + (lane & 1);
+  const float2 a = __half22float2(bits_h2(ks.x)), b = __half22float2(bits_h2(ks.y));
+  if constexpr (PAIRS) {
+    st.ks[at] = a.x, st.ks[32 + at] = a.y;
+    if constexpr (D == 128) st.ks[64 + at] = b.x, st.ks[96 + at] = b.y;
+  } else if constexpr (D == 128) {
+    *reinterpret_cast<float4*>(&st.ks[4 * lane]) = make_float4(a.x, a.y, b.x, b.y);
   } else {
-    *reinterpret_cast<float2*>(st.ks[lane]) = a;
+    *reinterpret_cast<float2*>(&st.ks[2 * lane]) = a;
   }
   if constexpr (VALUES) {
-    const int at = (lane >> 1 & 3) * 8 + (lane >> 3) * 2 + (lane & 1);
     st.vs[0][at] = __low2half(bits_h2(vs.x));
     st.vs[1][at] = __high2half(bits_h2(vs.x));
     if constexpr (D == 128) {
@@ -366,7 +403,7 @@ __device__ __forceinline__ void kv4_take_keys(uint32_t (&ka)[D / 32], uint32_t (
   }
 }
 template <int D>
-__device__ __forceinline__ void kv4_take_scales(float (&s)[D / 32], const float (&row)[D / 32]) {
+__device__ __forceinline__ void kv4_take_scales(float (&s)[D / 32], const float* row) {
   if constexpr (D == 128) {
     const float4 x = *reinterpret_cast<const float4*>(row);
     s[0] = x.x, s[1] = x.y, s[2] = x.z, s[3] = x.w;
@@ -389,7 +426,7 @@ struct Kv4Smem {
     Kv4Stage<D, true> stage[2][kKv4Warps];
     float o[kKv4Warps][NT * 8][D + 4];   // when the stages are empty
   };
-  Kv4QueryShared<D> q[NT];
+  Kv4Query16<D> q;                       // NT = 2
   float sum[NT * 8][D];                  // the CTA's O, maxima and sums, read by its cluster
   float2 sum_ml[NT * 8];
   float2 ml[kKv4Warps][NT * 8];
@@ -506,15 +543,21 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
       }
       cp_async_commit();
     };
-    // the queries: NT = 1 in registers, else in shared memory, a tile per warp
+    // the queries: NT = 1 in registers, else in shared memory, 8 rows per warp
     Kv4Query<D> q;
     {
       uint4 raw[D / 32];
       const int tile = NT == 1 ? 0 : warp;
       if (tile < NT) Kv4Query<D>::raw(raw, p.q + (bh * p.rows + row0 + tile * 8) * D, n_rows - tile * 8, lane);
       fetch(u, stage0);
-      if (tile < NT) q.prepare(raw, p.scale_log2, lane);
-      if (NT > 1 && tile < NT) sm.q[tile].put(q, lane);
+      if (tile < NT) q.prepare(raw, p.scale_log2);
+      if (NT == 2 && tile < NT) sm.q.put(q, tile, lane);
+    }
+    float2 init[D / 32], factor;
+    if constexpr (NT == 1) {
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) init[w] = Kv4Query<D>::columns(q.start[w], lane);
+      factor = Kv4Query<D>::columns(q.factor, lane);
     }
     if (threadIdx.x < kRows) sm.limit[threadIdx.x] = p.limit(row0 + threadIdx.x, len);
     const bool whole = u0 == 0 && u1 == n_units;   // the CTA, or its cluster, has all of the segment
@@ -524,109 +567,122 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
         if (lane == 0) sm.offset[r] = off;
       }
     __syncthreads();
-    float o[NT][D / 16][4];
-    float m[NT][2], l[NT][2];
+    if constexpr (NT == 2) factor = make_float2(sm.q.factor[lane][0], sm.q.factor[lane][1]);
+    // O: with 8 rows O^T (channels along g, the lane's rows 2t, 2t + 1), with 16 O (its rows g, g + 8)
+    constexpr int kTiles = NT == 1 ? D / 16 : D / 8;
+    float o[kTiles][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
-      m[nt][0] = m[nt][1] = kKv4NoKey;
-      l[nt][0] = l[nt][1] = 0.0f;
-    }
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+    float m[2] = {kKv4NoKey, kKv4NoKey}, l[2] = {0.0f, 0.0f};   // of the lane's two rows
     const int all_see = p.causal ? max(0, len - p.Sq + 1) : len;   // keys that every row sees
-
     uint32_t odd = 0;   // the stage at hand
     for (; u < u1; u += u_step) {
       const int key0 = u * kKv4Unit;
       auto& st = sm.stage[odd][warp];
       const uint32_t here = stage0 + odd * kStageBytes;
       cp_async_wait<0>();
-      kv4_put_scales(st, ks, vs, lane);
+      kv4_put_scales<D, true, NT == 2>(st, ks, vs, lane);
       __syncwarp();   // the stage is there, and every lane is done with the other one
       odd ^= 1;
       fetch(u + u_step, stage0 + odd * kStageBytes);
-      float s[2][NT][4];
+      // s[i]: of the lane's rows and 2 keys; NT = 1: i = half h, keys 16 h + g (elements 0, 1: rows 2t,
+      // 2t + 1) and 16 h + 8 + g (2, 3); NT = 2: i = blk, keys 8 blk + 2 t, + 1 of row g (0, 1) and g + 8
+      float s[2 * NT][4];
+      if constexpr (NT == 1) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t ka[D / 32], kb[D / 32];
-        kv4_take_keys<D>(ka, kb, here + kv4_key_place<D>(lane), h);
-        float sa[D / 32], sb[D / 32];
-        kv4_take_scales<D>(sa, st.ks[16 * h + g]);
-        kv4_take_scales<D>(sb, st.ks[16 * h + 8 + g]);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t ka[D / 32], kb[D / 32];
+          kv4_take_keys<D>(ka, kb, here + kv4_key_place<D>(lane), h);
+          float sa[D / 32], sb[D / 32];
+          kv4_take_scales<D>(sa, &st.ks[(16 * h + g) * (D / 32)]);
+          kv4_take_scales<D>(sb, &st.ks[(16 * h + 8 + g) * (D / 32)]);
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w)
+          for (int w = 0; w < D / 32; ++w) kv4_score_group(s[h], w, ka[w], kb[w], sa[w], sb[w], q.b[w], init[w]);
+        }
+      } else {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (NT == 1)
-              kv4_score_group(s[h][nt], w, ka[w], kb[w], sa[w], sb[w], q.b[w], q.init[w]);
-            else
-              kv4_score_group(s[h][nt], w, ka[w], kb[w], sa[w], sb[w], sm.q[nt].b[w][lane], sm.q[nt].init[w][lane]);
-          }
+        for (int w = 0; w < D / 32; ++w) {
+          const uint4 qa = *reinterpret_cast<const uint4*>(sm.q.a[w][0][lane]);
+          const uint4 qb = *reinterpret_cast<const uint4*>(sm.q.a[w][1][lane]);
+          const float2 start = *reinterpret_cast<const float2*>(sm.q.start[w][lane]);
+          uint32_t k[4];   // key 8 blk + g, channels 32 w + 8 t ..
+          ldmatrix_x4<false>(k, (here + kv4_chunk<D>(lane, 0)) ^ (w << 4));
+          float sc[8];
+          *reinterpret_cast<float4*>(sc) = *reinterpret_cast<const float4*>(&st.ks[32 * w + 8 * t]);
+          *reinterpret_cast<float4*>(sc + 4) = *reinterpret_cast<const float4*>(&st.ks[32 * w + 8 * t + 4]);
+#pragma unroll
+          for (int blk = 0; blk < 4; ++blk)
+            kv4_score_group16(s[blk], w, k[blk], sc[2 * blk], sc[2 * blk + 1], qa, qb, start);
+        }
       }
       if (key0 + kKv4Unit > all_see) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int c = 0; c < 2; ++c) {
+          const int lim = sm.limit[NT == 1 ? 2 * t + c : g + 8 * c] - key0 - (NT == 1 ? g : 2 * t);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int lim = sm.limit[nt * 8 + 2 * t + c] - key0 - g;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (16 * h >= lim) s[h][nt][c] = -INFINITY;
-              if (16 * h + 8 >= lim) s[h][nt][2 + c] = -INFINITY;
+          for (int i = 0; i < 2 * NT; ++i) {
+            if (NT == 1) {
+              if (16 * i >= lim) s[i][c] = -INFINITY;
+              if (16 * i + 8 >= lim) s[i][2 + c] = -INFINITY;
+            } else {
+              if (8 * i >= lim) s[i][2 * c] = -INFINITY;
+              if (8 * i + 1 >= lim) s[i][2 * c + 1] = -INFINITY;
             }
           }
+        }
       }
       // the reference a row's exponentials are taken against moves only when a score passes it
       // by more than 8 (log2 units): P stays below 2^8, and most units need no reduction
-      uint32_t pb[2][NT][2];
-      bool grow = false;
-      float mx[NT][2];
-      float2 factor[NT];
+      float mx[2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        factor[nt] = NT == 1 ? q.factor : sm.q[nt].factor[lane];
-        mx[nt][0] = fmaxf(fmaxf(s[0][nt][0], s[0][nt][2]), fmaxf(s[1][nt][0], s[1][nt][2])) * factor[nt].x;
-        mx[nt][1] = fmaxf(fmaxf(s[0][nt][1], s[0][nt][3]), fmaxf(s[1][nt][1], s[1][nt][3])) * factor[nt].y;
-        grow |= mx[nt][0] > m[nt][0] + 8.0f;
-        grow |= mx[nt][1] > m[nt][1] + 8.0f;
+      for (int c = 0; c < 2; ++c) {
+        mx[c] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i)
+          mx[c] = fmaxf(mx[c], NT == 1 ? fmaxf(s[i][c], s[i][2 + c]) : fmaxf(s[i][2 * c], s[i][2 * c + 1]));
+        mx[c] *= c ? factor.y : factor.x;
       }
-      if (__any_sync(0xFFFFFFFFu, grow)) {
+      if (__any_sync(0xFFFFFFFFu, mx[0] > m[0] + 8.0f || mx[1] > m[1] + 8.0f)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int c = 0; c < 2; ++c) {
+          float x = mx[c];   // over the lanes that share the row
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x = mx[nt][c];
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-            x = fmaxf(x, m[nt][c]);
-            const float f = ex2_approx(m[nt][c] - x);
-            m[nt][c] = x;
-            l[nt][c] *= f;
+          for (int d = NT == 1 ? 4 : 1; d < (NT == 1 ? 32 : 4); d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, d));
+          x = fmaxf(x, m[c]);
+          const float f = ex2_approx(m[c] - x);
+          m[c] = x;
+          l[c] *= f;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              o[nt][i][c] *= f;
-              o[nt][i][2 + c] *= f;
-            }
+          for (int i = 0; i < kTiles; ++i) {
+            o[i][NT == 1 ? c : 2 * c] *= f;
+            o[i][NT == 1 ? 2 + c : 2 * c + 1] *= f;
           }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float e0 = ex2_approx(fmaf(s[h][nt][0], factor[nt].x, -m[nt][0]));
-          const float e1 = ex2_approx(fmaf(s[h][nt][1], factor[nt].y, -m[nt][1]));
-          const float e2 = ex2_approx(fmaf(s[h][nt][2], factor[nt].x, -m[nt][0]));
-          const float e3 = ex2_approx(fmaf(s[h][nt][3], factor[nt].y, -m[nt][1]));
-          l[nt][0] += e0 + e2;
-          l[nt][1] += e1 + e3;
-          pb[h][nt][0] = movmatrix(h2_bits(__floats2half2_rn(e0, e1)));
-          pb[h][nt][1] = movmatrix(h2_bits(__floats2half2_rn(e2, e3)));
         }
-      // O^T += V^T P^T, a group of 32 channels at a time: a transposed 8 x 8 block of 16-bit words
-      // is 4 channels (4 g ..) of the two keys 8 blk + 2 t, + 1
+      }
+      // P in fp16, NT = 1: P^T as the B operand (keys and rows change places: movmatrix), NT = 2: as A
+      uint32_t pf[2][2 * NT];
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) {
+        float e[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const bool second = NT == 1 ? (c & 1) : c >= 2;
+          e[c] = ex2_approx(fmaf(s[i][c], second ? factor.y : factor.x, -(second ? m[1] : m[0])));
+          l[second ? 1 : 0] += e[c];
+        }
+        const uint32_t p01 = h2_bits(__floats2half2_rn(e[0], e[1])), p23 = h2_bits(__floats2half2_rn(e[2], e[3]));
+        if constexpr (NT == 1) {
+          pf[i][0] = movmatrix(p01);
+          pf[i][1] = movmatrix(p23);
+        } else {
+          pf[i / 2][2 * (i % 2)] = p01;
+          pf[i / 2][2 * (i % 2) + 1] = p23;
+        }
+      }
+      // O += P V, a group of 32 channels at a time: a transposed 8 x 8 block of 16-bit words is 4
+      // channels (4 g ..) of the two keys 8 blk + 2 t, + 1
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         uint32_t v[4];
@@ -638,11 +694,13 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
           __half2 a[4], c[4];
           kv4_expand(v[2 * h], bits_h2(s2[2 * h]), a);
           kv4_expand(v[2 * h + 1], bits_h2(s2[2 * h + 1]), c);
+          if constexpr (NT == 1) {
+            mma_f16(o[2 * j], h2_bits(a[0]), h2_bits(a[1]), h2_bits(c[0]), h2_bits(c[1]), pf[h][0], pf[h][1]);
+            mma_f16(o[2 * j + 1], h2_bits(a[2]), h2_bits(a[3]), h2_bits(c[2]), h2_bits(c[3]), pf[h][0], pf[h][1]);
+          } else {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(o[nt][2 * j], h2_bits(a[0]), h2_bits(a[1]), h2_bits(c[0]), h2_bits(c[1]), pb[h][nt][0], pb[h][nt][1]);
-            mma_f16(o[nt][2 * j + 1], h2_bits(a[2]), h2_bits(a[3]), h2_bits(c[2]), h2_bits(c[3]), pb[h][nt][0],
-                    pb[h][nt][1]);
+            for (int i = 0; i < 4; ++i)   // channels 32 j + 4 n + i, n the output's column
+              mma_f16(o[4 * j + i], pf[h][0], pf[h][1], pf[h][2], pf[h][3], h2_bits(a[i]), h2_bits(c[i]));
           }
         }
       }
@@ -651,22 +709,27 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
 
     // ---- join the warps ----
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int c = 0; c < 2; ++c) {
+      float x = l[c];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float x = l[nt][c];
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 4);
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 8);
-        x += __shfl_xor_sync(0xFFFFFFFFu, x, 16);
-        const int r = nt * 8 + 2 * t + c;
-        if (g == 0) sm.ml[warp][r] = make_float2(m[nt][c], x);
-        // channels 32 j + 4 g ..: a row stride of 4 floats past a multiple of 32 spreads the
-        // quarter warps' rows over the banks
+      for (int d = NT == 1 ? 4 : 1; d < (NT == 1 ? 32 : 4); d <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+      const int r = NT == 1 ? 2 * t + c : g + 8 * c;
+      if ((NT == 1 ? g : t) == 0) sm.ml[warp][r] = make_float2(m[c], x);
+      // 4 channels at a time; a row stride of 4 floats past a multiple of 32 spreads the quarter
+      // warps' rows over the banks
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j)
-          *reinterpret_cast<float4*>(&sm.o[warp][r][32 * j + 4 * g]) =
-              make_float4(o[nt][2 * j][c], o[nt][2 * j][2 + c], o[nt][2 * j + 1][c], o[nt][2 * j + 1][2 + c]);
+      for (int j = 0; j < D / 32; ++j) {
+        float* to = &sm.o[warp][r][32 * j];
+        if constexpr (NT == 1) {
+          *reinterpret_cast<float4*>(to + 4 * g) = make_float4(o[2 * j][c], o[2 * j][2 + c], o[2 * j + 1][c], o[2 * j + 1][2 + c]);
+        } else {
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            *reinterpret_cast<float4*>(to + 8 * t + 4 * n) =
+                make_float4(o[4 * j][2 * c + n], o[4 * j + 1][2 * c + n], o[4 * j + 2][2 * c + n], o[4 * j + 3][2 * c + n]);
+        }
       }
+    }
     __syncthreads();
     const long long seg = static_cast<long long>(b) * per_b + in_b;
     const long long out0 = bh * p.rows + row0;
@@ -914,7 +977,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
       uint4 raw[D / 32];
       Kv4Query<D>::raw(raw, p.q + (bh * p.rows + i * 8) * D, p.rows - i * 8, lane);
       if (i == warp) fetch(u, stage0);
-      q.prepare(raw, p.scale_log2, lane);
+      q.prepare(raw, p.scale_log2);
       sm.q[i].put(q, lane);
     }
     if (warp * 8 >= p.rows) fetch(u, stage0);
@@ -931,7 +994,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
       auto& st = sm.stage[odd][warp];
       const uint32_t here = stage0 + odd * kStageBytes;
       cp_async_wait<0>();
-      kv4_put_scales(st, ks, ks, lane);
+      kv4_put_scales<D, false, false>(st, ks, ks, lane);
       __syncwarp();
       odd ^= 1;
       fetch(u + kKv4Warps, stage0 + odd * kStageBytes);
@@ -945,8 +1008,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
         uint32_t ka[D / 32], kb[D / 32];
         kv4_take_keys<D>(ka, kb, here + kv4_key_place<D>(lane), half);
         float sa[D / 32], sb[D / 32];
-        kv4_take_scales<D>(sa, st.ks[16 * half + g]);
-        kv4_take_scales<D>(sb, st.ks[16 * half + 8 + g]);
+        kv4_take_scales<D>(sa, &st.ks[(16 * half + g) * (D / 32)]);
+        kv4_take_scales<D>(sb, &st.ks[(16 * half + 8 + g) * (D / 32)]);
         for (int i = 0; i < p.rows; i += 8) {
           const auto& q = sm.q[i / 8];
           float s[4];
