@@ -469,7 +469,7 @@ int pasa_kprep_fp8_blocks(const void* k, void* k8, void* means, float* kscale, i
  *   starts  int32 [B], device, or NULL: `start` for every sequence (0 <= start, start + n <=
  *           Sk_cap, else PASA_ERR_SHAPE)
  *   counts  int32 [B], device, or NULL for n: only rows i < counts[b] are stored or read (a
- *           padded batch; the padding is not read)
+ *           padded batch)
  * Rows that fall outside 0 .. Sk_cap - 1 (from starts on the device) are skipped, and what
  * is not stored or read is left as it was. starts and counts need 4-byte alignment.
  */

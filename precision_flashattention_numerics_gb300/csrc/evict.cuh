@@ -24,19 +24,24 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 constexpr int kEvictBins = 4096;
+constexpr int kEvictPer = 32;                               // weights of a thread
+constexpr int kEvictChunk = kEvictThreads * kEvictPer;      // rows that a CTA holds in registers
 
-// One CTA per (sequence, kv head): the rows it keeps, ascending, -1 past the last. The
-// threshold is found in three passes over the weights (read from L2 after the first), by their
-// keys' bits 31 .. 20, 19 .. 10 and 9 .. 0: with 12 bits, weights of similar size spread over
-// several counters even in the first pass. Zeros, the weight of every row not yet looked at,
-// are counted by warp instead of one by one.
+// One CTA per (sequence, kv head): the rows it keeps, ascending, -1 past the last: the budget
+// largest keys, a recent row's key being above every weight's (kRecent) and that of a row past
+// the last below (kNone). The threshold is found in three passes over the keys, by bits 31 .. 20,
+// 19 .. 10 and 9 .. 0: with 12 bits, weights of similar size spread over several counters even in
+// the first pass. Zeros, the weight of every row not yet looked at, and recent rows are
+// counted apart, not one by one in the same counter. Up to 32768 rows are read once and stay in
+// registers; longer ones are read again (from L2) in every pass, a chunk at a time. A warp holds
+// a run of the chunk's rows, up to 32 a lane.
 __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const float* __restrict__ weights,
                                                                      const int* __restrict__ lengths,
                                                                      int* __restrict__ index, int Hkv, int Sk,
                                                                      long long cap, int budget, int recent) {
   __shared__ uint32_t hist[kEvictBins];
   __shared__ uint32_t s_warp[32], s_prefix, s_left;
-  __shared__ int s_gt[32], s_eq[32];
+  __shared__ int s_keep[32], s_eq[32];
   griddep_launch_dependents();
   const long long bh = blockIdx.x;
   const int len = lengths ? max(0, min(lengths[bh / Hkv], Sk)) : Sk;
@@ -47,104 +52,120 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const float
     for (int j = tid; j < budget; j += kEvictThreads) idx[j] = j < len ? j : -1;
     return;
   }
-  const int n = len - recent;           // candidates 0 .. n - 1
-  uint32_t left = budget - recent;      // how many of them stay
-  uint32_t prefix = 0;                  // the left-th largest candidate's key
-  const bool any = left > 0;
-  if (any) {
-    constexpr uint32_t kZero = 0x80000000u;
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 20 : pass == 1 ? 10 : 0;
-      const uint32_t mask = pass == 0 ? 0xFFFu : 0x3FFu;
-      for (int i = tid; i < kEvictBins; i += kEvictThreads) hist[i] = 0;
-      __syncthreads();
-      for (int j0 = 0; j0 < n; j0 += 8 * kEvictThreads) {
-        float x[8];
+  constexpr uint32_t kZero = 0x80000000u, kNone = 0u, kRecent = 0xFFFFFFFFu;
+  uint32_t left = budget;               // of the keys that match `prefix` so far, how many stay
+  uint32_t prefix = 0;                  // the budget-th largest key
+  const int chunks = (len + kEvictChunk - 1) / kEvictChunk;
+  const int per = chunks > 1 ? kEvictPer : (len + kEvictThreads - 1) / kEvictThreads;   // elements of a lane
+  uint32_t k[kEvictPer];                // element i: row `first` + 32 i of the chunk at hand
+  const int first = warp * (32 * per) + lane;
+  auto load = [&](int chunk) {
+    const int base = chunk * kEvictChunk + first;
+    // all loads first, without branches between them
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int j = j0 + i * kEvictThreads + tid;
-          x[i] = j < n ? w[j] : 0.0f;
-        }
+    for (int i = 0; i < kEvictPer; ++i)
+      k[i] = __float_as_uint(__ldg(w + (i < per ? min(base + 32 * i, len - 1) : 0)));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t k = weight_key(x[i]);
-          const bool in = j0 + i * kEvictThreads + tid < n &&
-                          (pass == 0 || (k >> (pass == 1 ? 20 : 10)) == (prefix >> (pass == 1 ? 20 : 10)));
-          const uint32_t zeros = __ballot_sync(0xFFFFFFFFu, in && k == kZero);
-          if (in && k != kZero) atomicAdd(&hist[(k >> shift) & mask], 1u);
-          if (zeros != 0 && lane == 0) atomicAdd(&hist[(kZero >> shift) & mask], static_cast<uint32_t>(__popc(zeros)));
-        }
-      }
-      __syncthreads();
-      // counters from the top, 4 to a thread: thread t has 4095 - 4 t .. 4092 - 4 t
-      uint32_t c[4], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i] = hist[kEvictBins - 1 - 4 * tid - i];
-        sum += c[i];
-      }
-      uint32_t before = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, before, d);
-        if (lane >= d) before += x;
-      }
-      if (lane == 31) s_warp[warp] = before;
-      __syncthreads();
-      uint32_t below = lane < warp ? s_warp[lane] : 0;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) below += __shfl_xor_sync(0xFFFFFFFFu, below, d);
-      before += below - sum;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (before < left && before + c[i] >= left) {   // one thread, one counter
-          s_prefix = prefix | (static_cast<uint32_t>(kEvictBins - 1 - 4 * tid - i) << shift);
-          s_left = left - before;
-        }
-        before += c[i];
-      }
-      __syncthreads();
-      prefix = s_prefix;
-      left = s_left;
-      __syncthreads();
+    for (int i = 0; i < kEvictPer; ++i) {
+      const int j = base + 32 * i;
+      const uint32_t key = weight_key(__uint_as_float(k[i]));
+      k[i] = i >= per || j >= len ? kNone : j >= len - recent ? kRecent : key;
     }
-  }
-  // Each warp takes a run of rows: how many of its keys pass, and how many equal the threshold, of
-  // which the first `left` in row order stay; then the row numbers.
-  const int run = (len + 1023) / 1024 * 32;
-  const int a = min(len, warp * run), e = min(len, a + run);
-  int gt = 0, eq = 0;
-  for (int j = a + lane; j < e; j += 32) {
-    const uint32_t k = weight_key(w[j]);
-    gt += j >= n || (any && k > prefix);
-    eq += any && j < n && k == prefix;
-  }
+  };
+  load(0);
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 20 : pass == 1 ? 10 : 0;
+    const int fixed = shift + 10;   // pass > 0: bits from here up are prefix's
+    const uint32_t bins = pass == 0 ? kEvictBins : 1024;
+    for (uint32_t i = tid; i < bins; i += kEvictThreads) hist[i] = 0;
+    __syncthreads();
+    int zeros = 0;
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+      if (chunks > 1) load(chunk);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    gt += __shfl_xor_sync(0xFFFFFFFFu, gt, d);
-    eq += __shfl_xor_sync(0xFFFFFFFFu, eq, d);
-  }
-  if (lane == 0) s_gt[warp] = gt, s_eq[warp] = eq;
-  __syncthreads();
-  int gt_before = lane < warp ? s_gt[lane] : 0, eq_before = lane < warp ? s_eq[lane] : 0;
+      for (int i = 0; i < kEvictPer; ++i) {
+        if (i >= per) break;
+        zeros += k[i] == kZero;
+        const bool in = 2u * k[i] + 2u > 2u;   // neither kNone nor kZero nor kRecent
+        if (in && (pass == 0 || ((k[i] ^ prefix) >> fixed) == 0)) atomicAdd(&hist[(k[i] >> shift) & (bins - 1)], 1u);
+      }
+    }
+    zeros = __reduce_add_sync(0xFFFFFFFFu, zeros);
+    if (lane == 0 && zeros > 0 && (pass == 0 || ((kZero ^ prefix) >> fixed) == 0))
+      atomicAdd(&hist[(kZero >> shift) & (bins - 1)], static_cast<uint32_t>(zeros));
+    if (tid == 0 && recent > 0 && (pass == 0 || ((kRecent ^ prefix) >> fixed) == 0))
+      atomicAdd(&hist[(kRecent >> shift) & (bins - 1)], static_cast<uint32_t>(recent));
+    __syncthreads();
+    // counters from the top, `mine` to a thread: thread t has bins - 1 - mine t, and down
+    const int mine = bins / kEvictThreads;
+    uint32_t c[4], sum = 0;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    gt_before += __shfl_xor_sync(0xFFFFFFFFu, gt_before, d);
-    eq_before += __shfl_xor_sync(0xFFFFFFFFu, eq_before, d);
+    for (int i = 0; i < 4; ++i) {
+      c[i] = i < mine ? hist[bins - 1 - mine * tid - i] : 0u;
+      sum += c[i];
+    }
+    uint32_t before = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, before, d);
+      if (lane >= d) before += x;
+    }
+    if (lane == 31) s_warp[warp] = before;
+    __syncthreads();
+    before += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s_warp[lane] : 0u) - sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (before < left && before + c[i] >= left) {   // one thread, one counter
+        s_prefix = prefix | ((bins - 1 - mine * tid - i) << shift);
+        s_left = left - before;
+      }
+      before += c[i];
+    }
+    __syncthreads();
+    prefix = s_prefix;
+    left = s_left;
   }
-  int eq_left = any ? static_cast<int>(left) - eq_before : 0;   // equal keys that still stay
-  int pos = gt_before + min(eq_before, any ? static_cast<int>(left) : 0);
-  const uint32_t lower = (1u << lane) - 1u;
-  for (int j0 = a; j0 < e; j0 += 32) {
-    const int j = j0 + lane;
-    const uint32_t k = j < e ? weight_key(w[j]) : 0u;
-    const bool same = j < e && any && j < n && k == prefix;
-    const uint32_t m_same = __ballot_sync(0xFFFFFFFFu, same);
-    const bool keep = (j < e && (j >= n || (any && k > prefix))) || (same && __popc(m_same & lower) < eq_left);
-    const uint32_t m_keep = __ballot_sync(0xFFFFFFFFu, keep);
-    if (keep) idx[pos + __popc(m_keep & lower)] = j;
-    pos += __popc(m_keep);
-    eq_left -= __popc(m_same);
+  // Of the keys equal to the threshold the first `left` in row order stay. Per chunk: each warp's
+  // counts, then the row numbers.
+  int pos0 = 0, eq_left0 = static_cast<int>(left);   // before the chunk
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    if (chunks > 1) load(chunk);
+    const int base = chunk * kEvictChunk + first;
+    int gt = 0, eq = 0;
+#pragma unroll
+    for (int i = 0; i < kEvictPer; ++i) {
+      if (i >= per) break;
+      gt += k[i] > prefix;
+      eq += k[i] == prefix;
+    }
+    gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+    eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+    __syncthreads();   // the counts of the chunk before are read
+    if (lane == 0) s_keep[warp] = gt, s_eq[warp] = eq;
+    __syncthreads();
+    const int gt_warp = s_keep[lane], eq_warp = s_eq[lane];
+    const int gt_before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? gt_warp : 0);
+    const int eq_before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? eq_warp : 0);
+    const int gt_all = __reduce_add_sync(0xFFFFFFFFu, gt_warp), eq_all = __reduce_add_sync(0xFFFFFFFFu, eq_warp);
+    int pos = pos0 + gt_before + min(eq_before, eq_left0);
+    int eq_left = max(0, eq_left0 - eq_before);
+    const uint32_t lower = (1u << lane) - 1u;
+#pragma unroll
+    for (int i = 0; i < kEvictPer; ++i) {
+      if (i >= per) break;
+      bool keep = k[i] > prefix;
+      const uint32_t same = __ballot_sync(0xFFFFFFFFu, k[i] == prefix);
+      if (same != 0) {
+        keep |= k[i] == prefix && __popc(same & lower) < eq_left;
+        eq_left = max(0, eq_left - __popc(same));
+      }
+      const uint32_t kept = __ballot_sync(0xFFFFFFFFu, keep);
+      if (keep) idx[pos + __popc(kept & lower)] = base + 32 * i;
+      pos += __popc(kept);
+    }
+    pos0 += gt_all + min(eq_all, eq_left0);
+    eq_left0 = max(0, eq_left0 - eq_all);
   }
 }
 
@@ -152,18 +173,25 @@ struct EvictPlanes {
   const unsigned char* src[kEvictPlanes + 1];
   unsigned char* dst[kEvictPlanes + 1];
   int row_bytes[kEvictPlanes + 1];
-  int width[kEvictPlanes + 1];          // bytes of a row that a CTA moves
-  int first_column[kEvictPlanes + 2];
+  int width[kEvictPlanes + 1];          // bytes of a row that a CTA moves: a column
+  int parts[kEvictPlanes + 1];          // CTAs of a column: each the rows of a round (in place one has all)
+  int first[kEvictPlanes + 2];          // blockIdx.y of a plane's first CTA
   int n;                                // planes; entry n - 1 are the weights
 };
 
-// Move rows idx[r0 .. r1): N rows to a thread and round, `lanes` threads with a T each to a row.
+// The word that a thread moves, and the rows that a CTA moves in a round.
+__host__ __device__ constexpr int move_word(int row_bytes) { return row_bytes % 16 == 0 ? 16 : row_bytes % 8 == 0 ? 8 : 4; }
+__host__ __device__ constexpr int move_rows_per_round(int row_bytes, int width) {
+  return kMoveThreads / ((width < row_bytes ? width : row_bytes) / move_word(row_bytes)) * 4;
+}
+
+// Move rows idx[r0 .. r1): 4 rows to a thread and round, `lanes` threads with a T each to a row.
 // A round's rows are all read before any is written, and a row's old place is never before its new
 // one, so in place a later round's rows are still there.
 template <typename T>
 __device__ __forceinline__ void move_rows(const unsigned char* src, unsigned char* dst, const int* idx, int row_bytes,
                                           int lanes, int r0, int r1, bool in_place) {
-  constexpr int N = 8;
+  constexpr int N = 4;
   const int per = kMoveThreads / lanes;   // rows of a block-wide step
   const int mine = threadIdx.x / lanes, at = threadIdx.x % lanes * static_cast<int>(sizeof(T));
   for (int base = r0; base < r1; base += per * N) {
@@ -187,30 +215,35 @@ __device__ __forceinline__ void move_rows(const unsigned char* src, unsigned cha
   }
 }
 
-// blockIdx.x: (sequence, kv head); blockIdx.y: a column of a plane's rows (a 32-byte sector in
-// place, where only columns can move side by side; up to 128 bytes otherwise); blockIdx.z: a
-// range of rows (all of them in place). The weights' CTAs also clear what is past the last row.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictPlanes pl, const int* __restrict__ index,
-                                                                  int* new_lengths, int Hkv, long long cap,
-                                                                  long long out_cap, int budget, int rows_per_cta) {
+// blockIdx.x: (sequence, kv head); blockIdx.y: a part of a column of a plane's rows (a column is a
+// 32-byte sector in place, where only columns can move side by side; up to 128 bytes otherwise).
+// The weights' first CTA also clears what is past the last row.
+__global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(EvictPlanes pl, const int* __restrict__ index,
+                                                                     int* new_lengths, int Hkv, long long cap,
+                                                                     long long out_cap, int budget) {
   const long long bh = blockIdx.x;
   int p = 0;
-  while (static_cast<int>(blockIdx.y) >= pl.first_column[p + 1]) ++p;
-  const int col = (blockIdx.y - pl.first_column[p]) * pl.width[p];
-  const int width = min(pl.width[p], pl.row_bytes[p] - col);
+  while (static_cast<int>(blockIdx.y) >= pl.first[p + 1]) ++p;
+  const int row_bytes = pl.row_bytes[p];
+  const int column = (blockIdx.y - pl.first[p]) / pl.parts[p], part = blockIdx.y - pl.first[p] - column * pl.parts[p];
+  const int col = column * pl.width[p];
+  const int width = min(pl.width[p], row_bytes - col);
   const bool in_place = pl.src[p] == pl.dst[p];
-  const unsigned char* src = pl.src[p] + bh * cap * pl.row_bytes[p] + col;
-  unsigned char* dst = pl.dst[p] + bh * out_cap * pl.row_bytes[p] + col;
-  const int r0 = blockIdx.z * rows_per_cta, r1 = min(budget, r0 + rows_per_cta);
-  griddep_wait();
+  const unsigned char* src = pl.src[p] + bh * cap * row_bytes + col;
+  unsigned char* dst = pl.dst[p] + bh * out_cap * row_bytes + col;
+  const int word = move_word(row_bytes);
+  const int lanes = width / word;
   const int* idx = index + bh * budget;
-  if (pl.row_bytes[p] % 16 == 0)
-    move_rows<uint4>(src, dst, idx, pl.row_bytes[p], width / 16, r0, r1, in_place);
-  else if (pl.row_bytes[p] % 8 == 0)
-    move_rows<uint2>(src, dst, idx, pl.row_bytes[p], width / 8, r0, r1, in_place);
+  const int rows = pl.parts[p] == 1 ? budget : move_rows_per_round(row_bytes, pl.width[p]);
+  const int a = part * rows, b = min(budget, a + rows);   // budget <= INT_MAX - 65536
+  griddep_wait();
+  if (word == 16)
+    move_rows<uint4>(src, dst, idx, row_bytes, lanes, a, b, in_place);
+  else if (word == 8)
+    move_rows<uint2>(src, dst, idx, row_bytes, lanes, a, b, in_place);
   else
-    move_rows<uint32_t>(src, dst, idx, pl.row_bytes[p], width / 4, r0, r1, in_place);
-  if (p != pl.n - 1 || blockIdx.z != 0) return;
+    move_rows<uint32_t>(src, dst, idx, row_bytes, lanes, a, b, in_place);
+  if (p != pl.n - 1 || part != 0) return;
   // how many rows there are (all heads of a sequence keep as many), by the first -1
   int lo = 0, hi = budget;
   while (lo < hi) {

@@ -73,7 +73,8 @@ __device__ __forceinline__ uint32_t kv4_codes(const uint32_t (&xin)[4], __half& 
   // a group that is not finite, or so small that its scale has fewer than 8 bits and |x / s| may
   // pass 7 by more than rounding: the same in its 4 lanes
   const bool odd = !(a <= 65504.0f) || a < 7.0f * 0x1p-14f;
-  if (__any_sync(0xFFFFFFFFu, odd)) {
+  const bool odds = __any_sync(0xFFFFFFFFu, odd);
+  if (odds) {
     float b = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -88,7 +89,7 @@ __device__ __forceinline__ uint32_t kv4_codes(const uint32_t (&xin)[4], __half& 
   }
   const float sixteen_bits = __uint_as_float((__float_as_uint(a * (1.0f / 7.0f)) + 0x80u) & 0xFFFFFF00u);
   scale = __float2half_rn(round_8bits(sixteen_bits));
-  if (__any_sync(0xFFFFFFFFu, odd)) {
+  if (odds) {
     const __half2 top = __hmul2(__half2half2(scale), __float2half2_rn(7.0f));
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = h2_bits(__hmax2(__hmin2(bits_h2(x[i]), top), __hneg2(top)));
@@ -100,8 +101,12 @@ __device__ __forceinline__ uint32_t kv4_codes(const uint32_t (&xin)[4], __half& 
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(bits_h2(x[i]));
     // 12582912 = 1.5 * 2^23: the integer code + 8 lands in the low bits of the float
-    y[2 * i] = __float_as_uint(fmaf(f.x, r, 768.0f) + (12582912.0f + 8.0f - 768.0f));
-    y[2 * i + 1] = __float_as_uint(fmaf(f.y, r, 768.0f) + (12582912.0f + 8.0f - 768.0f));
+    constexpr float kToInt = 12582912.0f + 8.0f - 768.0f;
+    float lo, hi;
+    ffma2(lo, hi, f.x, f.y, r, r, 768.0f, 768.0f);
+    fadd2(lo, hi, lo, hi, kToInt, kToInt);
+    y[2 * i] = __float_as_uint(lo);
+    y[2 * i + 1] = __float_as_uint(hi);
   }
   uint32_t b[4];
 #pragma unroll
@@ -133,13 +138,17 @@ __global__ void __launch_bounds__(kKv4StoreThreads) kv4_append_kernel(
 #pragma unroll
     for (int j = 0; j < kKv4StoreRows; ++j) {
       const int i = i0 + j * kv4_block_rows<D>();
-      row[j] = i < win.n ? win.row(b, i) : -1;
       xk[j] = xv[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (row[j] >= 0) {
+      if (i < win.n) {   // rows past counts too: waiting for the count first takes longer
         const long long from = (static_cast<long long>(plane) * win.n + i) * D + u * 8;
         xk[j] = __ldcs(reinterpret_cast<const uint4*>(k + from));
         xv[j] = __ldcs(reinterpret_cast<const uint4*>(v + from));
       }
+    }
+#pragma unroll
+    for (int j = 0; j < kKv4StoreRows; ++j) {
+      const int i = i0 + j * kv4_block_rows<D>();
+      row[j] = i < win.n ? win.row(b, i) : -1;
     }
     uint4 sh = make_uint4(0u, 0u, 0u, 0u);   // x - 0 = x
     if (shift) sh = *reinterpret_cast<const uint4*>(shift + static_cast<long long>(plane) * D + u * 8);

@@ -1676,15 +1676,20 @@ int pasa_cache_evict(const void* const* planes, void* const* out_planes, const i
   if (in_place && (apart || out_cap != Sk_cap)) return PASA_ERR_SHAPE;
   pasa::EvictPlanes pl = {};
   pl.n = n_planes + 1;
+  long long blocks = 0;
   for (int i = 0; i <= n_planes; ++i) {
     const bool w = i == n_planes;
     pl.src[i] = static_cast<const unsigned char*>(w ? static_cast<const void*>(weights) : planes[i]);
     pl.dst[i] = static_cast<unsigned char*>(w ? static_cast<void*>(out_weights) : out_planes[i]);
     pl.row_bytes[i] = w ? 4 : row_bytes[i];
     pl.width[i] = in_place ? 32 : 128;
-    pl.first_column[i + 1] = pl.first_column[i] + (pl.row_bytes[i] + pl.width[i] - 1) / pl.width[i];
+    const int rows = pasa::move_rows_per_round(pl.row_bytes[i], pl.width[i]);
+    pl.parts[i] = in_place ? 1 : static_cast<int>((static_cast<long long>(budget) + rows - 1) / rows);
+    blocks += static_cast<long long>(pl.parts[i]) * ((pl.row_bytes[i] + pl.width[i] - 1) / pl.width[i]);
+    if (blocks > 65535) return PASA_ERR_SHAPE;   // grid.y
+    pl.first[i + 1] = static_cast<int>(blocks);
   }
-  if (pl.first_column[pl.n] > 65535) return PASA_ERR_SHAPE;
+  if (Sk > INT_MAX - 65536 || budget > INT_MAX - 65536) return PASA_ERR_SHAPE;   // row numbers of a round
   int rc = check_device();
   if (rc != PASA_OK) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1693,11 +1698,10 @@ int pasa_cache_evict(const void* const* planes, void* const* out_planes, const i
                                                                        recent);
   rc = launch_status();
   if (rc != PASA_OK) return rc;
-  const int rows_per_cta = in_place ? budget : std::max(256, (budget + 65534) / 65535);
-  const dim3 grid(planes_bh, pl.first_column[pl.n], (budget + rows_per_cta - 1) / rows_per_cta);
+  const dim3 grid(planes_bh, pl.first[pl.n]);
   const cudaError_t e = launch_kernel(pasa::evict_move_kernel, grid, dim3(pasa::kMoveThreads), 0, st, true, pl, index,
                                       new_lengths, Hkv, static_cast<long long>(Sk_cap), static_cast<long long>(out_cap),
-                                      budget, rows_per_cta);
+                                      budget);
   return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
 
