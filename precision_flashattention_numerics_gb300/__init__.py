@@ -10,6 +10,7 @@ Inference" (arXiv 2503.01873), Abstract.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -667,9 +668,15 @@ def cache_evict(planes, weights, budget: int, recent: int = 0, length: int | Non
     for i, (a, b) in enumerate(zip(planes, out)):
         if not isinstance(a, torch.Tensor) or a.dim() != 4:
             raise ValueError("expected planes [B,Hkv,cap,*]")
-        src.append(_check_cuda(a, f"planes[{i}]", a.dtype, (B, Hkv, cap, a.shape[3]), dev))
-        dst.append(_check_cuda(b, f"out[{i}]", a.dtype, (B, Hkv, out_cap, a.shape[3]), dev))
-        nbytes.append(a.shape[3] * a.element_size())
+        dtype, n = a.dtype, a.shape[3]
+        src.append(_check_cuda(a, f"planes[{i}]", dtype, (B, Hkv, cap, n), dev))
+        dst.append(src[-1] if a is b else _check_cuda(b, f"out[{i}]", dtype, (B, Hkv, out_cap, n), dev))
+        nbytes.append(n * dtype.itemsize)
+    # the C arrays planes and out_planes, one behind the other, and row_bytes
+    count = len(planes)
+    table = array.array("q", src + dst)
+    rows = array.array("i", nbytes)
+    at = table.buffer_info()[0]
     np_ = None if lengths is None else _check_cuda(lengths, "lengths", torch.int32, (B,), dev)
     if index is None:
         index = torch.empty((B, Hkv, max(budget, 0)), device=weights.device, dtype=torch.int32)
@@ -677,9 +684,7 @@ def cache_evict(planes, weights, budget: int, recent: int = 0, length: int | Non
         new_lengths = torch.empty((B,), device=weights.device, dtype=torch.int32)
     ip = _check_cuda(index, "index", torch.int32, (B, Hkv, max(budget, 0)), dev)
     nlp = _check_cuda(new_lengths, "new_lengths", torch.int32, (B,), dev)
-    count = len(planes)
-    rc = library().pasa_cache_evict((_P * count)(*src), (_P * count)(*dst), (_I * count)(*nbytes), count, wp, owp, np_,
-                                    ip, nlp, B, Hkv, Sk, cap, out_cap, budget, recent, stream)
+    rc = library().pasa_cache_evict(at, at + 8 * count, rows.buffer_info()[0], count, wp, owp, np_, ip, nlp, B, Hkv, Sk, cap, out_cap, budget, recent, stream)
     if rc != 0:
         raise PasaError(rc, "pasa_cache_evict")
     return index, new_lengths

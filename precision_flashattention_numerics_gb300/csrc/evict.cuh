@@ -12,9 +12,11 @@
 
 namespace pasa {
 
-constexpr int kEvictThreads = 1024;
+constexpr int kEvictThreads = 512;
+constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictPlanes = 8;     // planes of one cache
 constexpr int kMoveThreads = 256;
+constexpr int kEvictCluster = 8;    // CTAs of a (sequence, kv head), at most
 
 // Weights as unsigned numbers in the same order: NaN counts as -inf, -0 as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -23,42 +25,47 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-constexpr int kEvictBins = 4096;
-constexpr int kEvictPer = 32;                               // weights of a thread
+constexpr int kEvictBins = 2048;
+constexpr int kEvictPer = 16;                               // weights of a thread
 constexpr int kEvictChunk = kEvictThreads * kEvictPer;      // rows that a CTA holds in registers
 
-// One CTA per (sequence, kv head): the rows it keeps, ascending, -1 past the last: the budget
-// largest keys, a recent row's key being above every weight's (kRecent) and that of a row past
-// the last below (kNone). The threshold is found in three passes over the keys, by bits 31 .. 20,
-// 19 .. 10 and 9 .. 0: with 12 bits, weights of similar size spread over several counters even in
-// the first pass. Zeros, the weight of every row not yet looked at, and recent rows are
-// counted apart, not one by one in the same counter. Up to 32768 rows are read once and stay in
-// registers; longer ones are read again (from L2) in every pass, a chunk at a time. A warp holds
-// a run of the chunk's rows, up to 32 a lane.
+// A cluster of CTAs per (sequence, kv head), each with an equal run of its rows: the rows the head
+// keeps, ascending, -1 past the last: those with the budget largest keys, a recent row's key
+// being above every weight's (kRecent) and that of a row past the last below (kNone). The
+// threshold is found in three passes over the keys, by bits 31 .. 21, 20 .. 10 and 9 .. 0: with 11
+// bits, weights of similar size spread over several counters even in the first pass. Zeros, the
+// weight of every row not yet looked at, and recent rows are counted apart, not one by one in
+// the same counter. Every CTA adds up the counters of all (distributed shared memory) and finds
+// the same threshold. A CTA's first 8192 rows are read once and stay in registers; more are
+// read again (from L2) in every pass, a chunk at a time.
 __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const float* __restrict__ weights,
                                                                      const int* __restrict__ lengths,
                                                                      int* __restrict__ index, int Hkv, int Sk,
-                                                                     long long cap, int budget, int recent) {
-  __shared__ uint32_t hist[kEvictBins];
-  __shared__ uint32_t s_warp[32], s_prefix, s_left;
-  __shared__ int s_keep[32], s_eq[32];
+                                                                     long long cap, int budget, int recent, int cluster) {
+  __shared__ __align__(16) uint32_t hist[3][kEvictBins];
+  __shared__ uint32_t s_warp[kEvictWarps], s_prefix, s_left;
+  __shared__ int s_keep[kEvictWarps], s_eq[kEvictWarps];
+  __shared__ float2 s_part;   // this CTA's keys above and equal to the threshold, as integers' bits
   griddep_launch_dependents();
-  const long long bh = blockIdx.x;
+  const long long bh = blockIdx.x / cluster;
+  const int rank = blockIdx.x % cluster;
   const int len = lengths ? max(0, min(lengths[bh / Hkv], Sk)) : Sk;
   const float* w = weights + bh * cap;
   int* idx = index + bh * budget;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (len <= budget) {
-    for (int j = tid; j < budget; j += kEvictThreads) idx[j] = j < len ? j : -1;
+  if (len <= budget) {   // all CTAs of the cluster
+    for (int j = rank * kEvictThreads + tid; j < budget; j += cluster * kEvictThreads) idx[j] = j < len ? j : -1;
     return;
   }
   constexpr uint32_t kZero = 0x80000000u, kNone = 0u, kRecent = 0xFFFFFFFFu;
   uint32_t left = budget;               // of the keys that match `prefix` so far, how many stay
   uint32_t prefix = 0;                  // the budget-th largest key
-  const int chunks = (len + kEvictChunk - 1) / kEvictChunk;
-  const int per = chunks > 1 ? kEvictPer : (len + kEvictThreads - 1) / kEvictThreads;   // elements of a lane
+  const int part = (len + cluster - 1) / cluster;              // rows of a CTA
+  const int row0 = min(len, rank * part), row1 = min(len, row0 + part);
+  const int chunks = (part + kEvictChunk - 1) / kEvictChunk;
+  const int per = chunks > 1 ? kEvictPer : (part + kEvictThreads - 1) / kEvictThreads;   // elements of a lane
   uint32_t k[kEvictPer];                // element i: row `first` + 32 i of the chunk at hand
-  const int first = warp * (32 * per) + lane;
+  const int first = row0 + warp * (32 * per) + lane;
   auto load = [&](int chunk) {
     const int base = chunk * kEvictChunk + first;
     // all loads first, without branches between them
@@ -69,42 +76,48 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const float
     for (int i = 0; i < kEvictPer; ++i) {
       const int j = base + 32 * i;
       const uint32_t key = weight_key(__uint_as_float(k[i]));
-      k[i] = i >= per || j >= len ? kNone : j >= len - recent ? kRecent : key;
+      k[i] = i >= per || j >= row1 ? kNone : j >= len - recent ? kRecent : key;
     }
   };
   load(0);
+  for (int i = tid; i < 3 * kEvictBins / 4; i += kEvictThreads) reinterpret_cast<uint4*>(hist[0])[i] = make_uint4(0u, 0u, 0u, 0u);
+  __syncthreads();
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 20 : pass == 1 ? 10 : 0;
-    const int fixed = shift + 10;   // pass > 0: bits from here up are prefix's
-    const uint32_t bins = pass == 0 ? kEvictBins : 1024;
-    for (uint32_t i = tid; i < bins; i += kEvictThreads) hist[i] = 0;
-    __syncthreads();
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int fixed = pass == 1 ? 21 : 10;   // pass > 0: bits from here up are prefix's
+    const uint32_t bins = pass == 2 ? 1024 : kEvictBins;
     int zeros = 0;
     for (int chunk = 0; chunk < chunks; ++chunk) {
       if (chunks > 1) load(chunk);
 #pragma unroll
       for (int i = 0; i < kEvictPer; ++i) {
-        if (i >= per) break;
         zeros += k[i] == kZero;
         const bool in = 2u * k[i] + 2u > 2u;   // neither kNone nor kZero nor kRecent
-        if (in && (pass == 0 || ((k[i] ^ prefix) >> fixed) == 0)) atomicAdd(&hist[(k[i] >> shift) & (bins - 1)], 1u);
+        if (in && (pass == 0 || ((k[i] ^ prefix) >> fixed) == 0)) atomicAdd(&hist[pass][(k[i] >> shift) & (bins - 1)], 1u);
       }
     }
     zeros = __reduce_add_sync(0xFFFFFFFFu, zeros);
     if (lane == 0 && zeros > 0 && (pass == 0 || ((kZero ^ prefix) >> fixed) == 0))
-      atomicAdd(&hist[(kZero >> shift) & (bins - 1)], static_cast<uint32_t>(zeros));
-    if (tid == 0 && recent > 0 && (pass == 0 || ((kRecent ^ prefix) >> fixed) == 0))
-      atomicAdd(&hist[(kRecent >> shift) & (bins - 1)], static_cast<uint32_t>(recent));
-    __syncthreads();
-    // counters from the top, `mine` to a thread: thread t has bins - 1 - mine t, and down
-    const int mine = bins / kEvictThreads;
-    uint32_t c[4], sum = 0;
+      atomicAdd(&hist[pass][(kZero >> shift) & (bins - 1)], static_cast<uint32_t>(zeros));
+    if (tid == 0 && rank == 0 && recent > 0 && (pass == 0 || ((kRecent ^ prefix) >> fixed) == 0))
+      atomicAdd(&hist[pass][(kRecent >> shift) & (bins - 1)], static_cast<uint32_t>(recent));
+    if (cluster > 1) cluster_sync_all(); else __syncthreads();
+    // counters from the top, 4 to a thread: thread t has 2047 - 4 t .. 2044 - 4 t
+    uint32_t c[4] = {0u, 0u, 0u, 0u};
+    const uint32_t at = smem_u32(&hist[pass][kEvictBins - 4 - 4 * tid]);
+    float4 x[kEvictCluster];   // all loads first
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = i < mine ? hist[bins - 1 - mine * tid - i] : 0u;
-      sum += c[i];
+    for (int r = 0; r < kEvictCluster; ++r) {
+      x[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (r < cluster) x[r] = ld_cluster_float4(cluster > 1 ? mapa_shared(at, r) : at);
     }
+#pragma unroll
+    for (int r = 0; r < kEvictCluster; ++r) {
+      c[0] += __float_as_uint(x[r].w), c[1] += __float_as_uint(x[r].z);
+      c[2] += __float_as_uint(x[r].y), c[3] += __float_as_uint(x[r].x);
+    }
+    const uint32_t sum = c[0] + c[1] + c[2] + c[3];
     uint32_t before = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -117,7 +130,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const float
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (before < left && before + c[i] >= left) {   // one thread, one counter
-        s_prefix = prefix | ((bins - 1 - mine * tid - i) << shift);
+        s_prefix = prefix | ((kEvictBins - 1 - 4 * tid - i) << shift);
         s_left = left - before;
       }
       before += c[i];
@@ -126,25 +139,53 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const float
     prefix = s_prefix;
     left = s_left;
   }
-  // Of the keys equal to the threshold the first `left` in row order stay. Per chunk: each warp's
-  // counts, then the row numbers.
-  int pos0 = 0, eq_left0 = static_cast<int>(left);   // before the chunk
+  // Of the keys equal to the threshold the first `left` in row order stay. The CTA's counts and those
+  // of the CTAs before it, then per chunk each warp's counts and the row numbers.
+  int gt = 0, eq = 0;
   for (int chunk = 0; chunk < chunks; ++chunk) {
     if (chunks > 1) load(chunk);
-    const int base = chunk * kEvictChunk + first;
-    int gt = 0, eq = 0;
 #pragma unroll
     for (int i = 0; i < kEvictPer; ++i) {
-      if (i >= per) break;
       gt += k[i] > prefix;
       eq += k[i] == prefix;
     }
-    gt = __reduce_add_sync(0xFFFFFFFFu, gt);
-    eq = __reduce_add_sync(0xFFFFFFFFu, eq);
-    __syncthreads();   // the counts of the chunk before are read
-    if (lane == 0) s_keep[warp] = gt, s_eq[warp] = eq;
-    __syncthreads();
-    const int gt_warp = s_keep[lane], eq_warp = s_eq[lane];
+  }
+  gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+  eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+  if (lane == 0) s_keep[warp] = gt, s_eq[warp] = eq;
+  __syncthreads();
+  if (cluster > 1 && warp == 0) {
+    gt = __reduce_add_sync(0xFFFFFFFFu, lane < kEvictWarps ? s_keep[lane] : 0);
+    eq = __reduce_add_sync(0xFFFFFFFFu, lane < kEvictWarps ? s_eq[lane] : 0);
+    if (lane == 0) s_part = make_float2(__int_as_float(gt), __int_as_float(eq));
+  }
+  int pos0 = 0, eq_left0 = static_cast<int>(left);   // before the chunk
+  if (cluster > 1) {
+    cluster_sync_all();
+    // lane r has CTA r's
+    float2 x = make_float2(0.0f, 0.0f);
+    if (lane < rank) x = ld_cluster_float2(mapa_shared(smem_u32(&s_part), lane));
+    const int eq_ranks = __reduce_add_sync(0xFFFFFFFFu, __float_as_int(x.y));
+    pos0 = __reduce_add_sync(0xFFFFFFFFu, __float_as_int(x.x)) + min(eq_ranks, eq_left0);
+    eq_left0 = max(0, eq_left0 - eq_ranks);
+  }
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    const int base = chunk * kEvictChunk + first;
+    if (chunks > 1) {
+      load(chunk);
+      gt = 0, eq = 0;
+#pragma unroll
+      for (int i = 0; i < kEvictPer; ++i) {
+        gt += k[i] > prefix;
+        eq += k[i] == prefix;
+      }
+      gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+      eq = __reduce_add_sync(0xFFFFFFFFu, eq);
+      __syncthreads();   // the counts before are read
+      if (lane == 0) s_keep[warp] = gt, s_eq[warp] = eq;
+      __syncthreads();
+    }
+    const int gt_warp = lane < kEvictWarps ? s_keep[lane] : 0, eq_warp = lane < kEvictWarps ? s_eq[lane] : 0;
     const int gt_before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? gt_warp : 0);
     const int eq_before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? eq_warp : 0);
     const int gt_all = __reduce_add_sync(0xFFFFFFFFu, gt_warp), eq_all = __reduce_add_sync(0xFFFFFFFFu, eq_warp);
@@ -153,7 +194,6 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const float
     const uint32_t lower = (1u << lane) - 1u;
 #pragma unroll
     for (int i = 0; i < kEvictPer; ++i) {
-      if (i >= per) break;
       bool keep = k[i] > prefix;
       const uint32_t same = __ballot_sync(0xFFFFFFFFu, k[i] == prefix);
       if (same != 0) {
@@ -167,6 +207,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const float
     pos0 += gt_all + min(eq_all, eq_left0);
     eq_left0 = max(0, eq_left0 - eq_all);
   }
+  if (cluster > 1) cluster_sync_all();   // no CTA ends while another reads its counters
 }
 
 struct EvictPlanes {

@@ -448,18 +448,6 @@ __device__ __forceinline__ float kv4_offset(const Kv4Params& p, long long bh, in
   return s * p.scale;
 }
 
-__device__ __forceinline__ float2 ld_cluster_float2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 ld_cluster_float4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-
 // Write channels ch .. ch + 3 of a row, and with channel 0 its log-sum-exps.
 template <int D>
 __device__ __forceinline__ void kv4_finish(const Kv4Params& p, long long out, long long lse2_at, int ch, float4 x, float mm,

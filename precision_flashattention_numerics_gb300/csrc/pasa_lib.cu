@@ -1658,7 +1658,7 @@ int pasa_cache_evict(const void* const* planes, void* const* out_planes, const i
                      int Hkv, int Sk, int Sk_cap, int out_cap, int budget, int recent, void* stream) {
   if (!planes || !out_planes || !row_bytes || !weights || !out_weights || !index) return PASA_ERR_NULLPTR;
   if (B <= 0 || Hkv <= 0 || Sk <= 0 || Sk_cap < Sk) return PASA_ERR_SHAPE;
-  if (static_cast<long long>(B) * Hkv > INT_MAX) return PASA_ERR_SHAPE;
+  if (static_cast<long long>(B) * Hkv * pasa::kEvictCluster > INT_MAX) return PASA_ERR_SHAPE;
   if (budget <= 0 || recent < 0 || recent > budget || out_cap < budget) return PASA_ERR_SHAPE;
   if (n_planes < 1 || n_planes > pasa::kEvictPlanes) return PASA_ERR_UNSUPPORTED;
   if (!aligned16(weights) || !aligned16(out_weights) || !aligned16(index) || !aligned4(lengths) || !aligned4(new_lengths))
@@ -1694,12 +1694,16 @@ int pasa_cache_evict(const void* const* planes, void* const* out_planes, const i
   if (rc != PASA_OK) return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned planes_bh = static_cast<unsigned>(B) * static_cast<unsigned>(Hkv);
-  pasa::evict_select_kernel<<<planes_bh, pasa::kEvictThreads, 0, st>>>(weights, lengths, index, Hkv, Sk, Sk_cap, budget,
-                                                                       recent);
-  rc = launch_status();
-  if (rc != PASA_OK) return rc;
+  // CTAs of a head: more while each has over 4096 rows and all fit the SMs one to each
+  int cluster = 1;
+  while (cluster < pasa::kEvictCluster && Sk > cluster * 4096 && planes_bh * cluster * 2 <= 152) cluster *= 2;
+  static std::atomic<unsigned long long> raised{0};
+  cudaError_t e = launch_clusters(pasa::evict_select_kernel, planes_bh * cluster, pasa::kEvictThreads, 0, 0, st, false,
+                                  cluster, raised, weights, lengths, index, Hkv, Sk, static_cast<long long>(Sk_cap), budget,
+                                  recent, cluster);
+  if (e != cudaSuccess) return cuda_fail(e);
   const dim3 grid(planes_bh, pl.first[pl.n]);
-  const cudaError_t e = launch_kernel(pasa::evict_move_kernel, grid, dim3(pasa::kMoveThreads), 0, st, true, pl, index,
+  e = launch_kernel(pasa::evict_move_kernel, grid, dim3(pasa::kMoveThreads), 0, st, true, pl, index,
                                       new_lengths, Hkv, static_cast<long long>(Sk_cap), static_cast<long long>(out_cap),
                                       budget);
   return e == cudaSuccess ? launch_status() : cuda_fail(e);
