@@ -505,6 +505,19 @@ int pasa_attn_fwd_decode_kv4(const void* q, const void* k4, const void* kscale, 
                              size_t workspace_bytes, void* stream);
 
 /*
+ * One decode step on a 4-bit cache: pasa_kv4_append of n rows of k and v (fp16 [B, Hkv, n, D])
+ * per sequence at starts[b] (or start), then pasa_attn_fwd_decode_kv4 with lengths starts[b] + n
+ * (or start + n, whatever Sk is), in one call. Results are bit-identical to the two calls; the
+ * decode kernel starts while the rows are stored and waits for them (griddepcontrol.wait) only
+ * before it reads the cache. All arguments are checked before anything is enqueued. Workspace as
+ * for the decode call (with start on the host: for Sk = start + n).
+ */
+int pasa_attn_fwd_decode_step_kv4(const void* q, const void* k, const void* v, void* k4, void* kscale, void* v4,
+                                  void* vscale, const void* shift, const int* starts, int start, void* o, float* lse,
+                                  float* weights, int B, int Hq, int Hkv, int Sq, int n, int Sk, int Sk_cap, int D,
+                                  int causal, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Eviction from a cache by accumulated attention weight. (No counterpart in the paper.) Of
  * each sequence with more than `budget` rows, every kv head keeps budget rows: its last
  * `recent` ones (0 <= recent <= budget) and, of the others, those with the largest

@@ -21,7 +21,7 @@ import torch
 __all__ = [
     "MODE_SHIFT_F16ACC", "MODE_SHIFT_F32ACC", "MODE_NAIVE_F16ACC", "MODE_NOSHIFT_F32ACC", "MODE_SHIFT_F16ALL", "MODE_SHIFT_FP8", "MODE_NAIVE_FP8", "kprep_fp8", "attn_fwd_fp8",
     "PasaError", "attn_fwd", "attn_fwd_alloc", "attn_fwd_fused", "attn_fwd_shifted", "attn_fwd_stats", "kshift", "workspace_bytes", "check_device_error", "block_rows",
-    "kv4_append", "kv4_read", "attn_fwd_decode_kv4", "cache_evict",
+    "kv4_append", "kv4_read", "attn_fwd_decode_kv4", "attn_fwd_decode_step_kv4", "cache_evict",
     "library", "library_path",
 ]
 
@@ -71,6 +71,7 @@ SIGNATURES = {
     "pasa_kv4_read": ([_P] * 7 + [_P, _I, _P] + [_I] * 5 + [_P], _I),
     "pasa_attn_fwd_decode_kv4_workspace_bytes": ([_I] * 7, _SZ),
     "pasa_attn_fwd_decode_kv4": ([_P] * 10 + [_I] * 8 + [_F, _P, _SZ, _P], _I),
+    "pasa_attn_fwd_decode_step_kv4": ([_P] * 9 + [_I] + [_P] * 3 + [_I] * 9 + [_F, _P, _SZ, _P], _I),
     "pasa_cache_evict": ([_P, _P, _P, _I] + [_P] * 5 + [_I] * 7 + [_P], _I),
     "pasa_check_device_error": ([_P, ctypes.POINTER(ctypes.c_ulonglong)], _I),
     "pasa_selftest_wait_timeout": ([_P], _I),
@@ -609,6 +610,16 @@ def decode_kv4_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: i
     return library().pasa_attn_fwd_decode_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, int(bool(weights)))
 
 
+def _decode_kv4_workspace(workspace, device, *sizes):
+    """(workspace, bytes needed): the caller's, or a new one where that is none or too small."""
+    if workspace is not None:
+        _check_cuda(workspace, "workspace", torch.uint8, None, device)
+    nbytes = decode_kv4_workspace_bytes(*sizes)
+    if nbytes and (workspace is None or workspace.numel() < nbytes):
+        workspace = torch.empty(nbytes, device=device, dtype=torch.uint8)
+    return workspace, nbytes
+
+
 def attn_fwd_decode_kv4(q, k4, kscale, v4, vscale, causal: bool = False, scale: float | None = None, shift=None,
                         length: int | None = None, lengths=None, weights=None, out=None, lse=None, workspace=None):
     """Decode attention on a 4-bit cache (see :func:`kv4_append`): q fp16 [B,Hq,Sq,D] with
@@ -629,16 +640,43 @@ def attn_fwd_decode_kv4(q, k4, kscale, v4, vscale, causal: bool = False, scale: 
     lp = _check_cuda(lse, "lse", torch.float32, (B, Hq, Sq), dev)
     np_ = None if lengths is None else _check_cuda(lengths, "lengths", torch.int32, (B,), dev)
     wp = None if weights is None else _check_cuda(weights, "weights", torch.float32, (B, Hkv, cap), dev)
-    nbytes = decode_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, weights is not None)
-    if workspace is not None:
-        _check_cuda(workspace, "workspace", torch.uint8, None, dev)
-    if nbytes and (workspace is None or workspace.numel() < nbytes):
-        workspace = torch.empty(nbytes, device=q.device, dtype=torch.uint8)
+    workspace, nbytes = _decode_kv4_workspace(workspace, dev, B, Hq, Hkv, Sq, Sk, D, weights is not None)
     rc = library().pasa_attn_fwd_decode_kv4(qp, *ptrs, sp, np_, op, lp, wp, B, Hq, Hkv, Sq, Sk, cap, D, int(bool(causal)),
                                       float(scale) if scale is not None else 0.0,
                                       workspace.data_ptr() if nbytes else None, nbytes, stream)
     if rc != 0:
         raise PasaError(rc, "pasa_attn_fwd_decode_kv4")
+    return out, lse
+
+
+def attn_fwd_decode_step_kv4(q, k, v, k4, kscale, v4, vscale, start, causal: bool = False, scale: float | None = None,
+                             shift=None, length: int | None = None, weights=None, out=None, lse=None, workspace=None):
+    """Append the new rows k, v [B,Hkv,n,D] at `start` (an int, or an int32 tensor [B]) and decode
+    on start + n rows, in one call (the decode kernel overlaps the append): :func:`kv4_append`
+    and :func:`attn_fwd_decode_kv4`. length: with a tensor, an upper bound on start + n (default: the
+    cache's rows). Returns (o, lse)."""
+    dev, stream = _here()
+    ptrs, sp, (B, Hkv, cap, D) = _check_kv4(k4, kscale, v4, vscale, shift, dev)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("expected q [B,Hq,Sq,D] and k, v [B,Hkv,n,D]")
+    _, Hq, Sq, _ = q.shape
+    n = k.shape[2]
+    starts, first = _per_sequence(start, "start", B, dev)
+    Sk = first + n if starts is None else cap if length is None else _int32(length, "length")
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, Hq, Sq), device=q.device, dtype=torch.float32) if lse is None else lse
+    qp = _check_cuda(q, "q", torch.float16, (B, Hq, Sq, D), dev)
+    kp = _check_cuda(k, "k", torch.float16, (B, Hkv, n, D), dev)
+    vp = _check_cuda(v, "v", torch.float16, (B, Hkv, n, D), dev)
+    op = _check_cuda(out, "out", torch.float16, (B, Hq, Sq, D), dev)
+    lp = _check_cuda(lse, "lse", torch.float32, (B, Hq, Sq), dev)
+    wp = None if weights is None else _check_cuda(weights, "weights", torch.float32, (B, Hkv, cap), dev)
+    workspace, nbytes = _decode_kv4_workspace(workspace, dev, B, Hq, Hkv, Sq, Sk, D, weights is not None)
+    rc = library().pasa_attn_fwd_decode_step_kv4(qp, kp, vp, *ptrs, sp, starts, first, op, lp, wp, B, Hq, Hkv, Sq, n, Sk,
+                                                 cap, D, int(bool(causal)), float(scale) if scale is not None else 0.0,
+                                                 workspace.data_ptr() if nbytes else None, nbytes, stream)
+    if rc != 0:
+        raise PasaError(rc, "pasa_attn_fwd_decode_step_kv4")
     return out, lse
 
 
@@ -679,12 +717,13 @@ def cache_evict(planes, weights, budget: int, recent: int = 0, length: int | Non
     at = table.buffer_info()[0]
     np_ = None if lengths is None else _check_cuda(lengths, "lengths", torch.int32, (B,), dev)
     if index is None:
-        index = torch.empty((B, Hkv, max(budget, 0)), device=weights.device, dtype=torch.int32)
+        index = torch.empty((B, Hkv, max(budget, 0)), device=dev, dtype=torch.int32)
     if new_lengths is None:
-        new_lengths = torch.empty((B,), device=weights.device, dtype=torch.int32)
+        new_lengths = torch.empty((B,), device=dev, dtype=torch.int32) if np_ is None else torch.empty_like(lengths)
     ip = _check_cuda(index, "index", torch.int32, (B, Hkv, max(budget, 0)), dev)
     nlp = _check_cuda(new_lengths, "new_lengths", torch.int32, (B,), dev)
-    rc = library().pasa_cache_evict(at, at + 8 * count, rows.buffer_info()[0], count, wp, owp, np_, ip, nlp, B, Hkv, Sk, cap, out_cap, budget, recent, stream)
+    rc = library().pasa_cache_evict(at, at + 8 * count, rows.buffer_info()[0], count, wp, owp, np_, ip, nlp, B, Hkv, Sk,
+                                    cap, out_cap, budget, recent, stream)
     if rc != 0:
         raise PasaError(rc, "pasa_cache_evict")
     return index, new_lengths

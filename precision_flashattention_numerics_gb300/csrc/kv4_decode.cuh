@@ -51,7 +51,7 @@ struct Kv4Params {
   float* part_o;     // [gridDim.x + segments][tile rows][D]
   float2* part_ml;   // [gridDim.x + segments][tile rows]: max (log2 units), sum
   float* lse2;       // [segments][tile rows]: log2-sum-exp2 of the shifted scores, for the weights pass
-  int B, Hkv, g, Sq, rows, row_tiles;      // rows = g * Sq query rows of a kv head
+  int B, Hkv, Sq, rows, row_tiles;         // rows = Hq / Hkv * Sq query rows of a kv head
   int Sk, cap, causal;
   int len_add;       // added to lengths[] (a step call appends that many rows first)
   int ctas;          // gridDim.x of the stream-K decode
@@ -471,7 +471,6 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
   const int g = lane >> 2, t = lane & 3;
   const int rank = STREAM_K ? 0 : static_cast<int>(blockIdx.x % p.cluster);
   griddep_launch_dependents();
-  griddep_wait();   // rows that the call's append kernel stores
   const uint64_t policy = evict_first_policy();
 
   // this CTA's segments: (b, h, row tile) in order, its rounds in all, and the first one's number
@@ -482,7 +481,10 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
     const Kv4Lengths lengths(p);
     const int total = lengths.sum(p.B) * per_b;
     const int ctas = min(total, static_cast<int>(gridDim.x));
-    if (static_cast<int>(blockIdx.x) >= ctas) return;
+    if (static_cast<int>(blockIdx.x) >= ctas) {
+      griddep_wait();   // every CTA: what is behind this kernel waits for this kernel only
+      return;
+    }
     const Kv4Share share(total, ctas);
     int place = share.first(blockIdx.x);
     todo = share.first(blockIdx.x + 1) - place;
@@ -500,6 +502,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
     todo = n_units;
   }
 
+  griddep_wait();   // the rows that a step's append stores; nothing so far is its
   while (true) {
     const long long bh = static_cast<long long>(b) * p.Hkv + in_b / p.row_tiles;
     const int row0 = in_b % p.row_tiles * kRows;

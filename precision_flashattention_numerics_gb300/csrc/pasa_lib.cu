@@ -1599,26 +1599,34 @@ size_t pasa_attn_fwd_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Sq, 
   return kv4_plan(B, Hq, Hkv, Sq, Sk, D, weights != 0).total;
 }
 
-int pasa_attn_fwd_decode_kv4(const void* q, const void* k4, const void* kscale, const void* v4, const void* vscale,
-                             const void* shift, const int* lengths, void* o, float* lse, float* weights, int B, int Hq,
-                             int Hkv, int Sq, int Sk, int Sk_cap, int D, int causal, float scale, void* workspace,
-                             size_t workspace_bytes, void* stream) {
+// The checks of a decode call, and its layout.
+static int kv4_decode_check(const void* q, const void* k4, const void* kscale, const void* v4, const void* vscale,
+                            const void* shift, const int* lengths, const void* o, const float* lse, const float* weights,
+                            int B, int Hq, int Hkv, int Sq, int Sk, int Sk_cap, int D, const void* workspace,
+                            size_t workspace_bytes, Kv4Plan* plan) {
   if (!q || !o) return PASA_ERR_NULLPTR;
-  int rc = kv4_validate(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
+  const int rc = kv4_validate(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
   if (rc != PASA_OK) return rc;
   if (Hq <= 0 || Sq <= 0 || Sk <= 0 || Hq % Hkv != 0 || Sk_cap < Sk) return PASA_ERR_SHAPE;
   if (static_cast<long long>(Hq / Hkv) * Sq > pasa::kTileRows) return PASA_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(weights) || !aligned4(lengths))
     return PASA_ERR_ALIGN;
-  const Kv4Plan pl = kv4_plan(B, Hq, Hkv, Sq, Sk, D, weights != nullptr);
+  *plan = kv4_plan(B, Hq, Hkv, Sq, Sk, D, weights != nullptr);
   // grids and weights fit an int
-  if (pl.segments * ((Sk + pasa::kKv4Unit - 1) / pasa::kKv4Unit + pasa::kKv4SegmentStart) > INT_MAX) return PASA_ERR_SHAPE;
-  if (pl.total > 0) {
-    if (!workspace || workspace_bytes < pl.total) return PASA_ERR_WORKSPACE;
+  if (plan->segments * ((Sk + pasa::kKv4Unit - 1) / pasa::kKv4Unit + pasa::kKv4SegmentStart) > INT_MAX) return PASA_ERR_SHAPE;
+  if (plan->total > 0) {
+    if (!workspace || workspace_bytes < plan->total) return PASA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PASA_ERR_ALIGN;
   }
-  rc = check_device();
-  if (rc != PASA_OK) return rc;
+  return PASA_OK;
+}
+
+// The kernels of a checked decode call. len_add: added to lengths[]; pdl: the kernel ahead on the
+// stream is this call's append, which the decode waits for before it reads codes and scales.
+static int kv4_decode_enqueue(const Kv4Plan& pl, const void* q, const void* k4, const void* kscale, const void* v4,
+                              const void* vscale, const void* shift, const int* lengths, int len_add, void* o, float* lse,
+                              float* weights, int B, int Hq, int Hkv, int Sq, int Sk, int Sk_cap, int D, int causal,
+                              float scale, void* workspace, cudaStream_t st, bool pdl) {
   if (!(scale > 0.0f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt(static_cast<float>(D));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   pasa::Kv4Params p = {};
@@ -1629,6 +1637,7 @@ int pasa_attn_fwd_decode_kv4(const void* q, const void* k4, const void* kscale, 
   p.vscale = static_cast<const __half*>(vscale);
   p.shift = static_cast<const __half*>(shift);
   p.lengths = lengths;
+  p.len_add = len_add;
   p.o = static_cast<__half*>(o);
   p.lse = lse;
   p.weights = weights;
@@ -1637,9 +1646,8 @@ int pasa_attn_fwd_decode_kv4(const void* q, const void* k4, const void* kscale, 
   p.lse2 = reinterpret_cast<float*>(ws + pl.lse2);
   p.B = B;
   p.Hkv = Hkv;
-  p.g = Hq / Hkv;
   p.Sq = Sq;
-  p.rows = p.g * Sq;
+  p.rows = Hq / Hkv * Sq;
   p.row_tiles = pl.row_tiles;
   p.Sk = Sk;
   p.cap = Sk_cap;
@@ -1648,9 +1656,41 @@ int pasa_attn_fwd_decode_kv4(const void* q, const void* k4, const void* kscale, 
   p.cluster = pl.cluster;
   p.scale = scale;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = D == 64 ? kv4_decode_launch<64>(p, pl, st, false) : kv4_decode_launch<128>(p, pl, st, false);
+  const cudaError_t e = D == 64 ? kv4_decode_launch<64>(p, pl, st, pdl) : kv4_decode_launch<128>(p, pl, st, pdl);
   return e == cudaSuccess ? launch_status() : cuda_fail(e);
+}
+
+int pasa_attn_fwd_decode_kv4(const void* q, const void* k4, const void* kscale, const void* v4, const void* vscale,
+                             const void* shift, const int* lengths, void* o, float* lse, float* weights, int B, int Hq,
+                             int Hkv, int Sq, int Sk, int Sk_cap, int D, int causal, float scale, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  Kv4Plan pl;
+  int rc = kv4_decode_check(q, k4, kscale, v4, vscale, shift, lengths, o, lse, weights, B, Hq, Hkv, Sq, Sk, Sk_cap, D,
+                            workspace, workspace_bytes, &pl);
+  if (rc != PASA_OK) return rc;
+  rc = check_device();
+  if (rc != PASA_OK) return rc;
+  return kv4_decode_enqueue(pl, q, k4, kscale, v4, vscale, shift, lengths, 0, o, lse, weights, B, Hq, Hkv, Sq, Sk, Sk_cap,
+                            D, causal, scale, workspace, static_cast<cudaStream_t>(stream), false);
+}
+
+int pasa_attn_fwd_decode_step_kv4(const void* q, const void* k, const void* v, void* k4, void* kscale, void* v4,
+                                  void* vscale, const void* shift, const int* starts, int start, void* o, float* lse,
+                                  float* weights, int B, int Hq, int Hkv, int Sq, int n, int Sk, int Sk_cap, int D,
+                                  int causal, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (n <= 0) return PASA_ERR_SHAPE;
+  if (!starts) {   // every sequence has start + n rows in the end
+    if (start < 0 || static_cast<long long>(start) + n > Sk_cap) return PASA_ERR_SHAPE;
+    Sk = start + n;
+  }
+  Kv4Plan pl;
+  int rc = kv4_decode_check(q, k4, kscale, v4, vscale, shift, starts, o, lse, weights, B, Hq, Hkv, Sq, Sk, Sk_cap, D,
+                            workspace, workspace_bytes, &pl);
+  if (rc != PASA_OK) return rc;
+  rc = pasa_kv4_append(k, v, shift, k4, kscale, v4, vscale, starts, start, nullptr, B, Hkv, n, Sk_cap, D, stream);
+  if (rc != PASA_OK) return rc;
+  return kv4_decode_enqueue(pl, q, k4, kscale, v4, vscale, shift, starts, n, o, lse, weights, B, Hq, Hkv, Sq, Sk, Sk_cap, D,
+                            causal, scale, workspace, static_cast<cudaStream_t>(stream), true);
 }
 
 int pasa_cache_evict(const void* const* planes, void* const* out_planes, const int* row_bytes, int n_planes,

@@ -315,6 +315,41 @@ def test_calls_in_a_row_on_one_workspace_and_on_another_stream():
         assert torch.equal(o, want[i % 3][0]) and torch.equal(lse, want[i % 3][1])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,per_sequence,weights", [(1, True, False), (1, False, True), (3, True, True), (200, True, False)])
+def test_step_equals_append_and_decode(n, per_sequence, weights, D):
+    """Bit for bit, again and again on one stream (the decode kernel starts while rows are stored)."""
+    p = pasa()
+    B, Hq, H, cap = 3, 8, 2, 3000
+    rng = np.random.default_rng(n)
+    kt, vt = to_dev(rows(rng, B, H, cap, D, "bias"), rows(rng, B, H, cap, D, "plain"))
+    qs = to_dev(rng.standard_normal((6, B, Hq, min(n, 5), D)).astype(np.float16))[0]
+    shift = kt[:, :, 0].contiguous()
+    first = torch.tensor([1234, 0, 2100] if per_sequence else [700] * 3).int().cuda()
+    caches = [new_cache(B, H, cap, D) for _ in range(2)]
+    accs = [torch.zeros((B, H, cap), device="cuda") if weights else None for _ in range(2)]
+    for c in caches:
+        p.kv4_append(kt, vt, *c, counts=first, shift=shift)
+    pos = first.clone()
+    outs = []
+    for i in range(4):   # no synchronisation in between
+        a = i * n
+        k1, v1 = kt[:, :, a:a + n].contiguous(), vt[:, :, a:a + n].contiguous()
+        start = pos.clone() if per_sequence else 700 + a
+        got = p.attn_fwd_decode_step_kv4(qs[i], k1, v1, *caches[0], start, causal=True, shift=shift, weights=accs[0])
+        p.kv4_append(k1, v1, *caches[1], start=start, shift=shift)
+        want = p.attn_fwd_decode_kv4(qs[i], *caches[1], causal=True, shift=shift, weights=accs[1],
+                                     **({"lengths": pos + n} if per_sequence else {"length": 700 + a + n}))
+        outs.append((got, want))
+        pos = pos + n
+    for got, want in outs:
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for a, b in zip(caches[0], caches[1]):
+        assert torch.equal(a, b)
+    if weights:
+        assert torch.equal(accs[0], accs[1])
+
+
 def test_captured_steps_follow_the_lengths_and_share_a_workspace():
     """A decode step (append one row, attend, gather weights) captured once and replayed as the
     sequences grow, twice in two graphs that share a workspace: equal to eager calls."""

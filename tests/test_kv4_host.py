@@ -139,6 +139,23 @@ def test_decode_refusals(lib):
     assert lib.pasa_attn_fwd_decode_kv4_workspace_bytes(1, 8, 2, 33, 5000, 128, 0) == 0
 
 
+def test_step_refusals(lib):
+    def step(k=FAKE, v=FAKE, starts=0, start=49999, n=1, Sq=1, Sk=1, cap=50000, D=128, o=FAKE, ws=FAKE, nbytes=1 << 30):
+        p = lambda x: P(x) if x else None   # noqa: E731
+        c = [P(FAKE)] * 4
+        return lib.pasa_attn_fwd_decode_step_kv4(P(FAKE), p(k), p(v), *c, None, p(starts), start, p(o), P(FAKE), None, 1, 8,
+                                                 2, Sq, n, Sk, cap, D, 1, 0.0, p(ws), nbytes, None)
+
+    assert step(o=0) == -1
+    for bad in ({"n": 0}, {"start": 50000}, {"start": -1}, {"starts": FAKE, "Sk": 50001}, {"starts": FAKE, "Sk": 0}):
+        assert step(**bad) == -2, bad
+    assert step(Sq=33) == -3 and step(D=32) == -3
+    assert step(ws=0) == -7 and step(nbytes=16) == -7             # 50000 rows, whatever Sk says
+    assert step(starts=MIS4, Sk=50000) == -4
+    # what the append refuses is refused before anything is enqueued: the decode's checks passed
+    assert step(k=0) == -1 and step(v=MIS16) == -4
+
+
 def test_evict_refusals(lib):
     def evict(planes=(FAKE, FAKE), out=(FAKE * 2, FAKE * 2), rb=(64, 8), n=None, w=FAKE, ow=FAKE * 2, lengths=0,
               index=FAKE, new=0, B=1, H=2, Sk=64, cap=64, out_cap=32, budget=32, recent=4):
