@@ -16,7 +16,7 @@ constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictPlanes = 8;     // planes of one cache
 constexpr int kMoveThreads = 256;
-constexpr int kEvictCluster = 8;    // CTAs of a (sequence, kv head), at most
+constexpr int kEvictCluster = 4;    // CTAs of a (sequence, kv head), at most
 
 // Weights as unsigned numbers in the same order: NaN counts as -inf, -0 as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {

@@ -50,9 +50,9 @@ __device__ __forceinline__ float round_8bits(float x) {
   return __uint_as_float(u & 0xFFFF0000u);
 }
 
-// The codes of 8 channels, one nibble each (bits 4i .. 4i + 3: channel i), and the group's
-// scale; x: 8 fp16 in 4 registers. Called by the 4 lanes of a group together (aligned groups
-// of 4 lanes hold the 32 channels).
+// The codes of 16 channels, one nibble each (bits 4i .. 4i + 3 of the first word: channel i), and the
+// group's scale; x: 16 fp16 in 8 registers. Called by the 2 lanes of a group together (aligned
+// pairs of lanes hold the 32 channels).
 //
 // Both quotients are only needed rounded, so products with reciprocals do. max|x| / 7 to 8 bits: a
 // tie is a 9-bit number t with max|x| = 7 t; any other quotient of an 11-bit number is at least
@@ -62,112 +62,117 @@ __device__ __forceinline__ float round_8bits(float x) {
 // s 8, and both are multiples of a power of two no smaller than s * 2^-12. So x * (1 / s), off by
 // at most 7 * 2^-22, is first rounded to a multiple of 2^-14 (by adding 768), and then to an integer
 // (by adding 1.5 * 2^23 - 768), ties to even.
-__device__ __forceinline__ uint32_t kv4_codes(const uint32_t (&xin)[4], __half& scale) {
-  uint32_t x[4] = {xin[0], xin[1], xin[2], xin[3]};
-  __half2 m2 = __hmax2_nan(__hmax2_nan(__habs2(bits_h2(x[0])), __habs2(bits_h2(x[1]))),
-                           __hmax2_nan(__habs2(bits_h2(x[2])), __habs2(bits_h2(x[3]))));
+__device__ __forceinline__ uint2 kv4_codes(const uint32_t (&xin)[8], __half& scale) {
+  uint32_t x[8];
+  __half2 m2 = __float2half2_rn(0.0f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = xin[i];
+    m2 = __hmax2_nan(m2, __habs2(bits_h2(x[i])));
+  }
   m2 = __hmax2_nan(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 1));
-  m2 = __hmax2_nan(m2, __shfl_xor_sync(0xFFFFFFFFu, m2, 2));
-  const __half m = __hmax_nan(__low2half(m2), __high2half(m2));
-  float a = __half2float(m);
+  float a = __half2float(__hmax_nan(__low2half(m2), __high2half(m2)));
   // a group that is not finite, or so small that its scale has fewer than 8 bits and |x / s| may
-  // pass 7 by more than rounding: the same in its 4 lanes
+  // pass 7 by more than rounding: the same in its 2 lanes
   const bool odd = !(a <= 65504.0f) || a < 7.0f * 0x1p-14f;
   const bool odds = __any_sync(0xFFFFFFFFu, odd);
   if (odds) {
     float b = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       float2 f = __half22float2(bits_h2(x[i]));
       f.x = f.x == f.x ? fminf(fmaxf(f.x, -65504.0f), 65504.0f) : 0.0f;
       f.y = f.y == f.y ? fminf(fmaxf(f.y, -65504.0f), 65504.0f) : 0.0f;
       b = fmaxf(b, fmaxf(fabsf(f.x), fabsf(f.y)));
       x[i] = h2_bits(__float22half2_rn(f));
     }
-    b = fmaxf(b, __shfl_xor_sync(0xFFFFFFFFu, b, 1));
-    a = fmaxf(b, __shfl_xor_sync(0xFFFFFFFFu, b, 2));
+    a = fmaxf(b, __shfl_xor_sync(0xFFFFFFFFu, b, 1));
   }
   const float sixteen_bits = __uint_as_float((__float_as_uint(a * (1.0f / 7.0f)) + 0x80u) & 0xFFFFFF00u);
   scale = __float2half_rn(round_8bits(sixteen_bits));
   if (odds) {
     const __half2 top = __hmul2(__half2half2(scale), __float2half2_rn(7.0f));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = h2_bits(__hmax2(__hmin2(bits_h2(x[i]), top), __hneg2(top)));
+    for (int i = 0; i < 8; ++i) x[i] = h2_bits(__hmax2(__hmin2(bits_h2(x[i]), top), __hneg2(top)));
   }
   const float s = __half2float(scale);
   const float r = s > 0.0f ? rcp_approx(s) : 0.0f;
-  uint32_t y[8];
+  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(bits_h2(x[i]));
-    // 12582912 = 1.5 * 2^23: the integer code + 8 lands in the low bits of the float
-    constexpr float kToInt = 12582912.0f + 8.0f - 768.0f;
-    float lo, hi;
-    ffma2(lo, hi, f.x, f.y, r, r, 768.0f, 768.0f);
-    fadd2(lo, hi, lo, hi, kToInt, kToInt);
-    y[2 * i] = __float_as_uint(lo);
-    y[2 * i + 1] = __float_as_uint(hi);
+  for (int half = 0; half < 2; ++half) {
+    uint32_t b[4];   // low byte: two codes (1 .. 15 each)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(bits_h2(x[4 * half + i]));
+      // 12582912 = 1.5 * 2^23: the integer code + 8 lands in the low bits of the float
+      constexpr float kToInt = 12582912.0f + 8.0f - 768.0f;
+      float lo, hi;
+      ffma2(lo, hi, f.x, f.y, r, r, 768.0f, 768.0f);
+      fadd2(lo, hi, lo, hi, kToInt, kToInt);
+      b[i] = __float_as_uint(hi) * 16u + __float_as_uint(lo);
+    }
+    w[half] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
   }
-  uint32_t b[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = y[2 * i + 1] * 16u + y[2 * i];   // low byte: two codes (1 .. 15 each)
-  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  return make_uint2(w[0], w[1]);
 }
 
-// Rows a thread of the store kernels handles, kv4_block_rows apart.
-constexpr int kKv4StoreRows = 4;
-template <int D>
-__host__ __device__ constexpr int kv4_block_rows() { return kKv4StoreThreads / (D / 8); }
+// Rows of a thread, a block's rows apart; it takes the same channels of each, of K and V, of one
+// (sequence, kv head) (blockIdx.y). Both kernels are HBM-bound: 4 D bytes of fp16 and 9 D / 8 of codes
+// and scales per row, one way or the other. Storing, a thread takes 16 channels, so that two lanes
+// have a group and its scale's arithmetic is shared by more (4 x 8 heads x 8192 rows, D = 128: 27.5 us,
+// 0.93 of the copy rate; 36 us with 8 channels). Reading back, it takes 8, whose 16 bytes a warp
+// stores without gaps (28.4 us; 41 us with 16, whose stores each fill half sectors).
+constexpr int kKv4AppendRows = 2;
+constexpr int kKv4ReadRows = 4;
 
-// Store rows of k and v [B, H, n, D] in the cache. A thread takes the same 8 channels (16 bytes
-// in, 4 bytes of codes out) of a few rows of K and V; blockIdx.y: (sequence, kv head). HBM-bound:
-// 4 D bytes in and 9 D / 8 out per row.
+__device__ __forceinline__ void load16(uint32_t (&x)[8], const __half* p) {
+  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p)), b = __ldcs(reinterpret_cast<const uint4*>(p) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// Store rows of k and v [B, H, n, D] in the cache.
 template <int D>
 __global__ void __launch_bounds__(kKv4StoreThreads) kv4_append_kernel(
     const __half* __restrict__ k, const __half* __restrict__ v, const __half* __restrict__ shift,
     uint8_t* __restrict__ k4, __half* __restrict__ kscale, uint8_t* __restrict__ v4, __half* __restrict__ vscale,
     int planes, int H, Kv4Window win) {
   griddep_launch_dependents();
-  constexpr int kPer = D / 8;   // threads per row
+  constexpr int kPer = D / 16;   // threads per row
+  constexpr int kRows = kKv4StoreThreads / kPer, N = kKv4AppendRows;
   const int u = threadIdx.x % kPer;
-  const int i0 = blockIdx.x * (kKv4StoreRows * kv4_block_rows<D>()) + threadIdx.x / kPer;
+  const int i0 = blockIdx.x * (N * kRows) + threadIdx.x / kPer;
   for (int plane = blockIdx.y; plane < planes; plane += gridDim.y) {
     const int b = plane / H;
-    long long row[kKv4StoreRows];
-    uint4 xk[kKv4StoreRows], xv[kKv4StoreRows];
+    long long row[N];
+    uint32_t xk[N][8] = {}, xv[N][8] = {};
+    const __half* kp = k + (static_cast<long long>(plane) * win.n + i0) * D + u * 16;
+    const __half* vp = v + (static_cast<long long>(plane) * win.n + i0) * D + u * 16;
 #pragma unroll
-    for (int j = 0; j < kKv4StoreRows; ++j) {
-      const int i = i0 + j * kv4_block_rows<D>();
-      xk[j] = xv[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < win.n) {   // rows past counts too: waiting for the count first takes longer
-        const long long from = (static_cast<long long>(plane) * win.n + i) * D + u * 8;
-        xk[j] = __ldcs(reinterpret_cast<const uint4*>(k + from));
-        xv[j] = __ldcs(reinterpret_cast<const uint4*>(v + from));
+    for (int j = 0; j < N; ++j)
+      if (i0 + j * kRows < win.n) {   // rows past counts too: waiting for the count first takes longer
+        load16(xk[j], kp + j * kRows * D);
+        load16(xv[j], vp + j * kRows * D);
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kKv4StoreRows; ++j) {
-      const int i = i0 + j * kv4_block_rows<D>();
+    for (int j = 0; j < N; ++j) {
+      const int i = i0 + j * kRows;
       row[j] = i < win.n ? win.row(b, i) : -1;
     }
-    uint4 sh = make_uint4(0u, 0u, 0u, 0u);   // x - 0 = x
-    if (shift) sh = *reinterpret_cast<const uint4*>(shift + static_cast<long long>(plane) * D + u * 8);
+    uint32_t sh[8] = {};   // x - 0 = x
+    if (shift) load16(sh, shift + static_cast<long long>(plane) * D + u * 16);
 #pragma unroll
-    for (int j = 0; j < kKv4StoreRows; ++j) {
-      const uint32_t x[4] = {h2_bits(__hsub2_rn(bits_h2(xk[j].x), bits_h2(sh.x))),
-                             h2_bits(__hsub2_rn(bits_h2(xk[j].y), bits_h2(sh.y))),
-                             h2_bits(__hsub2_rn(bits_h2(xk[j].z), bits_h2(sh.z))),
-                             h2_bits(__hsub2_rn(bits_h2(xk[j].w), bits_h2(sh.w)))};
-      const uint32_t y[4] = {xv[j].x, xv[j].y, xv[j].z, xv[j].w};
+    for (int j = 0; j < N; ++j) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xk[j][i] = h2_bits(__hsub2_rn(bits_h2(xk[j][i]), bits_h2(sh[i])));
       __half sk, sv;
-      const uint32_t ck = kv4_codes(x, sk), cv = kv4_codes(y, sv);
+      const uint2 ck = kv4_codes(xk[j], sk), cv = kv4_codes(xv[j], sv);
       if (row[j] >= 0) {
         const long long at = static_cast<long long>(plane) * win.cap + row[j];
-        *reinterpret_cast<uint32_t*>(k4 + at * (D / 2) + u * 4) = ck;
-        *reinterpret_cast<uint32_t*>(v4 + at * (D / 2) + u * 4) = cv;
-        if ((u & 3) == 0) {
-          kscale[at * (D / kKv4Group) + u / 4] = sk;
-          vscale[at * (D / kKv4Group) + u / 4] = sv;
+        *reinterpret_cast<uint2*>(k4 + at * (D / 2) + u * 8) = ck;
+        *reinterpret_cast<uint2*>(v4 + at * (D / 2) + u * 8) = cv;
+        if ((u & 1) == 0) {
+          kscale[at * (D / kKv4Group) + u / 2] = sk;
+          vscale[at * (D / kKv4Group) + u / 2] = sv;
         }
       }
     }
@@ -193,26 +198,30 @@ __device__ __forceinline__ uint4 kv4_values8(uint32_t w, __half s) {
   return make_uint4(h2_bits(__lows2half2(p[0], p[1])), h2_bits(__lows2half2(p[2], p[3])),
                     h2_bits(__highs2half2(p[0], p[1])), h2_bits(__highs2half2(p[2], p[3])));
 }
+__device__ __forceinline__ uint4 add8(uint4 x, uint4 y) {
+  return make_uint4(h2_bits(__hadd2_rn(bits_h2(x.x), bits_h2(y.x))), h2_bits(__hadd2_rn(bits_h2(x.y), bits_h2(y.y))),
+                    h2_bits(__hadd2_rn(bits_h2(x.z), bits_h2(y.z))), h2_bits(__hadd2_rn(bits_h2(x.w), bits_h2(y.w))));
+}
 
 // Read cache rows back as fp16: fp16_rn(s * c + shift) for keys, s * c for values, into
-// k, v [B, H, n, D]; output rows without a cache row are left as they are. Laid out as
-// kv4_append_kernel.
+// k, v [B, H, n, D]; output rows without a cache row are left as they are.
 template <int D>
 __global__ void __launch_bounds__(kKv4StoreThreads) kv4_read_kernel(
     const uint8_t* __restrict__ k4, const __half* __restrict__ kscale, const uint8_t* __restrict__ v4,
     const __half* __restrict__ vscale, const __half* __restrict__ shift, __half* __restrict__ k,
     __half* __restrict__ v, int planes, int H, Kv4Window win) {
-  constexpr int kPer = D / 8;
+  constexpr int kPer = D / 8;   // threads per row
+  constexpr int kRows = kKv4StoreThreads / kPer, N = kKv4ReadRows;
   const int u = threadIdx.x % kPer;
-  const int i0 = blockIdx.x * (kKv4StoreRows * kv4_block_rows<D>()) + threadIdx.x / kPer;
+  const int i0 = blockIdx.x * (N * kRows) + threadIdx.x / kPer;
   for (int plane = blockIdx.y; plane < planes; plane += gridDim.y) {
     const int b = plane / H;
-    long long row[kKv4StoreRows];
-    uint32_t ck[kKv4StoreRows], cv[kKv4StoreRows];
-    __half sk[kKv4StoreRows], sv[kKv4StoreRows];
+    long long row[N];
+    uint32_t ck[N], cv[N];
+    __half sk[N], sv[N];
 #pragma unroll
-    for (int j = 0; j < kKv4StoreRows; ++j) {
-      const int i = i0 + j * kv4_block_rows<D>();
+    for (int j = 0; j < N; ++j) {
+      const int i = i0 + j * kRows;
       row[j] = i < win.n ? win.row(b, i) : -1;
       ck[j] = cv[j] = 0u;
       sk[j] = sv[j] = __ushort_as_half(0);
@@ -227,15 +236,10 @@ __global__ void __launch_bounds__(kKv4StoreThreads) kv4_read_kernel(
     uint4 sh = make_uint4(0u, 0u, 0u, 0u);
     if (shift) sh = *reinterpret_cast<const uint4*>(shift + static_cast<long long>(plane) * D + u * 8);
 #pragma unroll
-    for (int j = 0; j < kKv4StoreRows; ++j) {
+    for (int j = 0; j < N; ++j) {
       if (row[j] < 0) continue;
-      const long long to = (static_cast<long long>(plane) * win.n + i0 + j * kv4_block_rows<D>()) * D + u * 8;
-      uint4 x = kv4_values8(ck[j], sk[j]);
-      x.x = h2_bits(__hadd2_rn(bits_h2(x.x), bits_h2(sh.x)));
-      x.y = h2_bits(__hadd2_rn(bits_h2(x.y), bits_h2(sh.y)));
-      x.z = h2_bits(__hadd2_rn(bits_h2(x.z), bits_h2(sh.z)));
-      x.w = h2_bits(__hadd2_rn(bits_h2(x.w), bits_h2(sh.w)));
-      *reinterpret_cast<uint4*>(k + to) = x;
+      const long long to = (static_cast<long long>(plane) * win.n + i0 + j * kRows) * D + u * 8;
+      *reinterpret_cast<uint4*>(k + to) = add8(kv4_values8(ck[j], sk[j]), sh);
       *reinterpret_cast<uint4*>(v + to) = kv4_values8(cv[j], sv[j]);
     }
   }

@@ -1433,13 +1433,13 @@ int kv4_validate(const void* k4, const void* kscale, const void* v4, const void*
 
 // kv4_append and kv4_read share their arguments: n rows of k and v from cache row `start` on.
 int kv4_window(const void* k, const void* v, const int* starts, int start, const int* counts, int n, int B, int Hkv,
-               int Sk_cap, int D, pasa::Kv4Window* win, dim3* grid) {
+               int Sk_cap, int D, bool append, pasa::Kv4Window* win, dim3* grid) {
   if (!k || !v) return PASA_ERR_NULLPTR;
   if (n <= 0) return PASA_ERR_SHAPE;
   if (!starts && (start < 0 || static_cast<long long>(start) + n > Sk_cap)) return PASA_ERR_SHAPE;
   if (!aligned16(k) || !aligned16(v) || !aligned4(starts) || !aligned4(counts)) return PASA_ERR_ALIGN;
   if (n > INT_MAX - 256) return PASA_ERR_SHAPE;   // row numbers of a block's last threads
-  const int per_block = pasa::kKv4StoreRows * (D == 64 ? pasa::kv4_block_rows<64>() : pasa::kv4_block_rows<128>());
+  const int per_block = append ? pasa::kKv4AppendRows * (pasa::kKv4StoreThreads / (D / 16)) : pasa::kKv4ReadRows * (pasa::kKv4StoreThreads / (D / 8));
   *win = pasa::Kv4Window{starts, counts, start, n, Sk_cap};
   *grid = dim3(static_cast<unsigned>((n + per_block - 1) / per_block), static_cast<unsigned>(std::min(B * Hkv, 65535)));
   return PASA_OK;
@@ -1460,10 +1460,6 @@ struct Kv4Plan {
   size_t part_o, part_ml, lse2, total;   // workspace: byte offsets and size
 };
 
-#ifndef CU
-#define CU 4
-#endif
-constexpr int kKv4ClusterUnits = CU;
 
 Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   Kv4Plan pl = {};
@@ -1475,7 +1471,15 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   const int units = (Sk + pasa::kKv4Unit - 1) / pasa::kKv4Unit;
   pl.cluster = 1;
   while (pl.cluster < 8 && pl.segments * pl.cluster * 2 <= pl.ctas && units > pasa::kKv4Warps * pl.cluster) pl.cluster *= 2;
-  pl.stream_k = units > pasa::kKv4Warps * pl.cluster * kKv4ClusterUnits;
+  // A cluster per segment needs one launch and no workspace, but few segments leave SMs idle, and an
+  // uneven batch waits for its longest sequence. GPU us with 4 kv heads, 7 rows, D = 128, cluster against
+  // stream-K, by sequences, keys and rounds of a warp: 1 x 8192 (4) 9.0 / 8.6, 1 x 12288 (6) 11.1 / 9.2,
+  // 1 x 16384 (8) 13.6 / 9.4, where the launches that stream-K adds cost the host 8 us; with the SMs
+  // filled 8 x 8192 (4) 14.2 / 16.3, 8 x 32768 (16) 36.1 / 35.2, and without clusters (their segments
+  // follow one another as SMs get free) 64 x 2048 (8) 20.3 / 30.1, 64 x 4096 (16) 35.2 / 43.1.
+  const int rounds = (units + pasa::kKv4Warps * pl.cluster - 1) / (pasa::kKv4Warps * pl.cluster);
+  const bool filled = pl.segments * pl.cluster * 4 >= pl.ctas * 3;
+  pl.stream_k = rounds > (!filled ? 6 : pl.cluster > 1 ? 8 : 16);
   if (pl.stream_k) pl.cluster = 1;
   const size_t tile = static_cast<size_t>(8 * pl.nt);
   const size_t slots = pl.stream_k ? static_cast<size_t>(pl.ctas + pl.segments) : 0;
@@ -1562,7 +1566,7 @@ int pasa_kv4_append(const void* k, const void* v, const void* shift, void* k4, v
   if (rc != PASA_OK) return rc;
   pasa::Kv4Window win;
   dim3 grid;
-  rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, &win, &grid);
+  rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, true, &win, &grid);
   if (rc != PASA_OK) return rc;
   rc = check_device();
   if (rc != PASA_OK) return rc;
@@ -1581,7 +1585,7 @@ int pasa_kv4_read(const void* k4, const void* kscale, const void* v4, const void
   if (rc != PASA_OK) return rc;
   pasa::Kv4Window win;
   dim3 grid;
-  rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, &win, &grid);
+  rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, false, &win, &grid);
   if (rc != PASA_OK) return rc;
   rc = check_device();
   if (rc != PASA_OK) return rc;
