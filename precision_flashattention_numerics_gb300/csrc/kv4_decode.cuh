@@ -3,27 +3,36 @@
 // row gets. One shift per kv head and channel is the same for every key of a row, so
 // q . shift cancels in the softmax and only enters the log-sum-exp.
 //
-// kv4_decode_kernel. HBM-bound: 9 D / 8 bytes per cached row of K and V against 4 rows D
-// flops. A warp takes 32 keys at a time from global memory straight into registers and
-// multiplies with mma.sync m16n8k16 (fp16 in, fp32 out):
-//   S^T[key][row] = K' Q^T:  A = K' (16 keys x 16 channels), B = Q^T (16 channels x 8 rows);
-//   O^T[channel][row] += V^T P^T:  A = V^T (16 channels x 16 keys), B = P^T (16 keys x 8 rows).
-// tcgen05 takes its operands from shared or tensor memory, so the expanded codes (4 times the
-// bytes that HBM delivers) would cross shared memory twice; the register operands of mma.sync
-// need neither trip, and with 8 or 16 rows the tensor work is small. Channels and
-// keys are numbered inside an MMA so that a thread's operands are the consecutive bytes it
-// loads: lane (g, t) = (lane / 4, lane % 4) loads channels t * D/4 .. of keys g, g + 8, .. for
-// S and channels g * D/8 .. of keys 2t, 2t + 1, .. for O. S^T comes out with keys along the
-// lanes' g and P^T is needed with keys along t: one movmatrix per 8 x 8 block.
-// Every code times its scale is exact in fp16 (the scale has 8 significant bits), so K' and V
-// enter the MMAs as the cache's values themselves; P is rounded to fp16 (relative 2^-11, as in
-// the other decode kernels); scores, maxima, sums and O stay fp32.
+// kv4_decode_kernel. HBM-bound for up to 8 rows: 9 D / 8 bytes per cached row of K and V against
+// 4 rows D flops. A warp takes 32 keys at a time: codes by cp.async to its own two stages of shared
+// memory, from there by ldmatrix into the registers of mma.sync m16n8k16 (fp16 in, fp32 out):
+//   8 rows:  S^T[key][row] = K' Q^T (A = K', 16 keys), O^T[channel][row] += V^T P^T (A = V^T);
+//   16 rows: S[row][key] = Q K'^T (A = Q), O[row][channel] += P V (A = P).
+// The rows' side is 8 or 16 wide, so that little of an MMA is padding. tcgen05 takes its operands
+// from shared or tensor memory, where the expanded codes, four times the bytes that HBM delivers,
+// would have to be written and read again; mma.sync takes them from the registers they
+// are expanded in.
+//   - Keys are not expanded at all: a code masked out of its byte is a subnormal fp16 number, and
+//     what it lacks of its value (the -8, the scale) is a constant of the accumulator and one fp32
+//     product per score and group of 32 channels (Kv4Query).
+//   - Values are expanded to s c, exact in fp16 as s has 8 significant bits. ldmatrix.trans gives a
+//     lane 4 channels of two neighbouring keys, the pair that the MMA wants in a register.
+//   - P is rounded to fp16 (relative 2^-11, as in the other decode kernels). Scores, maxima, sums and
+//     O are fp32.
 //
-// Work split. With `stream_k` the 32-key units of all (sequence, kv head, row tile) segments
-// are numbered in order and CTA c takes the c-th of gridDim.x equal ranges, so uneven lengths
-// keep all SMs equally busy. A segment inside one CTA is finished there; otherwise its CTAs
-// leave (O, max, sum) partials and kv4_merge_kernel joins them. Without it, CTA s takes segment
-// s whole: one launch, no workspace.
+// Work split. A segment is a (sequence, kv head, tile of 8 or 16 rows). Either a cluster of CTAs takes
+// a segment, warps interleaved, and joins through distributed shared memory: one launch, no workspace.
+// Or (STREAM_K) the segments' rounds are numbered in order and CTA c takes the c-th of gridDim.x equal
+// ranges, so that uneven lengths keep all SMs equally busy; a segment inside one CTA is finished
+// there, else its CTAs leave (O, max, sum) partials that kv4_merge_kernel joins. Which one is
+// chosen on the host by the sizes.
+//
+// Measured, GPU time of a call: 8 sequences x 4 kv heads x 32768 keys, D = 128, 7 rows: 34.3 us
+// for 151 MB, 0.66 of the copy rate; x 131072 keys 108 us, 0.84. Per 32 keys a warp issues about
+// 540 instructions, 135 cycles of an SM's issue slots where HBM takes 199; the shared-out ranges
+// run at 225. The rest is the start (lengths, shares and the first burst of codes, 4 us) and the
+// join. Expanding keys like values took 650 instructions (39.5 us); a third CTA per SM needs 80
+// registers and spills (44 us).
 #pragma once
 
 #include <cmath>
@@ -48,8 +57,8 @@ struct Kv4Params {
   __half* o;
   float* lse;        // or nullptr
   float* weights;    // [B, Hkv, cap] or nullptr
-  float* part_o;     // [gridDim.x + segments][tile rows][D]
-  float2* part_ml;   // [gridDim.x + segments][tile rows]: max (log2 units), sum
+  float* part_o;     // [2 gridDim.x][tile rows][D]: a CTA's first segment, and its last
+  float2* part_ml;   // [2 gridDim.x][tile rows]: max (log2 units), sum
   float* lse2;       // [segments][tile rows]: log2-sum-exp2 of the shifted scores, for the weights pass
   int B, Hkv, Sq, rows, row_tiles;         // rows = Hq / Hkv * Sq query rows of a kv head
   int Sk, cap, causal;
@@ -503,7 +512,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
   }
 
   griddep_wait();   // the rows that a step's append stores; nothing so far is its
-  while (true) {
+  for (int nth = 0;; nth = 1) {   // 0: the CTA's first segment
     const long long bh = static_cast<long long>(b) * p.Hkv + in_b / p.row_tiles;
     const int row0 = in_b % p.row_tiles * kRows;
     const int n_rows = min(kRows, p.rows - row0);
@@ -749,7 +758,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
       } else if (whole) {
         kv4_finish<D>(p, out0 + r, seg * kRows + r, ch, x, mm, ll, sm.offset[r]);
       } else {
-        const long long slot = (blockIdx.x + seg) * kRows + r;
+        const long long slot = (2 * blockIdx.x + nth) * kRows + r;   // only its first and last are shared
         *reinterpret_cast<float4*>(p.part_o + slot * D + ch) = x;
         if (ch == 0) p.part_ml[slot] = make_float2(mm, ll);
       }
@@ -848,13 +857,15 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
   griddep_wait();   // the partials
   // every partial's max and sum at once, then its factor
   constexpr int kMine = (kKv4MaxCtas + 255) / 256;
-  const long long first = (c0 + seg) * tile_rows + r;   // partial c0 + i of the row: + i * tile_rows
+  // the row's partial of CTA c0 + i: that of its first segment, but c0 may have begun with another one
+  const int begun = share.first(c0) < t0 ? 1 : 0;
+  auto slot = [&](int i) { return (2ll * (c0 + i) + (i == 0 ? begun : 0)) * tile_rows + r; };
   float2 ml[kMine];
   float mm = kKv4NoKey;
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
     const int c = i * 256 + threadIdx.x;
-    ml[i] = c < n ? p.part_ml[first + static_cast<long long>(c) * tile_rows] : make_float2(kKv4NoKey, 0.0f);
+    ml[i] = c < n ? p.part_ml[slot(c)] : make_float2(kKv4NoKey, 0.0f);
     mm = fmaxf(mm, ml[i].x);
   }
 #pragma unroll
@@ -878,16 +889,16 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
   float acc[D / 32];
 #pragma unroll
   for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
-  const float* part = p.part_o + first * D + lane * (D / 32);
+  const float* part = p.part_o + lane * (D / 32);
 #pragma unroll 4
   for (int c = warp; c < n; c += 8) {
     const float f = factor[c];
     if constexpr (D == 128) {
-      const float4 x = *reinterpret_cast<const float4*>(part + static_cast<long long>(c) * tile_rows * D);
+      const float4 x = *reinterpret_cast<const float4*>(part + slot(c) * D);
       acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]);
       acc[2] = fmaf(f, x.z, acc[2]), acc[3] = fmaf(f, x.w, acc[3]);
     } else {
-      const float2 x = *reinterpret_cast<const float2*>(part + static_cast<long long>(c) * tile_rows * D);
+      const float2 x = *reinterpret_cast<const float2*>(part + slot(c) * D);
       acc[0] = fmaf(f, x.x, acc[0]), acc[1] = fmaf(f, x.y, acc[1]);
     }
   }

@@ -1453,6 +1453,8 @@ int launch_status() {
 // How a decode call is laid out: query rows in tiles of 8 (NT = 1) or 16, and either one CTA per
 // (sequence, kv head, row tile), or a fixed number of CTAs sharing all their keys evenly with
 // partial results in the workspace.
+constexpr int kKv4MaxKeys = INT_MAX - 65536;   // key numbers past the last unit's fit an int
+
 struct Kv4Plan {
   int nt, row_tiles, ctas, cluster;
   bool stream_k;
@@ -1482,7 +1484,7 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   pl.stream_k = rounds > (!filled ? 6 : pl.cluster > 1 ? 8 : 16);
   if (pl.stream_k) pl.cluster = 1;
   const size_t tile = static_cast<size_t>(8 * pl.nt);
-  const size_t slots = pl.stream_k ? static_cast<size_t>(pl.ctas + pl.segments) : 0;
+  const size_t slots = pl.stream_k ? static_cast<size_t>(2 * pl.ctas) : 0;
   pl.part_o = 0;
   pl.part_ml = align_up(slots * tile * D * 4, 256);
   pl.lse2 = pl.part_ml + align_up(slots * tile * 8, 256);
@@ -1598,7 +1600,8 @@ int pasa_kv4_read(const void* k4, const void* kscale, const void* v4, const void
 }
 
 size_t pasa_attn_fwd_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int weights) {
-  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Sq <= 0 || Sk <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
+  if (B <= 0 || Hq <= 0 || Hkv <= 0 || Sq <= 0 || Sk <= 0 || Hq % Hkv != 0 || Sk > kKv4MaxKeys || (D != 64 && D != 128))
+    return 0;
   if (static_cast<long long>(Hq / Hkv) * Sq > pasa::kTileRows) return 0;
   return kv4_plan(B, Hq, Hkv, Sq, Sk, D, weights != 0).total;
 }
@@ -1611,7 +1614,7 @@ static int kv4_decode_check(const void* q, const void* k4, const void* kscale, c
   if (!q || !o) return PASA_ERR_NULLPTR;
   const int rc = kv4_validate(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
   if (rc != PASA_OK) return rc;
-  if (Hq <= 0 || Sq <= 0 || Sk <= 0 || Hq % Hkv != 0 || Sk_cap < Sk) return PASA_ERR_SHAPE;
+  if (Hq <= 0 || Sq <= 0 || Sk <= 0 || Hq % Hkv != 0 || Sk_cap < Sk || Sk > kKv4MaxKeys) return PASA_ERR_SHAPE;
   if (static_cast<long long>(Hq / Hkv) * Sq > pasa::kTileRows) return PASA_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(weights) || !aligned4(lengths))
     return PASA_ERR_ALIGN;

@@ -125,7 +125,7 @@ def test_decode_refusals(lib):
     for name in ("q", "k4", "ks", "v4", "vs", "o", "lse", "shift", "weights"):
         assert dec(**{name: MIS16}) == -4
     assert dec(lengths=MIS4) == -4
-    for bad in ({"B": 0}, {"Hq": 0}, {"Hkv": 0}, {"Hq": 7}, {"Sq": 0}, {"Sk": 0}, {"cap": 49999}):
+    for bad in ({"B": 0}, {"Hq": 0}, {"Hkv": 0}, {"Hq": 7}, {"Sq": 0}, {"Sk": 0}, {"cap": 49999}, {"Sk": 2 ** 31 - 1, "cap": 2 ** 31 - 1}):
         assert dec(**bad, nbytes=1 << 30) == -2, bad
     assert dec(D=96, nbytes=1 << 30) == -3
     assert dec(Sq=33, nbytes=1 << 30) == -3                           # 4 heads x 33 rows
