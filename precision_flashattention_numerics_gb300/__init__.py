@@ -683,45 +683,51 @@ def attn_fwd_decode_step_kv4(q, k, v, k4, kscale, v4, vscale, start, causal: boo
 def cache_evict(planes, weights, budget: int, recent: int = 0, length: int | None = None, lengths=None, out=None,
                 out_weights=None, index=None, new_lengths=None):
     """Keep `budget` rows of every sequence that has more: per kv head the last `recent` and the
-    heaviest of the others, in their old order (pasa_cache_evict). planes: the cache's tensors
+    heaviest of the others, in their old order (pasa_cache_evict). planes: a list of the cache's tensors
     [B,Hkv,cap,*], e.g. (k4, kscale, v4, vscale) or fp16 (k, v); weights fp32 [B,Hkv,cap]. The
     sequences hold `length` rows (default cap) or lengths[b] (int32 [B]). In place, or into out (tensors
     [B,Hkv,out_cap,*]) and out_weights (fp32 [B,Hkv,out_cap]). Returns (index int32 [B,Hkv,budget]:
     the old rows, -1 past the last; new_lengths int32 [B])."""
     dev, stream = _here()
-    planes, budget, recent = list(planes), _int32(budget, "budget"), _int32(recent, "recent")
+    budget, recent = _int32(budget, "budget"), _int32(recent, "recent")
     if not isinstance(weights, torch.Tensor) or weights.dim() != 3:
         raise ValueError("expected weights [B,Hkv,cap]")
     if (out is None) != (out_weights is None):
         raise ValueError("out and out_weights go together")
-    out, out_weights = (planes, weights) if out is None else (list(out), out_weights)
-    if not isinstance(out_weights, torch.Tensor) or out_weights.dim() != 3 or len(out) != len(planes):
+    if out is None:
+        out, out_weights = planes, weights
+    count = len(planes)
+    if not isinstance(out_weights, torch.Tensor) or out_weights.dim() != 3 or len(out) != count:
         raise ValueError("expected out_weights [B,Hkv,out_cap] and as many out tensors as planes")
     B, Hkv, cap = weights.shape
     out_cap = out_weights.shape[2]
     Sk = cap if length is None else _int32(length, "length")
     wp = _check_cuda(weights, "weights", torch.float32, (B, Hkv, cap), dev)
-    owp = _check_cuda(out_weights, "out_weights", torch.float32, (B, Hkv, out_cap), dev)
+    owp = wp if out_weights is weights else _check_cuda(out_weights, "out_weights", torch.float32, (B, Hkv, out_cap), dev)
     src, dst, nbytes = [], [], []
-    for i, (a, b) in enumerate(zip(planes, out)):
+    for a, b in zip(planes, out):
         if not isinstance(a, torch.Tensor) or a.dim() != 4:
             raise ValueError("expected planes [B,Hkv,cap,*]")
         dtype, n = a.dtype, a.shape[3]
-        src.append(_check_cuda(a, f"planes[{i}]", dtype, (B, Hkv, cap, n), dev))
-        dst.append(src[-1] if a is b else _check_cuda(b, f"out[{i}]", dtype, (B, Hkv, out_cap, n), dev))
+        ap = _check_cuda(a, "a plane", dtype, (B, Hkv, cap, n), dev)
+        src.append(ap)
+        dst.append(ap if a is b else _check_cuda(b, "an out tensor", dtype, (B, Hkv, out_cap, n), dev))
         nbytes.append(n * dtype.itemsize)
-    # the C arrays planes and out_planes, one behind the other, and row_bytes
-    count = len(planes)
-    table = array.array("q", src + dst)
-    rows = array.array("i", nbytes)
-    at = table.buffer_info()[0]
     np_ = None if lengths is None else _check_cuda(lengths, "lengths", torch.int32, (B,), dev)
+    shape = (B, Hkv, budget if budget > 0 else 0)
     if index is None:
-        index = torch.empty((B, Hkv, max(budget, 0)), device=dev, dtype=torch.int32)
+        index = torch.empty(shape, device=dev, dtype=torch.int32)
+        ip = index.data_ptr()
+    else:
+        ip = _check_cuda(index, "index", torch.int32, shape, dev)
     if new_lengths is None:
-        new_lengths = torch.empty((B,), device=dev, dtype=torch.int32) if np_ is None else torch.empty_like(lengths)
-    ip = _check_cuda(index, "index", torch.int32, (B, Hkv, max(budget, 0)), dev)
-    nlp = _check_cuda(new_lengths, "new_lengths", torch.int32, (B,), dev)
+        new_lengths = torch.empty((B,), device=dev, dtype=torch.int32)
+        nlp = new_lengths.data_ptr()
+    else:
+        nlp = _check_cuda(new_lengths, "new_lengths", torch.int32, (B,), dev)
+    # the C arrays planes and out_planes, one behind the other, and row_bytes
+    table, rows = array.array("q", src + dst), array.array("i", nbytes)
+    at = table.buffer_info()[0]
     rc = library().pasa_cache_evict(at, at + 8 * count, rows.buffer_info()[0], count, wp, owp, np_, ip, nlp, B, Hkv, Sk,
                                     cap, out_cap, budget, recent, stream)
     if rc != 0:
