@@ -1718,6 +1718,10 @@ int pasa_cache_evict(const void* const* planes, void* const* out_planes, const i
     if (!aligned16(planes[i]) || !aligned16(out_planes[i])) return PASA_ERR_ALIGN;
     in_place |= planes[i] == out_planes[i];
     apart |= planes[i] != out_planes[i];
+    // a plane listed twice would be moved by two CTAs at once
+    if (out_planes[i] == static_cast<void*>(out_weights)) return PASA_ERR_SHAPE;
+    for (int j = 0; j < i; ++j)
+      if (out_planes[i] == out_planes[j]) return PASA_ERR_SHAPE;
   }
   // a cache moves in place as a whole, in a cache of the same size
   if (in_place && (apart || out_cap != Sk_cap)) return PASA_ERR_SHAPE;

@@ -48,6 +48,7 @@ CASES = [
     (1, 2, 40000, 40000, 4200, 4096, 128, None, "ties"),
     (1, 1, 70001, 70001, 70001, 30011, 1, None, "plain"),
     (2, 2, 50, 60, 200, 100, 3, [50, 20], "plain"),          # a budget that nothing reaches
+    (20, 4, 8300, 8300, 700, 512, 30, None, "ties"),         # many heads: a CTA for each, in two chunks
 ]
 
 

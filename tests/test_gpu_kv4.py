@@ -290,6 +290,32 @@ def test_offsets_past_32_bits():
     del cache, w
 
 
+def test_more_heads_than_a_grid_dimension_and_no_lse():
+    """70000 sequences of two rows, their outputs without a log-sum-exp (the C ABI's NULL)."""
+    B, D = 70000, 64
+    rng = np.random.default_rng(4)
+    k, v = rows(rng, B, 1, 2, D, "plain"), rows(rng, B, 1, 2, D, "plain")
+    q = rng.standard_normal((B, 1, 1, D)).astype(np.float16)
+    cache = new_cache(B, 1, 2, D)
+    kt, vt, qt = to_dev(k, v, q)
+    p = pasa()
+    p.kv4_append(kt, vt, *cache)
+    kr, vr = (x.cpu().numpy().astype(np.float64) for x in p.kv4_read(*cache, 2))
+    assert np.array_equal(kr, kv4.values(*kv4.quantise(k))) and np.array_equal(vr, kv4.values(*kv4.quantise(v)))
+    o = torch.full_like(qt, 9)
+    rc = p.library().pasa_attn_fwd_decode_kv4(qt.data_ptr(), *(c.data_ptr() for c in cache), None, None, o.data_ptr(), None,
+                                              None, B, 1, 1, 1, 2, 2, D, 1, 0.0, None, 0,
+                                              torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    x = np.einsum("bid,bjd->bj", q[:, 0].astype(np.float64), kr[:, 0]) / 8
+    w = np.exp(x - x.max(1, keepdims=True))
+    w /= w.sum(1, keepdims=True)
+    want = np.einsum("bj,bjd->bd", w, vr[:, 0])
+    # P's and the output's rounding (2^-11 each of at most max|v|), scores within 2^-16 of |x| < 40
+    bound = np.abs(vr[:, 0]).max(1) * (2.0 ** -10 + 40 * 2.0 ** -15)
+    assert (np.abs(o[:, 0, 0].cpu().numpy() - want) <= bound).all()
+
+
 # ---- streams, graphs, workspaces ----
 
 def small(B=3, Hq=14, H=2, Sk=2600, D=128, seed=0):
@@ -316,6 +342,37 @@ def test_calls_in_a_row_on_one_workspace_and_on_another_stream():
     side.synchronize()
     for i, (o, lse) in enumerate(got):
         assert torch.equal(o, want[i % 3][0]) and torch.equal(lse, want[i % 3][1])
+
+
+def test_two_threads_on_two_streams():
+    """Calls of all kinds at once, each thread on a stream of its own: equal to calls one by one."""
+    import threading
+
+    p = pasa()
+    sets = [small(seed=7, Sk=30000, B=2, D=64), small(seed=8, Sk=1500)]
+    want = [p.attn_fwd_decode_kv4(q, *c, shift=s) for q, c, s in sets]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            q, c, s = sets[i]
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got[i].append(p.attn_fwd_decode_kv4(q, *c, shift=s))
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:   # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
 
 
 @pytest.mark.parametrize("D", [64, 128])

@@ -157,7 +157,7 @@ def test_step_refusals(lib):
 
 
 def test_evict_refusals(lib):
-    def evict(planes=(FAKE, FAKE), out=(FAKE * 2, FAKE * 2), rb=(64, 8), n=None, w=FAKE, ow=FAKE * 2, lengths=0,
+    def evict(planes=(FAKE, FAKE * 3), out=(FAKE * 2, FAKE * 4), rb=(64, 8), n=None, w=FAKE * 5, ow=FAKE * 6, lengths=0,
               index=FAKE, new=0, B=1, H=2, Sk=64, cap=64, out_cap=32, budget=32, recent=4):
         p = lambda x: P(x) if x else None   # noqa: E731
         k = max(len(planes), len(out))
@@ -176,10 +176,13 @@ def test_evict_refusals(lib):
                 {"lengths": MIS4}, {"new": MIS4}):
         assert evict(**bad) == -4, bad
     # in place: everything, and in a cache of the same size
-    same = {"out": (FAKE, FAKE), "ow": FAKE, "out_cap": 64}
+    same = {"out": (FAKE, FAKE * 3), "ow": FAKE * 5, "out_cap": 64}
     assert evict(**{**same, "out_cap": 32}) == -2
     assert evict(**{**same, "ow": FAKE * 2}) == -2
     assert evict(**{**same, "out": (FAKE, FAKE * 2)}) == -2
+    # two outputs in one place
+    assert evict(out=(FAKE * 2, FAKE * 2)) == -2 and evict(out=(FAKE * 2, FAKE * 6)) == -2
+    assert evict(**{**same, "planes": (FAKE, FAKE), "out": (FAKE, FAKE)}) == -2
     if not torch.cuda.is_available():
         assert evict(**same) in (-3, -5) and evict() in (-3, -5)   # nothing wrong but the device
 
