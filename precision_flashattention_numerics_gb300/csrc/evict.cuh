@@ -49,10 +49,22 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const float
   griddep_launch_dependents();
   const long long bh = blockIdx.x / cluster;
   const int rank = blockIdx.x % cluster;
-  const int len = lengths ? max(0, min(lengths[bh / Hkv], Sk)) : Sk;
   const float* w = weights + bh * cap;
   int* idx = index + bh * budget;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int part = (Sk + cluster - 1) / cluster;   // rows of a CTA, by Sk: its loads wait for no length
+  const int row0 = min(Sk, rank * part);
+  const int chunks = (part + kEvictChunk - 1) / kEvictChunk;
+  const int per = chunks > 1 ? kEvictPer : (part + kEvictThreads - 1) / kEvictThreads;   // elements of a lane
+  uint32_t k[kEvictPer];                // element i: row `first` + 32 i of the chunk at hand
+  const int first = row0 + warp * (32 * per) + lane;
+  auto fetch = [&](int chunk) {   // the weights' bits, without branches between the loads
+    const int base = chunk * kEvictChunk + first;
+#pragma unroll
+    for (int i = 0; i < kEvictPer; ++i) k[i] = __float_as_uint(__ldg(w + (i < per ? min(base + 32 * i, Sk - 1) : 0)));
+  };
+  fetch(0);
+  const int len = lengths ? max(0, min(lengths[bh / Hkv], Sk)) : Sk;
   if (len <= budget) {   // all CTAs of the cluster
     for (int j = rank * kEvictThreads + tid; j < budget; j += cluster * kEvictThreads) idx[j] = j < len ? j : -1;
     return;
@@ -60,18 +72,9 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const float
   constexpr uint32_t kZero = 0x80000000u, kNone = 0u, kRecent = 0xFFFFFFFFu;
   uint32_t left = budget;               // of the keys that match `prefix` so far, how many stay
   uint32_t prefix = 0;                  // the budget-th largest key
-  const int part = (len + cluster - 1) / cluster;              // rows of a CTA
-  const int row0 = min(len, rank * part), row1 = min(len, row0 + part);
-  const int chunks = (part + kEvictChunk - 1) / kEvictChunk;
-  const int per = chunks > 1 ? kEvictPer : (part + kEvictThreads - 1) / kEvictThreads;   // elements of a lane
-  uint32_t k[kEvictPer];                // element i: row `first` + 32 i of the chunk at hand
-  const int first = row0 + warp * (32 * per) + lane;
-  auto load = [&](int chunk) {
+  const int row1 = min(len, row0 + part);
+  auto to_keys = [&](int chunk) {
     const int base = chunk * kEvictChunk + first;
-    // all loads first, without branches between them
-#pragma unroll
-    for (int i = 0; i < kEvictPer; ++i)
-      k[i] = __float_as_uint(__ldg(w + (i < per ? min(base + 32 * i, len - 1) : 0)));
 #pragma unroll
     for (int i = 0; i < kEvictPer; ++i) {
       const int j = base + 32 * i;
@@ -79,7 +82,11 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const float
       k[i] = i >= per || j >= row1 ? kNone : j >= len - recent ? kRecent : key;
     }
   };
-  load(0);
+  auto load = [&](int chunk) {
+    fetch(chunk);
+    to_keys(chunk);
+  };
+  to_keys(0);
   for (int i = tid; i < 3 * kEvictBins / 4; i += kEvictThreads) reinterpret_cast<uint4*>(hist[0])[i] = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
 #pragma unroll 1

@@ -355,10 +355,13 @@ __device__ __forceinline__ void kv4_score_group16(float (&acc)[4], int w, uint32
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(qa.x), "r"(qa.y), "r"(qa.z), "r"(qa.w), "r"(k & lo), "r"(k8 & lo), "f"(start.x), "f"(start.y));
   mma_f16(d, qb.x, qb.y, qb.z, qb.w, k & hi, k8 & hi);
-  acc[0] = w == 0 ? s0 * d[0] : fmaf(s0, d[0], acc[0]);
-  acc[1] = w == 0 ? s1 * d[1] : fmaf(s1, d[1], acc[1]);
-  acc[2] = w == 0 ? s0 * d[2] : fmaf(s0, d[2], acc[2]);
-  acc[3] = w == 0 ? s1 * d[3] : fmaf(s1, d[3], acc[3]);
+  if (w == 0) {
+    fmul2(acc[0], acc[1], d[0], d[1], s0, s1);
+    fmul2(acc[2], acc[3], d[2], d[3], s0, s1);
+  } else {
+    ffma2(acc[0], acc[1], d[0], d[1], s0, s1, acc[0], acc[1]);
+    ffma2(acc[2], acc[3], d[2], d[3], s0, s1, acc[2], acc[3]);
+  }
 }
 
 // One stage of a warp: 32 rows of key and value codes and their scales. Where a lane needs keys by
@@ -575,7 +578,8 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
-    float m[2] = {kKv4NoKey, kKv4NoKey}, l[2] = {0.0f, 0.0f};   // of the lane's two rows
+    // of the lane's two rows; with 16 rows the sums of even and odd keys apart
+    float m[2] = {kKv4NoKey, kKv4NoKey}, l[2 * NT] = {};
     const int all_see = p.causal ? max(0, len - p.Sq + 1) : len;   // keys that every row sees
     uint32_t odd = 0;   // the stage at hand
     for (; u < u1; u += u_step) {
@@ -653,7 +657,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
           x = fmaxf(x, m[c]);
           const float f = ex2_approx(m[c] - x);
           m[c] = x;
-          l[c] *= f;
+          if (NT == 1) l[c] *= f; else l[NT * c] *= f, l[NT * c + NT - 1] *= f;
 #pragma unroll
           for (int i = 0; i < kTiles; ++i) {
             o[i][NT == 1 ? c : 2 * c] *= f;
@@ -665,12 +669,23 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
       uint32_t pf[2][2 * NT];
 #pragma unroll
       for (int i = 0; i < 2 * NT; ++i) {
+        // pairs: NT = 1 (row 2t, row 2t + 1), NT = 2 two keys of row g, then of row g + 8
         float e[4];
+        if constexpr (NT == 1) {
+          ffma2(e[0], e[1], s[i][0], s[i][1], factor.x, factor.y, -m[0], -m[1]);
+          ffma2(e[2], e[3], s[i][2], s[i][3], factor.x, factor.y, -m[0], -m[1]);
+        } else {
+          ffma2(e[0], e[1], s[i][0], s[i][1], factor.x, factor.x, -m[0], -m[0]);
+          ffma2(e[2], e[3], s[i][2], s[i][3], factor.y, factor.y, -m[1], -m[1]);
+        }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const bool second = NT == 1 ? (c & 1) : c >= 2;
-          e[c] = ex2_approx(fmaf(s[i][c], second ? factor.y : factor.x, -(second ? m[1] : m[0])));
-          l[second ? 1 : 0] += e[c];
+        for (int c = 0; c < 4; ++c) e[c] = ex2_approx(e[c]);
+        if constexpr (NT == 1) {
+          fadd2(l[0], l[1], l[0], l[1], e[0], e[1]);
+          fadd2(l[0], l[1], l[0], l[1], e[2], e[3]);
+        } else {
+          fadd2(l[0], l[1], l[0], l[1], e[0], e[1]);
+          fadd2(l[2], l[3], l[2], l[3], e[2], e[3]);
         }
         const uint32_t p01 = h2_bits(__floats2half2_rn(e[0], e[1])), p23 = h2_bits(__floats2half2_rn(e[2], e[3]));
         if constexpr (NT == 1) {
@@ -710,7 +725,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
     // ---- join the warps ----
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float x = l[c];
+      float x = NT == 1 ? l[c] : l[NT * c] + l[NT * c + NT - 1];
 #pragma unroll
       for (int d = NT == 1 ? 4 : 1; d < (NT == 1 ? 32 : 4); d <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
       const int r = NT == 1 ? 2 * t + c : g + 8 * c;
