@@ -44,9 +44,12 @@
 
 namespace pasa {
 
-constexpr int kKv4Warps = 8;
+// Warps of a CTA and CTAs of an SM, by the tile's rows / 8: 2 x 8 warps of 128 registers, or with 16 rows, whose
+// accumulators take twice as many, 1 x 12 of 168 (16 rows x 131072 keys x 8: 145 us; 2 x 8, which spill, 159).
+__host__ __device__ constexpr int kv4_warps(int nt) { return nt == 1 ? 8 : 12; }
+__host__ __device__ constexpr int kv4_ctas(int nt) { return nt == 1 ? 304 : 152; }   // on 152 SMs
+constexpr int kKv4WeightsWarps = 8;
 constexpr int kKv4Unit = 32;    // keys a warp takes at a time
-constexpr int kKv4MaxCtas = 304;       // two CTAs on each of 152 SMs
 constexpr int kKv4SegmentStart = 2;    // rounds that the start and end of a segment cost a CTA
 
 struct Kv4Params {
@@ -84,8 +87,9 @@ __device__ __forceinline__ int kv4_units(int len) { return (len + kKv4Unit - 1) 
 
 // A segment's weight when segments are shared out: its rounds (a unit for each warp of a CTA: what
 // is shared is whole rounds, so that no warp idles in the middle), and kKv4SegmentStart.
-__device__ __forceinline__ int kv4_weight(int units) {
-  return units == 0 ? 0 : (units + kKv4Warps - 1) / kKv4Warps + kKv4SegmentStart;
+__device__ __forceinline__ int kv4_rounds(int units, int warps) { return (units + warps - 1) / warps; }
+__device__ __forceinline__ int kv4_weight(int units, int warps) {
+  return units == 0 ? 0 : kv4_rounds(units, warps) + kKv4SegmentStart;
 }
 
 // The weights of all sequences (per kv head and row tile), looked at by a whole warp: their sum, the
@@ -94,12 +98,15 @@ __device__ __forceinline__ int kv4_weight(int units) {
 // weights of a call fit an int (checked on the host).
 struct Kv4Lengths {
   const Kv4Params& p;
+  int warps;       // of a CTA
   int len, upto;   // lane l: length l of the first 32, and their weights up to it
-  __device__ __forceinline__ explicit Kv4Lengths(const Kv4Params& params) : p(params) { block(0, len, upto); }
+  __device__ __forceinline__ Kv4Lengths(const Kv4Params& params, int cta_warps) : p(params), warps(cta_warps) {
+    block(0, len, upto);
+  }
   __device__ __forceinline__ void block(int b0, int& l, int& sum) const {
     const int lane = threadIdx.x & 31;
     l = b0 + lane < p.B ? p.length(b0 + lane) : 0;
-    sum = kv4_weight(kv4_units(l));
+    sum = kv4_weight(kv4_units(l), warps);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int x = __shfl_up_sync(0xFFFFFFFFu, sum, d);
@@ -124,7 +131,7 @@ struct Kv4Lengths {
       if (past != 0) {
         const int lane = __ffs(past) - 1;
         length = __shfl_sync(0xFFFFFFFFu, l, lane);
-        place -= (__shfl_sync(0xFFFFFFFFu, s, lane) - kv4_weight(kv4_units(length))) * per_b;
+        place -= (__shfl_sync(0xFFFFFFFFu, s, lane) - kv4_weight(kv4_units(length), warps)) * per_b;
         return b0 + lane;
       }
       place -= __shfl_sync(0xFFFFFFFFu, s, 31) * per_b;
@@ -435,13 +442,13 @@ constexpr float kKv4NoKey = -3.0e38f;   // a running maximum before the first ke
 template <int D, int NT>
 struct Kv4Smem {
   union {
-    Kv4Stage<D, true> stage[2][kKv4Warps];
-    float o[kKv4Warps][NT * 8][D + 4];   // when the stages are empty
+    Kv4Stage<D, true> stage[2][kv4_warps(NT)];
+    float o[kv4_warps(NT)][NT * 8][D + 4];   // when the stages are empty
   };
   Kv4Query16<D> q;                       // NT = 2
   float sum[NT * 8][D];                  // the CTA's O, maxima and sums, read by its cluster
   float2 sum_ml[NT * 8];
-  float2 ml[kKv4Warps][NT * 8];
+  float2 ml[kv4_warps(NT)][NT * 8];
   float offset[NT * 8];
   int limit[NT * 8];                     // keys a row sees
 };
@@ -474,11 +481,12 @@ __device__ __forceinline__ void kv4_finish(const Kv4Params& p, long long out, lo
 }
 
 template <int D, int NT, bool STREAM_K>
-__global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params p) {
+__global__ void __launch_bounds__(kv4_warps(NT) * 32, kv4_ctas(NT) / 152) kv4_decode_kernel(Kv4Params p) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   Kv4Smem<D, NT>& sm = *reinterpret_cast<Kv4Smem<D, NT>*>(smem_raw);
   constexpr int kRows = NT * 8;
-  constexpr int kThreads = kKv4Warps * 32;
+  constexpr int kWarps = kv4_warps(NT);
+  constexpr int kThreads = kWarps * 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int rank = STREAM_K ? 0 : static_cast<int>(blockIdx.x % p.cluster);
@@ -490,7 +498,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
   int in_b = 0;   // segment inside sequence b: h * row_tiles + row tile
   const int per_b = p.Hkv * p.row_tiles;
   if (STREAM_K) {
-    const Kv4Lengths lengths(p);
+    const Kv4Lengths lengths(p, kWarps);
     const int total = lengths.sum(p.B) * per_b;
     const int ctas = min(total, static_cast<int>(gridDim.x));
     if (static_cast<int>(blockIdx.x) >= ctas) {
@@ -502,7 +510,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
     todo = share.first(blockIdx.x + 1) - place;
     b = lengths.find(place, per_b, len);
     n_units = kv4_units(len);
-    const int weight = kv4_weight(n_units);
+    const int weight = kv4_weight(n_units, kWarps);
     in_b = place / weight;
     r0 = place - in_b * weight - kKv4SegmentStart;   // its first rounds stand for its start
   } else {
@@ -521,18 +529,18 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
     const int n_rows = min(kRows, p.rows - row0);
     int u0 = 0, u1 = n_units;
     if (STREAM_K) {
-      const int r1 = min((n_units + kKv4Warps - 1) / kKv4Warps, r0 + todo);
+      const int r1 = min(kv4_rounds(n_units, kWarps), r0 + todo);
       todo -= r1 - r0;
-      u0 = max(0, r0) * kKv4Warps;
-      u1 = min(n_units, r1 * kKv4Warps);
+      u0 = max(0, r0) * kWarps;
+      u1 = min(n_units, r1 * kWarps);
       if (u0 >= u1) return;   // the range ends in what a segment's start weighs
     }
-    const int u_step = STREAM_K ? kKv4Warps : kKv4Warps * p.cluster;
+    const int u_step = STREAM_K ? kWarps : kWarps * p.cluster;
 
     // ---- the warp's share of units u0 .. u1 ----
-    int u = u0 + rank * kKv4Warps + warp;
+    int u = u0 + rank * kWarps + warp;
     const uint32_t stage0 = smem_u32(&sm.stage[0][warp]);
-    constexpr uint32_t kStageBytes = sizeof(Kv4Stage<D, true>) * kKv4Warps, kValues = kKv4Unit * D / 2;
+    constexpr uint32_t kStageBytes = sizeof(Kv4Stage<D, true>) * kWarps, kValues = kKv4Unit * D / 2;
     uint2 ks = make_uint2(0u, 0u), vs = make_uint2(0u, 0u);   // row scales of the unit last fetched
     auto fetch = [&](int unit, uint32_t stage) {
       if (unit < u1) {
@@ -565,7 +573,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
     if (threadIdx.x < kRows) sm.limit[threadIdx.x] = p.limit(row0 + threadIdx.x, len);
     const bool whole = u0 == 0 && u1 == n_units;   // the CTA, or its cluster, has all of the segment
     if (whole && rank == 0 && p.lse)
-      for (int r = warp; r < n_rows; r += kKv4Warps) {
+      for (int r = warp; r < n_rows; r += kWarps) {
         const float off = kv4_offset<D>(p, bh, row0 + r, lane);
         if (lane == 0) sm.offset[r] = off;
       }
@@ -752,16 +760,16 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
     // a thread: 4 channels of a row, the row's maximum and sum with them
     for (int idx = threadIdx.x; idx < n_rows * (D / 4); idx += kThreads) {
       const int r = idx / (D / 4), ch = idx % (D / 4) * 4;
-      float2 ml[kKv4Warps];
+      float2 ml[kWarps];
       float mm = kKv4NoKey, ll = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kKv4Warps; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         ml[w] = sm.ml[w][r];
         mm = fmaxf(mm, ml[w].x);
       }
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < kKv4Warps; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float f = ex2_approx(ml[w].x - mm);   // a warp without a key of this row has sum 0
         const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][r][ch]);
         ll = fmaf(f, ml[w].y, ll);
@@ -828,7 +836,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_decode_kernel(Kv4Params
 // the rows of sequences without a key. One CTA per (segment, row).
 template <int D>
 __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_rows) {
-  __shared__ float so[8][D], factor[kKv4MaxCtas];
+  __shared__ float so[8][D], factor[kv4_ctas(1)];
   __shared__ float s_m[8], s_l[8], s_off;
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -838,7 +846,8 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
   const long long in_b = seg % per_b;
   const long long bh = static_cast<long long>(b) * p.Hkv + in_b / p.row_tiles;
   const int r = blockIdx.y, row = static_cast<int>(in_b % p.row_tiles) * tile_rows + r;
-  const Kv4Lengths lengths(p);
+  const int warps = kv4_warps(tile_rows / 8);
+  const Kv4Lengths lengths(p, warps);
   // every CTA waits for the decode, also those without work: a kernel behind this one waits for
   // this one only
   if (row >= p.rows) {
@@ -856,7 +865,7 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
     }
     return;
   }
-  const int weight = kv4_weight(n_units);
+  const int weight = kv4_weight(n_units, warps);
   const int total = lengths.sum(p.B) * static_cast<int>(per_b);
   const Kv4Share share(total, min(total, p.ctas));
   const int t0 = lengths.sum(b) * static_cast<int>(per_b) + static_cast<int>(in_b) * weight;
@@ -871,7 +880,7 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
   }
   griddep_wait();   // the partials
   // every partial's max and sum at once, then its factor
-  constexpr int kMine = (kKv4MaxCtas + 255) / 256;
+  constexpr int kMine = (kv4_ctas(1) + 255) / 256;
   // the row's partial of CTA c0 + i: that of its first segment, but c0 may have begun with another one
   const int begun = share.first(c0) < t0 ? 1 : 0;
   auto slot = [&](int i) { return (2ll * (c0 + i) + (i == 0 ? begun : 0)) * tile_rows + r; };
@@ -941,19 +950,19 @@ __global__ void __launch_bounds__(256) kv4_merge_kernel(Kv4Params p, int tile_ro
 // per 32-key unit, each weight summed and stored by one lane: the same order every time.
 template <int D>
 struct Kv4WeightsSmem {
-  Kv4Stage<D, false> stage[2][kKv4Warps];
+  Kv4Stage<D, false> stage[2][kKv4WeightsWarps];
   float ref[128];            // a row's log2-sum-exp2
   int limit[128];
   Kv4QueryShared<D> q[16];   // as many as the rows have tiles of 8
 };
 
 template <int D>
-__global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Params p, int tile_rows) {
+__global__ void __launch_bounds__(kKv4WeightsWarps * 32, 2) kv4_weights_kernel(Kv4Params p, int tile_rows) {
   extern __shared__ __align__(128) unsigned char smem_raw[];
   Kv4WeightsSmem<D>& sm = *reinterpret_cast<Kv4WeightsSmem<D>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const Kv4Lengths lengths(p);
+  const Kv4Lengths lengths(p, kKv4WeightsWarps);
   const int total = lengths.sum(p.B) * p.Hkv;
   const int ctas = min(total, static_cast<int>(gridDim.x));
   if (static_cast<int>(blockIdx.x) >= ctas) {
@@ -964,20 +973,20 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
   int place = share.first(blockIdx.x), todo = share.first(blockIdx.x + 1) - place, len;
   int b = lengths.find(place, p.Hkv, len);
   int n_units = kv4_units(len);
-  int h = place / kv4_weight(n_units);
-  int r0 = place - h * kv4_weight(n_units) - kKv4SegmentStart;
+  int h = place / kv4_weight(n_units, kKv4WeightsWarps);
+  int r0 = place - h * kv4_weight(n_units, kKv4WeightsWarps) - kKv4SegmentStart;
   griddep_wait();   // lse2
   const uint64_t policy = evict_first_policy();
   while (true) {
     const long long bh = static_cast<long long>(b) * p.Hkv + h;
-    const int r1 = min((n_units + kKv4Warps - 1) / kKv4Warps, r0 + todo);
+    const int r1 = min(kv4_rounds(n_units, kKv4WeightsWarps), r0 + todo);
     todo -= r1 - r0;
-    const int u0 = max(0, r0) * kKv4Warps, u1 = min(n_units, r1 * kKv4Warps);
+    const int u0 = max(0, r0) * kKv4WeightsWarps, u1 = min(n_units, r1 * kKv4WeightsWarps);
     if (u0 >= u1) return;
     const uint8_t* k4 = p.k4 + bh * p.cap * (D / 2);
     const __half* kscale = p.kscale + bh * p.cap * (D / 32);
     const uint32_t stage0 = smem_u32(&sm.stage[0][warp]);
-    constexpr uint32_t kStageBytes = sizeof(Kv4Stage<D, false>) * kKv4Warps;
+    constexpr uint32_t kStageBytes = sizeof(Kv4Stage<D, false>) * kKv4WeightsWarps;
     uint2 ks = make_uint2(0u, 0u);
     auto fetch = [&](int unit, uint32_t stage) {
       if (unit < u1) {
@@ -989,7 +998,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
       cp_async_commit();
     };
     int u = u0 + warp;
-    for (int i = warp; i * 8 < p.rows; i += kKv4Warps) {
+    for (int i = warp; i * 8 < p.rows; i += kKv4WeightsWarps) {
       Kv4Query<D> q;
       uint4 raw[D / 32];
       Kv4Query<D>::raw(raw, p.q + (bh * p.rows + i * 8) * D, p.rows - i * 8, lane);
@@ -998,7 +1007,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
       sm.q[i].put(q, lane);
     }
     if (warp * 8 >= p.rows) fetch(u, stage0);
-    for (int r = threadIdx.x; r < (p.rows + 7) / 8 * 8; r += kKv4Warps * 32) {
+    for (int r = threadIdx.x; r < (p.rows + 7) / 8 * 8; r += kKv4WeightsWarps * 32) {
       // a row past the last, or without a key, weighs nothing
       sm.ref[r] = r < p.rows ? p.lse2[(bh * p.row_tiles + r / tile_rows) * tile_rows + r % tile_rows] : INFINITY;
       sm.limit[r] = p.limit(r, len);
@@ -1006,7 +1015,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
     __syncthreads();
     const int all_see = p.causal ? max(0, len - p.Sq + 1) : len;
     uint32_t odd = 0;
-    for (; u < u1; u += kKv4Warps) {
+    for (; u < u1; u += kKv4WeightsWarps) {
       const int key0 = u * kKv4Unit;
       auto& st = sm.stage[odd][warp];
       const uint32_t here = stage0 + odd * kStageBytes;
@@ -1014,7 +1023,7 @@ __global__ void __launch_bounds__(kKv4Warps * 32, 2) kv4_weights_kernel(Kv4Param
       kv4_put_scales<D, false, false>(st, ks, ks, lane);
       __syncwarp();
       odd ^= 1;
-      fetch(u + kKv4Warps, stage0 + odd * kStageBytes);
+      fetch(u + kKv4WeightsWarps, stage0 + odd * kStageBytes);
       const bool masked = key0 + kKv4Unit > all_see;
       const int key = key0 + g + 8 * t;   // the lane's weight
       float* weight = p.weights + bh * p.cap + key;

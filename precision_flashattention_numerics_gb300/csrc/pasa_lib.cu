@@ -1469,17 +1469,18 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   pl.nt = rows <= 8 ? 1 : 2;
   pl.row_tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
   pl.segments = static_cast<long long>(B) * Hkv * pl.row_tiles;
-  pl.ctas = pasa::kKv4MaxCtas;
+  pl.ctas = pasa::kv4_ctas(pl.nt);
   const int units = (Sk + pasa::kKv4Unit - 1) / pasa::kKv4Unit;
   pl.cluster = 1;
-  while (pl.cluster < 8 && pl.segments * pl.cluster * 2 <= pl.ctas && units > pasa::kKv4Warps * pl.cluster) pl.cluster *= 2;
+  const int warps = pasa::kv4_warps(pl.nt);
+  while (pl.cluster < 8 && pl.segments * pl.cluster * 2 <= pl.ctas && units > warps * pl.cluster) pl.cluster *= 2;
   // A cluster per segment needs one launch and no workspace, but few segments leave SMs idle, and an
   // uneven batch waits for its longest sequence. GPU us with 4 kv heads, 7 rows, D = 128, cluster against
   // stream-K, by sequences, keys and rounds of a warp: 1 x 8192 (4) 9.0 / 8.6, 1 x 12288 (6) 11.1 / 9.2,
   // 1 x 16384 (8) 13.6 / 9.4, where the launches that stream-K adds cost the host 8 us; with the SMs
   // filled 8 x 8192 (4) 14.2 / 16.3, 8 x 32768 (16) 36.1 / 35.2, and without clusters (their segments
   // follow one another as SMs get free) 64 x 2048 (8) 20.3 / 30.1, 64 x 4096 (16) 35.2 / 43.1.
-  const int rounds = (units + pasa::kKv4Warps * pl.cluster - 1) / (pasa::kKv4Warps * pl.cluster);
+  const int rounds = (units + warps * pl.cluster - 1) / (warps * pl.cluster);
   const bool filled = pl.segments * pl.cluster * 4 >= pl.ctas * 3;
   pl.stream_k = rounds > (!filled ? 6 : pl.cluster > 1 ? 8 : 16);
   if (pl.stream_k) pl.cluster = 1;
@@ -1535,7 +1536,7 @@ template <int D, int NT, bool STREAM_K>
 cudaError_t kv4_launch(const pasa::Kv4Params& p, unsigned grid, cudaStream_t st, bool pdl) {
   static std::atomic<unsigned long long> raised{0};
   constexpr int smem = static_cast<int>(sizeof(pasa::Kv4Smem<D, NT>));
-  return launch_clusters(pasa::kv4_decode_kernel<D, NT, STREAM_K>, grid, pasa::kKv4Warps * 32, smem, smem, st, pdl,
+  return launch_clusters(pasa::kv4_decode_kernel<D, NT, STREAM_K>, grid, pasa::kv4_warps(NT) * 32, smem, smem, st, pdl,
                          p.cluster, raised, p);
 }
 
@@ -1551,7 +1552,7 @@ cudaError_t kv4_decode_launch(const pasa::Kv4Params& p, const Kv4Plan& pl, cudaS
   if (e == cudaSuccess && p.weights) {
     const int smem = static_cast<int>(offsetof(pasa::Kv4WeightsSmem<D>, q) + sizeof(pasa::Kv4QueryShared<D>) * ((p.rows + 7) / 8));
     static std::atomic<unsigned long long> raised{0};
-    e = launch_clusters(pasa::kv4_weights_kernel<D>, static_cast<unsigned>(pl.ctas), pasa::kKv4Warps * 32, smem,
+    e = launch_clusters(pasa::kv4_weights_kernel<D>, pasa::kv4_ctas(1), pasa::kKv4WeightsWarps * 32, smem,
                         static_cast<int>(sizeof(pasa::Kv4WeightsSmem<D>)), st, true, 1, raised, p, tile);
   }
   return e;
