@@ -536,18 +536,32 @@ def _check_cuda(x, name: str, dtype, shape, device):
     raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
 
 
+_U8, _F16, _F32, _I32 = torch.uint8, torch.float16, torch.float32, torch.int32
+
+
 def _check_kv4(k4, kscale, v4, vscale, shift, device):
-    """The cache tensors' pointers, and (B, Hkv, cap, D)."""
+    """The cache tensors' pointers, and (B, Hkv, cap, D). All four in one expression: a call's
+    checks take as long as its launch."""
     if not isinstance(k4, torch.Tensor) or k4.dim() != 4:
         raise ValueError("expected k4 [B,Hkv,cap,D/2]")
-    B, Hkv, cap, half = k4.shape
-    codes, scales = (B, Hkv, cap, half), (B, Hkv, cap, half // 16)
-    ptrs = (_check_cuda(k4, "k4", torch.uint8, codes, device),
-            _check_cuda(kscale, "kscale", torch.float16, scales, device),
-            _check_cuda(v4, "v4", torch.uint8, codes, device),
-            _check_cuda(vscale, "vscale", torch.float16, scales, device))
-    sp = None if shift is None else _check_cuda(shift, "shift", torch.float16, (B, Hkv, 2 * half), device)
-    return ptrs, sp, (B, Hkv, cap, 2 * half)
+    codes = k4.shape
+    B, Hkv, cap, half = codes
+    scales = (B, Hkv, cap, half // 16)
+    try:
+        fine = (k4.dtype is _U8 and v4.dtype is _U8 and kscale.dtype is _F16 and vscale.dtype is _F16
+                and v4.shape == codes and kscale.shape == scales and vscale.shape == scales
+                and k4.get_device() == device and v4.get_device() == device
+                and kscale.get_device() == device and vscale.get_device() == device
+                and k4.is_contiguous() and v4.is_contiguous() and kscale.is_contiguous() and vscale.is_contiguous())
+    except AttributeError:
+        fine = False
+    if not fine:   # say which
+        _check_cuda(k4, "k4", _U8, codes, device)
+        _check_cuda(kscale, "kscale", _F16, scales, device)
+        _check_cuda(v4, "v4", _U8, codes, device)
+        _check_cuda(vscale, "vscale", _F16, scales, device)
+    sp = None if shift is None else _check_cuda(shift, "shift", _F16, (B, Hkv, 2 * half), device)
+    return (k4.data_ptr(), kscale.data_ptr(), v4.data_ptr(), vscale.data_ptr()), sp, (B, Hkv, cap, 2 * half)
 
 
 def _int32(x, name: str) -> int:
@@ -561,7 +575,7 @@ def _int32(x, name: str) -> int:
 def _per_sequence(x, name, B, device):
     """(pointer, value) of an argument that is one int or an int32 tensor [B]."""
     if isinstance(x, torch.Tensor):
-        return _check_cuda(x, name, torch.int32, (B,), device), 0
+        return _check_cuda(x, name, _I32, (B,), device), 0
     return None, _int32(x, name)
 
 
@@ -575,10 +589,10 @@ def kv4_append(k, v, k4, kscale, v4, vscale, start=0, counts=None, shift=None):
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("expected k, v [B,Hkv,n,D]")
     n = k.shape[2]
-    kp = _check_cuda(k, "k", torch.float16, (B, Hkv, n, D), dev)
-    vp = _check_cuda(v, "v", torch.float16, (B, Hkv, n, D), dev)
+    kp = _check_cuda(k, "k", _F16, (B, Hkv, n, D), dev)
+    vp = _check_cuda(v, "v", _F16, (B, Hkv, n, D), dev)
     starts, first = _per_sequence(start, "start", B, dev)
-    cp = None if counts is None else _check_cuda(counts, "counts", torch.int32, (B,), dev)
+    cp = None if counts is None else _check_cuda(counts, "counts", _I32, (B,), dev)
     rc = library().pasa_kv4_append(kp, vp, sp, *ptrs, starts, first, cp, B, Hkv, n, cap, D, stream)
     if rc != 0:
         raise PasaError(rc, "pasa_kv4_append")
@@ -595,10 +609,10 @@ def kv4_read(k4, kscale, v4, vscale, n: int, start=0, counts=None, shift=None, o
         out_k = new((B, Hkv, n, D), device=k4.device, dtype=torch.float16)
     if out_v is None:
         out_v = new((B, Hkv, n, D), device=k4.device, dtype=torch.float16)
-    kp = _check_cuda(out_k, "out_k", torch.float16, (B, Hkv, n, D), dev)
-    vp = _check_cuda(out_v, "out_v", torch.float16, (B, Hkv, n, D), dev)
+    kp = _check_cuda(out_k, "out_k", _F16, (B, Hkv, n, D), dev)
+    vp = _check_cuda(out_v, "out_v", _F16, (B, Hkv, n, D), dev)
     starts, first = _per_sequence(start, "start", B, dev)
-    cp = None if counts is None else _check_cuda(counts, "counts", torch.int32, (B,), dev)
+    cp = None if counts is None else _check_cuda(counts, "counts", _I32, (B,), dev)
     rc = library().pasa_kv4_read(*ptrs, sp, kp, vp, starts, first, cp, B, Hkv, n, cap, D, stream)
     if rc != 0:
         raise PasaError(rc, "pasa_kv4_read")
@@ -613,7 +627,7 @@ def decode_kv4_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: i
 def _decode_kv4_workspace(workspace, device, *sizes):
     """(workspace, bytes needed): the caller's, or a new one where that is none or too small."""
     if workspace is not None:
-        _check_cuda(workspace, "workspace", torch.uint8, None, device)
+        _check_cuda(workspace, "workspace", _U8, None, device)
     nbytes = decode_kv4_workspace_bytes(*sizes)
     if nbytes and (workspace is None or workspace.numel() < nbytes):
         workspace = torch.empty(nbytes, device=device, dtype=torch.uint8)
@@ -635,11 +649,11 @@ def attn_fwd_decode_kv4(q, k4, kscale, v4, vscale, causal: bool = False, scale: 
     Sk = cap if length is None else _int32(length, "length")
     out = torch.empty_like(q) if out is None else out
     lse = torch.empty((B, Hq, Sq), device=q.device, dtype=torch.float32) if lse is None else lse
-    qp = _check_cuda(q, "q", torch.float16, (B, Hq, Sq, D), dev)
-    op = _check_cuda(out, "out", torch.float16, (B, Hq, Sq, D), dev)
-    lp = _check_cuda(lse, "lse", torch.float32, (B, Hq, Sq), dev)
-    np_ = None if lengths is None else _check_cuda(lengths, "lengths", torch.int32, (B,), dev)
-    wp = None if weights is None else _check_cuda(weights, "weights", torch.float32, (B, Hkv, cap), dev)
+    qp = _check_cuda(q, "q", _F16, (B, Hq, Sq, D), dev)
+    op = _check_cuda(out, "out", _F16, (B, Hq, Sq, D), dev)
+    lp = _check_cuda(lse, "lse", _F32, (B, Hq, Sq), dev)
+    np_ = None if lengths is None else _check_cuda(lengths, "lengths", _I32, (B,), dev)
+    wp = None if weights is None else _check_cuda(weights, "weights", _F32, (B, Hkv, cap), dev)
     workspace, nbytes = _decode_kv4_workspace(workspace, dev, B, Hq, Hkv, Sq, Sk, D, weights is not None)
     rc = library().pasa_attn_fwd_decode_kv4(qp, *ptrs, sp, np_, op, lp, wp, B, Hq, Hkv, Sq, Sk, cap, D, int(bool(causal)),
                                       float(scale) if scale is not None else 0.0,
@@ -665,12 +679,12 @@ def attn_fwd_decode_step_kv4(q, k, v, k4, kscale, v4, vscale, start, causal: boo
     Sk = first + n if starts is None else cap if length is None else _int32(length, "length")
     out = torch.empty_like(q) if out is None else out
     lse = torch.empty((B, Hq, Sq), device=q.device, dtype=torch.float32) if lse is None else lse
-    qp = _check_cuda(q, "q", torch.float16, (B, Hq, Sq, D), dev)
-    kp = _check_cuda(k, "k", torch.float16, (B, Hkv, n, D), dev)
-    vp = _check_cuda(v, "v", torch.float16, (B, Hkv, n, D), dev)
-    op = _check_cuda(out, "out", torch.float16, (B, Hq, Sq, D), dev)
-    lp = _check_cuda(lse, "lse", torch.float32, (B, Hq, Sq), dev)
-    wp = None if weights is None else _check_cuda(weights, "weights", torch.float32, (B, Hkv, cap), dev)
+    qp = _check_cuda(q, "q", _F16, (B, Hq, Sq, D), dev)
+    kp = _check_cuda(k, "k", _F16, (B, Hkv, n, D), dev)
+    vp = _check_cuda(v, "v", _F16, (B, Hkv, n, D), dev)
+    op = _check_cuda(out, "out", _F16, (B, Hq, Sq, D), dev)
+    lp = _check_cuda(lse, "lse", _F32, (B, Hq, Sq), dev)
+    wp = None if weights is None else _check_cuda(weights, "weights", _F32, (B, Hkv, cap), dev)
     workspace, nbytes = _decode_kv4_workspace(workspace, dev, B, Hq, Hkv, Sq, Sk, D, weights is not None)
     rc = library().pasa_attn_fwd_decode_step_kv4(qp, kp, vp, *ptrs, sp, starts, first, op, lp, wp, B, Hq, Hkv, Sq, n, Sk,
                                                  cap, D, int(bool(causal)), float(scale) if scale is not None else 0.0,
@@ -702,8 +716,8 @@ def cache_evict(planes, weights, budget: int, recent: int = 0, length: int | Non
     B, Hkv, cap = weights.shape
     out_cap = out_weights.shape[2]
     Sk = cap if length is None else _int32(length, "length")
-    wp = _check_cuda(weights, "weights", torch.float32, (B, Hkv, cap), dev)
-    owp = wp if out_weights is weights else _check_cuda(out_weights, "out_weights", torch.float32, (B, Hkv, out_cap), dev)
+    wp = _check_cuda(weights, "weights", _F32, (B, Hkv, cap), dev)
+    owp = wp if out_weights is weights else _check_cuda(out_weights, "out_weights", _F32, (B, Hkv, out_cap), dev)
     src, dst, nbytes = [], [], []
     for a, b in zip(planes, out):
         if not isinstance(a, torch.Tensor) or a.dim() != 4:
@@ -713,18 +727,18 @@ def cache_evict(planes, weights, budget: int, recent: int = 0, length: int | Non
         src.append(ap)
         dst.append(ap if a is b else _check_cuda(b, "an out tensor", dtype, (B, Hkv, out_cap, n), dev))
         nbytes.append(n * dtype.itemsize)
-    np_ = None if lengths is None else _check_cuda(lengths, "lengths", torch.int32, (B,), dev)
+    np_ = None if lengths is None else _check_cuda(lengths, "lengths", _I32, (B,), dev)
     shape = (B, Hkv, budget if budget > 0 else 0)
     if index is None:
         index = torch.empty(shape, device=dev, dtype=torch.int32)
         ip = index.data_ptr()
     else:
-        ip = _check_cuda(index, "index", torch.int32, shape, dev)
+        ip = _check_cuda(index, "index", _I32, shape, dev)
     if new_lengths is None:
         new_lengths = torch.empty((B,), device=dev, dtype=torch.int32)
         nlp = new_lengths.data_ptr()
     else:
-        nlp = _check_cuda(new_lengths, "new_lengths", torch.int32, (B,), dev)
+        nlp = _check_cuda(new_lengths, "new_lengths", _I32, (B,), dev)
     # the C arrays planes and out_planes, one behind the other, and row_bytes
     table, rows = array.array("q", src + dst), array.array("i", nbytes)
     at = table.buffer_info()[0]
