@@ -83,11 +83,11 @@ struct Kv4Params {
   }
 };
 
-__device__ __forceinline__ int kv4_units(int len) { return (len + kKv4Unit - 1) / kKv4Unit; }
+__host__ __device__ __forceinline__ constexpr int kv4_units(int len) { return (len + kKv4Unit - 1) / kKv4Unit; }
 
 // A segment's weight when segments are shared out: its rounds (a unit for each warp of a CTA: what
 // is shared is whole rounds, so that no warp idles in the middle), and kKv4SegmentStart.
-__device__ __forceinline__ int kv4_rounds(int units, int warps) { return (units + warps - 1) / warps; }
+__host__ __device__ __forceinline__ constexpr int kv4_rounds(int units, int warps) { return (units + warps - 1) / warps; }
 __device__ __forceinline__ int kv4_weight(int units, int warps) {
   return units == 0 ? 0 : kv4_rounds(units, warps) + kKv4SegmentStart;
 }
@@ -955,9 +955,14 @@ struct Kv4WeightsSmem {
   int limit[128];
   Kv4QueryShared<D> q[16];   // as many as the rows have tiles of 8
 };
+constexpr int kKv4WeightsAlone = 120 * 1024;   // shared memory with which a CTA has its SM alone
+static_assert(sizeof(Kv4WeightsSmem<128>) <= kKv4WeightsAlone && 2 * sizeof(Kv4WeightsSmem<128>) <= 227 * 1024);
 
-template <int D>
-__global__ void __launch_bounds__(kKv4WeightsWarps * 32, 2) kv4_weights_kernel(Kv4Params p, int tile_rows) {
+template <int D, bool ALONE>
+__global__ void __launch_bounds__(kKv4WeightsWarps * 32, ALONE ? 1 : 2) kv4_weights_kernel(Kv4Params p, int tile_rows) {
+  // 16-key halves of a unit that go side by side: two take 185 registers, and with two CTAs per SM they spill
+  // (8 sequences x 131072 keys, 7 rows: 204 us against 173)
+  constexpr int kSide = ALONE ? 2 : 1;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   Kv4WeightsSmem<D>& sm = *reinterpret_cast<Kv4WeightsSmem<D>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1030,31 +1035,42 @@ __global__ void __launch_bounds__(kKv4WeightsWarps * 32, 2) kv4_weights_kernel(K
       const float old = key < len ? *weight : 0.0f;
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // keys g + 8 i
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t ka[D / 32], kb[D / 32];
-        kv4_take_keys<D>(ka, kb, here + kv4_key_place<D>(lane), half);
-        float sa[D / 32], sb[D / 32];
-        kv4_take_scales<D>(sa, &st.ks[(16 * half + g) * (D / 32)]);
-        kv4_take_scales<D>(sb, &st.ks[(16 * half + 8 + g) * (D / 32)]);
+      for (int half0 = 0; half0 < 2; half0 += kSide) {
+        uint32_t ka[kSide][D / 32], kb[kSide][D / 32];
+        float sa[kSide][D / 32], sb[kSide][D / 32];
+#pragma unroll
+        for (int n = 0; n < kSide; ++n) {
+          kv4_take_keys<D>(ka[n], kb[n], here + kv4_key_place<D>(lane), half0 + n);
+          kv4_take_scales<D>(sa[n], &st.ks[(16 * (half0 + n) + g) * (D / 32)]);
+          kv4_take_scales<D>(sb[n], &st.ks[(16 * (half0 + n) + 8 + g) * (D / 32)]);
+        }
         for (int i = 0; i < p.rows; i += 8) {
           const auto& q = sm.q[i / 8];
-          float s[4];
+          float s[kSide][4];
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w)
-            kv4_score_group(s, w, ka[w], kb[w], sa[w], sb[w], q.b[w][lane], q.init[w][lane]);
-          const float2 factor = q.factor[lane], ref = *reinterpret_cast<const float2*>(&sm.ref[i + 2 * t]);
-          float e[4] = {ex2_approx(fmaf(s[0], factor.x, -ref.x)), ex2_approx(fmaf(s[1], factor.y, -ref.y)),
-                        ex2_approx(fmaf(s[2], factor.x, -ref.x)), ex2_approx(fmaf(s[3], factor.y, -ref.y))};
-          if (masked) {
+          for (int w = 0; w < D / 32; ++w) {
+            const uint4 qb = q.b[w][lane];
+            const float2 init = q.init[w][lane];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int lim = sm.limit[i + 2 * t + c] - key0 - 16 * half - g;
-              if (lim <= 0) e[c] = 0.0f;
-              if (lim <= 8) e[2 + c] = 0.0f;
-            }
+            for (int n = 0; n < kSide; ++n)
+              kv4_score_group(s[n], w, ka[n][w], kb[n][w], sa[n][w], sb[n][w], qb, init);
           }
-          sum[2 * half] += e[0] + e[1];
-          sum[2 * half + 1] += e[2] + e[3];
+          const float2 factor = q.factor[lane], ref = *reinterpret_cast<const float2*>(&sm.ref[i + 2 * t]);
+#pragma unroll
+          for (int n = 0; n < kSide; ++n) {
+            float e[4] = {ex2_approx(fmaf(s[n][0], factor.x, -ref.x)), ex2_approx(fmaf(s[n][1], factor.y, -ref.y)),
+                          ex2_approx(fmaf(s[n][2], factor.x, -ref.x)), ex2_approx(fmaf(s[n][3], factor.y, -ref.y))};
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const int lim = sm.limit[i + 2 * t + c] - key0 - 16 * (half0 + n) - g;
+                if (lim <= 0) e[c] = 0.0f;
+                if (lim <= 8) e[2 + c] = 0.0f;
+              }
+            }
+            sum[2 * (half0 + n)] += e[0] + e[1];
+            sum[2 * (half0 + n) + 1] += e[2] + e[3];
+          }
         }
       }
 #pragma unroll

@@ -1550,10 +1550,19 @@ cudaError_t kv4_decode_launch(const pasa::Kv4Params& p, const Kv4Plan& pl, cudaS
     e = launch_kernel(pasa::kv4_merge_kernel<D>, dim3(static_cast<unsigned>(pl.segments), tile), dim3(256), 0, st, true,
                       p, tile);
   if (e == cudaSuccess && p.weights) {
-    const int smem = static_cast<int>(offsetof(pasa::Kv4WeightsSmem<D>, q) + sizeof(pasa::Kv4QueryShared<D>) * ((p.rows + 7) / 8));
-    static std::atomic<unsigned long long> raised{0};
-    e = launch_clusters(pasa::kv4_weights_kernel<D>, pasa::kv4_ctas(1), pasa::kKv4WeightsWarps * 32, smem,
-                        static_cast<int>(sizeof(pasa::Kv4WeightsSmem<D>)), st, true, 1, raised, p, tile);
+    // Two CTAs per SM share the longest cases best. Where one to each SM is enough, two would pile up on the SMs
+    // that the decode does not hold when they start; alone, a CTA has the registers to take both halves of a
+    // unit side by side. With more than 8 rows that counts: 112 rows x 4 heads, GPU us of a call alone / two,
+    // 8192 keys (136 rounds) 25.6 / 29.6, 131072 keys 194.6 / 187; with 7 rows x 8192 keys 12.7 / 12.3.
+    const int all = pasa::kv4_ctas(1);
+    int smem = static_cast<int>(offsetof(pasa::Kv4WeightsSmem<D>, q) + sizeof(pasa::Kv4QueryShared<D>) * ((p.rows + 7) / 8));
+    const int rounds = pasa::kv4_rounds(pasa::kv4_units(p.Sk), pasa::kKv4WeightsWarps) + pasa::kKv4SegmentStart;
+    const bool alone = p.rows > 8 && static_cast<long long>(p.B) * p.Hkv * rounds <= all / 2;
+    if (alone) smem = std::max(smem, pasa::kKv4WeightsAlone);
+    static std::atomic<unsigned long long> raised{0}, raised_alone{0};
+    e = launch_clusters(alone ? pasa::kv4_weights_kernel<D, true> : pasa::kv4_weights_kernel<D, false>,
+                        alone ? all / 2 : all, pasa::kKv4WeightsWarps * 32, smem, pasa::kKv4WeightsAlone, st, true, 1,
+                        alone ? raised_alone : raised, p, tile);
   }
   return e;
 }

@@ -179,6 +179,7 @@ DECODE = [
     (70, 2, 1, 1, 9000, 9000, 64, True, [(613 * i) % 9001 if i % 3 == 0 else i % 5 for i in range(70)], True),
     (3, 5, 5, 3, 4000, 4100, 64, False, [4100, -5, 2222], True),  # lengths past Sk and below 0
     (70, 2, 1, 1, 600, 600, 64, True, [(37 * i) % 601 for i in range(70)], True),   # many short sequences
+    (6, 36, 6, 2, 2500, 2600, 128, True, [2500, 0, 700, 2499, 1, 1800], True),      # 12 rows, more rounds than SMs
 ]
 
 
