@@ -27,8 +27,8 @@
 // there, else its CTAs leave (O, max, sum) partials that kv4_merge_kernel joins. Which one is
 // chosen on the host by the sizes.
 //
-// Measured, GPU time of a call: 8 sequences x 4 kv heads x 32768 keys, D = 128, 7 rows: 34.3 us
-// for 151 MB, 0.66 of the copy rate; x 131072 keys 108 us, 0.84. Per 32 keys a warp issues about
+// Measured, GPU time of a call: 8 sequences x 4 kv heads x 32768 keys, D = 128, 7 rows: 34.5 us
+// for 151 MB, 0.66 of the copy rate; x 131072 keys 109 us, 0.83. Per 32 keys a warp issues about
 // 540 instructions, 135 cycles of an SM's issue slots where HBM takes 199; the shared-out ranges
 // run at 225. The rest is the start (lengths, shares and the first burst of codes, 4 us) and the
 // join. Expanding keys like values took 650 instructions (39.5 us); a third CTA per SM needs 80
