@@ -619,7 +619,7 @@ def kv4_read(k4, kscale, v4, vscale, n: int, start=0, counts=None, shift=None, o
     return out_k, out_v
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=1024)   # of sizes only; a serving loop's lengths grow without end
 def decode_kv4_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: int, weights: bool = False) -> int:
     return library().pasa_attn_fwd_decode_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, int(bool(weights)))
 
