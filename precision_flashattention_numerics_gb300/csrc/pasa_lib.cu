@@ -1471,18 +1471,24 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   pl.segments = static_cast<long long>(B) * Hkv * pl.row_tiles;
   pl.ctas = pasa::kv4_ctas(pl.nt);
   const int units = (Sk + pasa::kKv4Unit - 1) / pasa::kKv4Unit;
-  pl.cluster = 1;
   const int warps = pasa::kv4_warps(pl.nt);
-  while (pl.cluster < 8 && pl.segments * pl.cluster * 2 <= pl.ctas && units > warps * pl.cluster) pl.cluster *= 2;
-  // A cluster per segment needs one launch and no workspace, but few segments leave SMs idle, and an
-  // uneven batch waits for its longest sequence. GPU us with 4 kv heads, 7 rows, D = 128, cluster against
-  // stream-K, by sequences, keys and rounds of a warp: 1 x 8192 (4) 9.0 / 8.6, 1 x 12288 (6) 11.1 / 9.2,
-  // 1 x 16384 (8) 13.6 / 9.4, where the launches that stream-K adds cost the host 8 us; with the SMs
-  // filled 8 x 8192 (4) 14.2 / 16.3, 8 x 32768 (16) 36.1 / 35.2, and without clusters (their segments
-  // follow one another as SMs get free) 64 x 2048 (8) 20.3 / 30.1, 64 x 4096 (16) 35.2 / 43.1.
-  const int rounds = (units + warps * pl.cluster - 1) / (warps * pl.cluster);
-  const bool filled = pl.segments * pl.cluster * 4 >= pl.ctas * 3;
-  pl.stream_k = rounds > (!filled ? 6 : pl.cluster > 1 ? 8 : 16);
+  // A cluster per segment: as many CTAs as find an SM each while all clusters run at once, but no more than
+  // take a round of their warps off. Clusters of c CTAs on 152 SMs (occupancy query; each stays
+  // within a GPC): one past the number costs a second wave (16 segments of 56 rows x 8192 keys: 14.1 us
+  // with 6 CTAs, 20.9 with 8), two CTAs on an SM about as much (16 of 7 rows x 4096 keys: 8.2 with 6, 9.6 with 8).
+  constexpr int kClusters[9] = {0, INT_MAX, 76, 46, 36, 28, 23, 15, 15};
+  int most = 8;
+  while (pl.segments > kClusters[most]) --most;
+  const int rounds = (units + warps * most - 1) / (warps * most);
+  pl.cluster = (units + warps * rounds - 1) / (warps * rounds);
+  // That needs one launch and no workspace, but few segments leave SMs idle, and an uneven batch
+  // waits for its longest sequence. GPU us with D = 128, cluster against stream-K, whose launches cost the host
+  // 8 us more, by segments x CTAs and rounds; 7 rows: 4 x 8 (6) 11.2 / 9.7, 8 x 8 (6) 11.3 / 11.3, 16 x 6 (8)
+  // 13.8 / 14.5, 96 x 1 (16) 21.1 / 20.4, 32 x 4 (16) 22.4 / 22.2, (24) 30.8 / 28.2, 64 x 2 (16) 22.5 / 22.6, (32) 39.1 /
+  // 35.1, 152 x 1 (16) 21.6 / 30.2; 16-row tiles: 8 x 8 (4) 14.3 / 12.7, 16 x 6 (6) 17.8 / 16.7, 28 x 5 (13) 30.1 / 33.4,
+  // 40 x 3 (15) 33.0 / 33.6, 112 x 1 (11) 24.8 / 32.4, 200 x 1 (22) 84.5 / 76.2.
+  const long long filled = pl.segments * most * 100 / 152;   // percent of the SMs
+  pl.stream_k = rounds > (filled < 50 ? 6 : filled < 70 ? 8 : 16);
   if (pl.stream_k) pl.cluster = 1;
   const size_t tile = static_cast<size_t>(8 * pl.nt);
   const size_t slots = pl.stream_k ? static_cast<size_t>(2 * pl.ctas) : 0;

@@ -180,6 +180,10 @@ DECODE = [
     (3, 5, 5, 3, 4000, 4100, 64, False, [4100, -5, 2222], True),  # lengths past Sk and below 0
     (70, 2, 1, 1, 600, 600, 64, True, [(37 * i) % 601 for i in range(70)], True),   # many short sequences
     (6, 36, 6, 2, 2500, 2600, 128, True, [2500, 0, 700, 2499, 1, 1800], True),      # 12 rows, more rounds than SMs
+    (1, 28, 4, 16, 3800, 3801, 128, True, None, True),       # 112 rows, clusters of 5
+    (2, 16, 2, 4, 4100, 4100, 64, True, [4100, 77], True),   # of 6
+    (1, 7, 1, 1, 1700, 1700, 128, True, None, True),         # of 7
+    (1, 10, 10, 1, 600, 600, 64, False, [555], False),       # of 3
 ]
 
 
