@@ -1462,11 +1462,21 @@ struct Kv4Plan {
   size_t part_o, part_ml, lse2, total;   // workspace: byte offsets and size
 };
 
+// Query rows of a tile.
+int kv4_tile(int rows) { return rows <= 8 ? 8 : 16; }
+
+// Whether a call's segments, each of its rounds and the weight of its start, fit an int: grids and shares are
+// ints. rows <= kTileRows, Sk <= kKv4MaxKeys. To be asked before kv4_plan.
+bool kv4_fits(int B, int Hkv, int rows, int Sk) {
+  const long long heads = static_cast<long long>(B) * Hkv;
+  const int units = (Sk + pasa::kKv4Unit - 1) / pasa::kKv4Unit, tile = kv4_tile(rows);
+  return heads <= INT_MAX && heads * ((rows + tile - 1) / tile) <= INT_MAX / (units + pasa::kKv4SegmentStart);
+}
 
 Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   Kv4Plan pl = {};
   const int rows = Hq / Hkv * Sq;
-  pl.nt = rows <= 8 ? 1 : 2;
+  pl.nt = kv4_tile(rows) / 8;
   pl.row_tiles = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
   pl.segments = static_cast<long long>(B) * Hkv * pl.row_tiles;
   pl.ctas = pasa::kv4_ctas(pl.nt);
@@ -1478,7 +1488,7 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   // with 6 CTAs, 20.9 with 8), two CTAs on an SM about as much (16 of 7 rows x 4096 keys: 8.2 with 6, 9.6 with 8).
   constexpr int kClusters[9] = {0, INT_MAX, 76, 46, 36, 28, 23, 15, 15};
   int most = 8;
-  while (pl.segments > kClusters[most]) --most;
+  while (most > 1 && pl.segments > kClusters[most]) --most;
   const int rounds = (units + warps * most - 1) / (warps * most);
   pl.cluster = (units + warps * rounds - 1) / (warps * rounds);
   // That needs one launch and no workspace, but few segments leave SMs idle, and an uneven batch
@@ -1619,6 +1629,7 @@ size_t pasa_attn_fwd_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Sq, 
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Sq <= 0 || Sk <= 0 || Hq % Hkv != 0 || Sk > kKv4MaxKeys || (D != 64 && D != 128))
     return 0;
   if (static_cast<long long>(Hq / Hkv) * Sq > pasa::kTileRows) return 0;
+  if (!kv4_fits(B, Hkv, Hq / Hkv * Sq, Sk)) return 0;
   return kv4_plan(B, Hq, Hkv, Sq, Sk, D, weights != 0).total;
 }
 
@@ -1634,9 +1645,8 @@ static int kv4_decode_check(const void* q, const void* k4, const void* kscale, c
   if (static_cast<long long>(Hq / Hkv) * Sq > pasa::kTileRows) return PASA_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(weights) || !aligned4(lengths))
     return PASA_ERR_ALIGN;
+  if (!kv4_fits(B, Hkv, Hq / Hkv * Sq, Sk)) return PASA_ERR_SHAPE;
   *plan = kv4_plan(B, Hq, Hkv, Sq, Sk, D, weights != nullptr);
-  // grids and weights fit an int
-  if (plan->segments * ((Sk + pasa::kKv4Unit - 1) / pasa::kKv4Unit + pasa::kKv4SegmentStart) > INT_MAX) return PASA_ERR_SHAPE;
   if (plan->total > 0) {
     if (!workspace || workspace_bytes < plan->total) return PASA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PASA_ERR_ALIGN;

@@ -196,3 +196,46 @@ def test_binding_refuses_host_tensors_and_large_ints():
         pasa._int32(2 ** 31, "start")
     with pytest.raises(TypeError):
         pasa._check_cuda(torch.zeros(4), "x", torch.float32, (4,), 0)
+
+
+# ---- sizes that no GPU holds ----
+
+HUGE = """
+import ctypes, sys
+lib = ctypes.CDLL(sys.argv[1])
+P, I = ctypes.c_void_p, ctypes.c_int
+size = lib.pasa_attn_fwd_decode_kv4_workspace_bytes
+size.restype = ctypes.c_size_t
+bad = []
+# B, Hq, Hkv, Sq, Sk: B * Hkv passes an int; B * Hkv * row tiles does; the segments' rounds do
+for B, Hq, Hkv, Sq, Sk, want in ((65536, 32768, 32768, 1, 100, -2), (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 1, 1, -2),
+                                 (32768, 131072, 8192, 8, 100, -2), (2 ** 31 - 1, 128, 1, 1, 1, -2),
+                                 (65536, 4096, 4096, 1, 1000, -2), (1024, 1024, 1024, 1, 2 ** 31 - 70000, -2)):
+    for weights in (0, 1):
+        got = size(B, Hq, Hkv, Sq, Sk, 64, weights)
+        if got != 0:
+            bad.append((B, Hq, Hkv, Sq, Sk, weights, got))
+    f = P(1 << 20)
+    for w in (None, f):
+        rc = lib.pasa_attn_fwd_decode_kv4(f, f, f, f, f, None, None, f, None, w, B, Hq, Hkv, Sq, Sk, Sk, 64, 1,
+                                          ctypes.c_float(0), f, ctypes.c_size_t(1 << 40), None)
+        step = lib.pasa_attn_fwd_decode_step_kv4(f, f, f, f, f, f, f, None, f, 0, f, None, w, B, Hq, Hkv, Sq, 1, Sk, Sk, 64,
+                                                 1, ctypes.c_float(0), f, ctypes.c_size_t(1 << 40), None)
+        if (rc, step) != (want, want):
+            bad.append((B, Hq, Hkv, Sq, Sk, rc, step))
+print("bad", bad)
+"""
+
+
+def test_more_segments_than_an_int_are_refused(lib):
+    """In a process of its own: a size that gets past the checks can end it."""
+    import subprocess
+    import sys
+
+    from precision_flashattention_numerics_gb300 import library_path
+
+    r = subprocess.run([sys.executable, "-c", HUGE, library_path], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout.strip() == "bad []", (r.returncode, r.stdout, r.stderr)
+    # the last size before an int's end has a layout, and only then the device is asked for
+    assert lib.pasa_attn_fwd_decode_kv4_workspace_bytes(8192, 8192, 8192, 1, 64, 64, 0) == 0
+    assert lib.pasa_attn_fwd_decode_kv4_workspace_bytes(8192, 8192, 8192, 1, 300, 64, 1) == 8192 * 8192 * 8 * 4
