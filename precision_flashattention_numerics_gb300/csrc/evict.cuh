@@ -265,10 +265,12 @@ __device__ __forceinline__ void move_rows(const unsigned char* src, unsigned cha
 
 // blockIdx.x: (sequence, kv head); blockIdx.y: a part of a column of a plane's rows (a column is a
 // 32-byte sector in place, where only columns can move side by side; up to 128 bytes otherwise).
-// The weights' first CTA also clears what is past the last row.
-__global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(EvictPlanes pl, const int* __restrict__ index,
-                                                                     int* new_lengths, int Hkv, long long cap,
-                                                                     long long out_cap, int budget) {
+// The weights' first CTA also clears what is past the last row. `index` is not __restrict__: the selection
+// writes it while this kernel already runs, so its loads must not count as those of constants, which
+// may go through the read-only cache or ahead of griddep_wait().
+__global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(EvictPlanes pl, const int* index, int* new_lengths,
+                                                                     int Hkv, long long cap, long long out_cap,
+                                                                     int budget) {
   const long long bh = blockIdx.x;
   int p = 0;
   while (static_cast<int>(blockIdx.y) >= pl.first[p + 1]) ++p;

@@ -208,3 +208,30 @@ def test_prompt_score_evict_decode(D):
             n_before = budget + 4
             total = cut()
     p.check_device_error()
+
+
+def test_calls_in_a_row_share_index_and_outputs():
+    """Twenty evictions of other weights behind one another into the same index, lengths and outputs, each result
+    copied on the stream: every move goes by the rows that its own selection, just ahead of it, wrote."""
+    p = pasa()
+    rng = np.random.default_rng(23)
+    B, H, cap, budget, recent = 4, 3, 1300, 700, 20
+    planes = [rng.integers(0, 256, (B, H, cap, n)).astype(np.uint8) for n in (64, 8)]
+    pt = to_dev(*planes)
+    ws = [make_weights(rng, B, H, cap, kind) for kind in ("plain", "ties", "odd", "equal") * 5]
+    wt = to_dev(*ws)
+    out = [torch.zeros((B, H, budget, x.shape[-1]), dtype=torch.uint8, device="cuda") for x in planes]
+    ow = torch.zeros((B, H, budget), device="cuda")
+    index = torch.zeros((B, H, budget), dtype=torch.int32, device="cuda")
+    new = torch.zeros((B,), dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    got = []
+    for w in wt:
+        p.cache_evict(pt, w, budget, recent, out=out, out_weights=ow, index=index, new_lengths=new)
+        got.append([x.clone() for x in (index, *out, ow)])
+    for w, (idx, *moved, kept) in zip(ws, got):
+        keep = np.array([[kv4.select(w[b, h], cap, budget, recent) for h in range(H)] for b in range(B)])
+        assert np.array_equal(idx.cpu().numpy(), keep)
+        for m, x in zip(moved, planes):
+            assert np.array_equal(m.cpu().numpy(), np.take_along_axis(x, keep[..., None], 2))
+        assert np.array_equal(kept.cpu().numpy(), np.take_along_axis(w, keep, 2), equal_nan=True)
