@@ -531,9 +531,10 @@ int pasa_attn_fwd_decode_step_kv4(const void* q, const void* k, const void* v, v
  *   weights, out_weights  fp32 [B, Hkv, Sk_cap] and [B, Hkv, out_cap]: the weights move with
  *            their rows; those past the new length become 0.
  *   In place: out_planes[i] == planes[i] for every i and out_weights == weights, with
- *            out_cap == Sk_cap; a mixture is PASA_ERR_SHAPE. Else no output may overlap an input. Two
- *            outputs in one place are PASA_ERR_SHAPE, and so is a budget beyond a launch's grid
- *            (8 million rows of 64 bytes).
+ *            out_cap == Sk_cap; a mixture is PASA_ERR_SHAPE. Else out_planes and out_weights share no
+ *            byte with planes and weights, nor in any case with one another: PASA_ERR_SHAPE too.
+ *            A budget beyond a launch's grid
+ *            (8 million rows of 64 bytes) is PASA_ERR_SHAPE.
  *   lengths  int32 [B], device, or NULL for Sk: rows of each sequence, within 0 .. Sk.
  *   index    int32 [B, Hkv, budget], out: the old row of each kept one, -1 past the last.
  *   new_lengths  int32 [B], out, or NULL: min(length, budget); may be `lengths` itself.

@@ -1419,6 +1419,20 @@ namespace {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// The memory of a tensor: rows * row_bytes bytes from `at` on (to the last address, if that is past it); none
+// for a null pointer. Two spans meet where they share a byte.
+struct Span {
+  uintptr_t begin = 0, end = 0;
+  Span() = default;
+  Span(const void* at, unsigned long long rows, unsigned long long row_bytes) {
+    if (!at) return;
+    unsigned long long bytes;
+    begin = reinterpret_cast<uintptr_t>(at);
+    if (__builtin_mul_overflow(rows, row_bytes, &bytes) || __builtin_add_overflow(begin, bytes, &end)) end = UINTPTR_MAX;
+  }
+  bool meets(const Span& x) const { return begin < x.end && x.begin < end; }
+};
+
 // The cache tensors and sizes that every kv4 entry point takes.
 int kv4_validate(const void* k4, const void* kscale, const void* v4, const void* vscale, const void* shift, int B,
                  int Hkv, int Sk_cap, int D) {
@@ -1751,6 +1765,18 @@ int pasa_cache_evict(const void* const* planes, void* const* out_planes, const i
   }
   // a cache moves in place as a whole, in a cache of the same size
   if (in_place && (apart || out_cap != Sk_cap)) return PASA_ERR_SHAPE;
+  // else a row could be written over before it is read, by another CTA. In place a tensor meets itself only.
+  const unsigned long long heads = static_cast<unsigned long long>(B) * Hkv;
+  Span from[pasa::kEvictPlanes + 1], to[pasa::kEvictPlanes + 1];
+  for (int i = 0; i < n_planes; ++i) {
+    from[i] = Span(planes[i], heads * Sk_cap, row_bytes[i]);
+    to[i] = Span(out_planes[i], heads * out_cap, row_bytes[i]);
+  }
+  from[n_planes] = Span(weights, heads * Sk_cap, 4);
+  to[n_planes] = Span(out_weights, heads * out_cap, 4);
+  for (int i = 0; i <= n_planes; ++i)
+    for (int j = 0; j <= n_planes; ++j)
+      if ((i != j || !in_place) && (to[i].meets(from[j]) || (i < j && to[i].meets(to[j])))) return PASA_ERR_SHAPE;
   pasa::EvictPlanes pl = {};
   pl.n = n_planes + 1;
   long long blocks = 0;

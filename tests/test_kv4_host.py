@@ -239,3 +239,35 @@ def test_more_segments_than_an_int_are_refused(lib):
     # the last size before an int's end has a layout, and only then the device is asked for
     assert lib.pasa_attn_fwd_decode_kv4_workspace_bytes(8192, 8192, 8192, 1, 64, 64, 0) == 0
     assert lib.pasa_attn_fwd_decode_kv4_workspace_bytes(8192, 8192, 8192, 1, 300, 64, 1) == 8192 * 8192 * 8 * 4
+
+
+def test_evict_refuses_what_overlaps(lib):
+    """Tensors that share bytes without being the same one in place: a CTA could write a row before another reads it."""
+    M = 1 << 20
+
+    def evict(planes, out, rb, w, ow, B=2, H=4, cap=1024, out_cap=512, budget=512):
+        n = len(planes)
+        arr = lambda t, x: (t * n)(*x)   # noqa: E731
+        return lib.pasa_cache_evict(arr(P, planes), arr(P, out), arr(ctypes.c_int, rb), n, P(w), P(ow), None, P(100 * M), None,
+                                    B, H, cap, cap, out_cap, budget, 4, None)
+
+    rb = (64, 8)                      # planes of 512 KB and 64 KB, weights of 32 KB; half of that when out_cap is 512
+    fine = dict(planes=(M, 2 * M), out=(3 * M, 4 * M), rb=rb, w=5 * M, ow=6 * M)
+    size, half = 2 * 4 * 1024, 2 * 4 * 512
+    if not torch.cuda.is_available():
+        assert evict(**fine) in (-3, -5)
+        # end to end, with no byte shared
+        assert evict(**{**fine, "out": (M + 64 * size, 2 * M - 8 * half)}) in (-3, -5)
+        assert evict(**{**fine, "out": fine["planes"], "ow": 5 * M, "out_cap": 1024}) in (-3, -5)
+    for bad in ({"out": (M + 64 * size - 16, 4 * M)}, {"out": (M - 64 * half + 16, 4 * M)},   # a plane's own source
+                {"out": (2 * M, M)},                                                         # each other's place
+                {"out": (3 * M, M + 16)}, {"out": (5 * M, 4 * M)}, {"out": (3 * M, 5 * M + 4 * size - 16)},
+                {"ow": M}, {"ow": 2 * M + 8 * size - 16}, {"ow": 5 * M + 16},
+                {"out": (3 * M, 3 * M + 64 * half - 16)}, {"ow": 4 * M + 16}):              # another output
+        assert evict(**{**fine, **bad}) == -2, bad
+    # in place, planes that overlap each other or the weights
+    for planes, w in (((M, M + 16), 5 * M), ((M, 2 * M), M + 64 * size - 16), ((M, 2 * M), 2 * M + 16)):
+        assert evict(planes=planes, out=planes, rb=rb, w=w, ow=w, out_cap=1024) == -2
+    # sizes whose bytes pass 64 bits
+    assert evict(planes=(M, 1 << 40), out=(1 << 41, 1 << 42), rb=(65536, 65536), w=1 << 43, ow=1 << 44, B=1 << 14, H=1 << 14,
+                 cap=2 ** 31 - 1, out_cap=2 ** 31 - 1, budget=64) == -2
