@@ -533,8 +533,9 @@ int pasa_attn_fwd_decode_step_kv4(const void* q, const void* k, const void* v, v
  *   In place: out_planes[i] == planes[i] for every i and out_weights == weights, with
  *            out_cap == Sk_cap; a mixture is PASA_ERR_SHAPE. Else out_planes and out_weights share no
  *            byte with planes and weights, nor in any case with one another: PASA_ERR_SHAPE too.
- *            A budget beyond a launch's grid
- *            (8 million rows of 64 bytes) is PASA_ERR_SHAPE.
+ *            So is, not in place, a budget beyond the move's grid: 65535 CTAs for the rows of all planes
+ *            and weights, which is 6.1 million rows of a 4-bit cache with D = 128, 2.0 million of
+ *            fp16 keys and values with D = 128.
  *   lengths  int32 [B], device, or NULL for Sk: rows of each sequence, within 0 .. Sk.
  *   index    int32 [B, Hkv, budget], out: the old row of each kept one, -1 past the last.
  *   new_lengths  int32 [B], out, or NULL: min(length, budget); may be `lengths` itself.

@@ -271,3 +271,30 @@ def test_evict_refuses_what_overlaps(lib):
     # sizes whose bytes pass 64 bits
     assert evict(planes=(M, 1 << 40), out=(1 << 41, 1 << 42), rb=(65536, 65536), w=1 << 43, ow=1 << 44, B=1 << 14, H=1 << 14,
                  cap=2 ** 31 - 1, out_cap=2 ** 31 - 1, budget=64) == -2
+
+
+@pytest.mark.parametrize("rb,most", [((64, 8, 64, 8), 6_100_480), ((32, 4, 32, 4), 9_586_688), ((256, 256), 2_033_536)])
+def test_largest_budget_of_an_eviction(lib, rb, most):
+    """CTAs of a budget: 256 threads move 4 words each (16, 8 or 4 bytes, as a row's bytes allow) of columns of up to
+    128 bytes, one grid row per CTA, 65535 in all. In place, where a CTA has all rows, no budget is refused."""
+    def ctas(budget):
+        n = 0
+        for b in (*rb, 4):
+            word = 16 if b % 16 == 0 else 8 if b % 8 == 0 else 4
+            rows = 256 // (min(b, 128) // word) * 4
+            n += -(-budget // rows) * -(-b // 128)
+        return n
+
+    def evict(budget, in_place=False):
+        k, M = len(rb), 1 << 40
+        src, dst = [M * (i + 1) for i in range(k)], [M * (20 + i) for i in range(k)]
+        dst = src if in_place else dst
+        arr = lambda t, x: (t * k)(*x)   # noqa: E731
+        return lib.pasa_cache_evict(arr(P, src), arr(P, dst), arr(ctypes.c_int, rb), k, P(M * 10), P(M * (10 if in_place else 30)),
+                                    None, P(M * 40), None, 1, 1, budget + 9, budget + 9, budget + (9 if in_place else 0), budget,
+                                    4, None)
+
+    assert ctas(most) <= 65535 < ctas(most + 1)
+    assert evict(most + 1) == -2
+    if not torch.cuda.is_available():
+        assert evict(most) in (-3, -5) and evict(most + 1, in_place=True) in (-3, -5)
