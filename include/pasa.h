@@ -471,7 +471,8 @@ int pasa_kprep_fp8_blocks(const void* k, void* k8, void* means, float* kscale, i
  *   counts  int32 [B], device, or NULL for n: only rows i < counts[b] are stored or read (a
  *           padded batch)
  * Rows that fall outside 0 .. Sk_cap - 1 (from starts on the device) are skipped, and what
- * is not stored or read is left as it was. starts and counts need 4-byte alignment.
+ * is not stored or read is left as it was. starts and counts need 4-byte alignment. What a call writes
+ * shares no byte with what it reads, and its outputs none with one another (PASA_ERR_SHAPE).
  */
 int pasa_kv4_append(const void* k, const void* v, const void* shift, void* k4, void* kscale, void* v4, void* vscale,
                     const int* starts, int start, const int* counts, int B, int Hkv, int n, int Sk_cap, int D,
@@ -497,6 +498,8 @@ int pasa_kv4_read(const void* k4, const void* kscale, const void* v4, const void
  *   workspace  device, 256-byte aligned, at least pasa_attn_fwd_decode_kv4_workspace_bytes(...)
  *            bytes (`weights` nonzero where the call passes weights; may be NULL where that is
  *            0), written before it is read, used on `stream` only.
+ * o, lse, weights and the workspace share no byte with one another or with what is read
+ * (PASA_ERR_SHAPE), but without `weights` o may be q itself.
  */
 size_t pasa_attn_fwd_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int weights);
 int pasa_attn_fwd_decode_kv4(const void* q, const void* k4, const void* kscale, const void* v4, const void* vscale,

@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <utility>
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -1445,6 +1446,28 @@ int kv4_validate(const void* k4, const void* kscale, const void* v4, const void*
   return PASA_OK;
 }
 
+// Whether `out` shares memory with one of `others`, or two of its own do.
+bool any_meet(std::initializer_list<Span> out, std::initializer_list<Span> others) {
+  for (const Span* a = out.begin(); a != out.end(); ++a) {
+    for (const Span* b = a + 1; b != out.end(); ++b)
+      if (a->meets(*b)) return true;
+    for (const Span& b : others)
+      if (a->meets(b)) return true;
+  }
+  return false;
+}
+
+// A call's cache tensors.
+struct Kv4Spans {
+  Span k4, kscale, v4, vscale, shift;
+  Kv4Spans(const void* k4p, const void* ksp, const void* v4p, const void* vsp, const void* shiftp, int B, int Hkv, int cap, int D) {
+    const unsigned long long heads = static_cast<unsigned long long>(B) * Hkv, rows = heads * cap;
+    k4 = Span(k4p, rows, D / 2), v4 = Span(v4p, rows, D / 2);
+    kscale = Span(ksp, rows, D / 16), vscale = Span(vsp, rows, D / 16);
+    shift = Span(shiftp, heads, 2 * D);
+  }
+};
+
 // kv4_append and kv4_read share their arguments: n rows of k and v from cache row `start` on.
 int kv4_window(const void* k, const void* v, const int* starts, int start, const int* counts, int n, int B, int Hkv,
                int Sk_cap, int D, bool append, pasa::Kv4Window* win, dim3* grid) {
@@ -1601,23 +1624,41 @@ cudaError_t kv4_decode_launch(const pasa::Kv4Params& p, const Kv4Plan& pl, cudaS
 
 extern "C" {
 
-int pasa_kv4_append(const void* k, const void* v, const void* shift, void* k4, void* kscale, void* v4, void* vscale,
-                    const int* starts, int start, const int* counts, int B, int Hkv, int n, int Sk_cap, int D,
-                    void* stream) {
+// The checks of an append, and its launch.
+static int kv4_append_check(const void* k, const void* v, const void* shift, const void* k4, const void* kscale,
+                            const void* v4, const void* vscale, const int* starts, int start, const int* counts, int B,
+                            int Hkv, int n, int Sk_cap, int D, pasa::Kv4Window* win, dim3* grid) {
   int rc = kv4_validate(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
   if (rc != PASA_OK) return rc;
-  pasa::Kv4Window win;
-  dim3 grid;
-  rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, true, &win, &grid);
+  rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, true, win, grid);
   if (rc != PASA_OK) return rc;
-  rc = check_device();
-  if (rc != PASA_OK) return rc;
+  const Kv4Spans c(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
+  const unsigned long long rows = static_cast<unsigned long long>(B) * Hkv * n;
+  const bool shared = any_meet({c.k4, c.kscale, c.v4, c.vscale}, {Span(k, rows, 2 * D), Span(v, rows, 2 * D), c.shift,
+                                                                  Span(starts, B, 4), Span(counts, B, 4)});
+  return shared ? PASA_ERR_SHAPE : PASA_OK;
+}
+
+static int kv4_append_enqueue(const void* k, const void* v, const void* shift, void* k4, void* kscale, void* v4, void* vscale,
+                              int B, int Hkv, int D, const pasa::Kv4Window& win, dim3 grid, cudaStream_t st) {
   auto kern = D == 64 ? pasa::kv4_append_kernel<64> : pasa::kv4_append_kernel<128>;
-  kern<<<grid, pasa::kKv4StoreThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+  kern<<<grid, pasa::kKv4StoreThreads, 0, st>>>(
       static_cast<const __half*>(k), static_cast<const __half*>(v), static_cast<const __half*>(shift),
       static_cast<uint8_t*>(k4), static_cast<__half*>(kscale), static_cast<uint8_t*>(v4), static_cast<__half*>(vscale),
       B * Hkv, Hkv, win);
   return launch_status();
+}
+
+int pasa_kv4_append(const void* k, const void* v, const void* shift, void* k4, void* kscale, void* v4, void* vscale,
+                    const int* starts, int start, const int* counts, int B, int Hkv, int n, int Sk_cap, int D,
+                    void* stream) {
+  pasa::Kv4Window win;
+  dim3 grid;
+  int rc = kv4_append_check(k, v, shift, k4, kscale, v4, vscale, starts, start, counts, B, Hkv, n, Sk_cap, D, &win, &grid);
+  if (rc != PASA_OK) return rc;
+  rc = check_device();
+  if (rc != PASA_OK) return rc;
+  return kv4_append_enqueue(k, v, shift, k4, kscale, v4, vscale, B, Hkv, D, win, grid, static_cast<cudaStream_t>(stream));
 }
 
 int pasa_kv4_read(const void* k4, const void* kscale, const void* v4, const void* vscale, const void* shift, void* k,
@@ -1629,6 +1670,11 @@ int pasa_kv4_read(const void* k4, const void* kscale, const void* v4, const void
   dim3 grid;
   rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, false, &win, &grid);
   if (rc != PASA_OK) return rc;
+  const Kv4Spans c(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
+  const unsigned long long rows = static_cast<unsigned long long>(B) * Hkv * n;
+  if (any_meet({Span(k, rows, 2 * D), Span(v, rows, 2 * D)},
+               {c.k4, c.kscale, c.v4, c.vscale, c.shift, Span(starts, B, 4), Span(counts, B, 4)}))
+    return PASA_ERR_SHAPE;
   rc = check_device();
   if (rc != PASA_OK) return rc;
   auto kern = D == 64 ? pasa::kv4_read_kernel<64> : pasa::kv4_read_kernel<128>;
@@ -1666,6 +1712,20 @@ static int kv4_decode_check(const void* q, const void* k4, const void* kscale, c
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PASA_ERR_ALIGN;
   }
   return PASA_OK;
+}
+
+// Whether a decode call's outputs or workspace share memory with one another or with what it reads. Without
+// `weights` o may be q itself: the kernel that writes a row of o is the last to read that row of q.
+static bool kv4_decode_meets(const Kv4Plan& pl, const void* q, const void* k4, const void* kscale, const void* v4,
+                             const void* vscale, const void* shift, const int* lengths, const void* o, const float* lse,
+                             const float* weights, int B, int Hq, int Hkv, int Sq, int Sk_cap, int D, const void* workspace) {
+  const Kv4Spans c(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
+  const unsigned long long rows = static_cast<unsigned long long>(B) * Hq * Sq;
+  const Span qs(q, rows, 2 * D), os(o, rows, 2 * D), ls(lse, rows, 4);
+  const Span ws(weights, static_cast<unsigned long long>(B) * Hkv * Sk_cap, 4), work(pl.total ? workspace : nullptr, pl.total, 1);
+  const Span lens(lengths, B, 4);
+  return any_meet({os, ls, ws, work}, {c.k4, c.kscale, c.v4, c.vscale, c.shift, lens}) ||
+         any_meet({ls, ws, work}, {qs}) || ((weights || o != q) && os.meets(qs));
 }
 
 // The kernels of a checked decode call. len_add: added to lengths[]; pdl: the kernel ahead on the
@@ -1715,6 +1775,8 @@ int pasa_attn_fwd_decode_kv4(const void* q, const void* k4, const void* kscale, 
   int rc = kv4_decode_check(q, k4, kscale, v4, vscale, shift, lengths, o, lse, weights, B, Hq, Hkv, Sq, Sk, Sk_cap, D,
                             workspace, workspace_bytes, &pl);
   if (rc != PASA_OK) return rc;
+  if (kv4_decode_meets(pl, q, k4, kscale, v4, vscale, shift, lengths, o, lse, weights, B, Hq, Hkv, Sq, Sk_cap, D, workspace))
+    return PASA_ERR_SHAPE;
   rc = check_device();
   if (rc != PASA_OK) return rc;
   return kv4_decode_enqueue(pl, q, k4, kscale, v4, vscale, shift, lengths, 0, o, lse, weights, B, Hq, Hkv, Sq, Sk, Sk_cap,
@@ -1734,7 +1796,18 @@ int pasa_attn_fwd_decode_step_kv4(const void* q, const void* k, const void* v, v
   int rc = kv4_decode_check(q, k4, kscale, v4, vscale, shift, starts, o, lse, weights, B, Hq, Hkv, Sq, Sk, Sk_cap, D,
                             workspace, workspace_bytes, &pl);
   if (rc != PASA_OK) return rc;
-  rc = pasa_kv4_append(k, v, shift, k4, kscale, v4, vscale, starts, start, nullptr, B, Hkv, n, Sk_cap, D, stream);
+  pasa::Kv4Window win;
+  dim3 grid;
+  rc = kv4_append_check(k, v, shift, k4, kscale, v4, vscale, starts, start, nullptr, B, Hkv, n, Sk_cap, D, &win, &grid);
+  if (rc != PASA_OK) return rc;
+  const Kv4Spans c(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);   // what the append writes, and q
+  if (any_meet({c.k4, c.kscale, c.v4, c.vscale}, {Span(q, static_cast<unsigned long long>(B) * Hq * Sq, 2 * D)}))
+    return PASA_ERR_SHAPE;
+  if (kv4_decode_meets(pl, q, k4, kscale, v4, vscale, shift, starts, o, lse, weights, B, Hq, Hkv, Sq, Sk_cap, D, workspace))
+    return PASA_ERR_SHAPE;
+  rc = check_device();
+  if (rc != PASA_OK) return rc;
+  rc = kv4_append_enqueue(k, v, shift, k4, kscale, v4, vscale, B, Hkv, D, win, grid, static_cast<cudaStream_t>(stream));
   if (rc != PASA_OK) return rc;
   return kv4_decode_enqueue(pl, q, k4, kscale, v4, vscale, shift, starts, n, o, lse, weights, B, Hq, Hkv, Sq, Sk, Sk_cap, D,
                             causal, scale, workspace, static_cast<cudaStream_t>(stream), true);

@@ -501,3 +501,21 @@ def test_binding_refusals():
         p.kv4_append(k1, k1, *cache, start=2 ** 40)
     with pytest.raises(ValueError, match="current device is 1"):
         p._check_cuda(k1, "k", torch.float16, k1.shape, 1)     # a tensor of another device than the current one
+
+
+@pytest.mark.parametrize("Sk,D", [(900, 128), (40000, 64), (40000, 128)])
+def test_output_over_the_queries(Sk, D):
+    """out = q gives the same bits, in clusters and shared out; with weights it is refused, as is one tensor
+    for two outputs."""
+    p = pasa()
+    q, cache, shift = small(Sk=Sk, D=D, seed=9)
+    o, lse = p.attn_fwd_decode_kv4(q, *cache, shift=shift)
+    with pytest.raises(p.PasaError):
+        p.attn_fwd_decode_kv4(q, *cache, shift=shift, out=q, weights=torch.zeros((3, 2, Sk), device="cuda"))
+    x = torch.zeros((3, 2, 8, D), dtype=torch.float16, device="cuda")
+    with pytest.raises(p.PasaError):
+        p.kv4_read(*cache, 8, shift=shift, out_k=x, out_v=x)
+    with pytest.raises(p.PasaError):
+        p.kv4_append(x, x, cache[0], cache[1], cache[0], cache[3], shift=shift)
+    got, lse2 = p.attn_fwd_decode_kv4(q, *cache, shift=shift, out=q)
+    assert got is q and torch.equal(q, o) and torch.equal(lse2, lse)

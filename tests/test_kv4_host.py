@@ -298,3 +298,59 @@ def test_largest_budget_of_an_eviction(lib, rb, most):
     assert evict(most + 1) == -2
     if not torch.cuda.is_available():
         assert evict(most) in (-3, -5) and evict(most + 1, in_place=True) in (-3, -5)
+
+
+def test_store_and_decode_refuse_what_overlaps(lib):
+    """Outputs that share memory with an input or with each other. (o = q with weights: the weights pass would read the
+    output as queries. Two cache tensors in one place: rows of one over rows of the other.)"""
+    M = 1 << 20
+    B, Hq, H, Sq, n, cap, D = 2, 8, 2, 3, 5, 50000, 128      # 50000 rows: with a workspace
+    names = ("q", "k", "v", "k4", "ks", "v4", "vs", "shift", "starts", "counts", "o", "lse", "weights", "ws")
+    need = lib.pasa_attn_fwd_decode_kv4_workspace_bytes(B, Hq, H, Sq, cap, D, 1)
+    assert need > 0
+    size = {"q": B * Hq * Sq * 2 * D, "k": B * H * n * 2 * D, "k4": B * H * cap * D // 2, "ks": B * H * cap * D // 16,
+            "shift": B * H * 2 * D, "starts": 4 * B, "lse": B * Hq * Sq * 4, "weights": B * H * cap * 4, "ws": need}
+    size.update(v=size["k"], v4=size["k4"], vs=size["ks"], o=size["q"], counts=size["starts"])
+    at0 = {name: 64 * M * (i + 1) for i, name in enumerate(names)}
+
+    def calls(at):
+        p = {x: P(a) if a else None for x, a in at.items()}
+        c = [p[x] for x in ("k4", "ks", "v4", "vs")]
+        return {
+            "append": lambda: lib.pasa_kv4_append(p["k"], p["v"], p["shift"], *c, p["starts"], 0, p["counts"], B, H, n, cap, D, None),
+            "read": lambda: lib.pasa_kv4_read(*c, p["shift"], p["k"], p["v"], p["starts"], 0, p["counts"], B, H, n, cap, D, None),
+            "decode": lambda: lib.pasa_attn_fwd_decode_kv4(p["q"], *c, p["shift"], p["starts"], p["o"], p["lse"], p["weights"], B, Hq,
+                                                           H, Sq, cap, cap, D, 1, 0.0, p["ws"], need, None),
+            "step": lambda: lib.pasa_attn_fwd_decode_step_kv4(p["q"], p["k"], p["v"], *c, p["shift"], p["starts"], 0, p["o"], p["lse"],
+                                                              p["weights"], B, Hq, H, Sq, n, cap, cap, D, 1, 0.0, p["ws"], need, None),
+        }
+
+    cache = ["k4", "ks", "v4", "vs"]
+    # what each writes, and what it reads
+    writes = {"append": cache, "read": ["k", "v"], "decode": ["o", "lse", "weights", "ws"], "step": cache + ["o", "lse", "weights", "ws"]}
+    reads = {"append": ["k", "v", "shift", "starts", "counts"], "read": cache + ["shift", "starts", "counts"],
+             "decode": ["q"] + cache + ["shift", "starts"], "step": ["q", "shift", "starts"]}
+    fine = (-3, -5)
+    for call in writes:
+        if not torch.cuda.is_available():
+            assert calls(at0)[call]() in fine, call
+        for w in writes[call]:
+            for x in writes[call] + reads[call]:
+                if x == w:
+                    continue
+                step = 256 if w == "ws" else 16
+                at = dict(at0)
+                at[w] = at[x] + (size[x] - 1) // step * step       # w begins in x's last bytes
+                assert calls(at)[call]() == -2, (call, w, x)
+                at[w] = at[x] - (size[w] - 1) // step * step       # and ends in its first
+                assert calls(at)[call]() == -2, (call, w, x)
+                at[w] = at[x]
+                assert calls(at)[call]() == -2, (call, w, x)
+                if not torch.cuda.is_available():
+                    at[w] = at[x] + -(-size[x] // step) * step     # behind it
+                    assert calls(at)[call]() in fine, (call, w, x)
+    for call in ("decode", "step"):
+        same = {**at0, "o": at0["q"], "weights": 0}
+        assert calls({**same, "o": at0["q"] + 256})[call]() == -2
+        if not torch.cuda.is_available():
+            assert calls(same)[call]() in fine                    # without weights o may be q
