@@ -494,7 +494,9 @@ int pasa_kv4_read(const void* k4, const void* kscale, const void* v4, const void
  *            and LSE = -inf.
  *   weights  fp32 [B, Hkv, Sk_cap] or NULL: the softmax weight of cache row j, summed over the
  *            kv head's Hq / Hkv * Sq query rows, is added to weights[b, h, j] (j < lengths[b]),
- *            in the same order at every call.
+ *            in the same order at every call. A query row with a NaN or an infinity has an output and an
+ *            LSE of NaN, and makes the weights of the rows it sees NaN, for good; other query rows and
+ *            kv heads are as without it, and pasa_cache_evict takes such a weight for the smallest.
  *   workspace  device, 256-byte aligned, at least pasa_attn_fwd_decode_kv4_workspace_bytes(...)
  *            bytes (`weights` nonzero where the call passes weights; may be NULL where that is
  *            0), written before it is read, used on `stream` only.
