@@ -1,0 +1,301 @@
+"""GPU parity of the 4-bit cache's decode where its keys are shared out over a fixed number of CTAs
+(partial results in the workspace, joined by a merge kernel), the form of long caches, and of the
+operators in a row as a serving loop makes them.
+
+Bounds and the oracle are those of test_gpu_kv4.py. Every test that means the shared-out form
+asserts it: that form, and only it, needs a workspace without weights.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gpu_helpers import rel_errors, to_dev
+from oracle import kv4
+from test_gpu_kv4 import check, decode_bounds, new_cache, rows
+
+pytestmark = pytest.mark.gpu
+
+
+def pasa():
+    import precision_flashattention_numerics_gb300 as p
+
+    return p
+
+
+def shared_out(B, Hq, H, Sq, Sk, D):
+    return pasa().decode_kv4_workspace_bytes(B, Hq, H, Sq, Sk, D, False) > 0
+
+
+CASES = [
+    # B, Hq, Hkv, Sq, Sk, cap, D, causal, lengths (None: Sk), shifted
+    (3, 14, 2, 1, 20001, 20011, 128, True, [20001, 0, 7777], True),         # 7 rows, an empty sequence in the middle
+    (3, 14, 2, 1, 20000, 20000, 128, False, None, False),
+    (3, 30, 2, 1, 20000, 20000, 128, True, [20000, 33, 0], True),           # 15 rows of a 16-row tile
+    (2, 12, 1, 1, 40001, 40001, 128, True, [40001, 31], False),             # 12
+    (3, 14, 2, 4, 30000, 30003, 128, True, [30000, 0, 2], True),            # 28: two tiles; rows that see no key
+    (1, 28, 4, 4, 20000, 20000, 128, True, None, True),
+    (1, 16, 2, 16, 19000, 19000, 128, True, [18999], False),                # 128 rows: 8 tiles
+    (70, 2, 1, 1, 9000, 9000, 128, True, [(613 * i) % 9001 if i % 3 == 0 else i % 5 for i in range(70)], True),
+    (2, 4, 2, 2, 60000, 60000, 128, True, [0, 0], True),                    # nothing to share
+    (2, 4, 2, 2, 60000, 60000, 128, True, [1, 0], True),                    # one key
+    (1, 1, 1, 1, 90001, 90001, 128, True, [32 * 304 + 1], False),           # fewer keys than CTAs have rounds
+    (4, 2, 2, 1, 30000, 30000, 128, True, [30000, 256, 257, 29999], False),  # ends at and past a round
+    (3, 14, 2, 4, 30000, 30003, 64, True, [30000, 0, 2], True),
+]
+
+
+@pytest.mark.parametrize("weights", [False, True], ids=["", "weights"])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_shared_out_decode_parity(case, weights):
+    B, Hq, H, Sq, Sk, cap, D, causal, lengths, shifted = CASES[case]
+    assert shared_out(B, Hq, H, Sq, Sk, D)
+    rng = np.random.default_rng(300 + case)
+    k, v = rows(rng, B, H, cap, D, "bias" if shifted else "plain"), rows(rng, B, H, cap, D, "plain")
+    q = rng.standard_normal((B, Hq, Sq, D)).astype(np.float16)
+    shift = k[:, :, 0].copy() if shifted else None
+    kt, vt, qt = to_dev(k, v, q)
+    st = None if shift is None else to_dev(shift)[0]
+    cache = new_cache(B, H, cap, D)
+    p = pasa()
+    p.kv4_append(kt, vt, *cache, shift=st)
+    n = np.clip(lengths if lengths else [Sk] * B, 0, Sk)
+    for b in range(B):   # rows past the last: whatever was there
+        for x, fill in zip(cache, (255, float("nan"), 255, float("inf"))):
+            x[b, :, n[b]:] = fill
+    ref = kv4.decode(q, kv4.values(*kv4.quantise(k, shift)), kv4.values(*kv4.quantise(v)), n, causal, D ** -0.5, shift)
+    acc = torch.zeros((B, H, cap), device="cuda") if weights else None
+    if weights:
+        for b in range(B):
+            acc[b, :, n[b]:] = -7
+            ref["weights"][b, :, n[b]:] = -7
+    lt = torch.tensor(lengths).int().cuda() if lengths else None
+    # the workspace holds whatever was there: bytes of a NaN
+    ws = torch.full((p.decode_kv4_workspace_bytes(B, Hq, H, Sq, Sk, D, weights),), 255, dtype=torch.uint8, device="cuda")
+    got = p.attn_fwd_decode_kv4(qt, *cache, causal=causal, shift=st, length=Sk, lengths=lt, weights=acc, workspace=ws)
+    bounds = decode_bounds(ref, D ** -0.5, D, Hq // H, Sq, q, shift)
+    bounds[2][ref["weights"] < 0] = 0
+    check(got, ref, bounds, acc)
+    again = p.attn_fwd_decode_kv4(qt, *cache, causal=causal, shift=st, length=Sk, lengths=lt)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+def filled(B, Hq, H, Sk, D, seed, Sq=1):
+    rng = np.random.default_rng(seed)
+    kt, vt = to_dev(rows(rng, B, H, Sk, D, "bias"), rows(rng, B, H, Sk, D, "plain"))
+    qt = to_dev(rng.standard_normal((B, Hq, Sq, D)).astype(np.float16))[0]
+    cache, shift = new_cache(B, H, Sk, D), kt[:, :, 0].contiguous()
+    pasa().kv4_append(kt, vt, *cache, shift=shift)
+    return qt, cache, shift
+
+
+def test_calls_of_all_forms_share_one_workspace():
+    """Shared out over two lengths and two row counts, in clusters, with and without weights, one behind the
+    other on a stream and one workspace: the bits of calls with workspaces of their own."""
+    p = pasa()
+    B, H, D = 3, 2, 128
+    shapes = [(14, 20000, True), (14, 40000, False), (30, 40000, True), (14, 900, True), (30, 20000, False)]
+    sets = [(*filled(B, Hq, H, Sk, D, i), Hq, Sk, w) for i, (Hq, Sk, w) in enumerate(shapes)]
+    assert [shared_out(B, Hq, H, 1, Sk, D) for Hq, Sk, _ in shapes] == [True, True, True, False, True]
+    accs = [[torch.zeros((B, H, s[4]), device="cuda") if s[5] else None for s in sets] for _ in range(2)]
+    want = [p.attn_fwd_decode_kv4(q, *c, shift=sh, weights=a) for (q, c, sh, *_), a in zip(sets, accs[0])]
+    nbytes = max(p.decode_kv4_workspace_bytes(B, Hq, H, 1, Sk, D, w) for Hq, Sk, w in shapes)
+    assert nbytes > 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = []
+        for nth in range(4):
+            got.append([p.attn_fwd_decode_kv4(q, *c, shift=sh, weights=a if nth == 0 else None, workspace=ws)
+                        for (q, c, sh, *_), a in zip(sets, accs[1])])
+    side.synchronize()
+    for outs in got:
+        for (o, lse), (wo, wl) in zip(outs, want):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
+    for a, b in zip(*accs):
+        assert a is None or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("captured", [False, True], ids=["eager", "graph"])
+@pytest.mark.parametrize("D,Hq,cap", [(128, 14, 40000), (128, 30, 40000), (64, 14, 40000), (128, 14, 2600)])
+@pytest.mark.parametrize("weights", [False, True], ids=["", "weights"])
+def test_one_call_step_equals_its_parts(D, Hq, cap, weights, captured):
+    """attn_fwd_decode_step_kv4 as the batch grows unevenly (device positions), shared out and in clusters, four
+    steps without a synchronisation: bit for bit what the append and the decode give one by one. Captured: two graphs on one
+    workspace, each replayed for all steps."""
+    p = pasa()
+    B, H = 3, 2
+    assert shared_out(B, Hq, H, 1, cap, D) == (cap > 2600)
+    rng = np.random.default_rng(cap + Hq)
+    kt, vt = to_dev(rows(rng, B, H, cap, D, "bias"), rows(rng, B, H, cap, D, "plain"))
+    qs = to_dev(rng.standard_normal((4, B, Hq, 1, D)).astype(np.float16))[0]
+    first = torch.tensor([cap - 3, 0, cap // 3]).int().cuda()     # the last step of the first sequence falls outside
+    shift = kt[:, :, 0].contiguous()
+    new = [(kt[:, :, i:i + 1].contiguous(), vt[:, :, i:i + 1].contiguous()) for i in range(4)]
+
+    def state():
+        cache = new_cache(B, H, cap, D)
+        p.kv4_append(kt, vt, *cache, counts=first, shift=shift)
+        return cache, torch.zeros((B, H, cap), device="cuda") if weights else None, first.clone()
+
+    cache, acc, pos = state()
+    want = []
+    for i in range(4):
+        p.kv4_append(*new[i], *cache, start=pos, shift=shift)
+        pos += 1
+        want.append(p.attn_fwd_decode_kv4(qs[i], *cache, causal=True, shift=shift, lengths=pos, weights=acc))
+    torch.cuda.synchronize()
+    ws = torch.empty(max(1, p.decode_kv4_workspace_bytes(B, Hq, H, 1, cap, D, weights)), dtype=torch.uint8, device="cuda")
+
+    def step(s, q, k1, v1):
+        out = p.attn_fwd_decode_step_kv4(q, k1, v1, *s[0], s[2], causal=True, shift=shift, weights=s[1], workspace=ws)
+        s[2].add_(1)
+        return out
+
+    if captured:
+        states, graphs, ins, outs = [state(), state()], [], [], []
+        side = torch.cuda.Stream()
+        for s in states:
+            x = [qs[0].clone(), new[0][0].clone(), new[0][1].clone()]
+            side.wait_stream(torch.cuda.current_stream())
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                outs.append(step(s, *x))
+            graphs.append(g), ins.append(x)
+        torch.cuda.synchronize()
+        got = [[], []]
+        for i in range(4):
+            for j in range(2):
+                for a, b in zip(ins[j], (qs[i], *new[i])):
+                    a.copy_(b)
+                graphs[j].replay()
+                got[j].append([x.clone() for x in outs[j]])
+    else:
+        states = [state()]
+        got = [[step(states[0], qs[i], *new[i]) for i in range(4)]]
+    torch.cuda.synchronize()
+    for s, outs in zip(states, got):
+        for (o, lse), (wo, wl) in zip(outs, want):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
+        for a, b in zip(s[0], cache):
+            assert torch.equal(a, b)
+        assert s[1] is None or torch.equal(s[1], acc)
+
+
+@pytest.mark.parametrize("cap", [800, 14000])
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_through_steps_and_cuts(D, cap):
+    """The gathered weights of a serving loop, compared with the reference's running sums after every call: a window of
+    rows scores the prompt, the cache is cut in place, steps append a row and gather, with a second cut on the way.
+    Each call's bound is that of its own weights, and adding it to what was there rounds once (2^-24 of the
+    sum). Weights past a sequence's last row stay 0: an appended row starts at nothing."""
+    p = pasa()
+    B, Hq, H, W, recent = 2, 14, 2, 8, 40
+    S = cap - 100
+    budget = S * 3 // 7
+    g, scale = Hq // H, D ** -0.5
+    assert shared_out(B, Hq, H, 1, cap, D) == (cap > 800)
+    rng = np.random.default_rng(D + cap)
+    k, v = rows(rng, B, H, S + 6, D, "bias"), rows(rng, B, H, S + 6, D, "plain")
+    q = rng.standard_normal((B, Hq, S + 6, D)).astype(np.float16)
+    kt, vt, qt = to_dev(k, v, q)
+    part = lambda x, a, b: x[:, :, a:b].contiguous()   # noqa: E731
+    hs = k[:, :, 0].copy()
+    shift = to_dev(hs)[0]
+    cache = new_cache(B, H, cap, D)
+    p.kv4_append(part(kt, 0, S), part(vt, 0, S), *cache, shift=shift)
+    acc = torch.zeros((B, H, cap), device="cuda")
+    lengths = torch.tensor([S, S]).int().cuda()
+    kv, vv = kv4.values(*kv4.quantise(k[:, :, :S], hs)), kv4.values(*kv4.quantise(v[:, :, :S]))
+    total, bound = np.zeros((B, H, S)), np.zeros((B, H, S))
+
+    def compare(got, a, b):
+        nonlocal total, bound
+        n = kv.shape[2]
+        ref = kv4.decode(q[:, :, a:b], kv, vv, [n] * B, True, scale, hs)
+        bounds = decode_bounds(ref, scale, D, g, b - a, q[:, :, a:b], hs)
+        check(got, ref, bounds)
+        total = total + ref["weights"]
+        bound = bound + bounds[2] + 2.0 ** -24 * total * (1 + 2.0 ** -10)
+        w = acc.cpu().numpy().astype(np.float64)
+        assert (np.abs(w[:, :, :n] - total) <= bound).all()
+        assert (w[:, :, n:] == 0).all()
+
+    def cut():
+        nonlocal kv, vv, total, bound
+        w, n = acc.cpu().numpy(), kv.shape[2]
+        index, _ = p.cache_evict(cache, acc, budget, recent, lengths=lengths, new_lengths=lengths)
+        keep = np.array([[kv4.select(w[b, h], n, budget, recent) for h in range(H)] for b in range(B)])
+        assert np.array_equal(index.cpu().numpy(), keep) and lengths.tolist() == [budget] * B
+        kv, vv = (np.take_along_axis(x, keep[..., None], 2) for x in (kv, vv))
+        total, bound = (np.take_along_axis(x, keep, 2) for x in (total, bound))
+        w2 = acc.cpu().numpy()
+        assert np.array_equal(w2[:, :, :budget], np.take_along_axis(w, keep, 2)) and (w2[:, :, budget:] == 0).all()
+
+    got = p.attn_fwd_decode_kv4(part(qt, S - W, S), *cache, causal=True, shift=shift, lengths=lengths, weights=acc)
+    compare(got, S - W, S)
+    cut()
+    for i in range(S, S + 6):
+        if i == S + 4:
+            cut()
+        got = p.attn_fwd_decode_step_kv4(part(qt, i, i + 1), part(kt, i, i + 1), part(vt, i, i + 1), *cache, lengths,
+                                         causal=True, shift=shift, weights=acc)
+        lengths += 1
+        kv = np.concatenate([kv, kv4.values(*kv4.quantise(k[:, :, i:i + 1], hs))], 2)
+        vv = np.concatenate([vv, kv4.values(*kv4.quantise(v[:, :, i:i + 1]))], 2)
+        total, bound = (np.concatenate([x, np.zeros((B, H, 1))], 2) for x in (total, bound))
+        compare(got, i, i + 1)
+    p.check_device_error()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("Hq,Sk", [(16, 100), (16, 40000), (32, 100), (32, 40000)])   # 8 and 16 rows, two forms
+def test_a_query_that_is_not_finite_and_the_weights(Hq, Sk, bad):
+    """Its row's output and log-sum-exp are NaN, and so become the weights of the rows it sees in its kv head. The other
+    query rows, the other heads and the rows it does not see keep the bits of the call without it."""
+    p = pasa()
+    B, H, Sq, D = 1, 2, 2, 128
+    Hq = Hq // Sq
+    g = Hq // H
+    assert shared_out(B, Hq, H, Sq, Sk, D) == (Sk > 100)
+    q, cache, shift = filled(B, Hq, H, Sk, D, 31, Sq)
+    acc = torch.zeros((B, H, Sk), device="cuda")
+    o, lse = p.attn_fwd_decode_kv4(q, *cache, causal=True, shift=shift, weights=acc)
+    head = g + 1                      # of the second kv head; its first row sees all keys but the last
+    q[0, head, 0, 5] = bad
+    acc2 = torch.zeros_like(acc)
+    o2, lse2 = p.attn_fwd_decode_kv4(q, *cache, causal=True, shift=shift, weights=acc2)
+    assert torch.isnan(o2[0, head, 0]).all() and torch.isnan(lse2[0, head, 0])
+    keep = torch.ones((Hq, Sq), dtype=torch.bool, device="cuda")
+    keep[head, 0] = False
+    assert torch.equal(o[0][keep], o2[0][keep]) and torch.equal(lse[0][keep], lse2[0][keep])
+    assert torch.isnan(acc2[0, 1, :Sk - 1]).all()
+    assert torch.equal(acc[0, 0], acc2[0, 0]) and torch.equal(acc[0, 1, Sk - 1], acc2[0, 1, Sk - 1])
+    # an eviction takes those weights for the smallest: the recent rows stay, and the first of the others
+    index, _ = p.cache_evict(cache, acc2, 20, 5)
+    assert index[0, 1].tolist() == list(range(15)) + list(range(Sk - 5, Sk))
+
+
+def test_fp16_cache_cut_in_place_and_decoded():
+    """Eviction of fp16 keys and values in place, the shifted copy of the keys made again from the moved rows, then the
+    fp16 decode: the oracle's attention on the kept rows (the gates of the fp16 decode tests), at a budget that is no
+    multiple of a key block."""
+    p = pasa()
+    B, Hq, H, S, D, budget, recent = 2, 14, 2, 1500, 128, 700, 64
+    rng = np.random.default_rng(77)
+    k, v = rows(rng, B, H, S, D, "bias"), rows(rng, B, H, S, D, "plain")
+    q = rng.standard_normal((B, Hq, 1, D)).astype(np.float16)
+    w = rng.random((B, H, S)).astype(np.float32)
+    kt, vt, qt, wt = to_dev(k, v, q, w)
+    ks, means = p.kshift(kt)
+    index, new = p.cache_evict([kt, vt], wt, budget, recent)
+    keep = np.array([[kv4.select(w[b, h], S, budget, recent) for h in range(H)] for b in range(B)])
+    assert np.array_equal(index.cpu().numpy(), keep) and new.tolist() == [budget] * B
+    k2, v2 = (np.take_along_axis(x, keep[..., None], 2) for x in (k, v))
+    assert np.array_equal(kt[:, :, :budget].cpu().numpy(), k2) and np.array_equal(vt[:, :, :budget].cpu().numpy(), v2)
+    p.kshift_blocks(kt, ks, means, 0, length=budget)
+    o, _ = p.attn_fwd_decode(qt, ks, means, vt, mode=p.MODE_SHIFT_F32ACC, length=budget)
+    o_ref, _ = oracle.attention(q, k2, v2, causal=False)
+    assert rel_errors(o.cpu().numpy(), o_ref)[0] < 5e-3
+    p.check_device_error()
