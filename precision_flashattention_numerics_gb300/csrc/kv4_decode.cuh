@@ -49,6 +49,7 @@ namespace pasa {
 __host__ __device__ constexpr int kv4_warps(int nt) { return nt == 1 ? 8 : 12; }
 __host__ __device__ constexpr int kv4_ctas(int nt) { return nt == 1 ? 304 : 152; }   // on 152 SMs
 constexpr int kKv4WeightsWarps = 8;
+constexpr int kKv4Alone = 120 * 1024;   // dynamic shared memory with which a CTA has its SM alone
 constexpr int kKv4Unit = 32;    // keys a warp takes at a time
 constexpr int kKv4SegmentStart = 2;    // rounds that the start and end of a segment cost a CTA
 
@@ -955,8 +956,7 @@ struct Kv4WeightsSmem {
   int limit[128];
   Kv4QueryShared<D> q[16];   // as many as the rows have tiles of 8
 };
-constexpr int kKv4WeightsAlone = 120 * 1024;   // shared memory with which a CTA has its SM alone
-static_assert(sizeof(Kv4WeightsSmem<128>) <= kKv4WeightsAlone && 2 * sizeof(Kv4WeightsSmem<128>) <= 227 * 1024);
+static_assert(sizeof(Kv4WeightsSmem<128>) <= kKv4Alone && 2 * sizeof(Kv4WeightsSmem<128>) <= 227 * 1024);
 
 template <int D, bool ALONE>
 __global__ void __launch_bounds__(kKv4WeightsWarps * 32, ALONE ? 1 : 2) kv4_weights_kernel(Kv4Params p, int tile_rows) {

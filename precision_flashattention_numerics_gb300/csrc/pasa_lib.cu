@@ -1588,8 +1588,15 @@ cudaError_t launch_clusters(void (*kern)(Params...), unsigned grid, int block, i
 template <int D, int NT, bool STREAM_K>
 cudaError_t kv4_launch(const pasa::Kv4Params& p, unsigned grid, cudaStream_t st, bool pdl) {
   static std::atomic<unsigned long long> raised{0};
-  constexpr int smem = static_cast<int>(sizeof(pasa::Kv4Smem<D, NT>));
-  return launch_clusters(pasa::kv4_decode_kernel<D, NT, STREAM_K>, grid, pasa::kv4_warps(NT) * 32, smem, smem, st, pdl,
+  constexpr int need = static_cast<int>(sizeof(pasa::Kv4Smem<D, NT>)), most = std::max(need, pasa::kKv4Alone);
+  // In a step (pdl) the clusters' CTAs start while the append's still hold SMs, and would go two to an SM elsewhere: where
+  // there is an SM for each, it asks for one alone. GPU us of a step with 7 rows x 4 heads, two to an SM / alone / append and
+  // decode as two calls: 8 x 4096 keys 14.6 / 11.0 / 11.9, 16 x 4096 22.6 / 15.7 / 16.6, 24 x 2048 21.4 / 14.7 / 15.5, 1 x 2048
+  // 7.4 / 7.4 / 8.2, 512 new rows of 2 x 4096 11.0 / 8.8 / 9.7; with weights 8 x 4096 19.4 / 16.4, 6 x 4096 15.4 / 15.8.
+  // The decode call by itself takes the same either way (8 x 4096: 9.2), but with weights, whose kernel
+  // shares the SMs with it, longer alone (14.1 / 14.6).
+  const int smem = pdl && !STREAM_K && grid <= pasa::kv4_ctas(2) ? most : need;
+  return launch_clusters(pasa::kv4_decode_kernel<D, NT, STREAM_K>, grid, pasa::kv4_warps(NT) * 32, smem, most, st, pdl,
                          p.cluster, raised, p);
 }
 
@@ -1611,10 +1618,10 @@ cudaError_t kv4_decode_launch(const pasa::Kv4Params& p, const Kv4Plan& pl, cudaS
     int smem = static_cast<int>(offsetof(pasa::Kv4WeightsSmem<D>, q) + sizeof(pasa::Kv4QueryShared<D>) * ((p.rows + 7) / 8));
     const int rounds = pasa::kv4_rounds(pasa::kv4_units(p.Sk), pasa::kKv4WeightsWarps) + pasa::kKv4SegmentStart;
     const bool alone = p.rows > 8 && static_cast<long long>(p.B) * p.Hkv * rounds <= all / 2;
-    if (alone) smem = std::max(smem, pasa::kKv4WeightsAlone);
+    if (alone) smem = std::max(smem, pasa::kKv4Alone);
     static std::atomic<unsigned long long> raised{0}, raised_alone{0};
     e = launch_clusters(alone ? pasa::kv4_weights_kernel<D, true> : pasa::kv4_weights_kernel<D, false>,
-                        alone ? all / 2 : all, pasa::kKv4WeightsWarps * 32, smem, pasa::kKv4WeightsAlone, st, true, 1,
+                        alone ? all / 2 : all, pasa::kKv4WeightsWarps * 32, smem, pasa::kKv4Alone, st, true, 1,
                         alone ? raised_alone : raised, p, tile);
   }
   return e;
