@@ -640,7 +640,8 @@ def attn_fwd_decode_kv4(q, k4, kscale, v4, vscale, causal: bool = False, scale: 
     Hq / Hkv * Sq <= 128. The sequences hold `length` rows (default: all of the cache's) or
     lengths[b] (int32 tensor [B]; `length` is then an upper bound). With weights (fp32
     [B,Hkv,cap]) each cache row's softmax weight, summed over the kv head's query rows, is added
-    there. Returns (o, lse)."""
+    there (NaN for the rows that a query row with a NaN or an infinity sees). Outputs share no memory
+    with inputs, but without weights out may be q. Returns (o, lse)."""
     dev, stream = _here()
     ptrs, sp, (B, Hkv, cap, D) = _check_kv4(k4, kscale, v4, vscale, shift, dev)
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
@@ -700,7 +701,7 @@ def cache_evict(planes, weights, budget: int, recent: int = 0, length: int | Non
     heaviest of the others, in their old order (pasa_cache_evict). planes: a list of the cache's tensors
     [B,Hkv,cap,*], e.g. (k4, kscale, v4, vscale) or fp16 (k, v); weights fp32 [B,Hkv,cap]. The
     sequences hold `length` rows (default cap) or lengths[b] (int32 [B]). In place, or into out (tensors
-    [B,Hkv,out_cap,*]) and out_weights (fp32 [B,Hkv,out_cap]). Returns (index int32 [B,Hkv,budget]:
+    [B,Hkv,out_cap,*]) and out_weights (fp32 [B,Hkv,out_cap]) elsewhere. Returns (index int32 [B,Hkv,budget]:
     the old rows, -1 past the last; new_lengths int32 [B])."""
     dev, stream = _here()
     budget, recent = _int32(budget, "budget"), _int32(recent, "recent")

@@ -27,12 +27,15 @@
 // there, else its CTAs leave (O, max, sum) partials that kv4_merge_kernel joins. Which one is
 // chosen on the host by the sizes.
 //
-// Measured, GPU time of a call: 8 sequences x 4 kv heads x 32768 keys, D = 128, 7 rows: 34.5 us
-// for 151 MB, 0.66 of the copy rate; x 131072 keys 109 us, 0.83. Per 32 keys a warp issues about
-// 540 instructions, 135 cycles of an SM's issue slots where HBM takes 199; the shared-out ranges
-// run at 225. The rest is the start (lengths, shares and the first burst of codes, 4 us) and the
-// join. Expanding keys like values took 650 instructions (39.5 us); a third CTA per SM needs 80
-// registers and spills (44 us).
+// Measured, GPU time of a call in a replayed graph at 2070 MHz: 8 sequences x 4 kv heads x 32768 keys, D = 128, 7 rows:
+// 34.7 us for 151 MB, 0.65 of the copy rate; x 131072 keys 109.4 us, 0.83. The two differ by 239 cycles for each 32 keys of
+// an SM, where HBM alone takes 217 (0.91 of the copy rate) and a warp's 540 or so instructions take 135 of the SM's
+// issue slots. The other 9.7 us do not grow with the keys: 1.7 that any kernel takes in a graph, 3.2 for lengths, shares, the
+// first keys and the join (a call of this form with 32 keys in each sequence takes 4.9 without its merge), 2.8 for the
+// merge kernel (1.0 where it has nothing to join), and about 2 for the first burst of codes of all CTAs at once and an uneven
+// end. Expanding keys like values took 650 instructions (39.5 us); a third CTA per SM needs 80 registers and spills
+// (44 us). With D = 128 the kernels kept spill a little too, bytes stored by a thread: shared out 24 (8 rows) and 32 (16),
+// in clusters 4 and 0.
 #pragma once
 
 #include <cmath>
@@ -45,7 +48,7 @@
 namespace pasa {
 
 // Warps of a CTA and CTAs of an SM, by the tile's rows / 8: 2 x 8 warps of 128 registers, or with 16 rows, whose
-// accumulators take twice as many, 1 x 12 of 168 (16 rows x 131072 keys x 8: 145 us; 2 x 8, which spill, 159).
+// accumulators take twice as many, 1 x 12 of 168 (16 rows x 131072 keys x 8: 145 us; 2 x 8, which spill more, 159).
 __host__ __device__ constexpr int kv4_warps(int nt) { return nt == 1 ? 8 : 12; }
 __host__ __device__ constexpr int kv4_ctas(int nt) { return nt == 1 ? 304 : 152; }   // on 152 SMs
 constexpr int kKv4WeightsWarps = 8;

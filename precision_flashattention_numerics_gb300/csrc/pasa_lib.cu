@@ -1487,9 +1487,10 @@ int launch_status() {
   return e == cudaSuccess ? PASA_OK : cuda_fail(e);
 }
 
-// How a decode call is laid out: query rows in tiles of 8 (NT = 1) or 16, and either one CTA per
+// How a decode call is laid out: query rows in tiles of 8 (NT = 1) or 16, and either a cluster of CTAs per
 // (sequence, kv head, row tile), or a fixed number of CTAs sharing all their keys evenly with
-// partial results in the workspace.
+// partial results in the workspace. The numbers of CTAs and clusters (here, in kv4_ctas and in the eviction's
+// clusters) are those of GB300's 152 SMs: right on any number, chosen for that one.
 constexpr int kKv4MaxKeys = INT_MAX - 65536;   // key numbers past the last unit's fit an int
 
 struct Kv4Plan {
@@ -1612,8 +1613,10 @@ cudaError_t kv4_decode_launch(const pasa::Kv4Params& p, const Kv4Plan& pl, cudaS
   if (e == cudaSuccess && p.weights) {
     // Two CTAs per SM share the longest cases best. Where one to each SM is enough, two would pile up on the SMs
     // that the decode does not hold when they start; alone, a CTA has the registers to take both halves of a
-    // unit side by side. With more than 8 rows that counts: 112 rows x 4 heads, GPU us of a call alone / two,
-    // 8192 keys (136 rounds) 25.6 / 29.6, 131072 keys 194.6 / 187; with 7 rows x 8192 keys 12.7 / 12.3.
+    // unit side by side, which counts with more than 8 rows. GPU us of a call, two / alone, 4 heads: 112 rows x 1024 keys (24
+    // rounds) 16.3 / 15.6, x 4096 (72) 23.6 / 20.1, x 8192 (136) 28.1 / 24.6, x 9600 (160) 28.2 / 28.3, x 16384 (264) 35.6 /
+    // 36.0, x 131072 187 / 195; 56 rows x 8192 21.4 / 19.9; 28 rows x 8192 17.8 / 16.7, x 16384 23.6 / 23.6; 16 rows x 8192
+    // 16.4 / 15.9; 9 rows x 1024 10.6 / 10.4; 7 rows x 2048 8.5 / 8.4, x 8192 12.5 / 12.7.
     const int all = pasa::kv4_ctas(1);
     int smem = static_cast<int>(offsetof(pasa::Kv4WeightsSmem<D>, q) + sizeof(pasa::Kv4QueryShared<D>) * ((p.rows + 7) / 8));
     const int rounds = pasa::kv4_rounds(pasa::kv4_units(p.Sk), pasa::kKv4WeightsWarps) + pasa::kKv4SegmentStart;
