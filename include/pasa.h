@@ -543,7 +543,8 @@ int pasa_attn_fwd_decode_step_kv4(const void* q, const void* k, const void* v, v
  *            fp16 keys and values with D = 128.
  *   lengths  int32 [B], device, or NULL for Sk: rows of each sequence, within 0 .. Sk.
  *   index    int32 [B, Hkv, budget], out: the old row of each kept one, -1 past the last.
- *   new_lengths  int32 [B], out, or NULL: min(length, budget); may be `lengths` itself.
+ *   new_lengths  int32 [B], out, or NULL: min(length, budget); may be `lengths` itself. Apart from that
+ *            index and new_lengths share no memory with another tensor of the call.
  * A shifted or e4m3 copy of the keys (pasa_kshift, pasa_kprep_fp8) depends on whole key
  * blocks: make it again from the moved keys.
  */
