@@ -552,6 +552,59 @@ int pasa_cache_evict(const void* const* planes, void* const* out_planes, const i
                      const float* weights, float* out_weights, const int* lengths, int* index, int* new_lengths, int B,
                      int Hkv, int Sk, int Sk_cap, int out_cap, int budget, int recent, void* stream);
 
+/* Element types (the `in_type` and `out_type` arguments of pasa_rope). */
+#define PASA_TYPE_F16 0
+#define PASA_TYPE_BF16 1
+#define PASA_TYPE_F32 2
+
+/* How rotary frequencies are scaled for long contexts (`scaling` of pasa_rope_frequencies). */
+#define PASA_ROPE_PLAIN 0    /* f_i = base^(-2 i / rotary_dim) */
+#define PASA_ROPE_LINEAR 1   /* f_i / factor: positions squeezed into the original range */
+#define PASA_ROPE_BASE 2     /* base * factor^(R / (R - 2)): the slowest pair is squeezed, the fastest is not */
+#define PASA_ROPE_BY_PARTS 3 /* pairs that turn fewer than `low` times over original_length positions are squeezed
+                                by factor, those that turn more than `high` times stay, in between a blend */
+
+/*
+ * Rotary frequencies, on the HOST: inv_freq[i], i < rotary_dim / 2, in radians per position and in 64
+ * bits, for pasa_rope (copied to the device by the caller, once). (No counterpart in the
+ * paper: its Abstract's Q/K resonance is what rotary positions make of the channels. The scalings
+ * are those of arXiv 2306.15595 (linear) and arXiv 2309.00071, sections 3.1 (base) and 3.2 (by
+ * parts), with its ramp over r = original_length * f_i / 2 pi turns: f_i * (gamma + (1 - gamma) / factor), gamma = (r - low)
+ * / (high - low) within 0 .. 1.)
+ *   mscale  HOST, or NULL: the factor that goes with them: 0.1 ln(factor) + 1 by parts, else 1. (Both
+ *           of q and k are multiplied by it.)
+ * rotary_dim is even, 2 .. 256; base > 1; factor >= 1; original_length > 0, 0 <= low < high by parts.
+ * Else PASA_ERR_SHAPE, an unknown scaling is PASA_ERR_UNSUPPORTED. Arguments that a scaling does not take are not looked at.
+ */
+int pasa_rope_frequencies(double* inv_freq, float* mscale, int rotary_dim, double base, int scaling, double factor,
+                          double original_length, double low, double high);
+
+/*
+ * Rotary positions of q [B, Hq, S, D] and k [B, Hkv, S, D]: of each row's first rotary_dim channels, every pair (x, y)
+ * becomes (x cos a - y sin a, x sin a + y cos a) * mscale, a = position * inv_freq[i]; pairs are (i, i +
+ * rotary_dim / 2), or with `interleaved` (2i, 2i + 1). The other channels are copied. Angles are
+ * exact to fp32 at any position; the arithmetic is fp32, rounded once.
+ *   q_strides, k_strides  HOST arrays of 6: elements from one b, h and s to the next, of the input and
+ *              then of the output; channels are contiguous. Packed tensors [T, H, D], views of a
+ *              fused projection and [B, H, S, D] are all such. Any strides >= 0 and any alignment of the element
+ *              type are taken; rows on 16-byte boundaries with rotary_dim a multiple of 16 and D of 8 are fast.
+ *   k          with Hkv = 0: q alone, k, k_out and k_strides may be NULL
+ *   inv_freq   device, 64 bits, [rotary_dim / 2], 8-byte aligned
+ *   positions  int32 [B, S], device, contiguous, or NULL: token s of sequence b is at starts[b] + s (int32 [B],
+ *              device), or start + s where starts is NULL too. Negative positions turn backwards.
+ *   inverse    nonzero: by -a, which undoes the rotation (times mscale^2) and is its transpose: the gradient of
+ *              an input from that of the output.
+ *   in_type, out_type  PASA_TYPE_*; out_type is in_type or PASA_TYPE_F16 (a value past 65504 is stored as infinity)
+ * q_out may be q itself (same strides and type), and k_out k; otherwise outputs share no memory with inputs,
+ * with one another or within themselves (PASA_ERR_SHAPE; views side by side in the rows of one
+ * buffer do not count as sharing). D is even and at most 256, rotary_dim even and at most D, B * S and the channels of a call in
+ * units of 16 fit 31 and 32 bits, else PASA_ERR_SHAPE. An infinity or NaN spoils its own pair only.
+ */
+int pasa_rope(const void* q, void* q_out, const long long* q_strides, int Hq, const void* k, void* k_out,
+              const long long* k_strides, int Hkv, const double* inv_freq, const int* positions, const int* starts,
+              int start, int B, int S, int D, int rotary_dim, int interleaved, int inverse, float mscale, int in_type,
+              int out_type, void* stream);
+
 /*
  * Synchronise `stream` and read the device error word. Returns PASA_OK, PASA_ERR_TIMEOUT
  * (a pipeline wait gave up; `info`, if not NULL, receives the CTA index << 32 | wait site)

@@ -22,6 +22,7 @@ __all__ = [
     "MODE_SHIFT_F16ACC", "MODE_SHIFT_F32ACC", "MODE_NAIVE_F16ACC", "MODE_NOSHIFT_F32ACC", "MODE_SHIFT_F16ALL", "MODE_SHIFT_FP8", "MODE_NAIVE_FP8", "kprep_fp8", "attn_fwd_fp8",
     "PasaError", "attn_fwd", "attn_fwd_alloc", "attn_fwd_fused", "attn_fwd_shifted", "attn_fwd_stats", "kshift", "workspace_bytes", "check_device_error", "block_rows",
     "kv4_append", "kv4_read", "attn_fwd_decode_kv4", "attn_fwd_decode_step_kv4", "cache_evict",
+    "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BASE", "ROPE_BY_PARTS", "rope_frequencies", "rope",
     "library", "library_path",
 ]
 
@@ -32,6 +33,10 @@ MODE_NOSHIFT_F32ACC = 3
 MODE_SHIFT_F16ALL = 4   # mode 0 with an fp16 PV accumulator and an fp16 running row sum
 MODE_SHIFT_FP8 = 5      # e4m3 Q and shifted keys, fp32 score accumulation (D = 128)
 MODE_NAIVE_FP8 = 6      # e4m3 Q and raw keys, no shift (D = 128)
+ROPE_PLAIN = 0          # how rope_frequencies scales for long contexts
+ROPE_LINEAR = 1
+ROPE_BASE = 2
+ROPE_BY_PARTS = 3
 MEAN_GRID = 0           # block average rules for kshift
 MEAN_PLAIN = 1
 
@@ -41,7 +46,7 @@ _lock = threading.Lock()
 _lib = None
 
 # exported symbols and their ctypes signatures, mirroring include/pasa.h
-_P, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_P, _I, _F, _SZ, _D = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_double
 SIGNATURES = {
     "pasa_block_rows": ([_I], _I),
     "pasa_attn_fwd": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P], _I),
@@ -73,6 +78,8 @@ SIGNATURES = {
     "pasa_attn_fwd_decode_kv4": ([_P] * 10 + [_I] * 8 + [_F, _P, _SZ, _P], _I),
     "pasa_attn_fwd_decode_step_kv4": ([_P] * 9 + [_I] + [_P] * 3 + [_I] * 9 + [_F, _P, _SZ, _P], _I),
     "pasa_cache_evict": ([_P, _P, _P, _I] + [_P] * 5 + [_I] * 7 + [_P], _I),
+    "pasa_rope_frequencies": ([_P, _P, _I, _D, _I, _D, _D, _D, _D], _I),
+    "pasa_rope": ([_P] * 3 + [_I] + [_P] * 3 + [_I] + [_P] * 3 + [_I] * 7 + [_F, _I, _I, _P], _I),
     "pasa_check_device_error": ([_P, ctypes.POINTER(ctypes.c_ulonglong)], _I),
     "pasa_selftest_wait_timeout": ([_P], _I),
     "pasa_selftest_exp2": ([_P, _P, _P, _I, _P], _I),
@@ -748,6 +755,94 @@ def cache_evict(planes, weights, budget: int, recent: int = 0, length: int | Non
     if rc != 0:
         raise PasaError(rc, "pasa_cache_evict")
     return index, new_lengths
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+                     original_length: float = 0.0, low: float = 1.0, high: float = 32.0, device="cuda"):
+    """(inv_freq, mscale) for :func:`rope`: the radians per position of rotary_dim / 2 pairs, an fp64
+    tensor on `device`, scaled for long contexts by a ROPE_* rule (ROPE_BY_PARTS: pairs that turn less than
+    `low` times over original_length positions are slowed by factor, those that turn more than `high`
+    times are not)."""
+    n = _int32(rotary_dim, "rotary_dim")
+    freq = torch.empty(max(0, n // 2), dtype=torch.float64)
+    mscale = ctypes.c_float(1.0)
+    rc = library().pasa_rope_frequencies(freq.data_ptr(), ctypes.addressof(mscale), n, float(base), int(scaling), float(factor),
+                                         float(original_length), float(low), float(high))
+    if rc != 0:
+        raise PasaError(rc, "pasa_rope_frequencies")
+    return freq.to(device), mscale.value
+
+
+_ROPE_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _rope_strides(x, name, dtype, shape, device):
+    """The strides of b, h and s of [B,H,S,D], or of packed [T,H,D] (B = 1)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA {dtype} tensor")
+    if x.get_device() != device:
+        raise ValueError(f"{name} is on device {x.get_device()}, the current device is {device}")
+    if x.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    *st, last = x.stride()
+    if last != 1:
+        raise ValueError(f"{name}'s channels are not contiguous")
+    return st if len(st) == 3 else [0, st[1], st[0]]
+
+
+def rope(q, k, inv_freq, positions=None, start=0, interleaved: bool = False, mscale: float = 1.0, inverse: bool = False,
+         out_q=None, out_k=None):
+    """Rotary positions of q [B,Hq,S,D] and k [B,Hkv,S,D], or packed [T,Hq,D] and [T,Hkv,D] (k may be None):
+    fp16, bf16 or fp32, any strides with contiguous channels. inv_freq: fp64 [R/2], see
+    :func:`rope_frequencies`; the first R channels turn, in pairs (i, i + R/2) or, interleaved, (2i, 2i + 1).
+    positions: int32 [B,S] (packed: [T]); without them token s is at start + s, start an int or int32 [B].
+    inverse turns back, which is also the gradient: dq, dk = rope(dout_q, dout_k, ..., inverse=True).
+    out_q and out_k are new fp16 tensors unless given: of the inputs' type or fp16; q and k themselves for a
+    rotation in place. Returns (out_q, out_k)."""
+    dev, stream = _here()
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("expected q [B,Hq,S,D] or [T,Hq,D]")
+    packed = q.dim() == 3
+    if packed:
+        (S, Hq, D), B = q.shape, 1
+    else:
+        B, Hq, S, D = q.shape
+    dtype = q.dtype
+    if dtype not in _ROPE_TYPES:
+        raise TypeError("q must be fp16, bf16 or fp32")
+    if k is None:
+        if out_k is not None:
+            raise ValueError("out_k without k")
+        Hkv, kshape = 0, None
+    else:
+        if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+            raise ValueError("expected k [B,Hkv,S,D] or [T,Hkv,D], as q")
+        Hkv = k.shape[1]
+        kshape = (S, Hkv, D) if packed else (B, Hkv, S, D)
+    if out_q is None:
+        out_q = torch.empty(q.shape, device=q.device, dtype=torch.float16 if out_k is None else out_k.dtype)
+    out_dtype = out_q.dtype
+    if out_k is None and k is not None:
+        out_k = torch.empty(kshape, device=q.device, dtype=out_dtype)
+    if out_dtype not in _ROPE_TYPES:
+        raise TypeError("outputs must be fp16, bf16 or fp32")
+    table = array.array("q", _rope_strides(q, "q", dtype, q.shape, dev) + _rope_strides(out_q, "out_q", out_dtype, q.shape, dev))
+    if k is not None:
+        table.extend(_rope_strides(k, "k", dtype, kshape, dev) + _rope_strides(out_k, "out_k", out_dtype, kshape, dev))
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("expected inv_freq [R/2]")
+    R = 2 * inv_freq.shape[0]
+    fp = _check_cuda(inv_freq, "inv_freq", torch.float64, (R // 2,), dev)
+    pp = None if positions is None else _check_cuda(positions, "positions", _I32, (S,) if packed else (B, S), dev)
+    starts, first = _per_sequence(start, "start", B, dev)
+    at = table.buffer_info()[0]
+    rc = library().pasa_rope(q.data_ptr(), out_q.data_ptr(), at, Hq, None if k is None else k.data_ptr(),
+                             None if k is None else out_k.data_ptr(), at + 48, Hkv, fp, pp, starts, first, B, S, D, R,
+                             int(bool(interleaved)), int(bool(inverse)), float(mscale), _ROPE_TYPES[dtype],
+                             _ROPE_TYPES[out_dtype], stream)
+    if rc != 0:
+        raise PasaError(rc, "pasa_rope")
+    return out_q, out_k
 
 
 def selftest_wait_timeout():

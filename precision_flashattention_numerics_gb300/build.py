@@ -1,44 +1,75 @@
-"""Build libpasa.so in-tree with nvcc for sm_103a (one translation unit, seconds)."""
+"""Build libpasa.so in-tree with nvcc for sm_103a: one object for each csrc/*.cu, side by side, then
+linked. An object is made again when its source, or a header it included, is newer."""
 from __future__ import annotations
 
 import os
 import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-SRC = os.path.join(HERE, "csrc", "pasa_lib.cu")
+CSRC = os.path.join(HERE, "csrc")
+OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpasa.so")
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",
     "-gencode", "arch=compute_103a,code=sm_103a",
-    "-shared", "-Xcompiler", "-fPIC",
+    "-Xcompiler", "-fPIC",
 ]
 
 
-def _sources():
-    out = [os.path.join(HERE, "..", "include", "pasa.h")]
-    for f in sorted(os.listdir(os.path.join(HERE, "csrc"))):
-        out.append(os.path.join(HERE, "csrc", f))
-    return out
+def _units():
+    return sorted(f[:-3] for f in os.listdir(CSRC) if f.endswith(".cu"))
+
+
+def _newer(target: str, sources) -> bool:
+    """Whether target is missing or older than one of its sources (a missing source counts as new)."""
+    if not os.path.exists(target):
+        return True
+    t = os.path.getmtime(target)
+    return any(not os.path.exists(s) or os.path.getmtime(s) > t for s in sources)
+
+
+def _depends(unit: str):
+    """What the object of a unit was made from: this file, and the sources its dependency file lists."""
+    try:
+        with open(os.path.join(OBJ, unit + ".d")) as f:
+            listed = f.read().replace("\\\n", " ").partition(":")[2].split()
+    except OSError:
+        return [os.path.join(CSRC, unit + ".missing")]
+    return [os.path.abspath(__file__)] + [s for s in listed if os.path.abspath(s).startswith(os.path.dirname(HERE))]
+
+
+def _stale(unit: str) -> bool:
+    return _newer(os.path.join(OBJ, unit + ".o"), _depends(unit))
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(s) > t for s in _sources())
+    return any(_stale(u) for u in _units()) or _newer(LIB, [os.path.join(OBJ, u + ".o") for u in _units()])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/pasa_lib.cu into libpasa.so next to this file; returns its path."""
+    """Compile the units that changed and link libpasa.so next to this file; returns its path."""
     if not force and not needs_build():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *NVCC_FLAGS, "-o", tmp, SRC]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    os.makedirs(OBJ, exist_ok=True)
+    tag = f".tmp{os.getpid()}"
+    running = []
+    for unit in _units():
+        if force or _stale(unit):
+            obj, dep = os.path.join(OBJ, unit + ".o"), os.path.join(OBJ, unit + ".d")
+            cmd = [nvcc, *NVCC_FLAGS, "-c", "-MMD", "-MF", dep + tag, "-o", obj + tag, os.path.join(CSRC, unit + ".cu")]
+            if verbose:
+                cmd.insert(1, "-Xptxas=-v")
+            running.append((subprocess.Popen(cmd), obj, dep))
+    failed = [p.args for p, _, _ in running if p.wait() != 0]   # all of them end before one is reported
+    if failed:
+        raise subprocess.CalledProcessError(1, failed[0])
+    for _, obj, dep in running:
+        os.replace(dep + tag, dep)
+        os.replace(obj + tag, obj)
+    subprocess.run([nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", "-o", LIB + tag,
+                    *(os.path.join(OBJ, u + ".o") for u in _units())], check=True)
+    os.replace(LIB + tag, LIB)
     return LIB
 
 

@@ -19,12 +19,15 @@
 #include "attn_fwd2s.cuh"
 #include "decode_fwd.cuh"
 #include "evict.cuh"
+#include "host_util.cuh"
 #include "kv4_decode.cuh"
 #include "kv4_store.cuh"
 #include "kshift.cuh"
 #include "ptx.cuh"
 
 namespace pasa {
+
+thread_local int t_last_cuda_error = 0;
 
 // Site tag the self-test below records in the device error word.
 constexpr uint32_t kSelftestSite = 0x5E1F7E57u;
@@ -65,57 +68,6 @@ __global__ void exp2_selftest_kernel(const float* __restrict__ x, float* __restr
 }  // namespace pasa
 
 namespace {
-
-thread_local int t_last_cuda_error = 0;
-
-int cuda_fail(cudaError_t e) {
-  t_last_cuda_error = static_cast<int>(e);
-  return PASA_ERR_CUDA;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
-}
-
-// 3-D fp16 view [planes, rows, D] of a contiguous tensor, 128-byte swizzled boxes of
-// 64 x box_rows x 1 elements.
-// 3-D map (D, rows, planes) with 128-byte rows per box chunk: 64 fp16 or 128 one-byte elements.
-// 3-D map over [planes][rows][D] with planes stride_rows rows apart (0: rows, dense).
-int make_map(CUtensorMap* m, const void* base, int D, long long rows, long long planes, int box_rows,
-             int elem_bytes = 2, long long stride_rows = 0) {
-  auto enc = encode_fn();
-  if (!enc) return cuda_fail(cudaErrorNotSupported);
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(planes)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * elem_bytes, static_cast<cuuint64_t>(stride_rows > 0 ? stride_rows : rows) * D * elem_bytes};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem_bytes), static_cast<cuuint32_t>(box_rows), 1};
-  cuuint32_t es[3] = {1, 1, 1};
-  CUresult r = enc(m, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                   const_cast<void*>(base), dims, strides, box, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
-  return PASA_OK;
-}
-
-int check_device() {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e);
-  return pasa_device_supported(dev) ? PASA_OK : PASA_ERR_UNSUPPORTED;
-}
 
 bool fp8_mode(int mode) { return mode == PASA_MODE_SHIFT_FP8 || mode == PASA_MODE_NAIVE_FP8; }
 
@@ -177,27 +129,6 @@ int kshift_dispatch(const void* k, void* ks, void* means, float* kscale, int B, 
     return launch_kshift<128, pasa::kRawFp8>(k, ks, means, kscale, B, H, Sk, st, first_block, cap);
   return D == 64 ? launch_kshift<64, pasa::kShiftF16>(k, ks, means, nullptr, B, H, Sk, st, first_block, cap)
                  : launch_kshift<128, pasa::kShiftF16>(k, ks, means, nullptr, B, H, Sk, st, first_block, cap);
-}
-
-// Launch `kern` on `st`; with pdl, by programmatic stream serialization: the kernel may start
-// while the kernel queued just ahead of it (the key preparation of the same call) still
-// runs, and waits for it with griddep_wait() before reading what it writes.
-template <typename... Params, typename... Args>
-cudaError_t launch_kernel(void (*kern)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t st, bool pdl,
-                          Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  if (pdl) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
 template <int D, bool F16ACC, bool SHIFT, bool CAUSAL, bool STATS, bool F16PV = false, bool FP8 = false>
@@ -962,19 +893,11 @@ int pasa_selftest_exp2(const float* x, float* poly, float* mufu, int n, void* st
 int pasa_check_device_error(void* stream, unsigned long long* info) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
-  int word = 0;
-  unsigned long long inf = 0;
-  e = cudaMemcpyFromSymbol(&word, pasa::g_device_error, sizeof(int));
-  if (e != cudaSuccess) return cuda_fail(e);
-  e = cudaMemcpyFromSymbol(&inf, pasa::g_device_error_info, sizeof(inf));
-  if (e != cudaSuccess) return cuda_fail(e);
-  if (word == pasa::kDeviceOk) return PASA_OK;
-  const int zero = 0;
-  const unsigned long long zero64 = 0;
-  cudaMemcpyToSymbol(pasa::g_device_error, &zero, sizeof(int));
-  cudaMemcpyToSymbol(pasa::g_device_error_info, &zero64, sizeof(zero64));
-  if (info) *info = inf;
-  return PASA_ERR_TIMEOUT;
+  // every translation unit has a word of its own; the first error found is reported, the others at the next calls
+  int rc = take_device_error(info);
+  if (rc == PASA_OK) rc = pasa::packed_take_device_error(info);
+  if (rc == PASA_OK) rc = pasa::tree_take_device_error(info);
+  return rc;
 }
 
 }  // extern "C"
@@ -1418,56 +1341,6 @@ extern "C" int pasa_attn_fwd_host(const void* q, const void* k, const void* v, v
 // ---------------------------------------------------------------------------------------
 namespace {
 
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-// The memory of a tensor: rows * row_bytes bytes from `at` on (to the last address, if that is past it); none
-// for a null pointer. Two spans meet where they share a byte.
-struct Span {
-  uintptr_t begin = 0, end = 0;
-  Span() = default;
-  Span(const void* at, unsigned long long rows, unsigned long long row_bytes) {
-    if (!at) return;
-    unsigned long long bytes;
-    begin = reinterpret_cast<uintptr_t>(at);
-    if (__builtin_mul_overflow(rows, row_bytes, &bytes) || __builtin_add_overflow(begin, bytes, &end)) end = UINTPTR_MAX;
-  }
-  bool meets(const Span& x) const { return begin < x.end && x.begin < end; }
-};
-
-// The cache tensors and sizes that every kv4 entry point takes.
-int kv4_validate(const void* k4, const void* kscale, const void* v4, const void* vscale, const void* shift, int B,
-                 int Hkv, int Sk_cap, int D) {
-  if (!k4 || !kscale || !v4 || !vscale) return PASA_ERR_NULLPTR;
-  if (B <= 0 || Hkv <= 0 || Sk_cap <= 0) return PASA_ERR_SHAPE;
-  if (static_cast<long long>(B) * Hkv > INT_MAX) return PASA_ERR_SHAPE;
-  if (D != 64 && D != 128) return PASA_ERR_UNSUPPORTED;
-  if (!aligned16(k4) || !aligned16(kscale) || !aligned16(v4) || !aligned16(vscale) || !aligned16(shift))
-    return PASA_ERR_ALIGN;
-  return PASA_OK;
-}
-
-// Whether `out` shares memory with one of `others`, or two of its own do.
-bool any_meet(std::initializer_list<Span> out, std::initializer_list<Span> others) {
-  for (const Span* a = out.begin(); a != out.end(); ++a) {
-    for (const Span* b = a + 1; b != out.end(); ++b)
-      if (a->meets(*b)) return true;
-    for (const Span& b : others)
-      if (a->meets(b)) return true;
-  }
-  return false;
-}
-
-// A call's cache tensors.
-struct Kv4Spans {
-  Span k4, kscale, v4, vscale, shift;
-  Kv4Spans(const void* k4p, const void* ksp, const void* v4p, const void* vsp, const void* shiftp, int B, int Hkv, int cap, int D) {
-    const unsigned long long heads = static_cast<unsigned long long>(B) * Hkv, rows = heads * cap;
-    k4 = Span(k4p, rows, D / 2), v4 = Span(v4p, rows, D / 2);
-    kscale = Span(ksp, rows, D / 16), vscale = Span(vsp, rows, D / 16);
-    shift = Span(shiftp, heads, 2 * D);
-  }
-};
-
 // kv4_append and kv4_read share their arguments: n rows of k and v from cache row `start` on.
 int kv4_window(const void* k, const void* v, const int* starts, int start, const int* counts, int n, int B, int Hkv,
                int Sk_cap, int D, bool append, pasa::Kv4Window* win, dim3* grid) {
@@ -1480,11 +1353,6 @@ int kv4_window(const void* k, const void* v, const int* starts, int start, const
   *win = pasa::Kv4Window{starts, counts, start, n, Sk_cap};
   *grid = dim3(static_cast<unsigned>((n + per_block - 1) / per_block), static_cast<unsigned>(std::min(B * Hkv, 65535)));
   return PASA_OK;
-}
-
-int launch_status() {
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? PASA_OK : cuda_fail(e);
 }
 
 // How a decode call is laid out: query rows in tiles of 8 (NT = 1) or 16, and either a cluster of CTAs per
@@ -1545,45 +1413,6 @@ Kv4Plan kv4_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, bool weights) {
   pl.lse2 = pl.part_ml + align_up(slots * tile * 8, 256);
   pl.total = pl.lse2 + (weights ? align_up(static_cast<size_t>(pl.segments) * tile * 4, 256) : 0);
   return pl;
-}
-
-// Launch `kern` in clusters of `cluster` CTAs with `smem` bytes of dynamic shared memory, `max_smem`
-// at most in any call. The limit on those is raised at the first launch on a device (bit of
-// `raised`), and again if a launch fails (the device was reset).
-template <typename... Params>
-cudaError_t launch_clusters(void (*kern)(Params...), unsigned grid, int block, int smem, int max_smem,
-                            cudaStream_t st, bool pdl, int cluster, std::atomic<unsigned long long>& raised, Params... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  cfg.attrs = attr;
-  if (pdl) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (cluster > 1) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attr[cfg.numAttrs].val.clusterDim.x = cluster;
-    attr[cfg.numAttrs].val.clusterDim.y = 1;
-    attr[cfg.numAttrs++].val.clusterDim.z = 1;
-  }
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (dev < 64 && (raised.load(std::memory_order_relaxed) & bit) != 0) {
-    e = cudaLaunchKernelEx(&cfg, kern, args...);
-    if (e == cudaSuccess) return e;
-    (void)cudaGetLastError();
-  }
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
-  if (e != cudaSuccess) return e;
-  e = cudaLaunchKernelEx(&cfg, kern, args...);
-  if (e == cudaSuccess) raised.fetch_or(bit, std::memory_order_relaxed);
-  return e;
 }
 
 template <int D, int NT, bool STREAM_K>

@@ -23,11 +23,11 @@ enum : int {
   kDeviceErrTimeout = 1,
 };
 
-// Defined here: the library is compiled as a single translation unit that includes this
-// header once. g_device_error and g_device_error_info latch the first timeout until the host
-// reads them (pasa_check_device_error); no kernel reads them.
-__device__ int g_device_error = 0;
-__device__ unsigned long long g_device_error_info = 0;
+// Defined here, static: each translation unit that includes this header has a word of its own, in
+// which g_device_error and g_device_error_info latch its first timeout until the host reads them
+// (pasa_check_device_error asks every unit); no kernel reads them.
+static __device__ int g_device_error = 0;
+static __device__ unsigned long long g_device_error_info = 0;
 
 constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;  // 2 s per wait
 

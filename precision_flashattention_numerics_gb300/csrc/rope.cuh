@@ -1,0 +1,203 @@
+// Rotary positions: the first R of a row's D channels are turned in pairs by angles that grow with
+// the token's position.
+//
+// A pair (x, y) of a token at position p becomes (x c - y s, x s + y c), c = mscale cos a, s = mscale
+// sin a, a = p * inv_freq[i]; pairs are (i, i + R / 2) (the half layout) or (2i, 2i + 1) (interleaved).
+// Backwards (the transpose, which is also the gradient) with -s.
+//
+// The angle. In fp32 the product p * inv_freq is off by half a unit of its last place, 0.03 radians
+// at p = 10^6; in fp64 it takes the few fp64 units of an SM as long as the whole kernel. Only
+// the fraction of a turn counts, so inv_freq / 2 pi is held as a 64-bit fraction of a turn and p times
+// it is one 64-bit integer product, whose overflow drops whole turns. Its upper 32 bits are the
+// fraction in units of 2^-32, and sinpi and cospi of them in fp32 are off by 2^-24 or so at
+// any position.
+//
+// HBM-bound: every channel is read once and written once, with 16-byte accesses. A thread takes two
+// vectors of 8 channels, which hold 8 whole pairs in either layout, of `per` heads of one token, so that
+// a token's 8 angles serve several rows. The table of fractions is made once per CTA (its fp64
+// arithmetic in every thread would take longer than the copy), behind the rows' loads.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ptx.cuh"
+
+namespace pasa {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeHeads = 4;   // heads of a thread at most
+constexpr int kRopeMaxD = 256;
+
+// One tensor [B, H, S, D], channels contiguous; strides in elements.
+struct RopeTensor {
+  const void* in;
+  void* out;
+  long long in_b, in_h, in_s, out_b, out_h, out_s;
+};
+
+struct RopeParams {
+  RopeTensor t[2];          // q and k
+  int Hq, heads;            // heads of q, and of both
+  const double* inv_freq;   // [R / 2] radians per position
+  const int* positions;     // [B, S], or nullptr:
+  const int* starts;        // [B], or nullptr: token s of sequence b is at starts[b] (or start) + s
+  int start;
+  int S, D, R;
+  unsigned tokens, slots, groups;   // B * S; head slots of a token; channel groups of a row
+  int per;                          // heads of a thread
+  float mscale, sign;
+};
+
+// The fraction of a turn per position as a 64-bit fixed-point number, and cos and sin of p times it.
+__device__ __forceinline__ unsigned long long rope_turns(double inv_freq) {
+  const double t = inv_freq * 0.15915494309189533577;   // 1 / 2 pi
+  return static_cast<unsigned long long>(__double2ll_rn((t - rint(t)) * 18446744073709551616.0));
+}
+__device__ __forceinline__ void rope_angle(unsigned long long turns, int p, float mscale, float sign, float& c, float& s) {
+  const unsigned long long a = turns * static_cast<unsigned long long>(static_cast<long long>(p));
+  // half turns in [-1, 1)
+  const float x = static_cast<float>(static_cast<int>(a >> 32)) * 0x1p-31f;
+  sincospif(x, &s, &c);
+  c *= mscale;
+  s *= mscale * sign;
+}
+
+__device__ __forceinline__ int rope_position(const RopeParams& p, unsigned token, unsigned b, unsigned s) {
+  if (p.positions) return p.positions[token];
+  return static_cast<int>(static_cast<unsigned>(p.starts ? p.starts[b] : p.start) + s);
+}
+
+// 8 channels as fp32, and back with one rounding each.
+__device__ __forceinline__ void rope_load8(float (&x)[8], const __half* p) {
+  const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x, x[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void rope_load8(float (&x)[8], const __nv_bfloat16* p) {
+  const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+}
+__device__ __forceinline__ void rope_load8(float (&x)[8], const float* p) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void rope_store8(__half* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]), pack_half2(x[4], x[5]), pack_half2(x[6], x[7]));
+}
+__device__ __forceinline__ void rope_store8(__nv_bfloat16* p, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void rope_store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ float rope_get(__half x) { return __half2float(x); }
+__device__ __forceinline__ float rope_get(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float rope_get(float x) { return x; }
+__device__ __forceinline__ void rope_put(__half* p, float x) { *p = __float2half_rn(x); }
+__device__ __forceinline__ void rope_put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void rope_put(float* p, float x) { *p = x; }
+
+// R a multiple of 16, D of 8, rows on 16-byte boundaries. Group g < R / 16 is 8 pairs; those behind them are 16
+// channels that are only copied (none of them where every tensor is turned in place).
+template <typename TIn, typename TOut, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ unsigned long long turns[kRopeMaxD / 2];
+  const unsigned id = blockIdx.x * kRopeThreads + threadIdx.x;
+  const unsigned row = id / p.groups, g = id - row * p.groups;
+  const unsigned token = row / p.slots, slot = row - token * p.slots;
+  const bool live = token < p.tokens;
+  const unsigned b = token / p.S, s = token - b * p.S;
+  const bool turn = static_cast<int>(g) < p.R / 16;
+  // channels of the two vectors
+  const int c0 = turn && !INTERLEAVED ? 8 * g : 16 * g;
+  const int c1 = turn && !INTERLEAVED ? p.R / 2 + 8 * g : 16 * g + 8;
+  const bool two = c1 < p.D;
+
+  const TIn* in[kRopeHeads];
+  TOut* out[kRopeHeads];
+  float x[kRopeHeads][2][8];
+#pragma unroll
+  for (int j = 0; j < kRopeHeads; ++j) {
+    const int head = slot + j * p.slots;
+    const bool there = live && j < p.per && head < p.heads;
+    const RopeTensor& t = p.t[there && head >= p.Hq ? 1 : 0];
+    const int h = there ? (head >= p.Hq ? head - p.Hq : head) : 0;
+    in[j] = there ? static_cast<const TIn*>(t.in) + b * t.in_b + h * t.in_h + s * t.in_s : nullptr;
+    out[j] = there ? static_cast<TOut*>(t.out) + b * t.out_b + h * t.out_h + s * t.out_s : nullptr;
+    if (there) {
+      rope_load8(x[j][0], in[j] + c0);
+      if (two) rope_load8(x[j][1], in[j] + c1);
+    }
+  }
+  const int at = live && turn ? rope_position(p, token, b, s) : 0;
+  if (threadIdx.x < p.R / 2) turns[threadIdx.x] = rope_turns(p.inv_freq[threadIdx.x]);
+  __syncthreads();
+  float c[8], sn[8];
+  if (turn) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rope_angle(turns[8 * g + i], at, p.mscale, p.sign, c[i], sn[i]);
+  }
+#pragma unroll
+  for (int j = 0; j < kRopeHeads; ++j) {
+    if (out[j] == nullptr) continue;
+    if (turn) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float& u = INTERLEAVED ? x[j][i / 4][2 * (i % 4)] : x[j][0][i];
+        float& v = INTERLEAVED ? x[j][i / 4][2 * (i % 4) + 1] : x[j][1][i];
+        const float y = u * c[i] - v * sn[i];
+        v = u * sn[i] + v * c[i];
+        u = y;
+      }
+    }
+    rope_store8(out[j] + c0, x[j][0]);
+    if (two) rope_store8(out[j] + c1, x[j][1]);
+  }
+}
+
+// Any even R and any strides: a thread takes one pair, or one channel behind the R, of one token and head.
+template <typename TIn, typename TOut, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ unsigned long long turns[kRopeMaxD / 2];
+  if (threadIdx.x < p.R / 2) turns[threadIdx.x] = rope_turns(p.inv_freq[threadIdx.x]);
+  __syncthreads();
+  const unsigned id = blockIdx.x * kRopeThreads + threadIdx.x;
+  const unsigned row = id / p.groups, g = id - row * p.groups;
+  const unsigned token = row / p.slots, head = row - token * p.slots;
+  if (token >= p.tokens) return;
+  const unsigned b = token / p.S, s = token - b * p.S;
+  const RopeTensor& t = p.t[static_cast<int>(head) >= p.Hq ? 1 : 0];
+  const int h = static_cast<int>(head) >= p.Hq ? head - p.Hq : head;
+  const TIn* in = static_cast<const TIn*>(t.in) + b * t.in_b + h * t.in_h + s * t.in_s;
+  TOut* out = static_cast<TOut*>(t.out) + b * t.out_b + h * t.out_h + s * t.out_s;
+  const int pairs = p.R / 2;
+  if (static_cast<int>(g) >= pairs) {
+    const int c = p.R + g - pairs;
+    rope_put(out + c, rope_get(in[c]));
+    return;
+  }
+  const int c0 = INTERLEAVED ? 2 * g : g, c1 = INTERLEAVED ? 2 * g + 1 : g + pairs;
+  const float u = rope_get(in[c0]), v = rope_get(in[c1]);
+  float c, sn;
+  rope_angle(turns[g], rope_position(p, token, b, s), p.mscale, p.sign, c, sn);
+  rope_put(out + c0, u * c - v * sn);
+  rope_put(out + c1, u * sn + v * c);
+}
+
+}  // namespace pasa
