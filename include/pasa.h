@@ -477,6 +477,15 @@ int pasa_kprep_fp8_blocks(const void* k, void* k8, void* means, float* kscale, i
 int pasa_kv4_append(const void* k, const void* v, const void* shift, void* k4, void* kscale, void* v4, void* vscale,
                     const int* starts, int start, const int* counts, int B, int Hkv, int n, int Sk_cap, int D,
                     void* stream);
+/* pasa_kv4_append of picked rows: row rows[b, i] of k and v (fp16 [B, Hkv, n_src, D]) is stored as cache row
+ * starts[b] + i, i < counts[b] (or n): the accepted ones of a sequence's drafted tokens, whose rows are
+ * not in the cache yet (pasa_attn_fwd_tree_kv4).
+ *   rows  int32 [B, n], device, 4-byte aligned; a number outside 0 .. n_src - 1 stores nothing and leaves its cache
+ *         row as it was, and one may stand more than once
+ * Other arguments and errors as pasa_kv4_append. */
+int pasa_kv4_append_rows(const void* k, const void* v, const void* shift, void* k4, void* kscale, void* v4, void* vscale,
+                         const int* rows, const int* starts, int start, const int* counts, int B, int Hkv, int n, int n_src,
+                         int Sk_cap, int D, void* stream);
 int pasa_kv4_read(const void* k4, const void* kscale, const void* v4, const void* vscale, const void* shift, void* k,
                   void* v, const int* starts, int start, const int* counts, int B, int Hkv, int n, int Sk_cap, int D,
                   void* stream);

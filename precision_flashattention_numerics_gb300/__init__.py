@@ -73,6 +73,7 @@ SIGNATURES = {
     "pasa_attn_fwd_host_plan": ([_I] * 9 + [_P, _I], _I),
     "pasa_release_host_streams": ([], _I),
     "pasa_kv4_append": ([_P] * 7 + [_P, _I, _P] + [_I] * 5 + [_P], _I),
+    "pasa_kv4_append_rows": ([_P] * 9 + [_I, _P] + [_I] * 6 + [_P], _I),
     "pasa_kv4_read": ([_P] * 7 + [_P, _I, _P] + [_I] * 5 + [_P], _I),
     "pasa_attn_fwd_decode_kv4_workspace_bytes": ([_I] * 7, _SZ),
     "pasa_attn_fwd_decode_kv4": ([_P] * 10 + [_I] * 8 + [_F, _P, _SZ, _P], _I),
@@ -586,11 +587,13 @@ def _per_sequence(x, name, B, device):
     return None, _int32(x, name)
 
 
-def kv4_append(k, v, k4, kscale, v4, vscale, start=0, counts=None, shift=None):
+def kv4_append(k, v, k4, kscale, v4, vscale, start=0, counts=None, shift=None, rows=None):
     """Store rows of k, v [B,Hkv,n,D] (fp16) in the 4-bit cache (k4, v4 uint8 [B,Hkv,cap,D/2];
     kscale, vscale fp16 [B,Hkv,cap,D/32]) from row `start` on (an int, or an int32 tensor [B]);
     with counts (int32 [B]) only the first counts[b] rows of each sequence. shift (fp16
-    [B,Hkv,D]) is subtracted from every key row and stays the same for the cache's life."""
+    [B,Hkv,D]) is subtracted from every key row and stays the same for the cache's life. rows (int32 [B,m]):
+    store these m rows of each sequence of k and v instead, in this order (accepted ones of drafted tokens);
+    numbers outside 0 .. n - 1 are skipped."""
     dev, stream = _here()
     ptrs, sp, (B, Hkv, cap, D) = _check_kv4(k4, kscale, v4, vscale, shift, dev)
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
@@ -600,6 +603,15 @@ def kv4_append(k, v, k4, kscale, v4, vscale, start=0, counts=None, shift=None):
     vp = _check_cuda(v, "v", _F16, (B, Hkv, n, D), dev)
     starts, first = _per_sequence(start, "start", B, dev)
     cp = None if counts is None else _check_cuda(counts, "counts", _I32, (B,), dev)
+    if rows is not None:
+        if not isinstance(rows, torch.Tensor) or rows.dim() != 2:
+            raise ValueError("expected rows [B,m]")
+        m = rows.shape[1]
+        rp = _check_cuda(rows, "rows", _I32, (B, m), dev)
+        rc = library().pasa_kv4_append_rows(kp, vp, sp, *ptrs, rp, starts, first, cp, B, Hkv, m, n, cap, D, stream)
+        if rc != 0:
+            raise PasaError(rc, "pasa_kv4_append_rows")
+        return
     rc = library().pasa_kv4_append(kp, vp, sp, *ptrs, starts, first, cp, B, Hkv, n, cap, D, stream)
     if rc != 0:
         raise PasaError(rc, "pasa_kv4_append")

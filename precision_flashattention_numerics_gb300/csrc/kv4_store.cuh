@@ -130,12 +130,14 @@ __device__ __forceinline__ void load16(uint32_t (&x)[8], const __half* p) {
   x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
-// Store rows of k and v [B, H, n, D] in the cache.
-template <int D>
+// Store rows of k and v [B, H, n, D] in the cache. PICK: row i of sequence b is row pick[b n + i] of k and v
+// [B, H, n_src, D] (accepted ones of drafted tokens); one outside 0 .. n_src - 1 is skipped. The row numbers
+// are read ahead of the rows, which is what the picking costs.
+template <int D, bool PICK>
 __global__ void __launch_bounds__(kKv4StoreThreads) kv4_append_kernel(
     const __half* __restrict__ k, const __half* __restrict__ v, const __half* __restrict__ shift,
     uint8_t* __restrict__ k4, __half* __restrict__ kscale, uint8_t* __restrict__ v4, __half* __restrict__ vscale,
-    int planes, int H, Kv4Window win) {
+    int planes, int H, Kv4Window win, const int* __restrict__ pick, int n_src) {
   griddep_launch_dependents();
   constexpr int kPer = D / 16;   // threads per row
   constexpr int kRows = kKv4StoreThreads / kPer, N = kKv4AppendRows;
@@ -145,18 +147,38 @@ __global__ void __launch_bounds__(kKv4StoreThreads) kv4_append_kernel(
     const int b = plane / H;
     long long row[N];
     uint32_t xk[N][8] = {}, xv[N][8] = {};
-    const __half* kp = k + (static_cast<long long>(plane) * win.n + i0) * D + u * 16;
-    const __half* vp = v + (static_cast<long long>(plane) * win.n + i0) * D + u * 16;
+    if constexpr (PICK) {
+      int from[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (i0 + j * kRows < win.n) {   // rows past counts too: waiting for the count first takes longer
-        load16(xk[j], kp + j * kRows * D);
-        load16(xv[j], vp + j * kRows * D);
+      for (int j = 0; j < N; ++j) {
+        const int i = i0 + j * kRows;
+        from[j] = i < win.n ? pick[static_cast<long long>(b) * win.n + i] : -1;
+        row[j] = i < win.n ? win.row(b, i) : -1;
       }
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int i = i0 + j * kRows;
-      row[j] = i < win.n ? win.row(b, i) : -1;
+      for (int j = 0; j < N; ++j) {
+        if (from[j] < 0 || from[j] >= n_src) {
+          row[j] = -1;
+          continue;
+        }
+        const long long at = (static_cast<long long>(plane) * n_src + from[j]) * D + u * 16;
+        load16(xk[j], k + at);
+        load16(xv[j], v + at);
+      }
+    } else {
+      const __half* kp = k + (static_cast<long long>(plane) * win.n + i0) * D + u * 16;
+      const __half* vp = v + (static_cast<long long>(plane) * win.n + i0) * D + u * 16;
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (i0 + j * kRows < win.n) {   // rows past counts too: waiting for the count first takes longer
+          load16(xk[j], kp + j * kRows * D);
+          load16(xv[j], vp + j * kRows * D);
+        }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int i = i0 + j * kRows;
+        row[j] = i < win.n ? win.row(b, i) : -1;
+      }
     }
     uint32_t sh[8] = {};   // x - 0 = x
     if (shift) load16(sh, shift + static_cast<long long>(plane) * D + u * 16);

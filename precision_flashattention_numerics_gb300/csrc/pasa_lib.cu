@@ -1463,28 +1463,32 @@ cudaError_t kv4_decode_launch(const pasa::Kv4Params& p, const Kv4Plan& pl, cudaS
 
 extern "C" {
 
-// The checks of an append, and its launch.
+// The checks of an append, and its launch. pick: the rows of k and v [B, Hkv, n_src, D] to store, or nullptr.
 static int kv4_append_check(const void* k, const void* v, const void* shift, const void* k4, const void* kscale,
                             const void* v4, const void* vscale, const int* starts, int start, const int* counts, int B,
-                            int Hkv, int n, int Sk_cap, int D, pasa::Kv4Window* win, dim3* grid) {
+                            int Hkv, int n, int Sk_cap, int D, pasa::Kv4Window* win, dim3* grid,
+                            const int* pick = nullptr, int n_src = 0) {
   int rc = kv4_validate(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
   if (rc != PASA_OK) return rc;
   rc = kv4_window(k, v, starts, start, counts, n, B, Hkv, Sk_cap, D, true, win, grid);
   if (rc != PASA_OK) return rc;
   const Kv4Spans c(k4, kscale, v4, vscale, shift, B, Hkv, Sk_cap, D);
-  const unsigned long long rows = static_cast<unsigned long long>(B) * Hkv * n;
-  const bool shared = any_meet({c.k4, c.kscale, c.v4, c.vscale}, {Span(k, rows, 2 * D), Span(v, rows, 2 * D), c.shift,
-                                                                  Span(starts, B, 4), Span(counts, B, 4)});
+  const unsigned long long rows = static_cast<unsigned long long>(B) * Hkv * (pick ? n_src : n);
+  const bool shared = any_meet({c.k4, c.kscale, c.v4, c.vscale},
+                               {Span(k, rows, 2 * D), Span(v, rows, 2 * D), c.shift, Span(starts, B, 4), Span(counts, B, 4),
+                                Span(pick, static_cast<unsigned long long>(B) * n, 4)});
   return shared ? PASA_ERR_SHAPE : PASA_OK;
 }
 
 static int kv4_append_enqueue(const void* k, const void* v, const void* shift, void* k4, void* kscale, void* v4, void* vscale,
-                              int B, int Hkv, int D, const pasa::Kv4Window& win, dim3 grid, cudaStream_t st) {
-  auto kern = D == 64 ? pasa::kv4_append_kernel<64> : pasa::kv4_append_kernel<128>;
+                              int B, int Hkv, int D, const pasa::Kv4Window& win, dim3 grid, cudaStream_t st,
+                              const int* pick = nullptr, int n_src = 0) {
+  auto kern = D == 64 ? (pick ? pasa::kv4_append_kernel<64, true> : pasa::kv4_append_kernel<64, false>)
+                      : (pick ? pasa::kv4_append_kernel<128, true> : pasa::kv4_append_kernel<128, false>);
   kern<<<grid, pasa::kKv4StoreThreads, 0, st>>>(
       static_cast<const __half*>(k), static_cast<const __half*>(v), static_cast<const __half*>(shift),
       static_cast<uint8_t*>(k4), static_cast<__half*>(kscale), static_cast<uint8_t*>(v4), static_cast<__half*>(vscale),
-      B * Hkv, Hkv, win);
+      B * Hkv, Hkv, win, pick, n_src);
   return launch_status();
 }
 
@@ -1498,6 +1502,23 @@ int pasa_kv4_append(const void* k, const void* v, const void* shift, void* k4, v
   rc = check_device();
   if (rc != PASA_OK) return rc;
   return kv4_append_enqueue(k, v, shift, k4, kscale, v4, vscale, B, Hkv, D, win, grid, static_cast<cudaStream_t>(stream));
+}
+
+int pasa_kv4_append_rows(const void* k, const void* v, const void* shift, void* k4, void* kscale, void* v4, void* vscale,
+                         const int* rows, const int* starts, int start, const int* counts, int B, int Hkv, int n, int n_src,
+                         int Sk_cap, int D, void* stream) {
+  if (!rows) return PASA_ERR_NULLPTR;
+  if (n_src <= 0) return PASA_ERR_SHAPE;
+  if (!aligned4(rows)) return PASA_ERR_ALIGN;
+  pasa::Kv4Window win;
+  dim3 grid;
+  int rc = kv4_append_check(k, v, shift, k4, kscale, v4, vscale, starts, start, counts, B, Hkv, n, Sk_cap, D, &win, &grid,
+                            rows, n_src);
+  if (rc != PASA_OK) return rc;
+  rc = check_device();
+  if (rc != PASA_OK) return rc;
+  return kv4_append_enqueue(k, v, shift, k4, kscale, v4, vscale, B, Hkv, D, win, grid, static_cast<cudaStream_t>(stream),
+                            rows, n_src);
 }
 
 int pasa_kv4_read(const void* k4, const void* kscale, const void* v4, const void* vscale, const void* shift, void* k,
