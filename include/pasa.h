@@ -615,6 +615,36 @@ int pasa_rope(const void* q, void* q_out, const long long* q_strides, int Hq, co
               int out_type, void* stream);
 
 /*
+ * PASA attention over packed sequences (same citation as pasa_attn_fwd): N sequences of different lengths side by side
+ * in token-major tensors, as a serving loop batches prompts. Sequence s has the query rows cu_q[s] .. cu_q[s + 1] - 1
+ * and the key rows cu_k[s] .. cu_k[s + 1] - 1, and attends to its own keys only; n queries on m keys, the mask
+ * bottom-right aligned: query i sees keys j <= i + m - n (so that a chunk of a prompt attends to all that went
+ * before). Key blocks of pasa_block_rows(D) rows are counted from a sequence's first key: K' and m are those
+ * of pasa_kshift on the sequence alone.
+ *   q, o       fp16 [Tq, Hq, D]; k, v fp16 [Tk, Hkv, D]
+ *   strides    HOST array of 8: elements from one token and from one head to the next, of q, k, v and o in this
+ *              order; positive multiples of 8, channels contiguous, tensors on 16-byte boundaries (PASA_ERR_ALIGN).
+ *              Views of a fused projection are such.
+ *   lse        fp32 [Hq, Tq] or NULL
+ *   cu_q, cu_k int32 [N + 1], device, not decreasing, within 0 .. Tq and 0 .. Tk; they may be one array. Others
+ *              are taken into that range, and give unspecified results. Sequences may be empty: a query
+ *              without a key gets O = 0 and LSE = -inf. Rows in front of the first and behind the last sequence are
+ *              not part of any: o and lse are left as they were there, and what q, k and v hold there,
+ *              as in other sequences, plays no part.
+ *   mode       PASA_MODE_* 0 .. 3; others are PASA_ERR_UNSUPPORTED
+ *   workspace  device, 256-byte aligned, at least pasa_attn_fwd_packed_workspace_bytes(...) bytes (0 for
+ *              invalid sizes), written before it is read, used on `stream` only
+ * o may be q itself (same strides); otherwise o, lse and the workspace share no memory with one another or with what is read
+ * (PASA_ERR_SHAPE). A key or value that is not finite spoils the queries of its own sequence in the tiles that
+ * read its block, also those whose mask hides it. (Tq + N) * Hq and (Tk / 128 + 1 + N) * Hkv fit an int, else PASA_ERR_SHAPE.
+ * All lengths are read on the device: one captured graph serves any cu_q and cu_k.
+ */
+size_t pasa_attn_fwd_packed_workspace_bytes(int N, int Hq, int Hkv, int Tq, int Tk, int D, int mode);
+int pasa_attn_fwd_packed(const void* q, const void* k, const void* v, void* o, const long long* strides, float* lse,
+                         const int* cu_q, const int* cu_k, int N, int Hq, int Hkv, int Tq, int Tk, int D, int causal,
+                         float scale, int mode, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Synchronise `stream` and read the device error word. Returns PASA_OK, PASA_ERR_TIMEOUT
  * (a pipeline wait gave up; `info`, if not NULL, receives the CTA index << 32 | wait site)
  * or PASA_ERR_CUDA. Reading the word clears it.

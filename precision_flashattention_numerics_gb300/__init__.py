@@ -23,6 +23,7 @@ __all__ = [
     "PasaError", "attn_fwd", "attn_fwd_alloc", "attn_fwd_fused", "attn_fwd_shifted", "attn_fwd_stats", "kshift", "workspace_bytes", "check_device_error", "block_rows",
     "kv4_append", "kv4_read", "attn_fwd_decode_kv4", "attn_fwd_decode_step_kv4", "cache_evict",
     "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BASE", "ROPE_BY_PARTS", "rope_frequencies", "rope",
+    "attn_fwd_packed", "packed_workspace_bytes",
     "library", "library_path",
 ]
 
@@ -79,6 +80,8 @@ SIGNATURES = {
     "pasa_attn_fwd_decode_kv4": ([_P] * 10 + [_I] * 8 + [_F, _P, _SZ, _P], _I),
     "pasa_attn_fwd_decode_step_kv4": ([_P] * 9 + [_I] + [_P] * 3 + [_I] * 9 + [_F, _P, _SZ, _P], _I),
     "pasa_cache_evict": ([_P, _P, _P, _I] + [_P] * 5 + [_I] * 7 + [_P], _I),
+    "pasa_attn_fwd_packed_workspace_bytes": ([_I] * 7, _SZ),
+    "pasa_attn_fwd_packed": ([_P] * 8 + [_I] * 7 + [_F, _I, _P, _SZ, _P], _I),
     "pasa_rope_frequencies": ([_P, _P, _I, _D, _I, _D, _D, _D, _D], _I),
     "pasa_rope": ([_P] * 3 + [_I] + [_P] * 3 + [_I] + [_P] * 3 + [_I] * 7 + [_F, _I, _I, _P], _I),
     "pasa_check_device_error": ([_P, ctypes.POINTER(ctypes.c_ulonglong)], _I),
@@ -855,6 +858,68 @@ def rope(q, k, inv_freq, positions=None, start=0, interleaved: bool = False, msc
     if rc != 0:
         raise PasaError(rc, "pasa_rope")
     return out_q, out_k
+
+
+@functools.lru_cache(maxsize=1024)   # of sizes only
+def packed_workspace_bytes(N: int, Hq: int, Hkv: int, Tq: int, Tk: int, D: int, mode: int) -> int:
+    return library().pasa_attn_fwd_packed_workspace_bytes(N, Hq, Hkv, Tq, Tk, D, mode)
+
+
+def _packed_strides(x, name, shape, device):
+    """The strides of token and head of an fp16 [T,H,D] tensor."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype is not _F16:
+        raise TypeError(f"{name} must be a CUDA fp16 tensor")
+    if x.get_device() != device:
+        raise ValueError(f"{name} is on device {x.get_device()}, the current device is {device}")
+    if x.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
+    row, head, last = x.stride()
+    if last != 1:
+        raise ValueError(f"{name}'s channels are not contiguous")
+    T, H, D = shape
+    head = head if H > 1 else D   # a dimension of one has any stride
+    return [row if T > 1 else H * head, head]
+
+
+def attn_fwd_packed(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float | None = None, mode: int = MODE_SHIFT_F16ACC,
+                    out=None, lse=None, return_lse: bool = True, workspace=None):
+    """Attention over packed sequences: q fp16 [Tq,Hq,D], k and v [Tk,Hkv,D] (strided views with contiguous
+    channels and 16-byte aligned rows, e.g. of a fused projection), sequence s in rows cu_q[s] .. cu_q[s+1] of q and
+    cu_k[s] .. cu_k[s+1] of k and v (int32 [N+1] on the device; cu_k None: cu_q). causal: query i of n sees
+    keys j <= i + m - n of its sequence's m. mode: MODE_* 0 .. 3. Rows outside every sequence are left as they
+    are in out and lse (0 and -inf in new ones). Returns (o [Tq,Hq,D], lse fp32 [Hq,Tq] or None)."""
+    dev, stream = _here()
+    for x in (q, k, v):
+        if not isinstance(x, torch.Tensor) or x.dim() != 3:
+            raise ValueError("expected q [Tq,Hq,D] and k, v [Tk,Hkv,D]")
+    Tq, Hq, D = q.shape
+    Tk, Hkv, _ = k.shape
+    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise ValueError("expected cu_q [N+1]")
+    N = cu_q.shape[0] - 1
+    cq = _check_cuda(cu_q, "cu_q", _I32, (N + 1,), dev)
+    ck = cq if cu_k is None else _check_cuda(cu_k, "cu_k", _I32, (N + 1,), dev)
+    if out is None:
+        out = torch.zeros((Tq, Hq, D), device=q.device, dtype=_F16)
+    if not return_lse:
+        lse = lp = None
+    else:
+        if lse is None:
+            lse = torch.full((Hq, Tq), float("-inf"), device=q.device, dtype=_F32)
+        lp = _check_cuda(lse, "lse", _F32, (Hq, Tq), dev)
+    table = array.array("q", _packed_strides(q, "q", q.shape, dev) + _packed_strides(k, "k", (Tk, Hkv, D), dev)
+                        + _packed_strides(v, "v", (Tk, Hkv, D), dev) + _packed_strides(out, "out", (Tq, Hq, D), dev))
+    nbytes = packed_workspace_bytes(N, Hq, Hkv, Tq, Tk, D, int(mode))
+    if workspace is not None:
+        _check_cuda(workspace, "workspace", _U8, None, dev)
+    if nbytes and (workspace is None or workspace.numel() < nbytes):
+        workspace = torch.empty(nbytes, device=q.device, dtype=_U8)
+    rc = library().pasa_attn_fwd_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), table.buffer_info()[0], lp, cq, ck,
+                                        N, Hq, Hkv, Tq, Tk, D, int(bool(causal)), float(scale) if scale is not None else 0.0,
+                                        int(mode), workspace.data_ptr() if nbytes else None, nbytes, stream)
+    if rc != 0:
+        raise PasaError(rc, "pasa_attn_fwd_packed")
+    return out, lse
 
 
 def selftest_wait_timeout():

@@ -6,6 +6,7 @@
 #include <climits>
 #include <cstddef>
 #include <cstdint>
+#include <cstring>
 #include <initializer_list>
 #include <utility>
 #include <cuda.h>
@@ -195,6 +196,85 @@ struct Kv4Spans {
     shift = Span(shiftp, heads, 2 * D);
   }
 };
+
+// A strided tensor [B, H, S, D] in bytes, for questions of shared memory.
+struct Strided {
+  uintptr_t at;
+  long long stride[3], n[3];   // of the dimensions, largest stride first
+  long long row;               // bytes of a row
+
+  Strided(const void* p, const long long* strides, long long B, long long H, long long S, long long D, long long size)
+      : at(reinterpret_cast<uintptr_t>(p)), stride{strides[0] * size, strides[1] * size, strides[2] * size}, n{B, H, S}, row(D * size) {
+    for (int i = 0; i < 3; ++i)
+      if (n[i] == 1) stride[i] = 0;   // a dimension of one has no stride
+    for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 2; ++j)
+        if (stride[j] < stride[j + 1]) std::swap(stride[j], stride[j + 1]), std::swap(n[j], n[j + 1]);
+  }
+  // The bytes that dimensions i .. 2 and a row span.
+  long long extent(int i) const {
+    long long e = row;
+    for (; i < 3; ++i) e += (n[i] - 1) * stride[i];
+    return e;
+  }
+  // Whether two of its rows share memory, as far as the strides tell.
+  bool folds() const {
+    for (int i = 0; i < 3; ++i)
+      if (n[i] > 1 && stride[i] < extent(i + 1)) return true;
+    return false;
+  }
+  bool same(const Strided& x) const {
+    return at == x.at && row == x.row && std::memcmp(stride, x.stride, sizeof stride) == 0 && std::memcmp(n, x.n, sizeof n) == 0;
+  }
+  // Whether the two share memory. Two views that lie side by side in one buffer's rows (q and k of a
+  // fused projection) do not; other views of one range count as sharing it.
+  bool meets(const Strided& x) const {
+    const uintptr_t end = at + extent(0), xend = x.at + x.extent(0);
+    if (end <= x.at || xend <= at) return false;
+    for (int i = 0; i < 3; ++i) {   // the first i strides alike, and what is inside them apart in every period of stride i - 1
+      if (stride[i] != x.stride[i] || stride[i] == 0) break;
+      const unsigned long long period = static_cast<unsigned long long>(stride[i]);
+      if (i > 0 && stride[i - 1] % stride[i] != 0) break;
+      const unsigned long long e = extent(i + 1), xe = x.extent(i + 1);
+      if (e > period || xe > period) break;
+      const unsigned long long d = x.at >= at ? (x.at - at) % period : (period - (at - x.at) % period) % period;
+      if (d >= e && d + xe <= period) return false;
+    }
+    return true;
+  }
+};
+
+// strides: of b, h and s; all at least 0, and their products with the sizes fit 62 bits with room.
+bool strides_fit(const long long* strides, long long B, long long H, long long S, long long D) {
+  const long long n[3] = {B, H, S};
+  long long sum = D;
+  for (int i = 0; i < 3; ++i) {
+    long long x;
+    if (strides[i] < 0) return false;
+    if (__builtin_mul_overflow(strides[i], n[i], &x) || __builtin_add_overflow(sum, x, &sum) || sum > (1ll << 58)) return false;
+  }
+  return true;
+}
+
+// A map of a strided fp16 tensor: its dimensions, channels first, the strides of the others in bytes, and the box;
+// 128-byte swizzle, elements past the tensor read as zeros.
+int make_strided_map(CUtensorMap* m, const void* base, std::initializer_list<long long> dims,
+                     std::initializer_list<long long> strides, std::initializer_list<long long> box) {
+  auto enc = encode_fn();
+  if (!enc) return cuda_fail(cudaErrorNotSupported);
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], es[5] = {1, 1, 1, 1, 1};
+  int n = 0;
+  for (long long x : dims) d[n++] = static_cast<cuuint64_t>(x);
+  int i = 0;
+  for (long long x : strides) st[i++] = static_cast<cuuint64_t>(x);
+  i = 0;
+  for (long long x : box) bx[i++] = static_cast<cuuint32_t>(x);
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, static_cast<cuuint32_t>(n), const_cast<void*>(base), d, st, bx, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PASA_OK : cuda_fail(cudaErrorInvalidValue);
+}
 
 // This unit's error word, read and cleared.
 int take_device_error(unsigned long long* info) {

@@ -342,10 +342,11 @@ kshift_kernel(const __half* __restrict__ k, void* __restrict__ kshift, __half* _
 // kernel's fp32 subtraction and fp16 rounding give (checked bit for bit in the tests).
 constexpr int kShiftRegThreads = 128;
 
+// One block of n <= BN rows, by a CTA of kShiftRegThreads threads: src and dst are its first rows (16-byte units;
+// rows src_row and dst_row units apart), mean its pseudo-average.
 template <int D, int BN>
-__global__ void __launch_bounds__(kShiftRegThreads)
-kshift_reg_kernel(const __half* __restrict__ k, __half* __restrict__ kshift, __half* __restrict__ means, int Sk,
-                  int nb, int j0, int cap, int nb_cap) {
+__device__ __forceinline__ void shift_block(const uint4* __restrict__ src, long long src_row, uint4* __restrict__ dst,
+                                            long long dst_row, uint4* __restrict__ mean, int n) {
   constexpr int U = D / 8;                       // 16-byte units per row
   constexpr int RG = kShiftRegThreads / U;       // row groups
   constexpr int RPT = BN / RG;                   // rows per thread
@@ -354,23 +355,18 @@ kshift_reg_kernel(const __half* __restrict__ k, __half* __restrict__ kshift, __h
   __shared__ uint32_t sh_max[NW][U][4];
   __shared__ uint32_t sh_sum[NW][U][8];
 
-  griddep_launch_dependents();   // as in kshift_kernel: a queued decode launch may start
-  const int j = j0 + blockIdx.x;
-  const int bh = blockIdx.y;
   const int tid = threadIdx.x;
   const int u = tid % U;
   const int rg = tid / U;
   const int warp = tid / 32;
-  const int row0 = j * BN;
-  const int n = min(BN, Sk - row0);
-  const uint4* src = reinterpret_cast<const uint4*>(k + (static_cast<size_t>(bh) * cap + row0) * D) + u;
-  uint4* dst = reinterpret_cast<uint4*>(kshift + (static_cast<size_t>(bh) * cap + row0) * D) + u;
+  src += u;
+  dst += u;
 
   uint4 x[RPT];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const int r = rg + i * RG;
-    x[i] = r < n ? __ldg(src + static_cast<size_t>(r) * U) : make_uint4(0, 0, 0, 0);
+    x[i] = r < n ? __ldg(src + r * src_row) : make_uint4(0, 0, 0, 0);
   }
   // 1. per-channel max |K| (16-bit lanes); an inf or NaN makes it >= 0x7C00
   uint32_t mx[4] = {0u, 0u, 0u, 0u};
@@ -456,8 +452,7 @@ kshift_reg_kernel(const __half* __restrict__ k, __half* __restrict__ kshift, __h
     const __half2 h2 = __floats2half2_rn(mf[2 * c], mf[2 * c + 1]);
     m2[c] = *reinterpret_cast<const uint32_t*>(&h2);
   }
-  if (rg == 0) reinterpret_cast<uint4*>(means + (static_cast<size_t>(bh) * nb_cap + j) * D)[u] =
-      make_uint4(m2[0], m2[1], m2[2], m2[3]);
+  if (rg == 0) mean[u] = make_uint4(m2[0], m2[1], m2[2], m2[3]);
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const int r = rg + i * RG;
@@ -467,9 +462,22 @@ kshift_reg_kernel(const __half* __restrict__ k, __half* __restrict__ kshift, __h
       asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o.y) : "r"(x[i].y), "r"(m2[1]));
       asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o.z) : "r"(x[i].z), "r"(m2[2]));
       asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o.w) : "r"(x[i].w), "r"(m2[3]));
-      dst[static_cast<size_t>(r) * U] = o;
+      dst[static_cast<size_t>(r) * dst_row] = o;
     }
   }
+}
+
+template <int D, int BN>
+__global__ void __launch_bounds__(kShiftRegThreads)
+kshift_reg_kernel(const __half* __restrict__ k, __half* __restrict__ kshift, __half* __restrict__ means, int Sk,
+                  int nb, int j0, int cap, int nb_cap) {
+  griddep_launch_dependents();   // as in kshift_kernel: a queued decode launch may start
+  const int j = j0 + blockIdx.x;
+  const int bh = blockIdx.y;
+  const int row0 = j * BN;
+  const size_t at = (static_cast<size_t>(bh) * cap + row0) * D;
+  shift_block<D, BN>(reinterpret_cast<const uint4*>(k + at), D / 8, reinterpret_cast<uint4*>(kshift + at), D / 8,
+                     reinterpret_cast<uint4*>(means + (static_cast<size_t>(bh) * nb_cap + j) * D), min(BN, Sk - row0));
 }
 
 }  // namespace pasa

@@ -1,0 +1,616 @@
+// Attention over packed sequences: token-major tensors [T, H, D] in which sequence s has the query rows
+// cu_q[s] .. cu_q[s + 1] and the key rows cu_k[s] .. cu_k[s + 1], all lengths on the device.
+//
+// Method as in attn_fwd_kernel ("Online Pseudo-average Shifting Attention (PASA) for Robust Low-precision
+// LLM Inference", arXiv 2503.01873, Abstract): every 128-key block of a sequence, counted from
+// its first key, is shifted by its pseudo-average, scores are accumulated in fp16 or fp32, the offsets q_i . m_j
+// are added back in fp32 in the online softmax.
+//
+// Two kernels. packed_prep_kernel shifts the keys (K' [Hkv, Tk, D], means [Hkv, slots, D]), and its first CTA
+// writes the list of query tiles, those with the most key blocks first, so that uneven lengths leave
+// no SM waiting at the end. packed_fwd_kernel takes a tile and a group of heads in each CTA.
+//
+// Tiles. A tile is 128 rows: `hg` query heads of one kv head (a divisor of Hq / Hkv) for each of 128 / hg tokens,
+// row r token r / hg and head r mod hg, which one TMA box brings. Several heads to a tile fill
+// the tiles of short sequences, where one head would leave most rows of its tile empty.
+//
+// Slots. Lengths are not known on the host, so key blocks get numbers that need no prefix sum: block j of
+// sequence s is slot cu_k[s] / 128 + s + j. Those are distinct (a sequence of L keys from row c on has ceil(L / 128) blocks
+// and floor((c + L) / 128) - floor(c / 128) + 1 slots to itself), and the sequence of a slot is found by a
+// search in cu_k. Query tiles are numbered likewise.
+//
+// Where a sequence ends inside a 128-key block, the block's last rows are another sequence's. Their scores are
+// masked like any other, and their values are set to zero in shared memory before the MMA reads them: a
+// probability of 0 does not make an infinity or NaN harmless.
+//
+// cu_q and cu_k are clamped to their tensors and every number from them to its buffer: offsets that do not
+// grow give unspecified results, but no access out of bounds.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include "attn_fwd.cuh"
+#include "kshift.cuh"
+#include "ptx.cuh"
+
+namespace pasa {
+namespace packed {
+
+constexpr int kKeys = 128;          // keys of a block
+constexpr int kPrepThreads = 128;
+constexpr int kBins = 1024;         // of the tiles' sort by their key blocks
+
+// One query tile: all that a CTA has to know.
+struct __align__(32) Tile {
+  int q0, tokens;   // first token row of q, and how many
+  int k0, keys;     // first key row of the sequence, and its keys
+  int limit;        // keys that the first token sees, before clamping; each further one sees `step` more
+  int step;         // 1 with the causal mask, else 0
+  int blocks;       // key blocks that the last token sees
+  int slot;         // of the sequence's first key block
+};
+
+struct Params {
+  const int *cu_q, *cu_k;
+  int N, Tq, Tk, Hq, Hkv;
+  int hg, tile_tokens;     // heads and tokens of a tile
+  int tile_slots, key_slots;
+  int causal, bin_shift;
+  float scale_log2, inv_scale_log2;
+  int* count;              // tiles in the list
+  Tile* tiles;
+  const __half* k;         // the raw keys, for the shift
+  long long k_row, k_head; // their strides
+  __half *kshift, *means;  // [Hkv, Tk, D], [Hkv, key_slots, D]
+  __half* o;
+  long long o_row, o_head;
+  float* lse;              // [Hq, Tq] or nullptr
+};
+
+__device__ __forceinline__ int offset(const int* cu, int s, int most) { return min(max(__ldg(cu + s), 0), most); }
+
+// The last s < n with cu[s] / per + s <= slot, by a whole warp: it probes 32 places at a time.
+__device__ __forceinline__ int find_sequence(const int* cu, int n, int most, int per, int slot) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;   // the answer is in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int s = lo + lane * step;
+    const bool before = s < hi && offset(cu, s, most) / per + s <= slot;
+    const uint32_t v = __ballot_sync(0xFFFFFFFFu, before) | 1u;   // lane 0: lo, by the loop's invariant
+    const int last = 31 - __clz(v);
+    lo += last * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+// The same by one thread.
+__device__ __forceinline__ int find_sequence_alone(const int* cu, int n, int most, int per, int slot) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (offset(cu, mid, most) / per + mid <= slot) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// The tile of a slot; false where there is none.
+__device__ __forceinline__ bool make_tile(const Params& p, int slot, Tile& t) {
+  const int s = find_sequence_alone(p.cu_q, p.N, p.Tq, p.tile_tokens, slot);
+  const int q0 = offset(p.cu_q, s, p.Tq), n = offset(p.cu_q, s + 1, p.Tq) - q0;
+  const long long first = static_cast<long long>(slot - (q0 / p.tile_tokens + s)) * p.tile_tokens;
+  if (first < 0 || first >= n) return false;
+  const int k0 = offset(p.cu_k, s, p.Tk), m = max(0, offset(p.cu_k, s + 1, p.Tk) - k0);
+  const int i0 = static_cast<int>(first);
+  t.q0 = q0 + i0;
+  t.tokens = min(p.tile_tokens, n - i0);
+  t.k0 = k0;
+  t.keys = m;
+  t.limit = p.causal ? i0 + 1 + m - n : m;
+  t.step = p.causal ? 1 : 0;
+  const int last = min(m, max(0, t.limit + t.step * (t.tokens - 1)));
+  t.blocks = (last + kKeys - 1) / kKeys;
+  t.slot = min(k0 / kKeys + s, p.key_slots - 1);
+  return true;
+}
+
+// The list of tiles, most key blocks first: a counting sort by one CTA. Tiles of one bin come in any order, which
+// no result depends on.
+__device__ __forceinline__ void plan_tiles(const Params& p) {
+  __shared__ int bins[kBins];
+  __shared__ int warp_sums[kPrepThreads / 32];
+  const int tid = threadIdx.x;
+  for (int i = tid; i < kBins; i += kPrepThreads) bins[i] = 0;
+  __syncthreads();
+  // a thread keeps what it finds of its first few slots for the second pass
+  constexpr int kKeep = 2;
+  Tile kept[kKeep];
+  bool there[kKeep];
+  auto bin_of = [&](const Tile& t) { return kBins - 1 - min(kBins - 1, t.blocks >> p.bin_shift); };
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    const int slot = i * kPrepThreads + tid;
+    there[i] = slot < p.tile_slots && make_tile(p, slot, kept[i]);
+    if (there[i]) atomicAdd(&bins[bin_of(kept[i])], 1);
+  }
+  for (int slot = kKeep * kPrepThreads + tid; slot < p.tile_slots; slot += kPrepThreads) {
+    Tile t;
+    if (make_tile(p, slot, t)) atomicAdd(&bins[bin_of(t)], 1);
+  }
+  __syncthreads();
+  // exclusive sums over the bins: 8 neighbouring ones a thread
+  constexpr int kPer = kBins / kPrepThreads;
+  int sum = 0, mine[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) mine[i] = bins[tid * kPer + i], sum += mine[i];
+  int upto = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+    if ((tid & 31) >= d) upto += x;
+  }
+  if ((tid & 31) == 31) warp_sums[tid >> 5] = upto;
+  __syncthreads();
+  int before = upto - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kPrepThreads / 32; ++w) {
+    if (w < (tid >> 5)) before += warp_sums[w];
+    total += warp_sums[w];
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    bins[tid * kPer + i] = before;
+    before += mine[i];
+  }
+  if (tid == 0) *p.count = total;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (there[i]) p.tiles[atomicAdd(&bins[bin_of(kept[i])], 1)] = kept[i];
+  for (int slot = kKeep * kPrepThreads + tid; slot < p.tile_slots; slot += kPrepThreads) {
+    Tile t;
+    if (make_tile(p, slot, t)) p.tiles[atomicAdd(&bins[bin_of(t)], 1)] = t;
+  }
+}
+
+// CTA 0 plans; CTA 1 + slot * Hkv + head shifts the key block of a slot (kshift_reg_kernel's arithmetic, bit for
+// bit, on rows k_row apart). HBM-bound: each key is read once and written once.
+template <int D>
+__global__ void __launch_bounds__(kPrepThreads) packed_prep_kernel(const __grid_constant__ Params p) {
+  griddep_launch_dependents();
+  if (blockIdx.x == 0) {
+    plan_tiles(p);
+    return;
+  }
+  const int slot = (blockIdx.x - 1) / p.Hkv, head = (blockIdx.x - 1) % p.Hkv;
+  const int s = find_sequence(p.cu_k, p.N, p.Tk, kKeys, slot);
+  const int k0 = offset(p.cu_k, s, p.Tk), m = offset(p.cu_k, s + 1, p.Tk) - k0;
+  const long long first = static_cast<long long>(slot - (k0 / kKeys + s)) * kKeys;
+  if (first < 0 || first >= m) return;
+  const int row0 = k0 + static_cast<int>(first);
+  const int n = min(kKeys, m - static_cast<int>(first));
+  shift_block<D, kKeys>(reinterpret_cast<const uint4*>(p.k + row0 * p.k_row + head * p.k_head), p.k_row / 8,
+                        reinterpret_cast<uint4*>(p.kshift + (static_cast<long long>(head) * p.Tk + row0) * D), D / 8,
+                        reinterpret_cast<uint4*>(p.means + (static_cast<long long>(head) * p.key_slots + slot) * D), n);
+}
+
+// One CTA: a tile of the list and a group of hg heads. Warp roles, TMEM and barriers as in attn_fwd_kernel
+// (warps 0-3 softmax and epilogue, one thread per row; 4 TMA; 5 score and offsets MMAs; 6 PV MMAs). Its waits are
+// all bounded (ptx.cuh).
+template <int D, bool F16ACC, bool SHIFT, int KST, int VST>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                  const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapO,
+                  const __grid_constant__ CUtensorMap mapM, const __grid_constant__ Params p) {
+  constexpr int BN = kKeys;
+  using Smem = AttnSmem<D, BN, KST, VST>;
+  static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory per CTA");
+  using TM = TmemMap<D, BN>;
+  extern __shared__ uint8_t smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+
+  if (tid == 0) {
+    mbar_init(&s.q_full, 1);
+    for (int i = 0; i < KST; ++i) { mbar_init(&s.k_full[i], 1); mbar_init(&s.k_empty[i], 1); }
+    for (int i = 0; i < VST; ++i) { mbar_init(&s.v_full[i], 1); mbar_init(&s.v_empty[i], 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.m_full[i], 1);
+      mbar_init(&s.m_empty[i], 1);
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.s_free[i], 4);
+    }
+    mbar_init(&s.p_full, 4);
+    mbar_init(&s.p_free, 1);
+    mbar_init(&s.o_full, 1);
+    mbar_init(&s.drain[0], 1);
+    mbar_init(&s.drain[1], 1);
+    s.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(&s.tmem_base, 512);
+    tmem_relinquish();
+  }
+  const int groups = p.Hq / p.hg;
+  const int item = blockIdx.x / groups, group = blockIdx.x % groups;
+  griddep_wait();   // the list, the shifted keys and the means; every CTA: a kernel behind this one waits for this one
+  const bool there = item < __ldcg(p.count);
+  Tile t = {};
+  if (there) {
+    const int4* rec = reinterpret_cast<const int4*>(p.tiles + item);
+    const int4 a = __ldcg(rec), b = __ldcg(rec + 1);
+    t = Tile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s.tmem_base;
+  volatile int* abort_flag = &s.abort_flag;
+  const int nblk = t.blocks;
+  const int rows = p.hg * p.tile_tokens;
+  const int hk = group / (p.Hq / p.Hkv / p.hg);
+
+  if (!there) {
+    // nothing to do but to give the TMEM back
+  } else if (warp == 4) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint32_t q_chunk = static_cast<uint32_t>(rows) * 128;
+      mbar_arrive_expect_tx(&s.q_full, q_chunk * Smem::kChunks);
+#pragma unroll
+      for (int c = 0; c < Smem::kChunks; ++c) tma_load_4d(s.q + c * Smem::kQChunk, &mapQ, &s.q_full, c * 64, 0, t.q0, group);
+      int k_issued = 0, v_issued = 0, m_issued = 0;
+      auto load_k = [&](int j) -> bool {
+        if (SHIFT && (j % kChunkBlocks) == 0) {
+          const int ci = j / kChunkBlocks, slot = ci & 1;
+          if (!mbar_wait(&s.m_empty[slot], ((ci >> 1) & 1) ^ 1, abort_flag, 0x1101)) return false;
+          mbar_arrive_expect_tx(&s.m_full[slot], Smem::kMTile);
+#pragma unroll
+          for (int c = 0; c < Smem::kChunks; ++c)
+            tma_load_3d(s.m[slot] + c * Smem::kMChunk, &mapM, &s.m_full[slot], c * 64, t.slot + j, hk);
+          m_issued = ci + 1;
+        }
+        const int ks = j % KST;
+        if (!mbar_wait(&s.k_empty[ks], ((j / KST) & 1) ^ 1, abort_flag, 0x1102)) return false;
+        mbar_arrive_expect_tx(&s.k_full[ks], Smem::kKTile);
+#pragma unroll
+        for (int c = 0; c < Smem::kChunks; ++c)
+          tma_load_3d(s.k[ks] + c * Smem::kKChunk, &mapK, &s.k_full[ks], c * 64, t.k0 + j * BN, hk);
+        k_issued = j + 1;
+        return true;
+      };
+      auto load_v = [&](int j) -> bool {
+        const int vs = j % VST;
+        if (!mbar_wait(&s.v_empty[vs], ((j / VST) & 1) ^ 1, abort_flag, 0x1103)) return false;
+        mbar_arrive_expect_tx(&s.v_full[vs], Smem::kVTile);
+#pragma unroll
+        for (int c = 0; c < Smem::kChunks; ++c)
+          tma_load_3d(s.v[vs] + c * Smem::kVChunk, &mapV, &s.v_full[vs], c * 64, t.k0 + j * BN, hk);
+        v_issued = j + 1;
+        return true;
+      };
+      bool pok = nblk == 0 || load_k(0);
+      for (int j = 0; pok && j < nblk; ++j) {
+        if (j + 1 < nblk && !load_k(j + 1)) break;
+        if (!load_v(j)) break;
+      }
+      if (*abort_flag) {
+        // Let every copy this warp issued land before the CTA's shared memory goes away.
+        const uint64_t t0 = globaltimer_ns();
+        auto drain = [&](uint64_t* bar, uint32_t parity) {
+          while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+          }
+        };
+        drain(&s.q_full, 0);
+        for (int j = max(0, k_issued - KST); j < k_issued; ++j) drain(&s.k_full[j % KST], (j / KST) & 1);
+        for (int j = max(0, v_issued - VST); j < v_issued; ++j) drain(&s.v_full[j % VST], (j / VST) & 1);
+        for (int ci = max(0, m_issued - 2); ci < m_issued; ++ci) drain(&s.m_full[ci & 1], (ci >> 1) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ------------------------------------------------------------------ QK issuer (see attn_fwd_kernel)
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_f16(kTileRows, BN, !F16ACC, false);
+      constexpr uint32_t id_c = idesc_f16(kTileRows, kChunkBlocks, true, false);
+      constexpr uint32_t hi_kmaj = sdesc_hi_sw128(1024);
+      const uint32_t q_lo = sdesc_lo(smem_u32(s.q), 16);
+      const uint32_t k_lo0 = sdesc_lo(smem_u32(s.k[0]), 16);
+      const uint32_t m_lo0 = sdesc_lo(smem_u32(s.m[0]), 16);
+      constexpr uint32_t kKStride = sizeof(s.k[0]) >> 4;
+      constexpr uint32_t kMStride = sizeof(s.m[0]) >> 4;
+      uint32_t qd[D / 16];
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) qd[kk] = q_lo + (((kk / 4) * Smem::kQChunk + (kk % 4) * 32) >> 4);
+      bool ok = mbar_wait(&s.q_full, 0, abort_flag, 0x1201);
+      const uint32_t tQ = tmem + TM::q;
+      constexpr int kQt = TM::kQtSteps;
+      if (ok && nblk > 0) {
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kQt; ++kk) tmem_cp_128x256b(tQ + kk * 8, qd[kk], hi_kmaj);
+      }
+      for (int j = 0; ok && j < nblk; ++j) {
+        const int ks = j % KST;
+        const int ci = j / kChunkBlocks;
+        const int sb = j & 1;
+        const bool chunk_start = SHIFT && (j % kChunkBlocks) == 0;
+        uint32_t kd[D / 16];
+        const uint32_t k_lo = k_lo0 + ks * kKStride;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) kd[kk] = k_lo + (((kk / 4) * Smem::kKChunk + (kk % 4) * 32) >> 4);
+        if (!mbar_wait(&s.k_full[ks], (j / KST) & 1, abort_flag, 0x1202)) break;
+        if (chunk_start && !mbar_wait(&s.m_full[ci & 1], (ci >> 1) & 1, abort_flag, 0x1203)) break;
+        if (j >= 2 && !mbar_wait(&s.s_free[sb], ((j >> 1) - 1) & 1, abort_flag, 0x1206)) break;
+        tc_fence_after();
+        if (chunk_start) {
+          const uint32_t m_lo = m_lo0 + (ci & 1) * kMStride;
+          const uint32_t tC = tmem + TM::c(ci & 1);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off_m = ((kk / 4) * Smem::kMChunk + (kk % 4) * 32) >> 4;
+            if (kk < kQt) mma_ts_w(tC, tQ + kk * 8, m_lo + off_m, hi_kmaj, id_c, kk > 0 ? 1u : 0u);
+            else mma_ss_w(tC, qd[kk], hi_kmaj, m_lo + off_m, hi_kmaj, id_c, kk > 0 ? 1u : 0u);
+          }
+        }
+        const uint32_t tS = tmem + TM::s(sb);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          if (kk < kQt) mma_ts_w(tS, tQ + kk * 8, kd[kk], hi_kmaj, id_s, kk > 0 ? 1u : 0u);
+          else mma_ss_w(tS, qd[kk], hi_kmaj, kd[kk], hi_kmaj, id_s, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&s.s_full[sb]);
+        mma_commit(&s.k_empty[ks]);
+        if (chunk_start) mma_commit(&s.m_empty[ci & 1]);
+      }
+      mma_commit(&s.drain[0]);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(&s.drain[0], 0) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+      }
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // ------------------------------------------------------------------ PV issuer
+    if (lane == 0) {
+      constexpr uint32_t id_o = idesc_f16(kTileRows, D, true, true);
+      constexpr uint32_t hi_v = sdesc_hi_sw128(1024);
+      const uint32_t v_lo0 = sdesc_lo(smem_u32(s.v[0]), Smem::kVChunk);
+      constexpr uint32_t kVStride = sizeof(s.v[0]) >> 4;
+      const uint32_t tO = tmem + TM::o;
+      const uint32_t tP = tmem + TM::p;
+      for (int j = 0; j < nblk; ++j) {
+        const int vs = j % VST;
+        uint32_t vd[BN / 16];
+        const uint32_t v_lo = v_lo0 + vs * kVStride;
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk) vd[kk] = v_lo + kk * (2048 >> 4);
+        if (!mbar_wait(&s.v_full[vs], (j / VST) & 1, abort_flag, 0x1204)) break;
+        if (!mbar_wait(&s.p_full, j & 1, abort_flag, 0x1205)) break;
+        tc_fence_after();
+        const uint32_t acc0 = j > 0 ? 1u : 0u;
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk) mma_ts_w(tO, tP + kk * 8, vd[kk], hi_v, id_o, kk > 0 ? 1u : acc0);
+        mma_commit(&s.p_free);
+        mma_commit(&s.v_empty[vs]);
+        if (j == nblk - 1) mma_commit(&s.o_full);
+      }
+      mma_commit(&s.drain[1]);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(&s.drain[1], 0) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ softmax + epilogue
+    const int r = tid;  // 0..127
+    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tO = tmem + lane_base + TM::o;
+    const uint32_t tP = tmem + lane_base + TM::p;
+    const int token = r / p.hg;
+    const bool live = token < t.tokens;
+    const int limit = live ? min(t.keys, max(0, t.limit + t.step * token)) : 0;
+    const float sl2 = p.scale_log2;
+    constexpr int kPairs = BN / 2;
+    float m_run = -INFINITY, l_run = 0.0f;
+    bool ok = true;
+    // values of the last block that are not this sequence's (none past the tensor, where TMA fills with zeros)
+    const int foreign = t.k0 + t.keys < p.Tk ? t.keys - (nblk - 1) * BN : BN;
+
+    for (int j = 0; ok && j < nblk; ++j) {
+      const int sb = j & 1;
+      if (!mbar_wait(&s.s_full[sb], (j >> 1) & 1, abort_flag, 0x1300)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t tS = tmem + lane_base + TM::s(sb);
+      uint32_t hp[F16ACC ? kPairs : 1];
+      float sv[F16ACC ? 1 : BN];
+      uint32_t cw = 0;
+      if constexpr (F16ACC) {
+        tmem_ld_scores_f16<BN>(tS, hp);
+      } else {
+#pragma unroll
+        for (int c = 0; c < BN / 16; ++c) tmem_ld_x16(tS + c * 16, reinterpret_cast<uint32_t*>(sv) + c * 16);
+      }
+      if (SHIFT) tmem_ld_x1(tmem + lane_base + TM::c((j / kChunkBlocks) & 1) + (j % kChunkBlocks), cw);
+      tmem_ld_wait();
+      if constexpr (F16ACC) reg_fence<kPairs>(hp);
+      else reg_fence<BN>(reinterpret_cast<uint32_t*>(sv));
+      reg_fence<1>(&cw);
+      tc_fence_before();
+      __syncwarp();
+      mbar_arrive_if(&s.s_free[sb], lane == 0);
+
+      const int cmax = limit - j * BN;
+      const float c_raw = SHIFT ? __uint_as_float(cw) : 0.0f;
+      float mx;
+      if constexpr (F16ACC) {
+        if (cmax < BN) {
+#pragma unroll
+          for (int c = 0; c < kPairs; ++c)
+            hp[c] = ((2 * c < cmax) ? (hp[c] & 0xFFFFu) : 0xFC00u) |
+                    ((2 * c + 1 < cmax) ? (hp[c] & 0xFFFF0000u) : 0xFC000000u);  // -inf when masked
+        }
+        uint32_t tmp[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) tmp[k] = hp[k];
+#pragma unroll
+        for (int c = 8; c < kPairs; ++c) tmp[c & 7] = hmax2(tmp[c & 7], hp[c]);
+        const uint32_t m1 = tree_h2<8, true>(tmp);
+        mx = fmaxf(half_lo_to_float(m1), half_lo_to_float(m1 >> 16));
+      } else {
+        if (cmax < BN) {
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (c >= cmax) sv[c] = -INFINITY;
+        }
+        float tmp[BN];
+#pragma unroll
+        for (int c = 0; c < BN; ++c) tmp[c] = sv[c];
+        mx = tree_max3<BN>(tmp);
+      }
+      const float bm = (mx == -INFINITY) ? -INFINITY : (mx + c_raw) * sl2;
+      const float m_new = fmaxf(m_run, bm);
+      const bool need = m_new > m_run + kRescaleLog2;
+      const bool later = j > 0;
+      const float alpha_n = ex2_approx(m_run - m_new);
+      const float alpha = need ? alpha_n : 1.0f;
+      l_run = (need && later) ? l_run * alpha_n : l_run;
+      m_run = (need || !later) ? m_new : m_run;
+      const bool rescale = __any_sync(0xffffffffu, need) && later;
+      float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      uint32_t pk[kPairs];
+      if constexpr (F16ACC) {
+        const float b16 = (m_run == -INFINITY) ? 0.0f : c_raw - m_run * p.inv_scale_log2;
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c) {
+          float y0, y1, x0, x1;
+          add_f16x2_f32(y0, y1, hp[c], b16);
+          fmul2(x0, x1, y0, y1, sl2, sl2);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          pk[c] = pack_half2(p0, p1);
+          const int a = (c & 3) * 2;
+          fadd2(rs[a], rs[a + 1], rs[a], rs[a + 1], p0, p1);
+        }
+      } else {
+        const float bias = (m_run == -INFINITY) ? 0.0f : c_raw * sl2 - m_run;
+#pragma unroll
+        for (int c = 0; c < kPairs; ++c) {
+          float x0, x1;
+          ffma2(x0, x1, sv[2 * c], sv[2 * c + 1], sl2, sl2, bias, bias);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          const int a = (c & 3) * 2;
+          fadd2(rs[a], rs[a + 1], rs[a], rs[a + 1], p0, p1);
+          pk[c] = pack_half2(p0, p1);
+        }
+      }
+      l_run += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+      if (j >= 1 && !mbar_wait(&s.p_free, (j - 1) & 1, abort_flag, 0x1320)) { ok = false; break; }
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < BN / 16; ++c) tmem_st_x8(tP + c * 8, pk + c * 8);
+      if (rescale) {
+        constexpr int kRc = 64;
+#pragma unroll
+        for (int b0 = 0; b0 < D; b0 += kRc) {
+          uint32_t w[kRc];
+#pragma unroll
+          for (int c = 0; c < kRc / 16; ++c) tmem_ld_x16(tO + b0 + c * 16, w + c * 16);
+          tmem_ld_wait();
+          reg_fence<kRc>(w);
+#pragma unroll
+          for (int e = 0; e < kRc; e += 2) {
+            float a, b;
+            fmul2(a, b, __uint_as_float(w[e]), __uint_as_float(w[e + 1]), alpha, alpha);
+            w[e] = __float_as_uint(a);
+            w[e + 1] = __float_as_uint(b);
+          }
+#pragma unroll
+          for (int c = 0; c < kRc / 16; ++c) tmem_st_x16(tO + b0 + c * 16, w + c * 16);
+        }
+      }
+      if (j == nblk - 1 && foreign < BN) {
+        // thread r: the zeros of value row r (one 128-byte row of each 64-channel chunk)
+        const int vs = j % VST;
+        if (!mbar_wait(&s.v_full[vs], (j / VST) & 1, abort_flag, 0x1321)) { ok = false; break; }
+        if (r >= foreign) {
+#pragma unroll
+          for (int c = 0; c < Smem::kChunks; ++c)
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              *reinterpret_cast<uint4*>(s.v[vs] + c * Smem::kVChunk + r * 128 + ((u ^ (r & 7)) * 16)) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      mbar_arrive_if(&s.p_full, lane == 0);
+    }
+
+    // epilogue: O / l -> fp16 -> swizzled staging (the Q buffer) -> TMA store, or for a sequence's last tile, whose
+    // box would run into the next sequence, row by row
+    const bool have_o = ok && nblk > 0;
+    if (have_o && !mbar_wait(&s.o_full, 0, abort_flag, 0x1310)) ok = false;
+    if (!have_o && !mbar_wait(&s.q_full, 0, abort_flag, 0x1330)) ok = false;
+    tc_fence_after();
+    const float inv_l = (l_run > 0.0f) ? 1.0f / l_run : 0.0f;
+    uint8_t* stage = s.q;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t w[16];
+      if (have_o && ok) {
+        tmem_ld_x16(tO + c * 16, w);
+        tmem_ld_wait();
+        reg_fence<16>(w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = 0u;
+      }
+      uint32_t h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        h[e] = pack_half2(__uint_as_float(w[2 * e]) * inv_l, __uint_as_float(w[2 * e + 1]) * inv_l);
+      const int chunk = (c * 16) / 64, u0 = (c * 16) % 64 / 8;
+      uint8_t* rowp = stage + chunk * Smem::kQChunk + r * 128;
+      *reinterpret_cast<uint4*>(rowp + ((u0 ^ (r & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(rowp + (((u0 + 1) ^ (r & 7)) * 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+    const bool whole = t.tokens == p.tile_tokens;
+    if (whole) fence_proxy_async_smem();
+    named_bar_sync(1, 128);
+    if (whole) {
+      if (r == 0) {
+#pragma unroll
+        for (int c = 0; c < Smem::kChunks; ++c) tma_store_4d(&mapO, stage + c * Smem::kQChunk, c * 64, 0, t.q0, group);
+        tma_store_commit();
+        tma_store_wait_all();
+      }
+    } else {
+      constexpr int kU = D / 8;   // 16-byte units of a row
+      for (int e = r; e < t.tokens * p.hg * kU; e += 128) {
+        const int row = e / kU, u = e % kU;
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + (u / 8) * Smem::kQChunk + row * 128 + (((u % 8) ^ (row & 7)) * 16));
+        __half* to = p.o + (t.q0 + row / p.hg) * p.o_row + (group * p.hg + row % p.hg) * p.o_head + u * 8;
+        *reinterpret_cast<uint4*>(to) = x;
+      }
+    }
+    if (p.lse != nullptr && live) {
+      const float lse = (l_run > 0.0f) ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+      p.lse[static_cast<long long>(group * p.hg + r % p.hg) * p.Tq + t.q0 + token] = lse;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace packed
+}  // namespace pasa

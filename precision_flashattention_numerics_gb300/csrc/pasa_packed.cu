@@ -1,72 +1,14 @@
 // libpasa.so: the C ABI of rotary positions and of attention over packed prompts (include/pasa.h).
+#include <algorithm>
 #include <cmath>
-#include <cstring>
 
 #include "host_util.cuh"
+#include "packed_fwd.cuh"
 #include "rope.cuh"
 
 namespace {
 
-// A strided tensor [B, H, S, D] in bytes, for questions of shared memory.
-struct Strided {
-  uintptr_t at;
-  long long stride[3], n[3];   // of the dimensions, largest stride first
-  long long row;               // bytes of a row
-
-  Strided(const void* p, const long long* strides, long long B, long long H, long long S, long long D, long long size)
-      : at(reinterpret_cast<uintptr_t>(p)), stride{strides[0] * size, strides[1] * size, strides[2] * size}, n{B, H, S}, row(D * size) {
-    for (int i = 0; i < 3; ++i)
-      if (n[i] == 1) stride[i] = 0;   // a dimension of one has no stride
-    for (int i = 0; i < 2; ++i)
-      for (int j = 0; j < 2; ++j)
-        if (stride[j] < stride[j + 1]) std::swap(stride[j], stride[j + 1]), std::swap(n[j], n[j + 1]);
-  }
-  // The bytes that dimensions i .. 2 and a row span.
-  long long extent(int i) const {
-    long long e = row;
-    for (; i < 3; ++i) e += (n[i] - 1) * stride[i];
-    return e;
-  }
-  // Whether two of its rows share memory, as far as the strides tell.
-  bool folds() const {
-    for (int i = 0; i < 3; ++i)
-      if (n[i] > 1 && stride[i] < extent(i + 1)) return true;
-    return false;
-  }
-  bool same(const Strided& x) const {
-    return at == x.at && row == x.row && std::memcmp(stride, x.stride, sizeof stride) == 0 && std::memcmp(n, x.n, sizeof n) == 0;
-  }
-  // Whether the two share memory. Two views that lie side by side in one buffer's rows (q and k of a
-  // fused projection) do not; other views of one range count as sharing it.
-  bool meets(const Strided& x) const {
-    const uintptr_t end = at + extent(0), xend = x.at + x.extent(0);
-    if (end <= x.at || xend <= at) return false;
-    for (int i = 0; i < 3; ++i) {   // the first i strides alike, and what is inside them apart in every period of stride i - 1
-      if (stride[i] != x.stride[i] || stride[i] == 0) break;
-      const unsigned long long period = static_cast<unsigned long long>(stride[i]);
-      if (i > 0 && stride[i - 1] % stride[i] != 0) break;
-      const unsigned long long e = extent(i + 1), xe = x.extent(i + 1);
-      if (e > period || xe > period) break;
-      const unsigned long long d = x.at >= at ? (x.at - at) % period : (period - (at - x.at) % period) % period;
-      if (d >= e && d + xe <= period) return false;
-    }
-    return true;
-  }
-};
-
 int type_size(int type) { return type == PASA_TYPE_F32 ? 4 : type == PASA_TYPE_F16 || type == PASA_TYPE_BF16 ? 2 : 0; }
-
-// strides: of b, h and s; all at least 0, and their products with the sizes fit 62 bits with room.
-bool strides_fit(const long long* strides, long long B, long long H, long long S, long long D) {
-  const long long n[3] = {B, H, S};
-  long long sum = D;
-  for (int i = 0; i < 3; ++i) {
-    long long x;
-    if (strides[i] < 0) return false;
-    if (__builtin_mul_overflow(strides[i], n[i], &x) || __builtin_add_overflow(sum, x, &sum) || sum > (1ll << 58)) return false;
-  }
-  return true;
-}
 
 // Whether every row starts on a 16-byte boundary.
 bool rows16(const void* p, const long long* strides, int size) {
@@ -79,6 +21,95 @@ void rope_launch(const pasa::RopeParams& p, bool vectors, bool interleaved, unsi
   auto kern = vectors ? (interleaved ? pasa::rope_kernel<TIn, TOut, true> : pasa::rope_kernel<TIn, TOut, false>)
                       : (interleaved ? pasa::rope_pairs_kernel<TIn, TOut, true> : pasa::rope_pairs_kernel<TIn, TOut, false>);
   kern<<<grid, pasa::kRopeThreads, 0, st>>>(p);
+}
+
+using PackedParams = pasa::packed::Params;
+
+// The query heads of a tile: of the divisors of a kv head's g, the one whose tiles take the least time if every
+// sequence has the mean length. A tile of d heads holds 128 / d tokens; long sequences want tiles without a spare row (g = 7:
+// 18 x 7 rows of 128), short ones tiles that are not mostly empty. Equal ones: more heads, whose rows of a
+// token lie side by side.
+int packed_heads(int g, int N, int Tq) {
+  const int mean = std::max(1, Tq / N);
+  int best = 1;
+  long long least = LLONG_MAX;
+  for (int d = 1; d <= std::min(g, pasa::kTileRows); ++d) {
+    if (g % d != 0) continue;
+    const int tokens = pasa::kTileRows / d;
+    const long long tiles = static_cast<long long>(g / d) * ((mean + tokens - 1) / tokens);
+    if (tiles <= least) least = tiles, best = d;
+  }
+  return best;
+}
+
+struct PackedPlan {
+  int hg, tile_tokens;
+  long long tile_slots, key_slots;
+  size_t tiles, kshift, means, total;   // workspace: byte offsets (the count is at 0) and size
+};
+
+bool packed_fits(int N, int Hq, int Hkv, int Tq, int Tk) {
+  if (N <= 0 || Hq <= 0 || Hkv <= 0 || Tq <= 0 || Tk <= 0 || Hq % Hkv != 0) return false;
+  // row numbers past a last tile or block, and grids, fit an int
+  if (Tq > INT_MAX - 512 || Tk > INT_MAX - 512 || N > INT_MAX - 512) return false;
+  return (static_cast<long long>(Tq) + N) * Hq <= INT_MAX && (Tk / pasa::packed::kKeys + 1ll + N) * Hkv < INT_MAX;
+}
+
+PackedPlan packed_plan(int N, int Hq, int Hkv, int Tq, int Tk, int D, int mode) {
+  PackedPlan pl = {};
+  pl.hg = packed_heads(Hq / Hkv, N, Tq);
+  pl.tile_tokens = pasa::kTileRows / pl.hg;
+  pl.tile_slots = static_cast<long long>(Tq / pl.tile_tokens) + N;
+  pl.key_slots = static_cast<long long>(Tk / pasa::packed::kKeys) + N;
+  const bool shift = mode == PASA_MODE_SHIFT_F16ACC || mode == PASA_MODE_SHIFT_F32ACC;
+  pl.tiles = 256;
+  pl.kshift = pl.tiles + align_up(static_cast<size_t>(pl.tile_slots) * sizeof(pasa::packed::Tile), 256);
+  pl.means = pl.kshift + (shift ? align_up(static_cast<size_t>(Hkv) * Tk * D * 2, 256) : 0);
+  pl.total = pl.means + (shift ? align_up(static_cast<size_t>(Hkv) * pl.key_slots * D * 2, 256) : 0);
+  return pl;
+}
+
+template <int D, bool F16ACC, bool SHIFT>
+int packed_launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
+                  const CUtensorMap& mm, const PackedParams& p, cudaStream_t st) {
+  // ring slots as in pasa_attn_fwd: 3 K + 2 V for D = 128 (201 KB), 4 + 4 for D = 64
+  constexpr int KST = D == 128 ? 3 : 4, VST = D == 128 ? 2 : 4;
+  const unsigned prep = 1u + (SHIFT ? static_cast<unsigned>(p.key_slots) * static_cast<unsigned>(p.Hkv) : 0u);
+  pasa::packed::packed_prep_kernel<D><<<prep, pasa::packed::kPrepThreads, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  auto kern = pasa::packed::packed_fwd_kernel<D, F16ACC, SHIFT, KST, VST>;
+  const int smem = static_cast<int>(sizeof(pasa::AttnSmem<D, pasa::packed::kKeys, KST, VST>)) + 1024;
+  static std::atomic<unsigned long long> raised{0};
+  const unsigned grid = static_cast<unsigned>(p.tile_slots) * static_cast<unsigned>(p.Hq / p.hg);
+  e = launch_clusters(kern, grid, pasa::kAttnThreads, smem, smem, st, true, 1, raised, mq, mk, mv, mo, mm, p);
+  return e == cudaSuccess ? launch_status() : cuda_fail(e);
+}
+
+template <int D>
+int packed_dispatch(int mode, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
+                    const CUtensorMap& mm, const PackedParams& p, cudaStream_t st) {
+  switch (mode) {
+    case PASA_MODE_SHIFT_F16ACC: return packed_launch<D, true, true>(mq, mk, mv, mo, mm, p, st);
+    case PASA_MODE_SHIFT_F32ACC: return packed_launch<D, false, true>(mq, mk, mv, mo, mm, p, st);
+    case PASA_MODE_NAIVE_F16ACC: return packed_launch<D, true, false>(mq, mk, mv, mo, mm, p, st);
+    case PASA_MODE_NOSHIFT_F32ACC: return packed_launch<D, false, false>(mq, mk, mv, mo, mm, p, st);
+    default: return PASA_ERR_UNSUPPORTED;
+  }
+}
+
+// Whether every row of [T, H, D] starts on a 16-byte boundary, and rows and heads do not fold onto one another.
+int packed_layout(const void* p, const long long* strides, int T, int H, int D) {
+  if (!aligned16(p) || strides[0] % 8 != 0 || strides[1] % 8 != 0) return PASA_ERR_ALIGN;
+  const long long s3[3] = {0, strides[1], strides[0]};
+  if (strides[0] <= 0 || strides[1] <= 0 || !strides_fit(s3, 1, H, T, D)) return PASA_ERR_SHAPE;
+  if (strides[0] >= (1ll << 38) || strides[1] * H >= (1ll << 38)) return PASA_ERR_SHAPE;   // of a TMA descriptor
+  return PASA_OK;
+}
+
+Strided packed_view(const void* p, const long long* strides, int T, int H, int D) {
+  const long long s3[3] = {0, strides[1], strides[0]};
+  return Strided(p, s3, 1, H, T, D, 2);
 }
 
 }  // namespace
@@ -197,6 +228,87 @@ int pasa_rope(const void* q, void* q_out, const long long* q_strides, int Hq, co
   else if (same) rope_launch<float, float>(p, vectors, interleaved, grid, st);
   else rope_launch<float, __half>(p, vectors, interleaved, grid, st);
   return launch_status();
+}
+
+size_t pasa_attn_fwd_packed_workspace_bytes(int N, int Hq, int Hkv, int Tq, int Tk, int D, int mode) {
+  if (!packed_fits(N, Hq, Hkv, Tq, Tk) || (D != 64 && D != 128)) return 0;
+  if (mode < PASA_MODE_SHIFT_F16ACC || mode > PASA_MODE_NOSHIFT_F32ACC) return 0;
+  return packed_plan(N, Hq, Hkv, Tq, Tk, D, mode).total;
+}
+
+int pasa_attn_fwd_packed(const void* q, const void* k, const void* v, void* o, const long long* strides, float* lse,
+                         const int* cu_q, const int* cu_k, int N, int Hq, int Hkv, int Tq, int Tk, int D, int causal,
+                         float scale, int mode, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k || !v || !o || !strides || !cu_q || !cu_k) return PASA_ERR_NULLPTR;
+  if (!packed_fits(N, Hq, Hkv, Tq, Tk)) return PASA_ERR_SHAPE;
+  if ((D != 64 && D != 128) || mode < PASA_MODE_SHIFT_F16ACC || mode > PASA_MODE_NOSHIFT_F32ACC) return PASA_ERR_UNSUPPORTED;
+  int rc;
+  if ((rc = packed_layout(q, strides, Tq, Hq, D)) != PASA_OK || (rc = packed_layout(k, strides + 2, Tk, Hkv, D)) != PASA_OK ||
+      (rc = packed_layout(v, strides + 4, Tk, Hkv, D)) != PASA_OK || (rc = packed_layout(o, strides + 6, Tq, Hq, D)) != PASA_OK)
+    return rc;
+  if (!aligned4(lse) || !aligned4(cu_q) || !aligned4(cu_k)) return PASA_ERR_ALIGN;
+  const PackedPlan pl = packed_plan(N, Hq, Hkv, Tq, Tk, D, mode);
+  if (!workspace || workspace_bytes < pl.total) return PASA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PASA_ERR_ALIGN;
+  // o may be q itself: a CTA reads the rows that it writes, and no other CTA's result depends on them
+  const Strided qs = packed_view(q, strides, Tq, Hq, D), ks = packed_view(k, strides + 2, Tk, Hkv, D);
+  const Strided vs = packed_view(v, strides + 4, Tk, Hkv, D), os = packed_view(o, strides + 6, Tq, Hq, D);
+  if (os.folds() || os.meets(ks) || os.meets(vs) || (os.meets(qs) && !os.same(qs))) return PASA_ERR_SHAPE;
+  const Span out(o, os.extent(0), 1), ls(lse, static_cast<unsigned long long>(Hq) * Tq, 4), work(workspace, pl.total, 1);
+  const Span cq(cu_q, N + 1ull, 4), ck(cu_k, N + 1ull, 4);
+  if (any_meet({ls, work}, {out, Span(q, qs.extent(0), 1), Span(k, ks.extent(0), 1), Span(v, vs.extent(0), 1), cq, ck}) ||
+      out.meets(cq) || out.meets(ck))
+    return PASA_ERR_SHAPE;
+  rc = check_device();
+  if (rc != PASA_OK) return rc;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt(static_cast<float>(D));
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PackedParams p = {};
+  p.cu_q = cu_q;
+  p.cu_k = cu_k;
+  p.N = N;
+  p.Tq = Tq;
+  p.Tk = Tk;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.hg = pl.hg;
+  p.tile_tokens = pl.tile_tokens;
+  p.tile_slots = static_cast<int>(pl.tile_slots);
+  p.key_slots = static_cast<int>(pl.key_slots);
+  p.causal = causal ? 1 : 0;
+  while ((Tk / pasa::packed::kKeys + 1) >> p.bin_shift >= pasa::packed::kBins) ++p.bin_shift;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.inv_scale_log2 = 1.0f / p.scale_log2;
+  p.count = reinterpret_cast<int*>(ws);
+  p.tiles = reinterpret_cast<pasa::packed::Tile*>(ws + pl.tiles);
+  p.k = static_cast<const __half*>(k);
+  p.k_row = strides[2];
+  p.k_head = strides[3];
+  p.kshift = reinterpret_cast<__half*>(ws + pl.kshift);
+  p.means = reinterpret_cast<__half*>(ws + pl.means);
+  p.o = static_cast<__half*>(o);
+  p.o_row = strides[6];
+  p.o_head = strides[7];
+  p.lse = lse;
+  const bool shift = mode == PASA_MODE_SHIFT_F16ACC || mode == PASA_MODE_SHIFT_F32ACC;
+  CUtensorMap mq, mk, mv, mo, mm;
+  // (channels, heads of a tile, tokens, tiles' groups of heads) of q and o; (channels, rows, heads) of keys and values
+  auto rows_map = [&](CUtensorMap* m, const void* at, const long long* s) {
+    return make_strided_map(m, at, {D, pl.hg, Tq, Hq / pl.hg}, {s[1] * 2, s[0] * 2, s[1] * 2 * pl.hg}, {64, pl.hg, pl.tile_tokens, 1});
+  };
+  auto keys_map = [&](CUtensorMap* m, const void* at, long long row, long long head) {
+    return make_strided_map(m, at, {D, Tk, Hkv}, {row * 2, head * 2}, {64, pasa::packed::kKeys, 1});
+  };
+  if ((rc = rows_map(&mq, q, strides)) != PASA_OK || (rc = rows_map(&mo, o, strides + 6)) != PASA_OK) return rc;
+  if ((rc = shift ? keys_map(&mk, p.kshift, D, static_cast<long long>(Tk) * D) : keys_map(&mk, k, strides[2], strides[3])) != PASA_OK)
+    return rc;
+  if ((rc = keys_map(&mv, v, strides[4], strides[5])) != PASA_OK) return rc;
+  mm = mk;   // unused without the shift
+  if (shift && (rc = make_strided_map(&mm, p.means, {D, pl.key_slots, Hkv}, {D * 2, pl.key_slots * D * 2},
+                                      {64, pasa::kChunkBlocks, 1})) != PASA_OK)
+    return rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return D == 64 ? packed_dispatch<64>(mode, mq, mk, mv, mo, mm, p, st) : packed_dispatch<128>(mode, mq, mk, mv, mo, mm, p, st);
 }
 
 }  // extern "C"
