@@ -532,6 +532,33 @@ int pasa_attn_fwd_decode_step_kv4(const void* q, const void* k, const void* v, v
                                   int causal, float scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Attention for a tree of drafted tokens on a 4-bit cache. (No counterpart in the paper.) The nodes of a sequence are
+ * several guesses of its next tokens that share what they have in common; node i sees the sequence's
+ * cached rows, its ancestors and itself:
+ *     O = softmax(scale * q K^T) V,  LSE = ln sum_j exp(scale * q . k_j)
+ * over the cache's values (K = s c + shift, V = s c) and the nodes' own keys and values, which are not in the cache:
+ * pasa_kv4_append_rows stores those of the accepted nodes afterwards.
+ *   q, o     fp16 [B, Hq, Sq, D], k, v fp16 [B, Hkv, Sq, D]: the nodes, Sq <= 128 (else PASA_ERR_UNSUPPORTED), any number of
+ *            heads; lse fp32 [B, Hq, Sq] or NULL
+ *   parents  int32 [B, Sq], device: the parent of each node, which comes before it; -1 (as any number that is not
+ *            before it) for a child of the last cached token. NULL: a chain, node i's parent is i - 1.
+ *   counts   int32 [B], device, or NULL for Sq: nodes of each sequence, taken as 0 below 0 and as Sq above Sq. The rows
+ *            of others get O = 0 and LSE = -inf, and what q, k, v and parents hold there is not read.
+ *   lengths  int32 [B], device, or NULL for Sk: cached rows of each sequence, taken as 0 below 0 and as Sk (>= 0) above
+ *            Sk. Rows past the last are not read.
+ *   shift    the cache's (it is subtracted from the nodes' keys with one fp16 rounding, and cancels in the softmax)
+ *   workspace  device, 256-byte aligned, at least pasa_attn_fwd_tree_kv4_workspace_bytes(...) bytes, written
+ *            before it is read, used on `stream` only
+ * A node's key or value that is not finite may spoil all nodes of its sequence and kv head. o, lse and the workspace share no
+ * memory with one another or with what is read (PASA_ERR_SHAPE).
+ */
+size_t pasa_attn_fwd_tree_kv4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D);
+int pasa_attn_fwd_tree_kv4(const void* q, const void* k, const void* v, const int* parents, const int* counts, const void* k4,
+                           const void* kscale, const void* v4, const void* vscale, const void* shift, const int* lengths, void* o,
+                           float* lse, int B, int Hq, int Hkv, int Sq, int Sk, int Sk_cap, int D, float scale, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
  * Eviction from a cache by accumulated attention weight. (No counterpart in the paper.) Of
  * each sequence with more than `budget` rows, every kv head keeps budget rows: its last
  * `recent` ones (0 <= recent <= budget) and, of the others, those with the largest

@@ -23,7 +23,7 @@ __all__ = [
     "PasaError", "attn_fwd", "attn_fwd_alloc", "attn_fwd_fused", "attn_fwd_shifted", "attn_fwd_stats", "kshift", "workspace_bytes", "check_device_error", "block_rows",
     "kv4_append", "kv4_read", "attn_fwd_decode_kv4", "attn_fwd_decode_step_kv4", "cache_evict",
     "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BASE", "ROPE_BY_PARTS", "rope_frequencies", "rope",
-    "attn_fwd_packed", "packed_workspace_bytes",
+    "attn_fwd_packed", "packed_workspace_bytes", "attn_fwd_tree_kv4", "tree_kv4_workspace_bytes",
     "library", "library_path",
 ]
 
@@ -79,6 +79,8 @@ SIGNATURES = {
     "pasa_attn_fwd_decode_kv4_workspace_bytes": ([_I] * 7, _SZ),
     "pasa_attn_fwd_decode_kv4": ([_P] * 10 + [_I] * 8 + [_F, _P, _SZ, _P], _I),
     "pasa_attn_fwd_decode_step_kv4": ([_P] * 9 + [_I] + [_P] * 3 + [_I] * 9 + [_F, _P, _SZ, _P], _I),
+    "pasa_attn_fwd_tree_kv4_workspace_bytes": ([_I] * 6, _SZ),
+    "pasa_attn_fwd_tree_kv4": ([_P] * 13 + [_I] * 7 + [_F, _P, _SZ, _P], _I),
     "pasa_cache_evict": ([_P, _P, _P, _I] + [_P] * 5 + [_I] * 7 + [_P], _I),
     "pasa_attn_fwd_packed_workspace_bytes": ([_I] * 7, _SZ),
     "pasa_attn_fwd_packed": ([_P] * 8 + [_I] * 7 + [_F, _I, _P, _SZ, _P], _I),
@@ -714,6 +716,48 @@ def attn_fwd_decode_step_kv4(q, k, v, k4, kscale, v4, vscale, start, causal: boo
                                                  workspace.data_ptr() if nbytes else None, nbytes, stream)
     if rc != 0:
         raise PasaError(rc, "pasa_attn_fwd_decode_step_kv4")
+    return out, lse
+
+
+@functools.lru_cache(maxsize=1024)   # of sizes only
+def tree_kv4_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: int) -> int:
+    return library().pasa_attn_fwd_tree_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D)
+
+
+def attn_fwd_tree_kv4(q, k, v, k4, kscale, v4, vscale, parents=None, scale: float | None = None, shift=None,
+                      length: int | None = None, lengths=None, counts=None, out=None, lse=None, workspace=None):
+    """Attention for a tree of drafted tokens on a 4-bit cache (see :func:`kv4_append`): q fp16 [B,Hq,n,D], the nodes' own
+    k and v fp16 [B,Hkv,n,D] (not in the cache; store the accepted ones with :func:`kv4_append`'s rows), n <= 128.
+    parents int32 [B,n]: each node's parent, -1 for a child of the last cached token (None: a chain); node i sees the
+    cached rows, its ancestors and itself. counts int32 [B]: nodes of each sequence (rows of others: o = 0, lse = -inf).
+    The cache holds `length` rows (default: all) or lengths[b] (int32 [B]; `length` is then an upper bound).
+    Returns (o, lse)."""
+    dev, stream = _here()
+    ptrs, sp, (B, Hkv, cap, D) = _check_kv4(k4, kscale, v4, vscale, shift, dev)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("expected q [B,Hq,n,D]")
+    _, Hq, Sq, _ = q.shape
+    Sk = cap if length is None else _int32(length, "length")
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, Hq, Sq), device=q.device, dtype=torch.float32) if lse is None else lse
+    qp = _check_cuda(q, "q", _F16, (B, Hq, Sq, D), dev)
+    kp = _check_cuda(k, "k", _F16, (B, Hkv, Sq, D), dev)
+    vp = _check_cuda(v, "v", _F16, (B, Hkv, Sq, D), dev)
+    op = _check_cuda(out, "out", _F16, (B, Hq, Sq, D), dev)
+    lp = _check_cuda(lse, "lse", _F32, (B, Hq, Sq), dev)
+    pp = None if parents is None else _check_cuda(parents, "parents", _I32, (B, Sq), dev)
+    np_ = None if lengths is None else _check_cuda(lengths, "lengths", _I32, (B,), dev)
+    cp = None if counts is None else _check_cuda(counts, "counts", _I32, (B,), dev)
+    if workspace is not None:
+        _check_cuda(workspace, "workspace", _U8, None, dev)
+    nbytes = tree_kv4_workspace_bytes(B, Hq, Hkv, Sq, Sk, D)
+    if nbytes and (workspace is None or workspace.numel() < nbytes):
+        workspace = torch.empty(nbytes, device=dev, dtype=_U8)
+    rc = library().pasa_attn_fwd_tree_kv4(qp, kp, vp, pp, cp, *ptrs, sp, np_, op, lp, B, Hq, Hkv, Sq, Sk, cap, D,
+                                          float(scale) if scale is not None else 0.0,
+                                          workspace.data_ptr() if nbytes else None, nbytes, stream)
+    if rc != 0:
+        raise PasaError(rc, "pasa_attn_fwd_tree_kv4")
     return out, lse
 
 
