@@ -276,6 +276,18 @@ int make_strided_map(CUtensorMap* m, const void* base, std::initializer_list<lon
   return r == CUDA_SUCCESS ? PASA_OK : cuda_fail(cudaErrorInvalidValue);
 }
 
+// Ask for an SM's memory to be split for `kern` as for the kernels with all of its shared memory that run next to it on the
+// stream: an SM whose split changes runs empty first. Once per device (bit of `asked`).
+template <typename... Params>
+void prefer_shared(void (*kern)(Params...), std::atomic<unsigned long long>& asked) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return;
+  const unsigned long long bit = 1ull << dev;
+  if ((asked.load(std::memory_order_relaxed) & bit) != 0) return;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) == cudaSuccess)
+    asked.fetch_or(bit, std::memory_order_relaxed);
+}
+
 // This unit's error word, read and cleared.
 int take_device_error(unsigned long long* info) {
   int word = 0;

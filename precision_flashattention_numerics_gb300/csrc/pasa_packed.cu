@@ -75,6 +75,8 @@ int packed_launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMa
   // ring slots as in pasa_attn_fwd: 3 K + 2 V for D = 128 (201 KB), 4 + 4 for D = 64
   constexpr int KST = D == 128 ? 3 : 4, VST = D == 128 ? 2 : 4;
   const unsigned prep = 1u + (SHIFT ? static_cast<unsigned>(p.key_slots) * static_cast<unsigned>(p.Hkv) : 0u);
+  static std::atomic<unsigned long long> asked{0};
+  prefer_shared(pasa::packed::packed_prep_kernel<D>, asked);
   pasa::packed::packed_prep_kernel<D><<<prep, pasa::packed::kPrepThreads, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
