@@ -197,16 +197,29 @@ __global__ void __launch_bounds__(kPrepThreads) packed_prep_kernel(const __grid_
                         reinterpret_cast<uint4*>(p.means + (static_cast<long long>(head) * p.key_slots + slot) * D), n);
 }
 
-// One CTA: a tile of the list and a group of hg heads. Warp roles, TMEM and barriers as in attn_fwd_kernel
-// (warps 0-3 softmax and epilogue, one thread per row; 4 TMA; 5 score and offsets MMAs; 6 PV MMAs). Its waits are
-// all bounded (ptx.cuh).
-template <int D, bool F16ACC, bool SHIFT, int KST, int VST>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+// Shared memory: attn_fwd_kernel's and, for two softmax sets, what they exchange.
+template <int D, int KST, int VST, int SETS>
+struct Smem : AttnSmem<D, kKeys, KST, VST> {
+  uint64_t pv_done[2];           // PV(j), by the parity of j: with two sets, one can come to its wait for PV(j) while PV(j - 1)
+                                 // still runs, and one barrier's phase of PV(j - 2) would look like PV(j)'s
+  uint64_t mx_full[4][SETS];     // [rows 32 q ..][set]: the set has published m of its block
+  float m_of[SETS][kTileRows];   // the maximum that a row's last block was taken with
+  float2 sums[SETS][kTileRows];  // in the end: a row's sum, and the maximum it is scaled to
+};
+__host__ __device__ constexpr int threads(int sets) { return (4 * sets + 3) * 32; }
+
+// One CTA: a tile of the list and a group of hg heads. Warp roles, TMEM and barriers as in attn_fwd_kernel (SETS = 1) and
+// attn_fwd_2set_kernel (SETS = 2, for D = 64, whose MMAs take half as long beside the same softmax): 4 warps of softmax and
+// epilogue, one thread per row, for each set, which take the blocks in turn; then a warp for TMA, one for the score and
+// offsets MMAs, one for PV. All waits are bounded (ptx.cuh).
+template <int D, bool F16ACC, bool SHIFT, int KST, int VST, int SETS>
+__global__ void __launch_bounds__(threads(SETS), 1)
 packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                   const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapO,
                   const __grid_constant__ CUtensorMap mapM, const __grid_constant__ Params p) {
   constexpr int BN = kKeys;
-  using Smem = AttnSmem<D, BN, KST, VST>;
+  using Smem = packed::Smem<D, KST, VST, SETS>;
+  constexpr int kTma = 4 * SETS, kQk = kTma + 1, kPv = kTma + 2;   // warps
   static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "shared memory per CTA");
   using TM = TmemMap<D, BN>;
   extern __shared__ uint8_t smem_raw[];
@@ -227,14 +240,15 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
       mbar_init(&s.s_free[i], 4);
     }
     mbar_init(&s.p_full, 4);
-    mbar_init(&s.p_free, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.pv_done[i], 1);
+    for (int i = 0; i < 4 * SETS; ++i) mbar_init(&s.mx_full[i / SETS][i % SETS], 1);
     mbar_init(&s.o_full, 1);
     mbar_init(&s.drain[0], 1);
     mbar_init(&s.drain[1], 1);
     s.abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kQk) {
     tmem_alloc(&s.tmem_base, 512);
     tmem_relinquish();
   }
@@ -259,7 +273,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
 
   if (!there) {
     // nothing to do but to give the TMEM back
-  } else if (warp == 4) {
+  } else if (warp == kTma) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
       const uint32_t q_chunk = static_cast<uint32_t>(rows) * 128;
@@ -315,7 +329,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
       }
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == kQk) {
     // ------------------------------------------------------------------ QK issuer (see attn_fwd_kernel)
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_f16(kTileRows, BN, !F16ACC, false);
@@ -376,7 +390,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
       }
     }
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == kPv) {
     // ------------------------------------------------------------------ PV issuer
     if (lane == 0) {
       constexpr uint32_t id_o = idesc_f16(kTileRows, D, true, true);
@@ -397,7 +411,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
         const uint32_t acc0 = j > 0 ? 1u : 0u;
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk) mma_ts_w(tO, tP + kk * 8, vd[kk], hi_v, id_o, kk > 0 ? 1u : acc0);
-        mma_commit(&s.p_free);
+        mma_commit(&s.pv_done[j & 1]);
         mma_commit(&s.v_empty[vs]);
         if (j == nblk - 1) mma_commit(&s.o_full);
       }
@@ -409,8 +423,9 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
-    const int r = tid;  // 0..127
-    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const int set = SETS == 1 ? 0 : warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tO = tmem + lane_base + TM::o;
     const uint32_t tP = tmem + lane_base + TM::p;
     const int token = r / p.hg;
@@ -418,12 +433,12 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
     const int limit = live ? min(t.keys, max(0, t.limit + t.step * token)) : 0;
     const float sl2 = p.scale_log2;
     constexpr int kPairs = BN / 2;
-    float m_run = -INFINITY, l_run = 0.0f;
+    float m_run = -INFINITY, l_run = 0.0f;   // with two sets: this one's sum, and the maximum it is scaled to
     bool ok = true;
     // values of the last block that are not this sequence's (none past the tensor, where TMA fills with zeros)
     const int foreign = t.k0 + t.keys < p.Tk ? t.keys - (nblk - 1) * BN : BN;
 
-    for (int j = 0; ok && j < nblk; ++j) {
+    for (int j = set; ok && j < nblk; j += SETS) {
       const int sb = j & 1;
       if (!mbar_wait(&s.s_full[sb], (j >> 1) & 1, abort_flag, 0x1300)) { ok = false; break; }
       tc_fence_after();
@@ -475,13 +490,26 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
         mx = tree_max3<BN>(tmp);
       }
       const float bm = (mx == -INFINITY) ? -INFINITY : (mx + c_raw) * sl2;
-      const float m_new = fmaxf(m_run, bm);
-      const bool need = m_new > m_run + kRescaleLog2;
+      float m_prev = m_run;   // what the block before was taken with
+      if (SETS == 2 && j > 0) {
+        if (!mbar_wait(&s.mx_full[quad][set ^ (SETS - 1)], ((j - 1) >> 1) & 1, abort_flag, 0x1340)) { ok = false; break; }
+        m_prev = s.m_of[set ^ (SETS - 1)][r];
+      }
+      const float m_new = fmaxf(m_prev, bm);
+      const bool need = m_new > m_prev + kRescaleLog2;
       const bool later = j > 0;
-      const float alpha_n = ex2_approx(m_run - m_new);
+      const float alpha_n = ex2_approx(m_prev - m_new);
       const float alpha = need ? alpha_n : 1.0f;
-      l_run = (need && later) ? l_run * alpha_n : l_run;
-      m_run = (need || !later) ? m_new : m_run;
+      const float m_cur = (need || !later) ? m_new : m_prev;
+      if constexpr (SETS == 2) {
+        s.m_of[set][r] = m_cur;
+        __syncwarp();
+        mbar_arrive_if(&s.mx_full[quad][set], lane == 0);
+        if (m_run != m_cur) l_run *= ex2_approx(m_run - m_cur);   // 0 while this set has no block yet
+      } else {
+        l_run = (need && later) ? l_run * alpha_n : l_run;
+      }
+      m_run = m_cur;
       const bool rescale = __any_sync(0xffffffffu, need) && later;
       float rs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       uint32_t pk[kPairs];
@@ -510,7 +538,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
         }
       }
       l_run += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
-      if (j >= 1 && !mbar_wait(&s.p_free, (j - 1) & 1, abort_flag, 0x1320)) { ok = false; break; }
+      if (j >= 1 && !mbar_wait(&s.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort_flag, 0x1320)) { ok = false; break; }
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < BN / 16; ++c) tmem_st_x8(tP + c * 8, pk + c * 8);
@@ -559,10 +587,20 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
     if (have_o && !mbar_wait(&s.o_full, 0, abort_flag, 0x1310)) ok = false;
     if (!have_o && !mbar_wait(&s.q_full, 0, abort_flag, 0x1330)) ok = false;
     tc_fence_after();
+    if constexpr (SETS == 2) {
+      s.sums[set][r] = make_float2(l_run, m_run);
+      named_bar_sync(1, 128 * SETS);
+      const float2 other = s.sums[set ^ (SETS - 1)][r];
+      const float m_f = fmaxf(m_run, other.y);   // what O is scaled to: the last block's
+      l_run = m_f == -INFINITY ? 0.0f : l_run * ex2_approx(m_run - m_f) + other.x * ex2_approx(other.y - m_f);
+      m_run = m_f;
+    }
     const float inv_l = (l_run > 0.0f) ? 1.0f / l_run : 0.0f;
     uint8_t* stage = s.q;
+    constexpr int kCols = D / SETS;   // of O, for a set
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
+    for (int c0 = 0; c0 < kCols / 16; ++c0) {
+      const int c = set * (kCols / 16) + c0;
       uint32_t w[16];
       if (have_o && ok) {
         tmem_ld_x16(tO + c * 16, w);
@@ -583,9 +621,9 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
     }
     const bool whole = t.tokens == p.tile_tokens;
     if (whole) fence_proxy_async_smem();
-    named_bar_sync(1, 128);
+    named_bar_sync(2, 128 * SETS);
     if (whole) {
-      if (r == 0) {
+      if (tid == 0) {
 #pragma unroll
         for (int c = 0; c < Smem::kChunks; ++c) tma_store_4d(&mapO, stage + c * Smem::kQChunk, c * 64, 0, t.q0, group);
         tma_store_commit();
@@ -593,14 +631,14 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
       }
     } else {
       constexpr int kU = D / 8;   // 16-byte units of a row
-      for (int e = r; e < t.tokens * p.hg * kU; e += 128) {
+      for (int e = tid; e < t.tokens * p.hg * kU; e += 128 * SETS) {
         const int row = e / kU, u = e % kU;
         const uint4 x = *reinterpret_cast<const uint4*>(stage + (u / 8) * Smem::kQChunk + row * 128 + (((u % 8) ^ (row & 7)) * 16));
         __half* to = p.o + (t.q0 + row / p.hg) * p.o_row + (group * p.hg + row % p.hg) * p.o_head + u * 8;
         *reinterpret_cast<uint4*>(to) = x;
       }
     }
-    if (p.lse != nullptr && live) {
+    if (p.lse != nullptr && live && set == 0) {
       const float lse = (l_run > 0.0f) ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
       p.lse[static_cast<long long>(group * p.hg + r % p.hg) * p.Tq + t.q0 + token] = lse;
     }
@@ -609,7 +647,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, 512);
+  if (warp == kQk) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace packed

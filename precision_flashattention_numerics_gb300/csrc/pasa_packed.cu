@@ -80,11 +80,12 @@ int packed_launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMa
   pasa::packed::packed_prep_kernel<D><<<prep, pasa::packed::kPrepThreads, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
-  auto kern = pasa::packed::packed_fwd_kernel<D, F16ACC, SHIFT, KST, VST>;
-  const int smem = static_cast<int>(sizeof(pasa::AttnSmem<D, pasa::packed::kKeys, KST, VST>)) + 1024;
+  constexpr int SETS = D == 64 ? 2 : 1;
+  auto kern = pasa::packed::packed_fwd_kernel<D, F16ACC, SHIFT, KST, VST, SETS>;
+  const int smem = static_cast<int>(sizeof(pasa::packed::Smem<D, KST, VST, SETS>)) + 1024;
   static std::atomic<unsigned long long> raised{0};
   const unsigned grid = static_cast<unsigned>(p.tile_slots) * static_cast<unsigned>(p.Hq / p.hg);
-  e = launch_clusters(kern, grid, pasa::kAttnThreads, smem, smem, st, true, 1, raised, mq, mk, mv, mo, mm, p);
+  e = launch_clusters(kern, grid, pasa::packed::threads(SETS), smem, smem, st, true, 1, raised, mq, mk, mv, mo, mm, p);
   return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
 
@@ -205,23 +206,28 @@ int pasa_rope(const void* q, void* q_out, const long long* q_strides, int Hq, co
   p.tokens = static_cast<unsigned>(tokens);
   p.mscale = mscale;
   p.sign = inverse ? -1.0f : 1.0f;
-  long long threads;
+  long long ctas;
   if (vectors) {
     p.groups = rotary_dim / 16 + (in_place ? 0 : (D - rotary_dim + 15) / 16);
-    // heads of a thread: as many as leave every SM its threads
-    p.per = pasa::kRopeHeads;
-    while (p.per > 1 && tokens * ((heads + p.per - 1) / p.per) * p.groups < 152ll * 1024) p.per /= 2;
-    p.slots = static_cast<unsigned>((heads + p.per - 1) / p.per);
+    // head slots of a token: as few as fill the SMs, so that a thread's angles serve many heads, and a few times more where a
+    // thread still has kRopeHeads heads (32768 tokens x 32 heads: 2 slots 106 us, 4 96, 8 98, 16 107)
+    p.slots = 1;
+    auto threads = [&] { return tokens * p.groups * p.slots; };
+    while (p.slots < heads && (threads() < 152ll * 1024 || (threads() < 152ll * 4096 && 2ll * pasa::kRopeHeads * p.slots <= heads)))
+      p.slots *= 2;
+    p.slots = static_cast<unsigned>(std::min<long long>({p.slots, heads, static_cast<long long>(pasa::kRopeThreads / p.groups)}));
+    p.cta_tokens = pasa::kRopeThreads / (p.groups * p.slots);
+    ctas = (tokens + p.cta_tokens - 1) / p.cta_tokens;
   } else {
     p.groups = rotary_dim / 2 + (in_place ? 0 : D - rotary_dim);
-    p.per = 1;
     p.slots = static_cast<unsigned>(heads);
+    long long threads;
+    if (__builtin_mul_overflow(tokens, heads * p.groups, &threads) || threads > 0xFFFFFF00ll - pasa::kRopeThreads) return PASA_ERR_SHAPE;
+    ctas = (threads + pasa::kRopeThreads - 1) / pasa::kRopeThreads;
   }
-  if (__builtin_mul_overflow(tokens, static_cast<long long>(p.slots) * p.groups, &threads) || threads > 0xFFFFFF00ll - pasa::kRopeThreads)
-    return PASA_ERR_SHAPE;
   const int rc = check_device();
   if (rc != PASA_OK) return rc;
-  const unsigned grid = static_cast<unsigned>((threads + pasa::kRopeThreads - 1) / pasa::kRopeThreads);
+  const unsigned grid = static_cast<unsigned>(ctas);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool same = in_type == out_type;
   if (in_type == PASA_TYPE_F16) rope_launch<__half, __half>(p, vectors, interleaved, grid, st);
