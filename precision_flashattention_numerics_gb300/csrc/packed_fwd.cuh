@@ -248,6 +248,13 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
     s.abort_flag = 0;
     fence_mbar_init();
   }
+  if (warp == kTma && lane == 0) {
+    tma_prefetch_desc(&mapQ);
+    tma_prefetch_desc(&mapK);
+    tma_prefetch_desc(&mapV);
+    tma_prefetch_desc(&mapO);
+    if (SHIFT) tma_prefetch_desc(&mapM);
+  }
   if (warp == kQk) {
     tmem_alloc(&s.tmem_base, 512);
     tmem_relinquish();
@@ -599,25 +606,27 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
     uint8_t* stage = s.q;
     constexpr int kCols = D / SETS;   // of O, for a set
 #pragma unroll
-    for (int c0 = 0; c0 < kCols / 16; ++c0) {
-      const int c = set * (kCols / 16) + c0;
-      uint32_t w[16];
+    for (int c0 = 0; c0 < kCols; c0 += 32) {
+      const int c = set * kCols + c0;
+      uint32_t w[32];
       if (have_o && ok) {
-        tmem_ld_x16(tO + c * 16, w);
+        tmem_ld_x16(tO + c, w);
+        tmem_ld_x16(tO + c + 16, w + 16);
         tmem_ld_wait();
-        reg_fence<16>(w);
+        reg_fence<32>(w);
       } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = 0u;
+        for (int e = 0; e < 32; ++e) w[e] = 0u;
       }
-      uint32_t h[8];
+      uint8_t* rowp = stage + c / 64 * Smem::kQChunk + r * 128;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        h[e] = pack_half2(__uint_as_float(w[2 * e]) * inv_l, __uint_as_float(w[2 * e + 1]) * inv_l);
-      const int chunk = (c * 16) / 64, u0 = (c * 16) % 64 / 8;
-      uint8_t* rowp = stage + chunk * Smem::kQChunk + r * 128;
-      *reinterpret_cast<uint4*>(rowp + ((u0 ^ (r & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(rowp + (((u0 + 1) ^ (r & 7)) * 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+      for (int u = 0; u < 4; ++u) {
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          h[e] = pack_half2(__uint_as_float(w[8 * u + 2 * e]) * inv_l, __uint_as_float(w[8 * u + 2 * e + 1]) * inv_l);
+        *reinterpret_cast<uint4*>(rowp + (((c % 64 / 8 + u) ^ (r & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+      }
     }
     const bool whole = t.tokens == p.tile_tokens;
     if (whole) fence_proxy_async_smem();
@@ -627,7 +636,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
 #pragma unroll
         for (int c = 0; c < Smem::kChunks; ++c) tma_store_4d(&mapO, stage + c * Smem::kQChunk, c * 64, 0, t.q0, group);
         tma_store_commit();
-        tma_store_wait_all();
+        tma_store_wait_read();   // the stage stays until it has been read; the rows land in their own time
       }
     } else {
       constexpr int kU = D / 8;   // 16-byte units of a row
