@@ -546,7 +546,7 @@ int pasa_attn_fwd_decode_step_kv4(const void* q, const void* k, const void* v, v
  *            of others get O = 0 and LSE = -inf, and what q, k, v and parents hold there is not read.
  *   lengths  int32 [B], device, or NULL for Sk: cached rows of each sequence, taken as 0 below 0 and as Sk (>= 0) above
  *            Sk. Rows past the last are not read.
- *   shift    the cache's (it is subtracted from the nodes' keys with one fp16 rounding, and cancels in the softmax)
+ *   shift    the cache's; the nodes' keys are taken as they are (q . shift, in fp32, is their distance from cached ones)
  *   workspace  device, 256-byte aligned, at least pasa_attn_fwd_tree_kv4_workspace_bytes(...) bytes (may be NULL
  *            where that is 0), written before it is read, used on `stream` only
  * A node's key or value that is not finite may spoil all nodes of its sequence and kv head. o, lse and the workspace share no

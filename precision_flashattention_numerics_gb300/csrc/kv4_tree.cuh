@@ -243,6 +243,19 @@ __device__ __forceinline__ void load_chunk(uint4& x, unsigned short& scale, cons
       : "l"(codes), "l"(scales), "r"(there ? 1u : 0u)
       : "memory");
 }
+// 16 bytes, or zeros where `there` is false, in one piece for the same reason.
+__device__ __forceinline__ uint4 load16_if(const void* from, bool there) {
+  uint4 x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(x.x), "=&r"(x.y), "=&r"(x.z), "=&r"(x.w)
+      : "l"(from), "r"(there ? 1u : 0u)
+      : "memory");
+  return x;
+}
 // A chunk, 32 channels of a row, to its four places in a tile: `at` and its neighbours by the units' numbers.
 __device__ __forceinline__ void put_chunk(uint32_t at, uint4 codes, unsigned short scale_bits) {
   const __half scale = __ushort_as_half(scale_bits);
@@ -361,23 +374,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
             fetch(i);
           }
         } else {
-          // the nodes: K - shift or V in fp16, rows past the last node 0
+          // the nodes: K or V in fp16, rows past the last node 0
 #pragma unroll
           for (int i = 0; i < kPer; ++i) fetch(i);
           const long long bh = seg.head();
           const __half* from = (values ? p.v : p.k) + bh * p.Sq * D;
           constexpr int kUnits = D / 8, kStep = kExpandThreads / kUnits;
           const int u = t % kUnits;
-          uint4 sh = make_uint4(0u, 0u, 0u, 0u);
-          if (p.shift && !values) sh = *reinterpret_cast<const uint4*>(p.shift + bh * D + u * 8);
-#pragma unroll 4
-          for (int r = t / kUnits; r < kKeys; r += kStep) {
-            uint4 y = make_uint4(0u, 0u, 0u, 0u);
-            if (r < seg.nodes) {
-              y = *reinterpret_cast<const uint4*>(from + r * D + u * 8);
-              y = make_uint4(hsub2_rn(y.x, sh.x), hsub2_rn(y.y, sh.y), hsub2_rn(y.z, sh.z), hsub2_rn(y.w, sh.w));   // x - 0 = x
+#pragma unroll 1
+          for (int r = t / kUnits; r < kKeys; r += 2 * kStep) {
+            uint4 y[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) y[i] = load16_if(from + (r + i * kStep) * D + u * 8, r + i * kStep < seg.nodes);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int row = r + i * kStep;
+              *reinterpret_cast<uint4*>(tile + (u / 8) * S::kChunk + row * 128 + (((u % 8) ^ (row & 7)) * 16)) = code_order(y[i]);
             }
-            *reinterpret_cast<uint4*>(tile + (u / 8) * S::kChunk + r * 128 + (((u % 8) ^ (r & 7)) * 16)) = code_order(y);
           }
         }
         fence_proxy_async_smem();   // the MMA reads the tile through the async proxy
@@ -490,14 +503,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
       const int* up = p.parents + static_cast<long long>(seg.b) * p.Sq;
       if (p.parents && seg.j0 == 0 && any_live)   // into L1, ahead of the walk
         asm volatile("prefetch.global.L1 [%0];" ::"l"(up + min(lane * 4, p.Sq - 1)));
-      // Q to shared memory; the QKs of the segment before are done, as both sets have come to its end
+      // Q to shared memory; the QKs of the segment before are done, as both sets have come to its end. And q . shift, which cached
+      // keys lack and the nodes' have: half of the channels each, exchanged through S's columns, which are free until Q is there.
       float offset = 0.0f;
+      const bool shifted = p.shift != nullptr && (seg.j0 == 0 || (p.lse != nullptr && seg.whole()));
       if (any_live) {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + (bh * p.rows + row) * D) + set * (D / 16);
         uint4 x[D / 16];
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) x[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-        if (p.shift && p.lse && seg.whole()) {
+        for (int i = 0; i < D / 16; ++i) x[i] = load16_if(src + i, live);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int u = set * (D / 16) + i;
+          *reinterpret_cast<uint4*>(s.q + (u / 8) * S::kChunk + r * 128 + (((u % 8) ^ (r & 7)) * 16)) = code_order(x[i]);
+        }
+        fence_proxy_async_smem();
+        if (shifted) {
           const uint4* sh = reinterpret_cast<const uint4*>(p.shift + bh * D) + set * (D / 16);
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
@@ -509,13 +530,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
               offset = fmaf(a.x, m.x, fmaf(a.y, m.y, offset));
             }
           }
+          tmem_st_x1(tmem_q + TM::sums(set), __float_as_uint(offset));
+          tmem_st_wait();
         }
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int u = set * (D / 16) + i;
-          *reinterpret_cast<uint4*>(s.q + (u / 8) * S::kChunk + r * 128 + (((u % 8) ^ (r & 7)) * 16)) = code_order(x[i]);
+      }
+      if (shifted) {
+        tc_fence_before();
+        named_bar_sync(1, 256);
+        tc_fence_after();
+        if (any_live) {
+          uint32_t other;
+          tmem_ld_x1(tmem_q + TM::sums(set ^ 1), other);
+          tmem_ld_wait();
+          reg_fence<1>(&other);
+          offset += __uint_as_float(other);
         }
-        fence_proxy_async_smem();
+        tc_fence_before();
       }
       __syncwarp();
       mbar_arrive_if(&s.q_full, lane == 0);
@@ -551,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
           // nothing of theirs is kept: but for the nodes, all rows have the same keys.
           const int keys = j == 0 ? 0 : seg.len - (n_blocks - j) * kKeys;
           const bool later = j > seg.j0;
+          const float less = j == 0 ? offset : 0.0f;   // the nodes' keys are not shifted
           float m_cur = m_w, l = 0.0f;
           auto scale_p = [&](int columns, float f) {   // 16 columns of P at a time
             const uint32_t f2 = pack_half2(f, f);
@@ -583,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < 10; ++e) top[e] = fmax3(sv[3 * e], sv[3 * e + 1], sv[3 * e + 2]);
             top[10] = fmaxf(sv[30], sv[31]);
-            const float m_new = fmaxf(m_cur, tree_max3<11>(top) * sl2);
+            const float m_new = fmaxf(m_cur, (tree_max3<11>(top) - less) * sl2);
             const bool need = m_new > m_cur + kRescaleLog2;
             if (__any_sync(0xffffffffu, need)) {
               const float f = need ? ex2_approx(m_cur - m_new) : 1.0f;
@@ -591,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
               l *= f;
               if (c > 0) scale_p(c * 16, f);
             }
-            const float bias = (m_cur == -INFINITY) ? 0.0f : -m_cur;
+            const float bias = (m_cur == -INFINITY) ? 0.0f : -less * sl2 - m_cur;
             float rs[4] = {0.f, 0.f, 0.f, 0.f};
             uint32_t pk[16];
 #pragma unroll
@@ -654,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
       // Only of the set that had the last item is this sure (the other may see the phase of two PVs before): so after the
       // barrier for both. Then the sets exchange their sums through S's columns.
       ok = named_bar_and(1, 256, ok);
-      uint32_t w16[16] = {__float_as_uint(l_w), __float_as_uint(m_w), __float_as_uint(offset)};
+      uint32_t w16[16] = {__float_as_uint(l_w), __float_as_uint(m_w)};
       if (ok) {
         tmem_st_x16(tmem_q + TM::sums(set), w16);
         tmem_st_wait();
@@ -666,8 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
         tmem_ld_x16(tmem_q + TM::sums(set ^ 1), w16);
         tmem_ld_wait();
         reg_fence<16>(w16);
-        const float3 other = make_float3(__uint_as_float(w16[0]), __uint_as_float(w16[1]), __uint_as_float(w16[2]));
-        offset += other.z;
+        const float2 other = make_float2(__uint_as_float(w16[0]), __uint_as_float(w16[1]));
         float m_run = fmaxf(m_w, other.y);   // what O is scaled to: the last block's
         float l_run = m_run == -INFINITY ? 0.0f : l_w * ex2_approx(m_w - m_run) + other.x * ex2_approx(other.y - m_run);
         if (!live) m_run = -INFINITY, l_run = 0.0f;

@@ -1,5 +1,5 @@
 """GPU parity of tree attention on the 4-bit cache against the definition in 64 bits, on the values that the cache
-holds (oracle/kv4.py, exact) and the nodes' keys fp16_rn(K - shift).
+holds (oracle/kv4.py, exact) and the nodes' own keys.
 
 Bounds (reference()). ds, a score's absolute error in natural-log units: the fp32 sum of D products errs by at most D 2^-22 of
 the sum of their magnitudes (each of D / 16 MMA steps adds 17 terms cut at 2^-23 of the largest); scaling, the
@@ -49,7 +49,7 @@ def path(parents, i):
 
 
 def reference(q, kn, vn, kv, vv, lengths, parents, counts, scale, shift):
-    """o, lse and bounds on their errors; kv, vv: the cache's values, kn, vn: the nodes' (all 64 bits)."""
+    """o, lse and bounds on their errors; kv, vv: the cache's values (without the shift), kn, vn: the nodes' (all 64 bits)."""
     q = q.astype(np.float64)
     B, Hq, n, D = q.shape
     H = kv.shape[1]
@@ -65,7 +65,8 @@ def reference(q, kn, vn, kv, vv, lengths, parents, counts, scale, shift):
             continue
         for h in range(Hq):
             g = h // (Hq // H)
-            k = np.concatenate([kv[b, g, :lengths[b]], kn[b, g]])
+            k = np.concatenate([kv[b, g, :lengths[b]], kn[b, g] - shift[b, g]])
+            raw = np.concatenate([np.abs(kv[b, g, :lengths[b]]), np.abs(kn[b, g]) + np.abs(shift[b, g])])   # of a score's products
             v = np.concatenate([vv[b, g, :lengths[b]], vn[b, g]])
             qs = q[b, h][alive]
             s = see[alive]
@@ -77,7 +78,7 @@ def reference(q, kn, vn, kv, vv, lengths, parents, counts, scale, shift):
             off = scale * (qs @ shift[b, g])
             lse[b, h, alive] = (top + np.log(total))[:, 0] + off
             o[b, h, alive] = p @ v
-            mag = scale * np.where(s, np.abs(qs) @ np.abs(k).T, 0).max(1)
+            mag = scale * np.where(s, np.abs(qs) @ raw.T, 0).max(1)
             ds = mag * (D * 2.0 ** -22 + 2.0 ** -20) + 2.0 ** -18
             dsum = ds + (s.sum(1) + 2) * 2.0 ** -23
             bl[b, h, alive] = (dsum + scale * (np.abs(qs) @ np.abs(shift[b, g])) * D * 2.0 ** -23
@@ -123,7 +124,7 @@ class Case:
             for x, fill in zip(self.cache, (255, float("nan"), 255, float("inf"))):
                 x[b, :, self.lengths[b]:] = fill
         self.held = kv4.values(*kv4.quantise(k, shift)), kv4.values(*kv4.quantise(v))
-        self.nodes = kv4.to_fp16(self.kn.astype(np.float64) - self.zero_shift[:, :, None]), self.vn.astype(np.float64)
+        self.nodes = self.kn.astype(np.float64), self.vn.astype(np.float64)
         foul = [x.copy() for x in (self.q, self.kn, self.vn, self.parents)]
         for b in range(B):
             for x in foul[:3]:
@@ -204,6 +205,25 @@ def test_large_growing_scores():
         c.q = np.abs(c.q)
         c.dev[0] = to_dev(c.q)[0]
         check(c.run(), c.reference())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_of_every_size(D):
+    """Cached rows up to fp16's largest values (scales past 2729, where a code is expanded in two steps), down to subnormal
+    scales, and rows of zeros."""
+    c = Case(720 + D, 2, 4, 2, 5, 700, 700, D, None, None, "tree", False)
+    rng = np.random.default_rng(D)
+    size = 2.0 ** rng.integers(-24, 16, (2, 2, 700, D // 32)).repeat(32, -1)
+    k = np.clip(rng.standard_normal((2, 2, 700, D)) * size, -65504, 65504)
+    v = np.clip(rng.standard_normal((2, 2, 700, D)) * size[:, :, ::-1], -60000, 60000)
+    k[:, :, ::50], v[:, :, 7::50] = 0, 0
+    k, v = k.astype(np.float16), v.astype(np.float16)
+    c.q = (c.q * 2.0 ** -12).astype(np.float16)      # scores of some tens
+    c.dev[0] = to_dev(c.q)[0]
+    pasa().kv4_append(*to_dev(k, v), *c.cache)
+    c.held = kv4.values(*kv4.quantise(k)), kv4.values(*kv4.quantise(v))
+    assert (kv4.quantise(k)[1] > 2729).any() and (kv4.quantise(v)[1] > 2729).any()
+    check(c.run(), c.reference())
 
 
 def test_offsets_past_32_bits():
@@ -301,8 +321,7 @@ def test_a_serving_loop_of_drafts():
         p.rope(tq, tk, f, positions=at, out_q=tq, out_k=tk)
         got = p.attn_fwd_tree_kv4(tq, tk, tv, *cache, tp, lengths=lengths, counts=tc, shift=shift)
         qn, kn, vn = (x.cpu().numpy() for x in (tq, tk, tv))
-        node_keys = kv4.to_fp16(kn.astype(np.float64) - sh[:, :, None])
-        check(got, reference(qn, node_keys, vn.astype(np.float64), *held, lengths.cpu().numpy(), parents, counts, D ** -0.5, sh))
+        check(got, reference(qn, kn.astype(np.float64), vn.astype(np.float64), *held, lengths.cpu().numpy(), parents, counts, D ** -0.5, sh))
         # the longest path of each tree is accepted
         best = [max((path(parents[b], i)[::-1] for i in range(counts[b])), key=len) for b in range(B)]
         accepted = np.array([len(x) for x in best], np.int32)
