@@ -835,18 +835,23 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = ROPE
 _ROPE_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
-def _rope_strides(x, name, dtype, shape, device):
-    """The strides of b, h and s of [B,H,S,D], or of packed [T,H,D] (B = 1)."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != dtype:
+def _strides(x, name: str, dtype, shape, device):
+    """The strides of a tensor of `dtype` and shape on `device` whose channels (its last dimension) are contiguous."""
+    try:
+        st = x.stride()
+        if x.dtype is dtype and x.get_device() == device and st[-1] == 1 and x.shape == shape:
+            return st
+    except AttributeError:
+        pass
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype != dtype:   # say what is wrong
         raise TypeError(f"{name} must be a CUDA {dtype} tensor")
     if x.get_device() != device:
         raise ValueError(f"{name} is on device {x.get_device()}, the current device is {device}")
     if x.shape != shape:
         raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
-    *st, last = x.stride()
-    if last != 1:
+    if st[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name}'s channels are not contiguous")
-    return st if len(st) == 3 else [0, st[1], st[0]]
+    return st
 
 
 def rope(q, k, inv_freq, positions=None, start=0, interleaved: bool = False, mscale: float = 1.0, inverse: bool = False,
@@ -885,9 +890,11 @@ def rope(q, k, inv_freq, positions=None, start=0, interleaved: bool = False, msc
         out_k = torch.empty(kshape, device=q.device, dtype=out_dtype)
     if out_dtype not in _ROPE_TYPES:
         raise TypeError("outputs must be fp16, bf16 or fp32")
-    table = array.array("q", _rope_strides(q, "q", dtype, q.shape, dev) + _rope_strides(out_q, "out_q", out_dtype, q.shape, dev))
+    views = [_strides(q, "q", dtype, q.shape, dev), _strides(out_q, "out_q", out_dtype, q.shape, dev)]
     if k is not None:
-        table.extend(_rope_strides(k, "k", dtype, kshape, dev) + _rope_strides(out_k, "out_k", out_dtype, kshape, dev))
+        views += _strides(k, "k", dtype, kshape, dev), _strides(out_k, "out_k", out_dtype, kshape, dev)
+    # of b, h and s; packed [T,H,D] is one sequence
+    table = array.array("q", [x for st in views for x in ((0, st[1], st[0]) if packed else st[:3])])
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
         raise ValueError("expected inv_freq [R/2]")
     R = 2 * inv_freq.shape[0]
@@ -911,18 +918,12 @@ def packed_workspace_bytes(N: int, Hq: int, Hkv: int, Tq: int, Tk: int, D: int, 
 
 def _packed_strides(x, name, shape, device):
     """The strides of token and head of an fp16 [T,H,D] tensor."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype is not _F16:
-        raise TypeError(f"{name} must be a CUDA fp16 tensor")
-    if x.get_device() != device:
-        raise ValueError(f"{name} is on device {x.get_device()}, the current device is {device}")
-    if x.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected {tuple(shape)}")
-    row, head, last = x.stride()
-    if last != 1:
-        raise ValueError(f"{name}'s channels are not contiguous")
+    row, head, _ = _strides(x, name, _F16, shape, device)
     T, H, D = shape
+    if T > 1 and H > 1:
+        return row, head
     head = head if H > 1 else D   # a dimension of one has any stride
-    return [row if T > 1 else H * head, head]
+    return (row if T > 1 else H * head), head
 
 
 def attn_fwd_packed(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float | None = None, mode: int = MODE_SHIFT_F16ACC,
@@ -933,11 +934,10 @@ def attn_fwd_packed(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float 
     keys j <= i + m - n of its sequence's m. mode: MODE_* 0 .. 3. Rows outside every sequence are left as they
     are in out and lse (0 and -inf in new ones). Returns (o [Tq,Hq,D], lse fp32 [Hq,Tq] or None)."""
     dev, stream = _here()
-    for x in (q, k, v):
-        if not isinstance(x, torch.Tensor) or x.dim() != 3:
-            raise ValueError("expected q [Tq,Hq,D] and k, v [Tk,Hkv,D]")
-    Tq, Hq, D = q.shape
-    Tk, Hkv, _ = k.shape
+    try:
+        (Tq, Hq, D), (Tk, Hkv, _) = q.shape, k.shape
+    except (AttributeError, ValueError):
+        raise ValueError("expected q [Tq,Hq,D] and k, v [Tk,Hkv,D]") from None
     if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 2:
         raise ValueError("expected cu_q [N+1]")
     N = cu_q.shape[0] - 1
@@ -951,8 +951,8 @@ def attn_fwd_packed(q, k, v, cu_q, cu_k=None, causal: bool = True, scale: float 
         if lse is None:
             lse = torch.full((Hq, Tq), float("-inf"), device=q.device, dtype=_F32)
         lp = _check_cuda(lse, "lse", _F32, (Hq, Tq), dev)
-    table = array.array("q", _packed_strides(q, "q", q.shape, dev) + _packed_strides(k, "k", (Tk, Hkv, D), dev)
-                        + _packed_strides(v, "v", (Tk, Hkv, D), dev) + _packed_strides(out, "out", (Tq, Hq, D), dev))
+    table = array.array("q", (*_packed_strides(q, "q", (Tq, Hq, D), dev), *_packed_strides(k, "k", (Tk, Hkv, D), dev),
+                              *_packed_strides(v, "v", (Tk, Hkv, D), dev), *_packed_strides(out, "out", (Tq, Hq, D), dev)))
     nbytes = packed_workspace_bytes(N, Hq, Hkv, Tq, Tk, D, int(mode))
     if workspace is not None:
         _check_cuda(workspace, "workspace", _U8, None, dev)
