@@ -663,7 +663,9 @@ int pasa_rope(const void* q, void* q_out, const long long* q_strides, int Hq, co
  *              invalid sizes), written before it is read, used on `stream` only
  * o may be q itself (same strides); otherwise o, lse and the workspace share no memory with one another or with what is read
  * (PASA_ERR_SHAPE). A key or value that is not finite spoils the queries of its own sequence in the tiles that
- * read its block, also those whose mask hides it. (Tq + N) * Hq and (Tk / 128 + 1 + N) * Hkv fit an int, else PASA_ERR_SHAPE.
+ * read its block, also those whose mask hides it. Calls with few query rows divide a long sequence's keys among CTAs, by
+ * the lengths of all sequences: the last bits of a sequence of more than 1920 keys may depend on its batch.
+ * (Tq + N) * Hq and (Tk / 128 + 1 + N) * Hkv fit an int, else PASA_ERR_SHAPE.
  * All lengths are read on the device: one captured graph serves any cu_q and cu_k.
  */
 size_t pasa_attn_fwd_packed_workspace_bytes(int N, int Hq, int Hkv, int Tq, int Tk, int D, int mode);

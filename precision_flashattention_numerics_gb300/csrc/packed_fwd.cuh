@@ -19,6 +19,14 @@
 // and floor((c + L) / 128) - floor(c / 128) + 1 slots to itself), and the sequence of a slot is found by a
 // search in cu_k. Query tiles are numbered likewise.
 //
+// Pieces. Where a tile has more key blocks than an even share of all work (a chunk of a prompt on a long context, one
+// long prompt with few heads), its blocks are divided among several CTAs, which leave partial results (O, max, sum)
+// that packed_merge_kernel joins. piece_blocks() decides from the lengths, on the device. Measured with and without (mode 1,
+// D = 128): 64 queries on 100000 keys, 32 heads on 8, 173 against 700 us; 128 on 20000, 1 on 8000 and 1 on 300, 28 on 4, 76
+// against 186; a prompt of 16384, one head, 92 against 109. What is not divided pays the launch that finds nothing to join: 107.7
+// against 104.5 us for four chunks. Kernels with and without PIECES are apart, as the little that it adds cost every
+// call 2 us.
+//
 // Where a sequence ends inside a 128-key block, the block's last rows are another sequence's. Their scores are
 // masked like any other, and their values are set to zero in shared memory before the MMA reads them: a
 // probability of 0 does not make an infinity or NaN harmless.
@@ -42,14 +50,29 @@ constexpr int kKeys = 128;          // keys of a block
 constexpr int kPrepThreads = 128;
 constexpr int kBins = 1024;         // of the tiles' sort by their key blocks
 
-// One query tile: all that a CTA has to know.
-struct __align__(32) Tile {
+// Pieces and their partial results: at most kMaxPieces, and none shorter than kMinPiece key blocks.
+constexpr int kSms = 152;
+constexpr int kWaves = 4, kMaxPieces = kWaves * kSms;   // of CTAs, one to an SM
+constexpr int kMinPiece = 8;
+constexpr int kPieceStart = 4;   // key blocks that the start and end of a CTA cost
+constexpr int kMergeThreads = 256, kMergeCtas = 2 * kSms;
+
+// One query tile, or a piece of its keys: all that a CTA has to know.
+struct __align__(16) Tile {
   int q0, tokens;   // first token row of q, and how many
   int k0, keys;     // first key row of the sequence, and its keys
   int limit;        // keys that the first token sees, before clamping; each further one sees `step` more
   int step;         // 1 with the causal mask, else 0
   int blocks;       // key blocks that the last token sees
   int slot;         // of the sequence's first key block
+  int pieces;       // of the tile; with more than one,
+  int part;         // the number of this one among all pieces
+  int unused[2];
+};
+// A tile in pieces.
+struct __align__(16) Split {
+  int q0, tokens;
+  int part, pieces;   // the first piece's number, and how many
 };
 
 struct Params {
@@ -59,8 +82,11 @@ struct Params {
   int tile_slots, key_slots;
   int causal, bin_shift;
   float scale_log2, inv_scale_log2;
-  int* count;              // tiles in the list
+  int* count;              // tiles and pieces in the list; tiles in pieces
   Tile* tiles;
+  Split* splits;           // with PIECES only, like the partial results
+  float* part_o;           // [pieces][groups of heads][D / 4][rows][4]
+  float2* part_ml;         // [pieces][groups of heads][rows]: max (log2 units), sum
   const __half* k;         // the raw keys, for the shift
   long long k_row, k_head; // their strides
   __half *kshift, *means;  // [Hkv, Tk, D], [Hkv, key_slots, D]
@@ -114,33 +140,91 @@ __device__ __forceinline__ bool make_tile(const Params& p, int slot, Tile& t) {
   const int last = min(m, max(0, t.limit + t.step * (t.tokens - 1)));
   t.blocks = (last + kKeys - 1) / kKeys;
   t.slot = min(k0 / kKeys + s, p.key_slots - 1);
+  t.pieces = 1;
+  t.part = 0;
   return true;
 }
 
-// The list of tiles, most key blocks first: a counting sort by one CTA. Tiles of one bin come in any order, which
+// The most key blocks of a piece, or INT_MAX where no tile is to be divided. `sum`, `longest` and `tiles` of all tiles' blocks, for each
+// group of heads. Pieces of c blocks at most are no more than tiles + sum / c, so w waves of CTAs hold them with
+// c = sum / (w SMs / groups - tiles), and take no longer than w (c + start) and the join. Undivided, the call takes longest +
+// start at least: tiles are only divided where that is more, so that it always pays.
+__device__ __forceinline__ int piece_blocks(const Params& p, long long sum, int longest, int tiles) {
+  const int groups = p.Hq / p.hg;
+  int best = INT_MAX;
+  long long least = (longest + kPieceStart) * 9ll / 10;   // by a tenth at least, for what the estimate leaves out
+  for (int w = 1; w <= kWaves; ++w) {
+    const int room = w * kSms / groups - tiles;
+    if (room <= 0) continue;
+    const long long c = max(static_cast<long long>(kMinPiece), (sum + room - 1) / room);
+    const long long time = w * (c + kPieceStart) + 5 + longest / c / 5;
+    if (c < longest && time < least) least = time, best = static_cast<int>(c);
+  }
+  return best;
+}
+
+// The list of tiles and pieces, most key blocks first: a counting sort by one CTA. Those of one bin come in any order, which
 // no result depends on.
+template <bool PIECES>
 __device__ __forceinline__ void plan_tiles(const Params& p) {
+  constexpr int kWarps = kPrepThreads / 32;
   __shared__ int bins[kBins];
-  __shared__ int warp_sums[kPrepThreads / 32];
-  const int tid = threadIdx.x;
+  __shared__ int warp_sums[kWarps], warp_tiles[kWarps], warp_most[kWarps];
+  __shared__ long long warp_blocks[kWarps];
+  __shared__ int parts, splits;
+  const int tid = threadIdx.x, lane = tid & 31;
   for (int i = tid; i < kBins; i += kPrepThreads) bins[i] = 0;
+  if (tid == 0) parts = splits = 0;
   __syncthreads();
-  // a thread keeps what it finds of its first few slots for the second pass
+  // a thread keeps what it finds of its first few slots for the later passes
   constexpr int kKeep = 2;
   Tile kept[kKeep];
   bool there[kKeep];
-  auto bin_of = [&](const Tile& t) { return kBins - 1 - min(kBins - 1, t.blocks >> p.bin_shift); };
+  auto bin_of = [&](int blocks) { return kBins - 1 - min(kBins - 1, blocks >> p.bin_shift); };
+  int tiles = 0, most = 0;
+  long long blocks = 0;
+  auto count = [&](const Tile& t) {
+    atomicAdd(&bins[bin_of(t.blocks)], 1);
+    if (PIECES) ++tiles, most = max(most, t.blocks), blocks += t.blocks;
+  };
 #pragma unroll
   for (int i = 0; i < kKeep; ++i) {
     const int slot = i * kPrepThreads + tid;
     there[i] = slot < p.tile_slots && make_tile(p, slot, kept[i]);
-    if (there[i]) atomicAdd(&bins[bin_of(kept[i])], 1);
+    if (there[i]) count(kept[i]);
   }
+#pragma unroll 1
   for (int slot = kKeep * kPrepThreads + tid; slot < p.tile_slots; slot += kPrepThreads) {
     Tile t;
-    if (make_tile(p, slot, t)) atomicAdd(&bins[bin_of(t)], 1);
+    if (make_tile(p, slot, t)) count(t);
   }
   __syncthreads();
+  int cap = INT_MAX;
+  if constexpr (PIECES) {
+    tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) blocks += __shfl_xor_sync(0xFFFFFFFFu, blocks, d);
+    if (lane == 0) warp_tiles[tid >> 5] = tiles, warp_most[tid >> 5] = most, warp_blocks[tid >> 5] = blocks;
+    __syncthreads();
+    tiles = most = 0, blocks = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) tiles += warp_tiles[w], most = max(most, warp_most[w]), blocks += warp_blocks[w];
+    cap = piece_blocks(p, blocks, most, tiles);
+    if (cap != INT_MAX) {   // count again
+      for (int i = tid; i < kBins; i += kPrepThreads) bins[i] = 0;
+      __syncthreads();
+#pragma unroll 1
+      for (int slot = tid; slot < p.tile_slots; slot += kPrepThreads) {
+        Tile t;
+        if (!make_tile(p, slot, t)) continue;
+        const int n = max(1, (t.blocks + cap - 1) / cap), base = t.blocks / n, more = t.blocks % n;
+        atomicAdd(&bins[bin_of(base)], n - more);
+        if (more > 0) atomicAdd(&bins[bin_of(base + 1)], more);
+      }
+      __syncthreads();
+    }
+  }
   // exclusive sums over the bins: 8 neighbouring ones a thread
   constexpr int kPer = kBins / kPrepThreads;
   int sum = 0, mine[kPer];
@@ -150,13 +234,13 @@ __device__ __forceinline__ void plan_tiles(const Params& p) {
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int x = __shfl_up_sync(0xFFFFFFFFu, upto, d);
-    if ((tid & 31) >= d) upto += x;
+    if (lane >= d) upto += x;
   }
-  if ((tid & 31) == 31) warp_sums[tid >> 5] = upto;
+  if (lane == 31) warp_sums[tid >> 5] = upto;
   __syncthreads();
   int before = upto - sum, total = 0;
 #pragma unroll
-  for (int w = 0; w < kPrepThreads / 32; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < (tid >> 5)) before += warp_sums[w];
     total += warp_sums[w];
   }
@@ -165,24 +249,54 @@ __device__ __forceinline__ void plan_tiles(const Params& p) {
     bins[tid * kPer + i] = before;
     before += mine[i];
   }
-  if (tid == 0) *p.count = total;
+  if (tid == 0) p.count[0] = total;
   __syncthreads();
+  if (!PIECES || cap == INT_MAX) {
 #pragma unroll
-  for (int i = 0; i < kKeep; ++i)
-    if (there[i]) p.tiles[atomicAdd(&bins[bin_of(kept[i])], 1)] = kept[i];
-  for (int slot = kKeep * kPrepThreads + tid; slot < p.tile_slots; slot += kPrepThreads) {
-    Tile t;
-    if (make_tile(p, slot, t)) p.tiles[atomicAdd(&bins[bin_of(t)], 1)] = t;
+    for (int i = 0; i < kKeep; ++i)
+      if (there[i]) p.tiles[atomicAdd(&bins[bin_of(kept[i].blocks)], 1)] = kept[i];
+#pragma unroll 1
+    for (int slot = kKeep * kPrepThreads + tid; slot < p.tile_slots; slot += kPrepThreads) {
+      Tile t;
+      if (make_tile(p, slot, t)) p.tiles[atomicAdd(&bins[bin_of(t.blocks)], 1)] = t;
+    }
+    if (PIECES && tid == 0) p.count[1] = 0;
+    return;
+  }
+  if constexpr (PIECES) {
+#pragma unroll 1
+    for (int slot = tid; slot < p.tile_slots; slot += kPrepThreads) {
+      Tile t;
+      if (!make_tile(p, slot, t)) continue;
+      const int n = max(1, (t.blocks + cap - 1) / cap), base = t.blocks / n, more = t.blocks % n;
+      t.pieces = n;
+      if (n > 1) {
+        t.part = atomicAdd(&parts, n);
+        p.splits[atomicAdd(&splits, 1)] = Split{t.q0, t.tokens, t.part, n};
+      }
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        t.blocks = base + (i < more ? 1 : 0);
+        p.tiles[atomicAdd(&bins[bin_of(t.blocks)], 1)] = t;
+        t.k0 += t.blocks * kKeys;
+        t.keys -= t.blocks * kKeys;
+        t.limit -= t.blocks * kKeys;
+        t.slot += t.blocks;
+        ++t.part;
+      }
+    }
+    __syncthreads();
+    if (tid == 0) p.count[1] = splits;
   }
 }
 
 // CTA 0 plans; CTA 1 + slot * Hkv + head shifts the key block of a slot (kshift_reg_kernel's arithmetic, bit for
 // bit, on rows k_row apart). HBM-bound: each key is read once and written once.
-template <int D>
+template <int D, bool PIECES>
 __global__ void __launch_bounds__(kPrepThreads) packed_prep_kernel(const __grid_constant__ Params p) {
   griddep_launch_dependents();
   if (blockIdx.x == 0) {
-    plan_tiles(p);
+    plan_tiles<PIECES>(p);
     return;
   }
   const int slot = (blockIdx.x - 1) / p.Hkv, head = (blockIdx.x - 1) % p.Hkv;
@@ -205,14 +319,15 @@ struct Smem : AttnSmem<D, kKeys, KST, VST> {
   uint64_t mx_full[4][SETS];     // [rows 32 q ..][set]: the set has published m of its block
   float m_of[SETS][kTileRows];   // the maximum that a row's last block was taken with
   float2 sums[SETS][kTileRows];  // in the end: a row's sum, and the maximum it is scaled to
+  int2 piece;                    // the tile's pieces and this one's number: out of the registers until the end
 };
 __host__ __device__ constexpr int threads(int sets) { return (4 * sets + 3) * 32; }
 
-// One CTA: a tile of the list and a group of hg heads. Warp roles, TMEM and barriers as in attn_fwd_kernel (SETS = 1) and
+// One CTA: a tile of the list, or with PIECES maybe a piece of one, and a group of hg heads. Warp roles, TMEM and barriers as in attn_fwd_kernel (SETS = 1) and
 // attn_fwd_2set_kernel (SETS = 2, for D = 64, whose MMAs take half as long beside the same softmax): 4 warps of softmax and
 // epilogue, one thread per row, for each set, which take the blocks in turn; then a warp for TMA, one for the score and
 // offsets MMAs, one for PV. All waits are bounded (ptx.cuh).
-template <int D, bool F16ACC, bool SHIFT, int KST, int VST, int SETS>
+template <int D, bool F16ACC, bool SHIFT, int KST, int VST, int SETS, bool PIECES>
 __global__ void __launch_bounds__(threads(SETS), 1)
 packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                   const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapO,
@@ -261,6 +376,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
   }
   const int groups = p.Hq / p.hg;
   const int item = blockIdx.x / groups, group = blockIdx.x % groups;
+  if (PIECES) griddep_launch_dependents();   // the join, which waits for all of this
   griddep_wait();   // the list, the shifted keys and the means; every CTA: a kernel behind this one waits for this one
   const bool there = item < __ldcg(p.count);
   Tile t = {};
@@ -268,6 +384,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
     const int4* rec = reinterpret_cast<const int4*>(p.tiles + item);
     const int4 a = __ldcg(rec), b = __ldcg(rec + 1);
     t = Tile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (PIECES && tid == 0) s.piece = __ldcg(reinterpret_cast<const int2*>(rec + 2));
   }
   tc_fence_before();
   __syncthreads();
@@ -602,7 +719,10 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
       l_run = m_f == -INFINITY ? 0.0f : l_run * ex2_approx(m_run - m_f) + other.x * ex2_approx(other.y - m_f);
       m_run = m_f;
     }
-    const float inv_l = (l_run > 0.0f) ? 1.0f / l_run : 0.0f;
+    const int2 piece = PIECES ? s.piece : make_int2(1, 0);
+    const bool part = piece.x > 1;
+    const float inv_l = part ? 1.0f : (l_run > 0.0f) ? 1.0f / l_run : 0.0f;
+    const long long at = static_cast<long long>(piece.y) * groups + group;   // of the partial results
     uint8_t* stage = s.q;
     constexpr int kCols = D / SETS;   // of O, for a set
 #pragma unroll
@@ -618,6 +738,14 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
 #pragma unroll
         for (int e = 0; e < 32; ++e) w[e] = 0u;
       }
+      if (part) {
+        float4* to = reinterpret_cast<float4*>(p.part_o) + (at * (D / 4) + c / 4) * kTileRows + r;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          to[u * kTileRows] = make_float4(__uint_as_float(w[4 * u]), __uint_as_float(w[4 * u + 1]), __uint_as_float(w[4 * u + 2]),
+                                          __uint_as_float(w[4 * u + 3]));
+        continue;
+      }
       uint8_t* rowp = stage + c / 64 * Smem::kQChunk + r * 128;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -628,7 +756,8 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
         *reinterpret_cast<uint4*>(rowp + (((c % 64 / 8 + u) ^ (r & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
       }
     }
-    const bool whole = t.tokens == p.tile_tokens;
+    if (part && set == 0) p.part_ml[at * kTileRows + r] = make_float2(m_run, l_run);
+    const bool whole = !part && t.tokens == p.tile_tokens;
     if (whole) fence_proxy_async_smem();
     named_bar_sync(2, 128 * SETS);
     if (whole) {
@@ -638,7 +767,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
         tma_store_commit();
         tma_store_wait_read();   // the stage stays until it has been read; the rows land in their own time
       }
-    } else {
+    } else if (!part) {
       constexpr int kU = D / 8;   // 16-byte units of a row
       for (int e = tid; e < t.tokens * p.hg * kU; e += 128 * SETS) {
         const int row = e / kU, u = e % kU;
@@ -647,7 +776,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
         *reinterpret_cast<uint4*>(to) = x;
       }
     }
-    if (p.lse != nullptr && live && set == 0) {
+    if (p.lse != nullptr && live && set == 0 && !part) {
       const float lse = (l_run > 0.0f) ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
       p.lse[static_cast<long long>(group * p.hg + r % p.hg) * p.Tq + t.q0 + token] = lse;
     }
@@ -657,6 +786,62 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
   __syncthreads();
   tc_fence_after();
   if (warp == kQk) tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of tiles. A CTA takes 8 channels of a tile's rows and group of heads, a thread 4 of one row.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads, 4) packed_merge_kernel(const __grid_constant__ Params p) {
+  static_assert(kMergeThreads == 2 * kTileRows, "two threads to a row");
+  const int groups = p.Hq / p.hg;
+  const int r = threadIdx.x % kTileRows;
+  griddep_wait();
+  const int todo = __ldcg(p.count + 1) * groups * (D / 8);
+#pragma unroll 1
+  for (int i = blockIdx.x; i < todo; i += gridDim.x) {
+    const int ch = (i % (D / 8) * 2 + threadIdx.x / kTileRows) * 4;
+    const int group = i / (D / 8) % groups;
+    const int4 rec = __ldcg(reinterpret_cast<const int4*>(p.splits + i / (D / 8) / groups));
+    const Split t = Split{rec.x, rec.y, rec.z, rec.w};
+    const int token = r / p.hg;
+    if (token >= t.tokens) continue;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float m_run = -INFINITY, l_run = 0.0f;
+    constexpr int kAtOnce = 4;
+#pragma unroll 1
+    for (int i0 = 0; i0 < t.pieces; i0 += kAtOnce) {
+      float2 ml[kAtOnce];
+      float4 v[kAtOnce];
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) {
+        const long long at = static_cast<long long>(t.part + i0 + e) * groups + group;
+        ml[e] = make_float2(-INFINITY, 0.0f);
+        v[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i0 + e < t.pieces) {
+          ml[e] = __ldcg(p.part_ml + at * kTileRows + r);
+          v[e] = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (at * (D / 4) + ch / 4) * kTileRows + r);
+        }
+      }
+      float top = m_run;
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) top = fmaxf(top, ml[e].x);
+      if (top == -INFINITY) continue;   // pieces of which the row sees nothing
+      const float f0 = ex2_approx(m_run - top);
+      l_run *= f0, x.x *= f0, x.y *= f0, x.z *= f0, x.w *= f0;
+      m_run = top;
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e) {
+        const float f = ex2_approx(ml[e].x - top);
+        l_run = fmaf(f, ml[e].y, l_run);
+        x.x = fmaf(f, v[e].x, x.x), x.y = fmaf(f, v[e].y, x.y), x.z = fmaf(f, v[e].z, x.z), x.w = fmaf(f, v[e].w, x.w);
+      }
+    }
+    const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+    const int head = group * p.hg + r % p.hg;
+    *reinterpret_cast<uint2*>(p.o + (t.q0 + token) * p.o_row + head * p.o_head + ch) =
+        make_uint2(pack_half2(x.x * inv, x.y * inv), pack_half2(x.z * inv, x.w * inv));
+    if (ch == 0 && p.lse)
+      p.lse[static_cast<long long>(head) * p.Tq + t.q0 + token] = l_run > 0.0f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+  }
 }
 
 }  // namespace packed

@@ -45,7 +45,8 @@ int packed_heads(int g, int N, int Tq) {
 struct PackedPlan {
   int hg, tile_tokens;
   long long tile_slots, key_slots;
-  size_t tiles, kshift, means, total;   // workspace: byte offsets (the count is at 0) and size
+  bool split;                           // whether tiles may be divided
+  size_t tiles, splits, part_o, part_ml, kshift, means, total;   // workspace: byte offsets (the counts are at 0) and size
 };
 
 bool packed_fits(int N, int Hq, int Hkv, int Tq, int Tk) {
@@ -62,41 +63,58 @@ PackedPlan packed_plan(int N, int Hq, int Hkv, int Tq, int Tk, int D, int mode) 
   pl.tile_slots = static_cast<long long>(Tq / pl.tile_tokens) + N;
   pl.key_slots = static_cast<long long>(Tk / pasa::packed::kKeys) + N;
   const bool shift = mode == PASA_MODE_SHIFT_F16ACC || mode == PASA_MODE_SHIFT_F32ACC;
+  // Only where CTAs may be too few for the SMs, and keys enough for two pieces: then the list has room for all pieces, and
+  // a launch more joins them (3 us where there is nothing to be joined).
+  const long long groups = Hq / pl.hg;
+  constexpr int kMaxPieces = pasa::packed::kMaxPieces;
+  pl.split = pl.tile_slots * groups < kMaxPieces && Tk >= 2 * pasa::packed::kMinPiece * pasa::packed::kKeys;
+  const size_t parts = pl.split ? kMaxPieces : 0;   // of all groups
+  const size_t list = std::max<size_t>(pl.tile_slots, parts);
   pl.tiles = 256;
-  pl.kshift = pl.tiles + align_up(static_cast<size_t>(pl.tile_slots) * sizeof(pasa::packed::Tile), 256);
+  pl.splits = pl.tiles + align_up(list * sizeof(pasa::packed::Tile), 256);
+  pl.part_o = pl.splits + align_up(parts / 2 * sizeof(pasa::packed::Split), 256);
+  pl.part_ml = pl.part_o + parts * pasa::kTileRows * D * 4;
+  pl.kshift = pl.part_ml + parts * pasa::kTileRows * 8;
   pl.means = pl.kshift + (shift ? align_up(static_cast<size_t>(Hkv) * Tk * D * 2, 256) : 0);
   pl.total = pl.means + (shift ? align_up(static_cast<size_t>(Hkv) * pl.key_slots * D * 2, 256) : 0);
   return pl;
 }
 
-template <int D, bool F16ACC, bool SHIFT>
+template <int D, bool F16ACC, bool SHIFT, bool PIECES>
 int packed_launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                   const CUtensorMap& mm, const PackedParams& p, cudaStream_t st) {
   // ring slots as in pasa_attn_fwd: 3 K + 2 V for D = 128 (201 KB), 4 + 4 for D = 64
   constexpr int KST = D == 128 ? 3 : 4, VST = D == 128 ? 2 : 4;
   const unsigned prep = 1u + (SHIFT ? static_cast<unsigned>(p.key_slots) * static_cast<unsigned>(p.Hkv) : 0u);
   static std::atomic<unsigned long long> asked{0};
-  prefer_shared(pasa::packed::packed_prep_kernel<D>, asked);
-  pasa::packed::packed_prep_kernel<D><<<prep, pasa::packed::kPrepThreads, 0, st>>>(p);
+  prefer_shared(pasa::packed::packed_prep_kernel<D, PIECES>, asked);
+  pasa::packed::packed_prep_kernel<D, PIECES><<<prep, pasa::packed::kPrepThreads, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
   constexpr int SETS = D == 64 ? 2 : 1;
-  auto kern = pasa::packed::packed_fwd_kernel<D, F16ACC, SHIFT, KST, VST, SETS>;
+  auto kern = pasa::packed::packed_fwd_kernel<D, F16ACC, SHIFT, KST, VST, SETS, PIECES>;
   const int smem = static_cast<int>(sizeof(pasa::packed::Smem<D, KST, VST, SETS>)) + 1024;
   static std::atomic<unsigned long long> raised{0};
-  const unsigned grid = static_cast<unsigned>(p.tile_slots) * static_cast<unsigned>(p.Hq / p.hg);
-  e = launch_clusters(kern, grid, pasa::packed::threads(SETS), smem, smem, st, true, 1, raised, mq, mk, mv, mo, mm, p);
+  const unsigned groups = static_cast<unsigned>(p.Hq / p.hg);
+  const unsigned most = std::max(static_cast<unsigned>(p.tile_slots), PIECES ? pasa::packed::kMaxPieces / groups : 0u);
+  e = launch_clusters(kern, most * groups, pasa::packed::threads(SETS), smem, smem, st, true, 1, raised, mq, mk, mv, mo, mm, p);
+  if constexpr (PIECES) {
+    static std::atomic<unsigned long long> merge_asked{0};
+    prefer_shared(pasa::packed::packed_merge_kernel<D>, merge_asked);
+    if (e == cudaSuccess)
+      e = launch_kernel(pasa::packed::packed_merge_kernel<D>, dim3(pasa::packed::kMergeCtas), dim3(pasa::packed::kMergeThreads), 0, st, true, p);
+  }
   return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
 
-template <int D>
+template <int D, bool PIECES>
 int packed_dispatch(int mode, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                     const CUtensorMap& mm, const PackedParams& p, cudaStream_t st) {
   switch (mode) {
-    case PASA_MODE_SHIFT_F16ACC: return packed_launch<D, true, true>(mq, mk, mv, mo, mm, p, st);
-    case PASA_MODE_SHIFT_F32ACC: return packed_launch<D, false, true>(mq, mk, mv, mo, mm, p, st);
-    case PASA_MODE_NAIVE_F16ACC: return packed_launch<D, true, false>(mq, mk, mv, mo, mm, p, st);
-    case PASA_MODE_NOSHIFT_F32ACC: return packed_launch<D, false, false>(mq, mk, mv, mo, mm, p, st);
+    case PASA_MODE_SHIFT_F16ACC: return packed_launch<D, true, true, PIECES>(mq, mk, mv, mo, mm, p, st);
+    case PASA_MODE_SHIFT_F32ACC: return packed_launch<D, false, true, PIECES>(mq, mk, mv, mo, mm, p, st);
+    case PASA_MODE_NAIVE_F16ACC: return packed_launch<D, true, false, PIECES>(mq, mk, mv, mo, mm, p, st);
+    case PASA_MODE_NOSHIFT_F32ACC: return packed_launch<D, false, false, PIECES>(mq, mk, mv, mo, mm, p, st);
     default: return PASA_ERR_UNSUPPORTED;
   }
 }
@@ -289,6 +307,9 @@ int pasa_attn_fwd_packed(const void* q, const void* k, const void* v, void* o, c
   p.inv_scale_log2 = 1.0f / p.scale_log2;
   p.count = reinterpret_cast<int*>(ws);
   p.tiles = reinterpret_cast<pasa::packed::Tile*>(ws + pl.tiles);
+  p.splits = reinterpret_cast<pasa::packed::Split*>(ws + pl.splits);
+  p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + pl.part_ml);
   p.k = static_cast<const __half*>(k);
   p.k_row = strides[2];
   p.k_head = strides[3];
@@ -316,7 +337,9 @@ int pasa_attn_fwd_packed(const void* q, const void* k, const void* v, void* o, c
                                       {64, pasa::kChunkBlocks, 1})) != PASA_OK)
     return rc;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return D == 64 ? packed_dispatch<64>(mode, mq, mk, mv, mo, mm, p, st) : packed_dispatch<128>(mode, mq, mk, mv, mo, mm, p, st);
+  const auto run = D == 64 ? (pl.split ? packed_dispatch<64, true> : packed_dispatch<64, false>)
+                           : (pl.split ? packed_dispatch<128, true> : packed_dispatch<128, false>);
+  return run(mode, mq, mk, mv, mo, mm, p, st);
 }
 
 }  // extern "C"

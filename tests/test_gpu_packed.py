@@ -144,6 +144,82 @@ def test_parity(case, mode):
         check(out, lse, q, k, v, cq, ck, causal, mode, 0.2)
 
 
+LONG = [
+    # tiles whose key blocks several CTAs share
+    ([64], [6000], 4, 1, 128, True),
+    ([64], [6001], 8, 2, 64, True),
+    ([1], [20000], 1, 1, 128, True),                          # one tile
+    ([1], [9000], 7, 1, 64, True),
+    ([4000], None, 1, 1, 64, True),                           # the long tiles of a prompt
+    ([3100], None, 2, 1, 128, True),
+    ([300, 0, 5, 20], [5000, 7, 2100, 20], 14, 2, 128, True), # divided and whole tiles
+    ([100, 1], [4099, 2049], 5, 5, 64, False),
+    ([2500], [2200], 1, 1, 128, True),                        # the first 300 see nothing, and few the last pieces
+    ([130, 7], [2048, 2176], 130, 1, 128, True),
+]
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2, 3])
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_shared_keys(case, mode):
+    lens_q, lens_k, Hq, Hkv, D, causal = LONG[case]
+    q, k, v, cq, ck = make(500 + case, lens_q, lens_k or lens_q, Hq, Hkv, D, bias=mode != 2, front=case % 3 * 2)
+    out, lse = run(q, k, v, cq, ck, causal=causal, mode=mode)
+    inside = check(out, lse, q, k, v, cq, ck, causal, mode)
+    assert (out[~torch.from_numpy(inside)] == 7).all() and (lse[:, ~torch.from_numpy(inside)] == 7).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_shared_keys_among_others(D):
+    """Queries of which the first pieces hold nothing that weighs, neighbours of NaN, strided views, in place of q, and no
+    result that changes from call to call."""
+    q, k, v, cq, ck = make(520 + D, [50, 40], [700, 3500], 4, 2, D, bias=False, front=9, tail=9)
+    k[ck[1] + 3000:ck[2]] *= 4                                # the maximum moves up in the last piece
+    want, lse = run(q, k, v, cq, ck, mode=1)
+    check(want, lse, q, k, v, cq, ck, True, 1)
+    foul = [x.copy() for x in (q, k, v)]
+    for x, c in zip(foul, (cq, ck, ck)):
+        x[:c[0]], x[c[2]:] = np.nan, np.inf
+    T = max(len(q), len(k))
+    fused = torch.full((T, 8, D), float("nan"), dtype=torch.float16, device="cuda")
+    qt, kt, vt, a, b = to_dev(*foul, cq, ck)
+    fused[:len(q), :4], fused[:len(k), 4:6], fused[:len(k), 6:] = qt, kt, vt
+    views = fused[:len(q), :4], fused[:len(k), 4:6], fused[:len(k), 6:]
+    ws = torch.full((pasa().packed_workspace_bytes(2, 4, 2, len(q), len(k), D, 1) + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    for i in range(3):
+        out, other = torch.full_like(want, 7), torch.full_like(lse, 7)
+        pasa().attn_fwd_packed(*views, a, b, mode=1, out=out, lse=other, workspace=ws)
+        assert torch.equal(out, want) and torch.equal(other, lse)
+    assert (ws[-256:] == 0xFF).all()
+    pasa().attn_fwd_packed(*views, a, b, mode=1, out=views[0], return_lse=False)
+    inside = slice(int(cq[0]), int(cq[-1]))
+    assert torch.equal(fused[inside, :4], want[inside]) and fused[:9, :4].isnan().all()
+
+
+def test_captured_call_divides_by_the_lengths():
+    """One graph: keys that are shared among CTAs, then lengths that need none of it, and none at all."""
+    q, k, v, _, _ = make(530, [200], [5000], 4, 1, 128, tail=0)
+    qt, kt, vt = to_dev(q, k, v)
+    a, b = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    out, lse = torch.zeros_like(qt), torch.zeros((4, 200), device="cuda")
+    ws = torch.empty(pasa().packed_workspace_bytes(3, 4, 1, 200, 5000, 128, 1), dtype=torch.uint8, device="cuda")
+    call = lambda: pasa().attn_fwd_packed(qt, kt, vt, a, b, out=out, lse=lse, workspace=ws, mode=1)   # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+        call()
+    for lens_q, lens_k in (([0, 70, 1], [9, 4800, 130]), ([200, 0, 0], [200, 0, 0]), ([0] * 3, [0] * 3), ([1, 1, 1], [2000, 900, 2100])):
+        cq, ck = cu(lens_q), cu(lens_k)
+        a.copy_(torch.from_numpy(cq)), b.copy_(torch.from_numpy(ck))
+        out.fill_(7), lse.fill_(7)
+        graph.replay()
+        inside = check(out, lse, q, k, v, cq, ck, True, 1)
+        assert (out[~torch.from_numpy(inside)] == 7).all()
+    pasa().check_device_error()
+
+
 @pytest.mark.parametrize("mode", [0, 3])
 @pytest.mark.parametrize("D", [64, 128])
 def test_a_sequence_does_not_depend_on_its_batch(D, mode):
