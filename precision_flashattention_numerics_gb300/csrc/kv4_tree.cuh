@@ -24,9 +24,16 @@
 // Items. A segment is a list of key blocks: first the nodes, then the cache's blocks from its last, partial one
 // on.
 //
-// Work split. The segments' items are numbered in order, a segment's start counting as kTreeStart items, and CTA c takes the
+// Work split. The segments' items are numbered in order, a segment's start counting as kStart items, and CTA c takes the
 // c-th of equal ranges: uneven lengths keep all SMs equally busy. A segment inside one CTA is finished there, else
 // its CTAs leave (O, max, sum) partials that kv4_tree_merge_kernel joins.
+//
+// The nodes' keys are taken as they are, cached ones lack the shift: the node block's scores lose q . shift in fp32. (Keys
+// rounded to fp16 after the shift is taken off moved the LSE of rows that see few keys by up to 4e-5.)
+//
+// Measured (GPU time per call): 16 nodes x 7 heads x 8 x 32768 keys 82 us, of which 79 here (issue 56%, tensor pipe 40%: the roles
+// wait for one another); 8 nodes on 300 keys 14.4 us; 61 nodes, 6 uneven sequences, D = 64 22.6 us. With 16 rows to a tile on the decode
+// kernel the first would take about 250 us.
 #pragma once
 
 #include <cstdint>
