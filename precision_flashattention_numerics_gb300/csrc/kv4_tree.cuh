@@ -31,7 +31,7 @@
 // The nodes' keys are taken as they are, cached ones lack the shift: the node block's scores lose q . shift in fp32. (Keys
 // rounded to fp16 after the shift is taken off moved the LSE of rows that see few keys by up to 4e-5.)
 //
-// Measured (GPU time per call): 16 nodes x 7 heads x 8 x 32768 keys 82 us, of which 79 here (issue 56%, tensor pipe 40%: the roles
+// Measured (GPU time per call): 16 nodes x 7 heads x 8 x 32768 keys 84.7 us, of which 79 here (issue 56%, tensor pipe 40%: the roles
 // wait for one another); 8 nodes on 300 keys 14.4 us; 61 nodes, 6 uneven sequences, D = 64 22.6 us. With 16 rows to a tile on the decode
 // kernel the first would take about 250 us.
 #pragma once
@@ -124,11 +124,11 @@ struct Range {
     if (p.ctas > 0) load(0, len0, nodes0, upto0);
   }
   __device__ __forceinline__ int per_b() const { return p.Hkv * p.row_tiles; }
-  // The range of this CTA.
-  __device__ __forceinline__ void start() {
+  // The range of a CTA: this one's in the attention kernel.
+  __device__ __forceinline__ void start(int cta) {
     if (p.ctas == 0) {
-      b = blockIdx.x / per_b();
-      in_b = blockIdx.x % per_b();
+      b = cta / per_b();
+      in_b = cta % per_b();
       len = p.length(b);
       nodes = p.count(b);
       n_items = items_of(len, nodes);
@@ -137,9 +137,9 @@ struct Range {
       return;
     }
     const int total = sum(p.B) * per_b(), ctas = min(total, p.ctas);
-    if (static_cast<int>(blockIdx.x) >= ctas) return;
-    int place = first_of(total, ctas, blockIdx.x);
-    todo = first_of(total, ctas, blockIdx.x + 1) - place;
+    if (cta >= ctas) return;
+    int place = first_of(total, ctas, cta);
+    todo = first_of(total, ctas, cta + 1) - place;
     int l = len0, n = nodes0, upto = upto0;
 #pragma unroll 1
     for (int b0 = 0;; b0 += 32) {   // place is less than the sum
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   volatile int* abort_flag = &s.abort_flag;
-  seg.start();
+  seg.start(blockIdx.x);
 
   if (warp >= kFirstExpand) {
     // ------------------------------------------------------------------ codes to fp16
@@ -771,25 +771,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
   if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// Join the partials of the segments that several CTAs shared, and write the rows of sequences without a node. A CTA takes
-// 8 channels of a segment's rows, a thread 4 of one row.
-template <int D>
+// Join the partials of the segments that several CTAs shared. A CTA takes 8 channels of a segment's rows, a thread 4 of
+// one row. With no more segments than CTAs that share them, blockIdx.x is a segment. With more, most of which end where they
+// began, it is a CTA c of the kernel before, and the segment the one in which the range of c ends, if it began there (512
+// segments on 1024 keys: with a CTA for each 81.6 us in all, so 71.8; 2048 of them: 320, 264). The blocks behind those write the rows of sequences without a node.
+template <int D, bool BY_SEGMENT>
 __global__ void __launch_bounds__(256) kv4_tree_merge_kernel(const __grid_constant__ Params p) {
-  const int per_b = p.Hkv * p.row_tiles;
-  const int b = blockIdx.x / per_b, in_b = blockIdx.x % per_b;
-  const int nodes = p.count(b);
+  const int per_b = p.Hkv * p.row_tiles, places = BY_SEGMENT ? p.B * per_b : p.ctas - 1;
+  if (static_cast<int>(blockIdx.x) >= places) {
+    griddep_wait();
+    const long long rows = static_cast<long long>(p.Hkv) * p.rows;   // of a sequence
+    const long long first = static_cast<long long>(blockIdx.y) * 256 + threadIdx.x, step = gridDim.y * 256ll;
+    for (int b = blockIdx.x - places; b < p.B; b += gridDim.x - places) {
+      if (p.count(b) != 0) continue;
+      uint4* to = reinterpret_cast<uint4*>(p.o + b * rows * D);
+      for (long long i = first; i < rows * (D / 8); i += step) to[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (long long i = first; p.lse && i < rows; i += step) p.lse[b * rows + i] = -INFINITY;
+    }
+    return;
+  }
+  int b, in_b, nodes;
+  if constexpr (BY_SEGMENT) {
+    b = blockIdx.x / per_b, in_b = blockIdx.x % per_b;
+    nodes = p.count(b);
+  } else {
+    Range next(p);
+    next.start(blockIdx.x + 1);
+    if (next.todo <= 0 || next.r0 <= 0) {   // no CTA behind this one, or it begins with a segment
+      griddep_wait();
+      return;
+    }
+    b = next.b, in_b = next.in_b, nodes = next.nodes;
+  }
   const int r = threadIdx.x % kRows, ch = (blockIdx.y * 2 + threadIdx.x / kRows) * 4;
   const int row = in_b % p.row_tiles * kRows + r;
   const long long bh = static_cast<long long>(b) * p.Hkv + in_b / p.row_tiles;
   griddep_wait();
-  if (row >= p.rows) return;
-  int2 parts = make_int2(0, 1);
-  if (nodes > 0) {
-    parts = __ldcg(p.parts + blockIdx.x);
-    if (parts.y == 0) return;   // finished where it was computed
-  }
-  // slots: the first part's, and the first of each of the following CTAs
-  const int n = nodes > 0 ? parts.y - (parts.x >> 1) : 0;
+  if (row >= p.rows || nodes == 0) return;
+  const int2 parts = __ldcg(p.parts + static_cast<long long>(b) * per_b + in_b);
+  if (parts.y == 0) return;   // finished where it was computed
+  // slots: the first part's, and the first of each of the following CTAs (kept in range where a call has failed and left no numbers)
+  const int slot0 = min(static_cast<unsigned>(parts.x), 2u * kCtas - 1), cta = slot0 >> 1, n = min(parts.y, kCtas) - cta;
+  if (!BY_SEGMENT && cta != static_cast<int>(blockIdx.x)) return;   // it began before
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float mm = -INFINITY, ll = 0.0f;
   if (row % p.Sq < nodes) {
@@ -800,7 +823,7 @@ __global__ void __launch_bounds__(256) kv4_tree_merge_kernel(const __grid_consta
       float4 v[kAtOnce];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
-        const long long slot = i0 + i == 0 ? parts.x : 2ll * ((parts.x >> 1) + i0 + i);
+        const long long slot = i0 + i == 0 ? slot0 : 2ll * (cta + i0 + i);
         ml[i] = make_float2(-INFINITY, 0.0f);
         v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (i0 + i < n) {

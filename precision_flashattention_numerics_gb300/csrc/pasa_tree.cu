@@ -41,12 +41,17 @@ template <int D>
 int tree_launch(const pasa::tree::Params& p, const TreePlan& pl, cudaStream_t st) {
   static std::atomic<unsigned long long> raised{0};
   const int smem = static_cast<int>(sizeof(pasa::tree::Smem<D>)) + 1024;
-  static std::atomic<unsigned long long> asked{0};
-  if (pl.ctas > 0) prefer_shared(pasa::tree::kv4_tree_merge_kernel<D>, asked);
+  static std::atomic<unsigned long long> asked[2];
+  const bool by_segment = pl.segments <= pl.ctas;
+  auto merge = by_segment ? pasa::tree::kv4_tree_merge_kernel<D, true> : pasa::tree::kv4_tree_merge_kernel<D, false>;
+  if (pl.ctas > 0) prefer_shared(merge, asked[by_segment]);
   const unsigned grid = static_cast<unsigned>(pl.ctas > 0 ? pl.ctas : pl.segments);
   cudaError_t e = launch_clusters(pasa::tree::kv4_tree_kernel<D>, grid, pasa::tree::kThreads, smem, smem, st, false, 1, raised, p);
-  if (e == cudaSuccess && pl.ctas > 0)
-    e = launch_kernel(pasa::tree::kv4_tree_merge_kernel<D>, dim3(static_cast<unsigned>(pl.segments), D / 8), dim3(256), 0, st, true, p);
+  if (e == cudaSuccess && pl.ctas > 0) {
+    const unsigned places = static_cast<unsigned>(by_segment ? pl.segments : pl.ctas - 1);
+    const unsigned fill = p.counts ? static_cast<unsigned>(std::min((p.B + 15) / 16, 64)) : 0;   // for sequences without a node
+    e = launch_kernel(merge, dim3(places + fill, D / 8), dim3(256), 0, st, true, p);
+  }
   return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
 

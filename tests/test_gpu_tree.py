@@ -180,6 +180,28 @@ def test_parity(case, shifted):
         check(c.run(scale=0.3), c.reference(0.3))
 
 
+MANY = [
+    # more segments than CTAs share, of which some end in the CTA where they began: B, Hq, Hkv, n, Sk, D, lengths, counts
+    (90, 4, 2, 3, 900, 128, [(97 * i) % 901 for i in range(90)], [i % 4 for i in range(90)]),
+    (90, 4, 2, 3, 900, 64, None, None),
+    (160, 2, 1, 2, 800, 64, [800 if i % 40 == 7 else i % 3 for i in range(160)], [2 * (i % 40 == 7) for i in range(160)]),
+    (200, 1, 1, 1, 1000, 128, [1000] * 200, [int(i == 131) for i in range(200)]),      # fewer items than CTAs
+    (20, 18, 2, 61, 700, 64, [(311 * i) % 701 for i in range(20)], [61 - 3 * i for i in range(20)]),   # tiles of rows
+]
+
+
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_more_segments_than_ctas(case):
+    B, Hq, H, n, Sk, D, lengths, counts = MANY[case]
+    c = Case(660 + case, B, Hq, H, n, Sk, Sk + 1, D, lengths, counts)
+    size = pasa().tree_kv4_workspace_bytes(B, Hq, H, n, Sk, D)
+    ws = torch.full((size + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = c.run(workspace=ws)
+    check(got, c.reference())
+    again = c.run(workspace=ws)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1]) and (ws[size:] == 0xFF).all()
+
+
 def test_a_chain_equals_the_causal_decode_on_a_cache_that_holds_it():
     """Against the library's own decode on the 4-bit cache, with nodes that the cache holds exactly."""
     c = Case(700, 2, 8, 2, 5, 600, 700, 128, None, None, "chain", False)
