@@ -83,6 +83,7 @@ struct Params {
   const int *cu_q, *cu_k;
   int N, Tq, Tk, Hq, Hkv;
   int hg, tile_tokens;     // heads and tokens of a tile
+  uint32_t tile_mul, tile_shift1, tile_shift2;   // x / tile_tokens is a product and two shifts
   int tile_slots, key_slots;
   int causal, bin_shift;
   float scale_log2, inv_scale_log2;
@@ -101,14 +102,14 @@ struct Params {
 
 __device__ __forceinline__ int offset(const int* cu, int s, int most) { return min(max(__ldg(cu + s), 0), most); }
 
-// The last s < n with cu[s] / per + s <= slot, by a whole warp: it probes 32 places at a time.
-__device__ __forceinline__ int find_sequence(const int* cu, int n, int most, int per, int slot) {
+// The last s < n with start(s) <= slot, of those from lo on, by a whole warp: it probes 32 places at a time.
+template <typename Start>
+__device__ __forceinline__ int find_sequence(int lo, int hi, int slot, Start start) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, hi = n;   // the answer is in [lo, hi)
-  while (hi - lo > 1) {
+  while (hi - lo > 1) {   // the answer is in [lo, hi)
     const int step = (hi - lo + 31) / 32;
     const int s = lo + lane * step;
-    const bool before = s < hi && offset(cu, s, most) / per + s <= slot;
+    const bool before = s < hi && start(s) <= slot;
     const uint32_t v = __ballot_sync(0xFFFFFFFFu, before) | 1u;   // lane 0: lo, by the loop's invariant
     const int last = 31 - __clz(v);
     lo += last * step;
@@ -116,22 +117,30 @@ __device__ __forceinline__ int find_sequence(const int* cu, int n, int most, int
   }
   return lo;
 }
-// The same by one thread.
-__device__ __forceinline__ int find_sequence_alone(const int* cu, int n, int most, int per, int slot) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (offset(cu, mid, most) / per + mid <= slot) lo = mid;
-    else hi = mid;
-  }
+// The number of a sequence's first tile.
+__device__ __forceinline__ int first_tile(const Params& p, int s) {
+  const uint32_t x = offset(p.cu_q, s, p.Tq), t = __umulhi(x, p.tile_mul);
+  return static_cast<int>((t + ((x - t) >> p.tile_shift1)) >> p.tile_shift2) + s;   // x / tile_tokens + s
+}
+// The sequences of 32 slots side by side, slot0 + lane: the one of the first by search from lo on, those of the others among
+// its 31 next ones, as each has a slot or more.
+__device__ __forceinline__ int find_sequences(const Params& p, int lo, int slot0, int& mine) {
+  const int lane = threadIdx.x & 31;
+  lo = find_sequence(lo, min(p.N, lo + kPrepThreads + 1), slot0, [&](int s) { return first_tile(p, s); });
+  const int start = lo + lane < p.N ? first_tile(p, lo + lane) : INT_MAX;
+  int at = 0;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+    if (__shfl_sync(0xFFFFFFFFu, start, at + d) <= slot0 + lane) at += d;
+  mine = lo + at;
   return lo;
 }
 
 // The tile of a slot; false where there is none.
-__device__ __forceinline__ bool make_tile(const Params& p, int slot, Tile& t) {
-  const int s = find_sequence_alone(p.cu_q, p.N, p.Tq, p.tile_tokens, slot);
+__device__ __forceinline__ bool make_tile(const Params& p, int slot, int s, Tile& t) {
+  if (slot >= p.tile_slots) return false;
   const int q0 = offset(p.cu_q, s, p.Tq), n = offset(p.cu_q, s + 1, p.Tq) - q0;
-  const long long first = static_cast<long long>(slot - (q0 / p.tile_tokens + s)) * p.tile_tokens;
+  const long long first = static_cast<long long>(slot - first_tile(p, s)) * p.tile_tokens;
   if (first < 0 || first >= n) return false;
   const int k0 = offset(p.cu_k, s, p.Tk), m = max(0, offset(p.cu_k, s + 1, p.Tk) - k0);
   const int i0 = static_cast<int>(first);
@@ -191,16 +200,22 @@ __device__ __forceinline__ void plan_tiles(const Params& p) {
     atomicAdd(&bins[bin_of(t.blocks)], 1);
     if (PIECES) ++tiles, most = max(most, t.blocks), blocks += t.blocks;
   };
+  const int tid0 = tid - lane;
+  int lo = find_sequence(0, p.N, min(tid0, p.tile_slots - 1), [&](int s) { return first_tile(p, s); });
+  const int lo0 = lo;
+  int seq;
 #pragma unroll
   for (int i = 0; i < kKeep; ++i) {
-    const int slot = i * kPrepThreads + tid;
-    there[i] = slot < p.tile_slots && make_tile(p, slot, kept[i]);
+    lo = find_sequences(p, lo, i * kPrepThreads + tid0, seq);
+    there[i] = make_tile(p, i * kPrepThreads + tid, seq, kept[i]);
     if (there[i]) count(kept[i]);
   }
+  const int lo1 = lo;
 #pragma unroll 1
-  for (int slot = kKeep * kPrepThreads + tid; slot < p.tile_slots; slot += kPrepThreads) {
+  for (int slot0 = kKeep * kPrepThreads + tid0; slot0 < p.tile_slots; slot0 += kPrepThreads) {
     Tile t;
-    if (make_tile(p, slot, t)) count(t);
+    lo = find_sequences(p, lo, slot0, seq);
+    if (make_tile(p, slot0 + lane, seq, t)) count(t);
   }
   __syncthreads();
   int cap = INT_MAX;
@@ -218,10 +233,12 @@ __device__ __forceinline__ void plan_tiles(const Params& p) {
     if (cap != INT_MAX) {   // count again
       for (int i = tid; i < kBins; i += kPrepThreads) bins[i] = 0;
       __syncthreads();
+      lo = lo0;
 #pragma unroll 1
-      for (int slot = tid; slot < p.tile_slots; slot += kPrepThreads) {
+      for (int slot0 = tid0; slot0 < p.tile_slots; slot0 += kPrepThreads) {
         Tile t;
-        if (!make_tile(p, slot, t)) continue;
+        lo = find_sequences(p, lo, slot0, seq);
+        if (!make_tile(p, slot0 + lane, seq, t)) continue;
         const int n = max(1, (t.blocks + cap - 1) / cap), base = t.blocks / n, more = t.blocks % n;
         atomicAdd(&bins[bin_of(base)], n - more);
         if (more > 0) atomicAdd(&bins[bin_of(base + 1)], more);
@@ -259,19 +276,23 @@ __device__ __forceinline__ void plan_tiles(const Params& p) {
 #pragma unroll
     for (int i = 0; i < kKeep; ++i)
       if (there[i]) p.tiles[atomicAdd(&bins[bin_of(kept[i].blocks)], 1)] = kept[i];
+    lo = lo1;
 #pragma unroll 1
-    for (int slot = kKeep * kPrepThreads + tid; slot < p.tile_slots; slot += kPrepThreads) {
+    for (int slot0 = kKeep * kPrepThreads + tid0; slot0 < p.tile_slots; slot0 += kPrepThreads) {
       Tile t;
-      if (make_tile(p, slot, t)) p.tiles[atomicAdd(&bins[bin_of(t.blocks)], 1)] = t;
+      lo = find_sequences(p, lo, slot0, seq);
+      if (make_tile(p, slot0 + lane, seq, t)) p.tiles[atomicAdd(&bins[bin_of(t.blocks)], 1)] = t;
     }
     if (PIECES && tid == 0) p.count[1] = 0;
     return;
   }
   if constexpr (PIECES) {
+    lo = lo0;
 #pragma unroll 1
-    for (int slot = tid; slot < p.tile_slots; slot += kPrepThreads) {
+    for (int slot0 = tid0; slot0 < p.tile_slots; slot0 += kPrepThreads) {
       Tile t;
-      if (!make_tile(p, slot, t)) continue;
+      lo = find_sequences(p, lo, slot0, seq);
+      if (!make_tile(p, slot0 + lane, seq, t)) continue;
       const int n = max(1, (t.blocks + cap - 1) / cap), base = t.blocks / n, more = t.blocks % n;
       t.pieces = n;
       if (n > 1) {
@@ -304,7 +325,7 @@ __global__ void __launch_bounds__(kPrepThreads) packed_prep_kernel(const __grid_
     return;
   }
   const int slot = (blockIdx.x - 1) / p.Hkv, head = (blockIdx.x - 1) % p.Hkv;
-  const int s = find_sequence(p.cu_k, p.N, p.Tk, kKeys, slot);
+  const int s = find_sequence(0, p.N, slot, [&](int i) { return offset(p.cu_k, i, p.Tk) / kKeys + i; });
   const int k0 = offset(p.cu_k, s, p.Tk), m = offset(p.cu_k, s + 1, p.Tk) - k0;
   const long long first = static_cast<long long>(slot - (k0 / kKeys + s)) * kKeys;
   if (first < 0 || first >= m) return;

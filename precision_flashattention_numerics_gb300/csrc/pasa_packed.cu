@@ -299,6 +299,11 @@ int pasa_attn_fwd_packed(const void* q, const void* k, const void* v, void* o, c
   p.Hkv = Hkv;
   p.hg = pl.hg;
   p.tile_tokens = pl.tile_tokens;
+  int bits = 0;   // of tile_tokens - 1
+  while ((1 << bits) < pl.tile_tokens) ++bits;
+  p.tile_mul = static_cast<uint32_t>((((1ull << bits) - pl.tile_tokens) << 32) / pl.tile_tokens + 1);
+  p.tile_shift1 = bits > 0 ? 1 : 0;
+  p.tile_shift2 = bits > 0 ? bits - 1 : 0;
   p.tile_slots = static_cast<int>(pl.tile_slots);
   p.key_slots = static_cast<int>(pl.key_slots);
   p.causal = causal ? 1 : 0;
