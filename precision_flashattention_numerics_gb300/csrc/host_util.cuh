@@ -201,12 +201,14 @@ struct Kv4Spans {
 struct Strided {
   uintptr_t at;
   long long stride[3], n[3];   // of the dimensions, largest stride first
+  long long given[6];          // strides and sizes of b, h and s
   long long row;               // bytes of a row
 
   Strided(const void* p, const long long* strides, long long B, long long H, long long S, long long D, long long size)
       : at(reinterpret_cast<uintptr_t>(p)), stride{strides[0] * size, strides[1] * size, strides[2] * size}, n{B, H, S}, row(D * size) {
     for (int i = 0; i < 3; ++i)
       if (n[i] == 1) stride[i] = 0;   // a dimension of one has no stride
+    for (int i = 0; i < 3; ++i) given[i] = stride[i], given[3 + i] = n[i];
     for (int i = 0; i < 2; ++i)
       for (int j = 0; j < 2; ++j)
         if (stride[j] < stride[j + 1]) std::swap(stride[j], stride[j + 1]), std::swap(n[j], n[j + 1]);
@@ -223,9 +225,9 @@ struct Strided {
       if (n[i] > 1 && stride[i] < extent(i + 1)) return true;
     return false;
   }
-  bool same(const Strided& x) const {
-    return at == x.at && row == x.row && std::memcmp(stride, x.stride, sizeof stride) == 0 && std::memcmp(n, x.n, sizeof n) == 0;
-  }
+  // Whether every element of the one is the other's of the same place: the sorted strides do not tell, as a transposed view
+  // with two equal sizes has the same ones.
+  bool same(const Strided& x) const { return at == x.at && row == x.row && std::memcmp(given, x.given, sizeof given) == 0; }
   // Whether the two share memory. Two views that lie side by side in one buffer's rows (q and k of a
   // fused projection) do not; other views of one range count as sharing it.
   bool meets(const Strided& x) const {

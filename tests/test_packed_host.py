@@ -76,3 +76,12 @@ def test_refuses_shared_memory(lib):
     for at in (Q, K, V, O, CQ, CK):
         assert call(lib, lse=at) == -2 and call(lib, ws=at) == -2
     assert call(lib, lse=WS + 1024) == -2 and call(lib, o=CQ) == -2
+
+
+def test_in_place_of_q_is_the_same_order_of_dimensions(lib):
+    """o as a transposed view of q, with as many heads as tokens, is not q itself."""
+    n, D = 8, 128
+    rows, turned, keys = [n * D, D], [D, n * D], [2 * D, D] * 2
+    for a, b in ((rows, turned), (turned, rows)):
+        assert call(lib, o=Q, Hq=n, Tq=n, strides=a + keys + a) in (0, -3, -5)
+        assert call(lib, o=Q, Hq=n, Tq=n, strides=a + keys + b) == -2

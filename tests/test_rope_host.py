@@ -136,3 +136,26 @@ def test_binding_refusals(pasa):
             pasa.rope(x, x, torch.zeros(32, dtype=torch.float64))
     with pytest.raises(pasa.PasaError):
         pasa.rope_frequencies(63, device="cpu")
+
+
+def test_rope_in_place_is_the_same_order_of_dimensions(pasa):
+    """A transposed view of q with as many heads as tokens (or sequences) has q's memory, sizes and set of strides, but
+    other elements in its places: it shares q's memory and is no rotation in place."""
+    lib = pasa.library()
+    n, D = 8, 64
+
+    def call(ins, outs, B=1, H=n, S=n, R=D, f=1 << 30, pos=1 << 31):
+        st = (ctypes.c_longlong * 6)(*ins, *outs)
+        return lib.pasa_rope(P(FAKE), P(FAKE), ctypes.cast(st, P), H, None, None, None, 0, P(f), P(pos), None, 0, B, S, D, R, 0, 0, 1.0, 0,
+                             0, None)
+
+    rows, turned = (0, D, n * D), (0, n * D, D)              # [T, H, D], and its transpose
+    assert call(rows, rows) != -2 and call(turned, turned) != -2
+    for R in (D, 32):
+        assert call(rows, turned, R=R) == -2 and call(turned, rows, R=R) == -2
+    whole = (n * n * D, n * D, D)                            # [B, H, S, D]
+    assert call(whole, whole, B=n) != -2
+    for other in ((n * D, n * n * D, D), (D, n * D, n * n * D), (n * n * D, D, n * D)):
+        assert call(whole, other, B=n) == -2, other
+    assert call((7, D, n * D), (9, D, n * D)) != -2          # the stride of a dimension of one says nothing
+    assert call((7, D, 5), (9, D, 3), S=1) != -2
