@@ -591,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
           const float less = j == 0 ? offset : 0.0f;   // the nodes' keys are not shifted
           float m_cur = m_w, l = 0.0f;
           auto scale_p = [&](int columns, float f) {   // 16 columns of P at a time
+            tmem_st_wait();   // they may just have been stored, and a load does not wait for stores by itself
             const uint32_t f2 = pack_half2(f, f);
 #pragma unroll 1
             for (int c = 0; c < columns; c += 16) {

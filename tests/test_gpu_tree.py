@@ -384,3 +384,23 @@ def test_binding_refusals():
     wide = [torch.zeros((2, h, 129, 64), dtype=torch.float16, device="cuda") for h in (4, 2, 2)]
     with pytest.raises(p.PasaError):
         p.attn_fwd_tree_kv4(*wide, *c.cache)
+
+
+@pytest.mark.parametrize("Sk", [512, 1280])
+@pytest.mark.parametrize("D", [64, 128])
+def test_maximum_moves_at_every_32_keys(D, Sk):
+    """A block is taken 32 keys at a time, and what is stored of its first keys is scaled when a later key raises the maximum by
+    more than 8 (log2 units). Here each 32 keys do so, in every block and in the order in which the kernel takes them."""
+    c = Case(770 + D, 1, 4, 1, 8, Sk, Sk, D, None, None, "tree", False)
+    i = np.arange(Sk)
+    step = (Sk // 128 - 1 - i // 128) * 4 + i % 128 // 32
+    k = np.broadcast_to((step * (1.8 if D == 64 else 1.3))[:, None], (1, 1, Sk, D)).astype(np.float16)
+    v = rows(np.random.default_rng(D), 1, 1, Sk, D, "plain")
+    pasa().kv4_append(*to_dev(k, v), *c.cache)
+    c.held = kv4.values(*kv4.quantise(k)), kv4.values(*kv4.quantise(v))
+    c.q = np.abs(c.q)
+    c.dev[0] = to_dev(c.q)[0]
+    x = c.scale * np.einsum("bhid,bgjd->hij", c.q.astype(np.float64), c.held[0])
+    top = np.stack([x[..., step == e].max(-1) for e in range(Sk // 32)])
+    assert (np.diff(top, axis=0) > 8.1 * np.log(2)).all()
+    check(c.run(), c.reference())
