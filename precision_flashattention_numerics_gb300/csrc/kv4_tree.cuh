@@ -14,7 +14,12 @@
 //               with the codes of its next block on their way to its registers
 // Codes are expanded to s c, which fp16 holds exactly. A word of 8 codes gives the channel order 0, 4, 1, 5, 2, 6, 3, 7 without
 // a shuffle; Q is brought to that order when it goes to shared memory, and the epilogue puts O's columns back. P is an
-// A operand in TMEM. Scores, maxima, sums and O are fp32, P is rounded to fp16 (2^-11).
+// A operand in TMEM. Scores, maxima, sums and O are fp32, P is rounded to fp16 once (2^-11 of a probability; 2^-24 of
+// the row's sum where it is subnormal): what scales it afterwards, when the maximum moves, are powers of two, as maxima are
+// whole numbers. (Maxima as they come, with factors in fp16, rounded the probabilities of a row's first blocks up to three times, and
+// O apart from the sum. Output errors, relative RMS, of which its own rounding is 2.0e-4: 300 keys 3.31e-4, so 2.90e-4. Where one key
+// has nearly all of a row's weight its probability was 1, which fp16 holds, and is no longer: 61 nodes, uneven, D = 64, 2.12e-4, so
+// 2.86e-4.)
 // P overwrites the scores it was made of, 32 columns of S giving 16 of P, so that a row needs 32 scores in registers at a time.
 // TMEM holds three S and O: with two S, both sets would wait for PV and QK of their next block before they go on.
 // Registers: a launch of 896 threads has 72 each, moved between the roles by setmaxnreg: 2 x 104 + 40 + 4 x 64 <= 7 x 72.
@@ -286,6 +291,9 @@ __device__ __forceinline__ void put_chunk(uint32_t at, uint4 codes, unsigned sho
     }
   }
 }
+
+// 2^d of a whole number d <= 0 or -inf, exactly; 0 below the least normal number.
+__device__ __forceinline__ float power_of_two(float d) { return d < -126.0f ? 0.0f : __int_as_float((static_cast<int>(d) + 127) << 23); }
 
 // The first n of 32 bits.
 __device__ __forceinline__ uint32_t first_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
@@ -584,25 +592,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
         tc_fence_after();
         if (any_live) {
           // 32 keys at a time: exponentials against the maximum at hand, which moves when a score passes it by more than 8
-          // (log2 units); what was taken against the one before is then scaled. Rows without a node have zeros for Q, and
+          // (log2 units); what was taken against the one before is then scaled. Maxima are whole numbers (rounded down, so that a
+          // row's largest probability is 1 at least, and its sum) and factors so powers of two: P, the sums and O are scaled
+          // without a rounding, but for probabilities that become subnormal in fp16. Rows without a node have zeros for Q, and
           // nothing of theirs is kept: but for the nodes, all rows have the same keys.
           const int keys = j == 0 ? 0 : seg.len - (n_blocks - j) * kKeys;
           const bool later = j > seg.j0;
           const float less = j == 0 ? offset : 0.0f;   // the nodes' keys are not shifted
           float m_cur = m_w, l = 0.0f;
           auto scale_p = [&](int columns, float f) {   // 16 columns of P at a time
-            tmem_st_wait();   // they may just have been stored, and a load does not wait for stores by itself
-            const uint32_t f2 = pack_half2(f, f);
+            f = fmaxf(f, 0x1p-48f);   // which leaves nothing of a probability in fp16
 #pragma unroll 1
-            for (int c = 0; c < columns; c += 16) {
-              uint32_t w[16];
-              tmem_ld_x16(tS + c, w);
-              tmem_ld_wait();
-              reg_fence<16>(w);
+            do {   // once, but where f is below fp16's least number, 2^-24
+              tmem_st_wait();   // they may just have been stored, and a load does not wait for stores by itself
+              const float f16 = fmaxf(f, 0x1p-24f);
+              const uint32_t f2 = pack_half2(f16, f16);
+#pragma unroll 1
+              for (int c = 0; c < columns; c += 16) {
+                uint32_t w[16];
+                tmem_ld_x16(tS + c, w);
+                tmem_ld_wait();
+                reg_fence<16>(w);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = hmul2(w[e], f2);
-              tmem_st_x16(tS + c, w);
-            }
+                for (int e = 0; e < 16; ++e) w[e] = hmul2(w[e], f2);
+                tmem_st_x16(tS + c, w);
+              }
+              f = fminf(f * 0x1p24f, 1.0f);
+            } while (__any_sync(0xffffffffu, f < 1.0f));
             tmem_st_wait();
           };
 #pragma unroll 1
@@ -622,11 +638,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
 #pragma unroll
             for (int e = 0; e < 10; ++e) top[e] = fmax3(sv[3 * e], sv[3 * e + 1], sv[3 * e + 2]);
             top[10] = fmaxf(sv[30], sv[31]);
-            const float m_new = fmaxf(m_cur, (tree_max3<11>(top) - less) * sl2);
-            const bool need = m_new > m_cur + kRescaleLog2;
+            const float most = (tree_max3<11>(top) - less) * sl2;
+            const bool need = most > m_cur + kRescaleLog2;
             if (__any_sync(0xffffffffu, need)) {
-              const float f = need ? ex2_approx(m_cur - m_new) : 1.0f;
-              if (need) m_cur = m_new;
+              const float m_new = need ? floorf(most) : m_cur;
+              const float f = need ? power_of_two(m_cur - m_new) : 1.0f;
+              m_cur = m_new;
               l *= f;
               if (c > 0) scale_p(c * 16, f);
             }
@@ -656,15 +673,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
           __syncwarp();
           mbar_arrive_if(&s.m_full[quad][set], lane == 0);
           if (__any_sync(0xffffffffu, m_end > m_cur)) {
-            const float f = m_end > m_cur ? ex2_approx(m_cur - m_end) : 1.0f;
+            const float f = m_end > m_cur ? power_of_two(m_cur - m_end) : 1.0f;
             l *= f;
             scale_p(kKeys / 2, f);
           }
-          if (m_w != m_end) l_w *= ex2_approx(m_w - m_end);   // 0 while this set has no block yet
+          if (m_w != m_end) l_w *= power_of_two(m_w - m_end);   // 0 while this set has no block yet
           l_w += l;
           m_w = m_end;
           if (__any_sync(0xffffffffu, later && m_end > m_prev)) {
-            const float alpha = m_end > m_prev ? ex2_approx(m_prev - m_end) : 1.0f;
+            const float alpha = m_end > m_prev ? power_of_two(m_prev - m_end) : 1.0f;
             if (!mbar_wait(&s.p_free[(it - 1) % kScores], ((it - 1) / kScores) & 1, abort_flag, 0x2502)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1

@@ -404,3 +404,40 @@ def test_maximum_moves_at_every_32_keys(D, Sk):
     top = np.stack([x[..., step == e].max(-1) for e in range(Sk // 32)])
     assert (np.diff(top, axis=0) > 8.1 * np.log(2)).all()
     check(c.run(), c.reference())
+
+
+@pytest.mark.parametrize("below", [0, 1])
+@pytest.mark.parametrize("D", [64, 128])
+def test_probabilities_are_rounded_once(D, below):
+    """One score holds the maximum and all others of a block are equal, so that whatever scales the block's probabilities scales
+    the whole output. below = 0: the block's maximum is less than the node's, so that its probabilities are scaled to that. below = 1: a
+    key behind the first 32 raises the maximum by more than 8 (log2 units).
+
+    The probabilities' errors, of reference()'s bounds: once to fp16 (2^-11 or, where they are subnormal, 2^-25), and 2^-25 for each
+    scaling that leaves them subnormal, which later ones at least halve: less than 2^-24 in all, against a sum of at
+    least 1. Scaling itself is by powers of two."""
+    H, g = 14, 128
+    c = Case(780 + D, 1, H * g, H, 1, 128, 128, D, None, None, "tree", False)
+    rng = np.random.default_rng(780 + below)
+    k = np.zeros((1, H, 128, D))
+    k[..., 1] = 7                                                  # every row's scale is 1; channel 1 of q is 0
+    code = np.arange(H) - 7.0
+    k[0, :, :, 0] = code[:, None]
+    k[0, :, 0 if below == 0 else 100, 0] = 7
+    node = rng.uniform(7.5, 11, H) if below == 0 else code - 40
+    weight = rng.uniform(0.05, 0.6, (H, g)) if below == 0 else 8.1 * np.log(2) / (7 - code)[:, None] * rng.uniform(1, 1.5, (H, g))
+    v = np.repeat(rng.uniform(0.5, 1, (1, 1, 1, D // 32)), 32, -1) * np.ones((1, H, 128, D))
+    if below == 1:
+        v[:, :, 100] = 0
+    c.q = np.zeros((1, H * g, 1, D), np.float16)
+    c.q[0, :, 0, 0] = weight.reshape(-1)
+    c.kn, c.vn = np.zeros((1, H, 1, D), np.float16), np.zeros((1, H, 1, D), np.float16)
+    c.kn[0, :, 0, 0] = node
+    k, v = k.astype(np.float16), v.astype(np.float16)
+    pasa().kv4_append(*to_dev(k, v), *c.cache)
+    c.held, c.nodes = (kv4.values(*kv4.quantise(k)), kv4.values(*kv4.quantise(v))), (c.kn.astype(np.float64), c.vn.astype(np.float64))
+    assert np.array_equal(c.held[0], k)
+    c.dev[:3] = to_dev(c.q, c.kn, c.vn)
+    o, lse, bo, bl = c.reference(1.0)
+    bo = bo + (np.abs(c.held[1]).sum(2)[:, :, None] * 2.0 ** -25).repeat(g, 1)
+    check(c.run(scale=1.0), (o, lse, bo, bl))
