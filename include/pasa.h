@@ -675,8 +675,9 @@ int pasa_attn_fwd_packed(const void* q, const void* k, const void* v, void* o, c
 
 /*
  * Synchronise `stream` and read the device error word. Returns PASA_OK, PASA_ERR_TIMEOUT
- * (a pipeline wait gave up; `info`, if not NULL, receives the CTA index << 32 | wait site)
- * or PASA_ERR_CUDA. Reading the word clears it.
+ * (a pipeline wait gave up; `info`, if not NULL, receives the CTA index << 32 | wait site of
+ * the first one) or PASA_ERR_CUDA. Reading the word clears it: one call reports all timeouts up to it,
+ * whichever kernels they happened in.
  */
 int pasa_check_device_error(void* stream, unsigned long long* info);
 
@@ -691,15 +692,16 @@ int pasa_device_supported(int device);
 
 /*
  * Exercises the failure-detection path without a fault. (The paper has no counterpart: this
- * is a library test hook.) It launches one CTA whose thread 0 waits, through the same
- * bounded mbarrier wait every kernel of the library uses, on a barrier that nothing arrives
+ * is a library test hook.) It launches one CTA for each group of kernels that keeps its errors
+ * apart (three, at the same time), whose thread 0 waits, through the same bounded mbarrier
+ * wait every kernel of the library uses, on a barrier that nothing arrives
  * on. After the library's wait limit (2 s of %globaltimer) the wait gives up and records a
  * timeout in the device error word, with site tag 0x5E1F7E57 as the low 32 bits of the
  * info word, and the kernel returns. It holds no TMA copy and no tensor memory, so the GPU
  * context stays usable: pasa_check_device_error(stream, &info) then returns
  * PASA_ERR_TIMEOUT with that tag and clears the word. If the word already holds an unread
  * error, the wait still runs to its limit and the word keeps the first error's info.
- *   stream  where the CTA runs. Returns PASA_OK once launched; errors as for every entry
+ *   stream  where the CTAs run. Returns PASA_OK once launched; errors as for every entry
  *           point (no supported device: PASA_ERR_UNSUPPORTED; a failed launch:
  *           PASA_ERR_CUDA).
  */

@@ -21,11 +21,12 @@ namespace pasa {
 
 extern thread_local int t_last_cuda_error;   // pasa_last_cuda_error
 
-// A translation unit's device error word (ptx.cuh): its timeout, if it holds one, goes to `info` and is
-// cleared. PASA_OK, PASA_ERR_TIMEOUT or PASA_ERR_CUDA. One function for each unit that has kernels
-// with bounded waits besides pasa_lib.cu; pasa_check_device_error asks them all.
-int packed_take_device_error(unsigned long long* info);
-int tree_take_device_error(unsigned long long* info);
+// The units with bounded waits besides pasa_lib.cu: take_device_error and launch_wait_selftest (below) of each one's
+// own device error record, for pasa_check_device_error and pasa_selftest_wait_timeout.
+int packed_take_device_error(DeviceError* found);
+int packed_wait_selftest(cudaStream_t st);
+int tree_take_device_error(DeviceError* found);
+int tree_wait_selftest(cudaStream_t st);
 
 }  // namespace pasa
 
@@ -290,21 +291,35 @@ void prefer_shared(void (*kern)(Params...), std::atomic<unsigned long long>& ask
     asked.fetch_or(bit, std::memory_order_relaxed);
 }
 
-// This unit's error word, read and cleared.
-int take_device_error(unsigned long long* info) {
-  int word = 0;
-  unsigned long long inf = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&word, pasa::g_device_error, sizeof(int));
+// This unit's error record, read and cleared: PASA_OK, PASA_ERR_TIMEOUT or PASA_ERR_CUDA.
+int take_device_error(pasa::DeviceError* found) {
+  cudaError_t e = cudaMemcpyFromSymbol(found, pasa::g_device_error, sizeof *found);
   if (e != cudaSuccess) return cuda_fail(e);
-  e = cudaMemcpyFromSymbol(&inf, pasa::g_device_error_info, sizeof(inf));
-  if (e != cudaSuccess) return cuda_fail(e);
-  if (word == pasa::kDeviceOk) return PASA_OK;
-  const int zero = 0;
-  const unsigned long long zero64 = 0;
-  cudaMemcpyToSymbol(pasa::g_device_error, &zero, sizeof(int));
-  cudaMemcpyToSymbol(pasa::g_device_error_info, &zero64, sizeof(zero64));
-  if (info) *info = inf;
-  return PASA_ERR_TIMEOUT;
+  if (found->word == pasa::kDeviceOk) return PASA_OK;
+  const pasa::DeviceError none = {};
+  e = cudaMemcpyToSymbol(pasa::g_device_error, &none, sizeof none);
+  return e == cudaSuccess ? PASA_ERR_TIMEOUT : cuda_fail(e);
+}
+
+// The failure-detection path without a fault: thread 0 waits, through the bounded mbarrier
+// wait every kernel of this library uses, on a barrier that nothing arrives on. The wait
+// gives up after kWaitTimeoutNs, records the timeout in this unit's record and returns;
+// the CTA holds no TMA copy and no tensor memory, so it simply ends. Units' launches behind one another overlap.
+__global__ void wait_selftest_kernel() {
+  __shared__ uint64_t bar;
+  __shared__ int abort_flag;
+  pasa::griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    pasa::mbar_init(&bar, 1);
+    pasa::fence_mbar_init();
+    (void)pasa::mbar_wait(&bar, 0, &abort_flag, 0x5E1F7E57u);   // the self-test's site tag
+  }
+  pasa::griddep_wait();
+}
+int launch_wait_selftest(cudaStream_t st, bool pdl) {
+  const cudaError_t e = launch_kernel(wait_selftest_kernel, dim3(1), dim3(32), 0, st, pdl);
+  return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
 
 }  // namespace

@@ -29,24 +29,6 @@ namespace pasa {
 
 thread_local int t_last_cuda_error = 0;
 
-// Site tag the self-test below records in the device error word.
-constexpr uint32_t kSelftestSite = 0x5E1F7E57u;
-
-// The failure-detection path without a fault: thread 0 waits, through the bounded mbarrier
-// wait every kernel of this library uses, on a barrier that nothing arrives on. The wait
-// gives up after kWaitTimeoutNs, records the timeout in the device error word and returns;
-// the CTA holds no TMA copy and no tensor memory, so it simply ends.
-__global__ void wait_selftest_kernel() {
-  __shared__ uint64_t bar;
-  __shared__ int abort_flag;
-  if (threadIdx.x == 0) {
-    abort_flag = 0;
-    mbar_init(&bar, 1);
-    fence_mbar_init();
-    (void)mbar_wait(&bar, 0, &abort_flag, kSelftestSite);
-  }
-}
-
 // Element i: the FMA-pipe exponential the softmax uses for part of its scores (poly) and the
 // MUFU one it uses for the rest (mufu), both of x[i]; pairs go through exp2_fma2 together.
 __global__ void exp2_selftest_kernel(const float* __restrict__ x, float* __restrict__ poly, float* __restrict__ mufu,
@@ -874,9 +856,11 @@ int pasa_attn_fwd_fused(const void* q, const void* k, const void* v, void* o, fl
 int pasa_selftest_wait_timeout(void* stream) {
   int rc = check_device();
   if (rc != PASA_OK) return rc;
-  pasa::wait_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>();
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? PASA_OK : cuda_fail(e);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = launch_wait_selftest(st, false);
+  if (rc == PASA_OK) rc = pasa::packed_wait_selftest(st);
+  if (rc == PASA_OK) rc = pasa::tree_wait_selftest(st);
+  return rc;
 }
 
 int pasa_selftest_exp2(const float* x, float* poly, float* mufu, int n, void* stream) {
@@ -893,11 +877,19 @@ int pasa_selftest_exp2(const float* x, float* poly, float* mufu, int n, void* st
 int pasa_check_device_error(void* stream, unsigned long long* info) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
-  // every translation unit has a word of its own; the first error found is reported, the others at the next calls
-  int rc = take_device_error(info);
-  if (rc == PASA_OK) rc = pasa::packed_take_device_error(info);
-  if (rc == PASA_OK) rc = pasa::tree_take_device_error(info);
-  return rc;
+  // every translation unit has a record of its own: all are read and cleared, and the earliest timeout is reported
+  int result = PASA_OK;
+  unsigned long long first = ULLONG_MAX;
+  for (int (*take)(pasa::DeviceError*) : {take_device_error, pasa::packed_take_device_error, pasa::tree_take_device_error}) {
+    pasa::DeviceError found;
+    const int rc = take(&found);
+    if (rc == PASA_ERR_CUDA) return rc;
+    if (rc == PASA_OK || found.at >= first) continue;
+    result = rc;
+    first = found.at;
+    if (info) *info = found.info;
+  }
+  return result;
 }
 
 }  // extern "C"

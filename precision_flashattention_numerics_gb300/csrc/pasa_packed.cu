@@ -136,7 +136,8 @@ Strided packed_view(const void* p, const long long* strides, int T, int H, int D
 }  // namespace
 
 namespace pasa {
-int packed_take_device_error(unsigned long long* info) { return take_device_error(info); }
+int packed_take_device_error(DeviceError* found) { return take_device_error(found); }
+int packed_wait_selftest(cudaStream_t st) { return launch_wait_selftest(st, true); }
 }  // namespace pasa
 
 extern "C" {

@@ -58,7 +58,8 @@ int tree_launch(const pasa::tree::Params& p, const TreePlan& pl, cudaStream_t st
 }  // namespace
 
 namespace pasa {
-int tree_take_device_error(unsigned long long* info) { return take_device_error(info); }
+int tree_take_device_error(DeviceError* found) { return take_device_error(found); }
+int tree_wait_selftest(cudaStream_t st) { return launch_wait_selftest(st, true); }
 }  // namespace pasa
 
 extern "C" {

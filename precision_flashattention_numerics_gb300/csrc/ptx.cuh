@@ -23,11 +23,14 @@ enum : int {
   kDeviceErrTimeout = 1,
 };
 
-// Defined here, static: each translation unit that includes this header has a word of its own, in
-// which g_device_error and g_device_error_info latch its first timeout until the host reads them
-// (pasa_check_device_error asks every unit); no kernel reads them.
-static __device__ int g_device_error = 0;
-static __device__ unsigned long long g_device_error_info = 0;
+// Defined here, static: each translation unit that includes this header has a record of its own, in
+// which its first timeout is latched until the host reads it (pasa_check_device_error asks every unit
+// and reports the earliest); no kernel reads it.
+struct DeviceError {
+  int word, unused;
+  unsigned long long info, at;   // CTA and wait site; when, by the global timer
+};
+static __device__ DeviceError g_device_error = {};
 
 constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;  // 2 s per wait
 
@@ -87,8 +90,9 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 // abort flag.
 __device__ __forceinline__ void record_timeout(volatile int* abort_flag, uint32_t site) {
   *abort_flag = 1;
-  if (atomicCAS(&g_device_error, kDeviceOk, kDeviceErrTimeout) == kDeviceOk) {
-    g_device_error_info = (static_cast<unsigned long long>(blockIdx.x) << 32) | site;
+  if (atomicCAS(&g_device_error.word, kDeviceOk, kDeviceErrTimeout) == kDeviceOk) {
+    g_device_error.info = (static_cast<unsigned long long>(blockIdx.x) << 32) | site;
+    g_device_error.at = globaltimer_ns();
   }
 }
 

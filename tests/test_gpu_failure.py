@@ -88,3 +88,19 @@ def test_unread_timeout_does_not_abort_later_launches():
     assert rmse <= 5e-3 and rmax <= 5e-2, (rmse, rmax)
     assert np.abs(lse.double().cpu().numpy() - lse_ref).max() <= 1e-2
     assert lib.pasa_check_device_error(stream, ctypes.byref(info)) == 0
+
+
+def test_one_check_clears_the_timeouts_of_all_kernels():
+    """The self-test's wait runs out in each of the three groups of kernels (decode and dense attention, packed
+    attention, drafted tokens): one check reports it, and nothing is left for a later, unrelated check."""
+    import precision_flashattention_numerics_gb300 as p
+
+    p.check_device_error()
+    t0 = time.monotonic()
+    p.selftest_wait_timeout()
+    with pytest.raises(p.PasaError) as exc:
+        p.check_device_error()
+    assert exc.value.status == PASA_ERR_TIMEOUT
+    assert time.monotonic() - t0 < 5.0          # the waits of 2 s run side by side
+    for _ in range(3):
+        p.check_device_error()
