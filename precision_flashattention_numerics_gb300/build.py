@@ -29,13 +29,17 @@ def _newer(target: str, sources) -> bool:
 
 
 def _depends(unit: str):
-    """What the object of a unit was made from: this file, and the sources its dependency file lists."""
+    """What the object of a unit was made from: this file, and the sources its dependency file lists, by their places relative to
+    csrc/, which a copied or moved tree keeps. Without the unit's own source there (no list, or one of another
+    kind) the object counts as old; the toolkit's headers, which have absolute paths, are not looked at."""
+    own = os.path.join(CSRC, unit + ".cu")
     try:
         with open(os.path.join(OBJ, unit + ".d")) as f:
             listed = f.read().replace("\\\n", " ").partition(":")[2].split()
     except OSError:
-        return [os.path.join(CSRC, unit + ".missing")]
-    return [os.path.abspath(__file__)] + [s for s in listed if os.path.abspath(s).startswith(os.path.dirname(HERE))]
+        listed = []
+    sources = [os.path.normpath(os.path.join(CSRC, s)) for s in listed if not os.path.isabs(s)]
+    return [os.path.abspath(__file__), own] + (sources if own in sources else [own + ".missing"])
 
 
 def _stale(unit: str) -> bool:
@@ -53,23 +57,34 @@ def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = os.environ.get("NVCC", "nvcc")
     os.makedirs(OBJ, exist_ok=True)
     tag = f".tmp{os.getpid()}"
-    running = []
-    for unit in _units():
-        if force or _stale(unit):
-            obj, dep = os.path.join(OBJ, unit + ".o"), os.path.join(OBJ, unit + ".d")
-            cmd = [nvcc, *NVCC_FLAGS, "-c", "-MMD", "-MF", dep + tag, "-o", obj + tag, os.path.join(CSRC, unit + ".cu")]
-            if verbose:
-                cmd.insert(1, "-Xptxas=-v")
-            running.append((subprocess.Popen(cmd), obj, dep))
-    failed = [p.args for p, _, _ in running if p.wait() != 0]   # all of them end before one is reported
-    if failed:
-        raise subprocess.CalledProcessError(1, failed[0])
-    for _, obj, dep in running:
-        os.replace(dep + tag, dep)
-        os.replace(obj + tag, obj)
-    subprocess.run([nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", "-o", LIB + tag,
-                    *(os.path.join(OBJ, u + ".o") for u in _units())], check=True)
-    os.replace(LIB + tag, LIB)
+    made = []   # under their final names
+
+    def place(path):
+        made.append(path)
+        return path + tag
+
+    try:
+        running = []
+        for unit in _units():
+            if force or _stale(unit):
+                # in csrc/ and with relative paths, so that the dependency file holds relative ones
+                cmd = [nvcc, *NVCC_FLAGS, "-c", "-MMD", "-MF", place(os.path.join(OBJ, unit + ".d")), "-o",
+                       place(os.path.join(OBJ, unit + ".o")), unit + ".cu"]
+                if verbose:
+                    cmd.insert(1, "-Xptxas=-v")
+                running.append(subprocess.Popen(cmd, cwd=CSRC))
+        failed = [p.args for p in running if p.wait() != 0]   # all of them end before one is reported
+        if failed:
+            raise subprocess.CalledProcessError(1, failed[0])
+        for path in made:
+            os.replace(path + tag, path)
+        subprocess.run([nvcc, "-shared", "-gencode", "arch=compute_103a,code=sm_103a", "-o", place(LIB),
+                        *(os.path.join(OBJ, u + ".o") for u in _units())], check=True)
+        os.replace(LIB + tag, LIB)
+    finally:
+        for path in made:
+            if os.path.exists(path + tag):
+                os.remove(path + tag)
     return LIB
 
 
