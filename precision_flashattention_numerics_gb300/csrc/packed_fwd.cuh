@@ -54,10 +54,11 @@ constexpr int kKeys = 128;          // keys of a block
 constexpr int kPrepThreads = 128;
 constexpr int kBins = 1024;         // of the tiles' sort by their key blocks
 
-// Pieces and their partial results: at most kMaxPieces, and none shorter than kMinPiece key blocks.
+// Pieces and their partial results: at most kMaxPieces, and of kMinPiece key blocks at least where their number is chosen.
 constexpr int kSms = 152;
 constexpr int kWaves = 4, kMaxPieces = kWaves * kSms;   // of CTAs, one to an SM
 constexpr int kMinPiece = 8;
+constexpr int kMinDivided = 2 * kMinPiece;   // blocks of the least tile that is divided: no sequence of fewer depends on its batch
 constexpr int kPieceStart = 4;   // key blocks that the start and end of a CTA cost
 constexpr int kMergeThreads = 256, kMergeCtas = 2 * kSms;
 
@@ -158,19 +159,24 @@ __device__ __forceinline__ bool make_tile(const Params& p, int slot, int s, Tile
   return true;
 }
 
-// The most key blocks of a piece, or INT_MAX where no tile is to be divided. `sum`, `longest` and `tiles` of all tiles' blocks, for each
+// How many pieces a tile of so many key blocks is in, of `cap` blocks each at most.
+__device__ __forceinline__ int pieces_of(int blocks, int cap) { return blocks < kMinDivided ? 1 : (blocks + cap - 1) / cap; }
+
+// The most key blocks of a piece, or INT_MAX where no tile is to be divided. `sum`, `longest` and `tiles` of all tiles' blocks, and
+// the longest of those that are too short to be divided, for each
 // group of heads. Pieces of c blocks at most are no more than tiles + sum / c, so w waves of CTAs hold them with
-// c = sum / (w SMs / groups - tiles), and take no longer than w (c + start) and the join. Undivided, the call takes longest +
-// start at least: tiles are only divided where that is more, so that it always pays.
-__device__ __forceinline__ int piece_blocks(const Params& p, long long sum, int longest, int tiles) {
+// c = sum / (w SMs / groups - tiles), and take no longer than w (c + start), or the longest that is not divided, and the join. Undivided,
+// the call takes longest + start at least: tiles are only divided where that is more, so that it always pays.
+__device__ __forceinline__ int piece_blocks(const Params& p, long long sum, int longest, int longest_short, int tiles) {
   const int groups = p.Hq / p.hg;
   int best = INT_MAX;
+  if (longest < kMinDivided) return best;
   long long least = (longest + kPieceStart) * 9ll / 10;   // by a tenth at least, for what the estimate leaves out
   for (int w = 1; w <= kWaves; ++w) {
     const int room = w * kSms / groups - tiles;
     if (room <= 0) continue;
     const long long c = max(static_cast<long long>(kMinPiece), (sum + room - 1) / room);
-    const long long time = w * (c + kPieceStart) + 5 + longest / c / 5;
+    const long long time = max(w * (c + kPieceStart), static_cast<long long>(longest_short + kPieceStart)) + 5 + longest / c / 5;
     if (c < longest && time < least) least = time, best = static_cast<int>(c);
   }
   return best;
@@ -182,7 +188,7 @@ template <bool PIECES>
 __device__ __forceinline__ void plan_tiles(const Params& p) {
   constexpr int kWarps = kPrepThreads / 32;
   __shared__ int bins[kBins];
-  __shared__ int warp_sums[kWarps], warp_tiles[kWarps], warp_most[kWarps];
+  __shared__ int warp_sums[kWarps], warp_tiles[kWarps], warp_most[kWarps], warp_short[kWarps];
   __shared__ long long warp_blocks[kWarps];
   __shared__ int parts, splits;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -194,11 +200,14 @@ __device__ __forceinline__ void plan_tiles(const Params& p) {
   Tile kept[kKeep];
   bool there[kKeep];
   auto bin_of = [&](int blocks) { return kBins - 1 - min(kBins - 1, blocks >> p.bin_shift); };
-  int tiles = 0, most = 0;
+  int tiles = 0, most = 0, most_short = 0;   // the longest tile, and of those that are not divided
   long long blocks = 0;
   auto count = [&](const Tile& t) {
     atomicAdd(&bins[bin_of(t.blocks)], 1);
-    if (PIECES) ++tiles, most = max(most, t.blocks), blocks += t.blocks;
+    if (PIECES) {
+      ++tiles, most = max(most, t.blocks), blocks += t.blocks;
+      if (t.blocks < kMinDivided) most_short = max(most_short, t.blocks);
+    }
   };
   const int tid0 = tid - lane;
   int lo = find_sequence(0, p.N, min(tid0, p.tile_slots - 1), [&](int s) { return first_tile(p, s); });
@@ -222,14 +231,21 @@ __device__ __forceinline__ void plan_tiles(const Params& p) {
   if constexpr (PIECES) {
     tiles = __reduce_add_sync(0xFFFFFFFFu, tiles);
     most = __reduce_max_sync(0xFFFFFFFFu, most);
+    most_short = __reduce_max_sync(0xFFFFFFFFu, most_short);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) blocks += __shfl_xor_sync(0xFFFFFFFFu, blocks, d);
-    if (lane == 0) warp_tiles[tid >> 5] = tiles, warp_most[tid >> 5] = most, warp_blocks[tid >> 5] = blocks;
+    if (lane == 0) {
+      warp_tiles[tid >> 5] = tiles, warp_blocks[tid >> 5] = blocks;
+      warp_most[tid >> 5] = most, warp_short[tid >> 5] = most_short;
+    }
     __syncthreads();
-    tiles = most = 0, blocks = 0;
+    tiles = most = most_short = 0, blocks = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) tiles += warp_tiles[w], most = max(most, warp_most[w]), blocks += warp_blocks[w];
-    cap = piece_blocks(p, blocks, most, tiles);
+    for (int w = 0; w < kWarps; ++w) {
+      tiles += warp_tiles[w], blocks += warp_blocks[w];
+      most = max(most, warp_most[w]), most_short = max(most_short, warp_short[w]);
+    }
+    cap = piece_blocks(p, blocks, most, most_short, tiles);
     if (cap != INT_MAX) {   // count again
       for (int i = tid; i < kBins; i += kPrepThreads) bins[i] = 0;
       __syncthreads();
@@ -239,7 +255,7 @@ __device__ __forceinline__ void plan_tiles(const Params& p) {
         Tile t;
         lo = find_sequences(p, lo, slot0, seq);
         if (!make_tile(p, slot0 + lane, seq, t)) continue;
-        const int n = max(1, (t.blocks + cap - 1) / cap), base = t.blocks / n, more = t.blocks % n;
+        const int n = pieces_of(t.blocks, cap), base = t.blocks / n, more = t.blocks % n;
         atomicAdd(&bins[bin_of(base)], n - more);
         if (more > 0) atomicAdd(&bins[bin_of(base + 1)], more);
       }
@@ -293,7 +309,7 @@ __device__ __forceinline__ void plan_tiles(const Params& p) {
       Tile t;
       lo = find_sequences(p, lo, slot0, seq);
       if (!make_tile(p, slot0 + lane, seq, t)) continue;
-      const int n = max(1, (t.blocks + cap - 1) / cap), base = t.blocks / n, more = t.blocks % n;
+      const int n = pieces_of(t.blocks, cap), base = t.blocks / n, more = t.blocks % n;
       t.pieces = n;
       if (n > 1) {
         t.part = atomicAdd(&parts, n);

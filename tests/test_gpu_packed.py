@@ -375,3 +375,19 @@ def test_binding_refusals():
                      ((torch.cat([qt, qt], 1)[:, 1:5][..., :64], kt, vt, a), {"mode": 7})):
         with pytest.raises(p.PasaError):
             p.attn_fwd_packed(*args, **kw)
+
+
+@pytest.mark.parametrize("mode", [0, 1, 3])
+@pytest.mark.parametrize("D", [64, 128])
+def test_up_to_1920_keys_beside_long_ones_nothing_depends_on_the_batch(D, mode):
+    """The long sequence's keys are divided among CTAs; those of up to 1920 keys are not, and give bit for bit what they give
+    alone. The others stay within their bounds."""
+    lens_q, lens_k = [1, 2, 1, 1, 3, 1, 1], [1024, 1025, 1100, 1500, 1920, 1921, 20000]
+    q, k, v, cq, ck = make(540 + D, lens_q, lens_k, 28, 4, D, bias=mode != 3)
+    want, lse = run(q, k, v, cq, ck, mode=mode)
+    check(want, lse, q, k, v, cq, ck, True, mode)
+    for s, (n, m) in enumerate(zip(lens_q, lens_k)):
+        a, c = cq[s], ck[s]
+        if m <= 1920:
+            one, one_lse = run(q[a:a + n], k[c:c + m], v[c:c + m], cu([n]), cu([m]), mode=mode)
+            assert torch.equal(one, want[a:a + n]) and torch.equal(one_lse, lse[:, a:a + n]), m
