@@ -391,3 +391,26 @@ def test_up_to_1920_keys_beside_long_ones_nothing_depends_on_the_batch(D, mode):
         if m <= 1920:
             one, one_lse = run(q[a:a + n], k[c:c + m], v[c:c + m], cu([n]), cu([m]), mode=mode)
             assert torch.equal(one, want[a:a + n]) and torch.equal(one_lse, lse[:, a:a + n]), m
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_offsets_that_do_not_grow_stay_inside_where_keys_are_divided(D):
+    """As test_offsets_that_do_not_grow_stay_inside, with keys enough that tiles come in pieces, offsets of q and k that are bad by
+    themselves, and a guard behind the workspace, where the pieces' lists and partial results lie."""
+    Tq, Tk, lo, hi = 200, 6000, -2 ** 31, 2 ** 31 - 1
+    q, k, v, _, _ = make(550, [Tq], [Tk], 4, 2, D, tail=0)
+    qt, kt, vt = to_dev(q, k, v)
+    lists_q = [0, 70, 200, 200], [0, 200, 100, 300], [-5, 400, 7, 1000], [200, 150, 100, 0], [0, hi, lo, 200], [199, 199, 199, 199], [lo, hi, lo, hi]
+    lists_k = [0, 3000, 5000, 6000], [0, 6000, 2500, 6000], [-5, 9000, 7, 8000], [6000, 4000, 2000, 0], [0, hi, lo, 6000], [lo, hi, lo, hi]
+    size = pasa().packed_workspace_bytes(3, 4, 2, Tq, Tk, D, 1)
+    for a in lists_q:
+        for b in lists_k:
+            cq, ck = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (a, b))
+            room = torch.full((Tq + 200, 4, D), 7.0, dtype=torch.float16, device="cuda")
+            lse = torch.full((6, Tq), 7.0, device="cuda")
+            ws = torch.full((size + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+            for mode in (1, 3):
+                pasa().attn_fwd_packed(qt, kt, vt, cq, ck, mode=mode, out=room[100:100 + Tq], lse=lse[1:5], workspace=ws)
+                pasa().check_device_error()
+            assert (room[:100] == 7).all() and (room[100 + Tq:] == 7).all() and (lse[0] == 7).all() and (lse[5] == 7).all(), (a, b)
+            assert (ws[size:] == 0xFF).all(), (a, b)
