@@ -861,8 +861,9 @@ def rope(q, k, inv_freq, positions=None, start=0, interleaved: bool = False, msc
     :func:`rope_frequencies`; the first R channels turn, in pairs (i, i + R/2) or, interleaved, (2i, 2i + 1).
     positions: int32 [B,S] (packed: [T]); without them token s is at start + s, start an int or int32 [B].
     inverse turns back, which is also the gradient: dq, dk = rope(dout_q, dout_k, ..., inverse=True).
-    out_q and out_k are new fp16 tensors unless given: of the inputs' type or fp16; q and k themselves for a
-    rotation in place. Returns (out_q, out_k)."""
+    out_q and out_k are new tensors unless given: fp16, which the attention takes, or with inverse of the inputs' type, as
+    gradients may not fit fp16. Given ones are of the inputs' type or fp16; q and k themselves for a rotation in place.
+    Returns (out_q, out_k)."""
     dev, stream = _here()
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("expected q [B,Hq,S,D] or [T,Hq,D]")
@@ -884,7 +885,7 @@ def rope(q, k, inv_freq, positions=None, start=0, interleaved: bool = False, msc
         Hkv = k.shape[1]
         kshape = (S, Hkv, D) if packed else (B, Hkv, S, D)
     if out_q is None:
-        out_q = torch.empty(q.shape, device=q.device, dtype=torch.float16 if out_k is None else out_k.dtype)
+        out_q = torch.empty(q.shape, device=q.device, dtype=out_k.dtype if out_k is not None else dtype if inverse else torch.float16)
     out_dtype = out_q.dtype
     if out_k is None and k is not None:
         out_k = torch.empty(kshape, device=q.device, dtype=out_dtype)

@@ -206,3 +206,22 @@ def test_captured_on_a_side_stream():
         graph.replay()
         want = pasa().rope(q, k, f, start=at)
         assert torch.equal(oq, want[0]) and torch.equal(ok, want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+def test_gradients_have_the_type_of_what_they_come_from(dtype):
+    """A gradient that fp16 cannot hold is not lost where no output is given: turned back, it keeps its type. Forward, the outputs are
+    fp16, which the attention takes."""
+    g = inputs(2, 3, 9, 64, dtype, 21) * (1.0 if dtype is torch.float16 else 1e6)
+    pos, (f, _) = places(2, 9, 5000, 22), pasa().rope_frequencies(64)
+    for k in (None, g[:, :1]):
+        dq, dk = pasa().rope(g, k, f, positions=pos, inverse=True)
+        assert dq.dtype is dtype and (k is None or dk.dtype is dtype)
+        close(dq, g, pos, f, inverse=True)
+        if k is not None:
+            close(dk, k, pos, f, inverse=True)
+    packed, _ = pasa().rope(g[0].transpose(0, 1), None, f, positions=pos[0], inverse=True)
+    assert torch.equal(packed.transpose(0, 1), dq[0])
+    assert pasa().rope(g, None, f, positions=pos)[0].dtype is torch.float16
+    half = torch.empty((2, 1, 9, 64), dtype=torch.float16, device="cuda")
+    assert pasa().rope(g, g[:, :1], f, positions=pos, inverse=True, out_k=half)[0].dtype is torch.float16
