@@ -633,8 +633,8 @@ int pasa_rope_frequencies(double* inv_freq, float* mscale, int rotary_dim, doubl
  *   in_type, out_type  PASA_TYPE_*; out_type is in_type or PASA_TYPE_F16 (a value past 65504 is stored as infinity)
  * q_out may be q itself (same strides and type), and k_out k; otherwise outputs share no memory with inputs,
  * with one another or within themselves (PASA_ERR_SHAPE; views side by side in the rows of one
- * buffer do not count as sharing). D is even and at most 256, rotary_dim even and at most D, B * S and the channels of a call in
- * units of 16 fit 31 and 32 bits, else PASA_ERR_SHAPE. An infinity or NaN spoils its own pair only.
+ * buffer do not count as sharing). D is even and at most 256, rotary_dim even and at most D; B * S and Hq + Hkv fit 31
+ * bits and, where rows are not fast, the pairs of a token (and its channels behind them) 32 bits, else PASA_ERR_SHAPE. An infinity or NaN spoils its own pair only.
  */
 int pasa_rope(const void* q, void* q_out, const long long* q_strides, int Hq, const void* k, void* k_out,
               const long long* k_strides, int Hkv, const double* inv_freq, const int* positions, const int* starts,

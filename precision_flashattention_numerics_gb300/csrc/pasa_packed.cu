@@ -188,7 +188,7 @@ int pasa_rope(const void* q, void* q_out, const long long* q_strides, int Hq, co
   void* outs[2] = {q_out, k_out};
   const long long* strides[2] = {q_strides, k_strides};
   const int H[2] = {Hq, Hkv}, tensors = Hkv > 0 ? 2 : 1;
-  bool vectors = rotary_dim % 16 == 0 && D % 8 == 0, in_place = true;
+  bool vectors = rotary_dim % 16 == 0 && D % 8 == 0 && heads <= INT_MAX - 1024, in_place = true;   // (a head past the last fits an int)
   pasa::RopeParams p = {};
   for (int i = 0; i < tensors; ++i) {
     if ((reinterpret_cast<uintptr_t>(ins[i]) & in_mask) != 0 || (reinterpret_cast<uintptr_t>(outs[i]) & out_mask) != 0)
@@ -222,10 +222,9 @@ int pasa_rope(const void* q, void* q_out, const long long* q_strides, int Hq, co
   p.S = S;
   p.D = D;
   p.R = rotary_dim;
-  p.tokens = static_cast<unsigned>(tokens);
   p.mscale = mscale;
   p.sign = inverse ? -1.0f : 1.0f;
-  long long ctas;
+  long long ctas, part = tokens;   // tokens of a launch
   if (vectors) {
     p.groups = rotary_dim / 16 + (in_place ? 0 : (D - rotary_dim + 15) / 16);
     // head slots of a token: as few as fill the SMs, so that a thread's angles serve many heads, and a few times more where a
@@ -240,20 +239,25 @@ int pasa_rope(const void* q, void* q_out, const long long* q_strides, int Hq, co
   } else {
     p.groups = rotary_dim / 2 + (in_place ? 0 : D - rotary_dim);
     p.slots = static_cast<unsigned>(heads);
-    long long threads;
-    if (__builtin_mul_overflow(tokens, heads * p.groups, &threads) || threads > 0xFFFFFF00ll - pasa::kRopeThreads) return PASA_ERR_SHAPE;
-    ctas = (threads + pasa::kRopeThreads - 1) / pasa::kRopeThreads;
+    const long long each = heads * p.groups;   // threads of a token
+    part = std::min(tokens, (0xFFFFFF00ll - pasa::kRopeThreads) / each);
+    if (part == 0) return PASA_ERR_SHAPE;
+    ctas = (part * each + pasa::kRopeThreads - 1) / pasa::kRopeThreads;
   }
   const int rc = check_device();
   if (rc != PASA_OK) return rc;
   const unsigned grid = static_cast<unsigned>(ctas);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool same = in_type == out_type;
-  if (in_type == PASA_TYPE_F16) rope_launch<__half, __half>(p, vectors, interleaved, grid, st);
-  else if (in_type == PASA_TYPE_BF16 && same) rope_launch<__nv_bfloat16, __nv_bfloat16>(p, vectors, interleaved, grid, st);
-  else if (in_type == PASA_TYPE_BF16) rope_launch<__nv_bfloat16, __half>(p, vectors, interleaved, grid, st);
-  else if (same) rope_launch<float, float>(p, vectors, interleaved, grid, st);
-  else rope_launch<float, __half>(p, vectors, interleaved, grid, st);
+  for (long long first = 0; first < tokens; first += part) {
+    p.token0 = static_cast<unsigned>(first);
+    p.tokens = static_cast<unsigned>(std::min(tokens, first + part));
+    if (in_type == PASA_TYPE_F16) rope_launch<__half, __half>(p, vectors, interleaved, grid, st);
+    else if (in_type == PASA_TYPE_BF16 && same) rope_launch<__nv_bfloat16, __nv_bfloat16>(p, vectors, interleaved, grid, st);
+    else if (in_type == PASA_TYPE_BF16) rope_launch<__nv_bfloat16, __half>(p, vectors, interleaved, grid, st);
+    else if (same) rope_launch<float, float>(p, vectors, interleaved, grid, st);
+    else rope_launch<float, __half>(p, vectors, interleaved, grid, st);
+  }
   return launch_status();
 }
 

@@ -49,6 +49,7 @@ struct RopeParams {
   int start;
   int S, D, R;
   unsigned tokens, slots, groups;   // B * S; head slots of a token; channel groups of a row
+  unsigned token0;                  // rope_pairs_kernel: the launch's tokens are token0 .. tokens - 1
   unsigned cta_tokens;              // of a CTA: kRopeThreads / (groups * slots), or 1
   float mscale, sign;
 };
@@ -203,7 +204,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   }
 }
 
-// Any even R and any strides: a thread takes one pair, or one channel behind the R, of one token and head.
+// Any even R and any strides: a thread takes one pair, or one channel behind the R, of one token and head. Threads of a launch are
+// counted in 32 bits; larger calls are launched in parts of whole tokens.
 template <typename TIn, typename TOut, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const __grid_constant__ RopeParams p) {
   __shared__ unsigned long long turns[kRopeMaxD / 2];
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_pairs_kernel(const __grid_c
   __syncthreads();
   const unsigned id = blockIdx.x * kRopeThreads + threadIdx.x;
   const unsigned row = id / p.groups, g = id - row * p.groups;
-  const unsigned token = row / p.slots, head = row - token * p.slots;
+  const unsigned t0 = row / p.slots, head = row - t0 * p.slots, token = p.token0 + t0;
   if (token >= p.tokens) return;
   const unsigned b = token / p.S, s = token - b * p.S;
   const RopeTensor& t = p.t[static_cast<int>(head) >= p.Hq ? 1 : 0];

@@ -225,3 +225,18 @@ def test_gradients_have_the_type_of_what_they_come_from(dtype):
     assert pasa().rope(g, None, f, positions=pos)[0].dtype is torch.float16
     half = torch.empty((2, 1, 9, 64), dtype=torch.float16, device="cuda")
     assert pasa().rope(g, g[:, :1], f, positions=pos, inverse=True, out_k=half)[0].dtype is torch.float16
+
+
+def test_more_than_32_bits_of_pairs():
+    """2^32 pairs and more, in place, which takes more than one launch: each token's heads hold the same pair and turn alike, once."""
+    T, H = 65600, 65536
+    x = torch.empty((T, H, 2), dtype=torch.float16, device="cuda")
+    x[..., 0], x[..., 1] = 1, 0.5
+    f = torch.tensor([0.01], dtype=torch.float64, device="cuda")
+    pasa().rope(x, None, f, out_q=x)
+    first = x[:, :1].clone()
+    for part in x.split(8192):
+        lead = part[:, :1]
+        assert bool((part == lead).all())
+    want = torch.tensor([1, 0.5], dtype=torch.float16).expand(1, 1, T, 2)
+    close(first.transpose(0, 1)[None], want, torch.arange(T)[None], f)

@@ -159,3 +159,22 @@ def test_rope_in_place_is_the_same_order_of_dimensions(pasa):
         assert call(whole, other, B=n) == -2, other
     assert call((7, D, n * D), (9, D, n * D)) != -2          # the stride of a dimension of one says nothing
     assert call((7, D, 5), (9, D, 3), S=1) != -2
+
+
+def test_rope_takes_calls_of_more_than_32_bits_of_pairs(pasa):
+    """B * S and the heads fit 31 bits, the pairs of one token 32 bits; those of a call may be more, also where rows are not on
+    16-byte boundaries."""
+    lib = pasa.library()
+
+    def call(H, S, D, R, B=1, Hkv=0):
+        # q and k in place, 2^50 bytes apart
+        st = (ctypes.c_longlong * 6)(*(H * S * D, D, H * D) * 2)
+        kt = (ctypes.c_longlong * 6)(*(Hkv * S * D, D, Hkv * D) * 2)
+        k = P(FAKE + (1 << 50)) if Hkv else None
+        return lib.pasa_rope(P(FAKE), P(FAKE), ctypes.cast(st, P), H, k, k, ctypes.cast(kt, P) if Hkv else None, Hkv, P(1 << 60), None, None,
+                             0, B, S, D, R, 0, 0, 1.0, 0, 0, None)
+
+    for good in ((65536, 65600, 2, 2), (40, 1 << 26, 128, 24), (1, 2 ** 31 - 1, 128, 6), (32, 1 << 27, 256, 250), (1 << 25, 1, 256, 254)):
+        assert call(*good) in (0, -3, -5), good
+    assert call(1 << 26, 1, 256, 254) == -2                                      # 2^32 pairs and more in one token
+    assert call(2 ** 31 - 1, 1, 16, 16) == -2 and call(2 ** 31 - 1, 1, 2, 2) in (0, -3, -5) and call(1 << 30, 1, 2, 2, Hkv=1 << 30) == -2
