@@ -9,14 +9,14 @@
 // at p = 10^6; in fp64 it takes the few fp64 units of an SM as long as the whole kernel. Only
 // the fraction of a turn counts, so inv_freq / 2 pi is held as a 64-bit fraction of a turn and p times
 // it is one 64-bit integer product, whose overflow drops whole turns. Its upper 32 bits are the
-// fraction in units of 2^-32, and sinpi and cospi of them in fp32 are off by 2^-24 or so at
-// any position.
+// fraction in units of 2^-32, and sinpi and cospi of them in fp32 are off by 2^-23 or so at
+// any position. (inv_freq / 2 pi itself is made in integers: rounded to fp64, the farthest
+// positions are off by 2^-22.8 radians at 1 radian a position, and by 2^-12 at 1000.)
 //
 // HBM-bound: every channel is read once and written once, with 16-byte accesses. A CTA takes a few tokens: its threads make the
 // cos and sin of their angles in shared memory, then a thread takes two vectors of 8 channels, which hold 8 whole
 // pairs in either layout, of one token and every `slots`-th head, with the angles in registers and the rows of two
-// heads on their way at a time, which leaves registers for 4 CTAs on an SM. The table of fractions is made once per CTA: its
-// fp64 arithmetic in every thread would take longer than the copy.
+// heads on their way at a time, which leaves registers for 4 CTAs on an SM. The table of fractions is made once per CTA.
 // Measured, 32768 tokens x 32 heads x 128 in fp16: 96 us for 537 MB, 0.83 of the copy rate (angles made by every thread for
 // 4 heads: 152 us; 4 heads at a time and 2 CTAs: 150; 1 head and 8 CTAs, which spills: 210).
 #pragma once
@@ -54,10 +54,20 @@ struct RopeParams {
   float mscale, sign;
 };
 
-// The fraction of a turn per position as a 64-bit fixed-point number, and cos and sin of p times it.
+// The fraction of a turn per position as a 64-bit fixed-point number, cut off, and cos and sin of p times it. The number's 53-bit
+// mantissa times 1 / 2 pi to 128 bits, in integers, and shifted by its exponent: no rounding, and no fp64 unit.
 __device__ __forceinline__ unsigned long long rope_turns(double inv_freq) {
-  const double t = inv_freq * 0.15915494309189533577;   // 1 / 2 pi
-  return static_cast<unsigned long long>(__double2ll_rn((t - rint(t)) * 18446744073709551616.0));
+  using u64 = unsigned long long;
+  constexpr u64 kHigh = 0xA2F9836E4E441529, kLow = 0xFC2757D1F534DDC0;   // 2^130 / 2 pi
+  const u64 bits = static_cast<u64>(__double_as_longlong(inv_freq));
+  const int shift = 66 + 1075 - static_cast<int>(bits >> 52 & 0x7FF);
+  if (shift < 0 || shift >= 192) return 0;   // below 2^-64 of a turn; from 2^119 radians on, infinite or NaN
+  const u64 m = (bits & 0xFFFFFFFFFFFFF) | 0x10000000000000;
+  const u64 p0 = m * kLow, p1 = m * kHigh + __umul64hi(m, kLow), p2 = __umul64hi(m, kHigh) + (p1 < m * kHigh ? 1 : 0);
+  const int word = shift >> 6, r = shift & 63;
+  const u64 low = word == 0 ? p0 : word == 1 ? p1 : p2, high = word == 0 ? p1 : word == 1 ? p2 : 0;
+  const u64 turns = low >> r | (high << 1) << (63 - r);
+  return bits >> 63 ? 0 - turns : turns;
 }
 __device__ __forceinline__ void rope_angle(unsigned long long turns, int p, float mscale, float sign, float& c, float& s) {
   const unsigned long long a = turns * static_cast<unsigned long long>(static_cast<long long>(p));

@@ -240,3 +240,26 @@ def test_more_than_32_bits_of_pairs():
         assert bool((part == lead).all())
     want = torch.tensor([1, 0.5], dtype=torch.float16).expand(1, 1, T, 2)
     close(first.transpose(0, 1)[None], want, torch.arange(T)[None], f)
+
+
+@pytest.mark.parametrize("R", [128, 24])
+def test_angles_of_fast_pairs_far_away(R):
+    """Against exact arithmetic (integers and fractions, 1 / 2 pi to 80 places): frequencies of many radians a position at the farthest
+    positions, where 64-bit products would be off by up to position * frequency * 2^-52 radians. Only what close() allows at
+    position 0 is allowed: an angle is off by at most 2^-64 of a turn for each position, 2^-33 turns in all, besides its rounding."""
+    from fractions import Fraction
+
+    turn = Fraction("0.15915494309189533576888376337251436203445964574045644874766734405889679763422653509")
+    rng = np.random.default_rng(23)
+    f = np.concatenate([[1.0, 12.5, 1000.7, 12345.678, 3e9, 0.5, 1e-9], 10.0 ** rng.uniform(-6, 6, R // 2 - 7)])
+    pos = np.array([2 ** 31 - 1, -2 ** 31, 10 ** 9 + 7, -123456789, 10 ** 6, 1, 0, -1], np.int32)
+    x = inputs(1, 2, len(pos), 128, torch.float32, 24)
+    out, _ = pasa().rope(x, None, torch.tensor(f).cuda(), positions=torch.tensor(pos)[None].cuda(), out_q=torch.empty_like(x))
+    a = 2 * np.pi * np.array([[float((Fraction(float(w)) * turn * int(p) + Fraction(1, 2)) % 1 - Fraction(1, 2)) for w in f] for p in pos])
+    u, v = (x.double().cpu().numpy()[0, :, :, s] for s in (slice(0, R // 2), slice(R // 2, R)))
+    got = out.double().cpu().numpy()[0]
+    for y, want in ((got[..., :R // 2], u * np.cos(a) - v * np.sin(a)), (got[..., R // 2:R], u * np.sin(a) + v * np.cos(a))):
+        off = np.abs(y - want)
+        tol = (np.abs(u) + np.abs(v)) * 2.0 ** -21 + np.abs(want) * 2.0 ** -24
+        assert (off <= tol).all(), (float((off / tol).max()), np.argwhere(off > tol)[:5])
+    assert np.array_equal(got[..., R:], x.double().cpu().numpy()[0, ..., R:])
