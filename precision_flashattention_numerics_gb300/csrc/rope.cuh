@@ -69,8 +69,8 @@ __device__ __forceinline__ unsigned long long rope_turns(double inv_freq) {
   const u64 turns = low >> r | (high << 1) << (63 - r);
   return bits >> 63 ? 0 - turns : turns;
 }
-__device__ __forceinline__ void rope_angle(unsigned long long turns, int p, float mscale, float sign, float& c, float& s) {
-  const unsigned long long a = turns * static_cast<unsigned long long>(static_cast<long long>(p));
+__device__ __forceinline__ void rope_angle(unsigned long long turns, long long p, float mscale, float sign, float& c, float& s) {
+  const unsigned long long a = turns * static_cast<unsigned long long>(p);
   // half turns in [-1, 1)
   const float x = static_cast<float>(static_cast<int>(a >> 32)) * 0x1p-31f;
   sincospif(x, &s, &c);
@@ -78,9 +78,10 @@ __device__ __forceinline__ void rope_angle(unsigned long long turns, int p, floa
   s *= mscale * sign;
 }
 
-__device__ __forceinline__ int rope_position(const RopeParams& p, unsigned token, unsigned b, unsigned s) {
+// A start and its tokens may pass 32 bits.
+__device__ __forceinline__ long long rope_position(const RopeParams& p, unsigned token, unsigned b, unsigned s) {
   if (p.positions) return p.positions[token];
-  return static_cast<int>(static_cast<unsigned>(p.starts ? p.starts[b] : p.start) + s);
+  return static_cast<long long>(p.starts ? p.starts[b] : p.start) + s;
 }
 
 // 8 channels as they are in memory, as fp32, and back with one rounding each.

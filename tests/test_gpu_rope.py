@@ -263,3 +263,17 @@ def test_angles_of_fast_pairs_far_away(R):
         tol = (np.abs(u) + np.abs(v)) * 2.0 ** -21 + np.abs(want) * 2.0 ** -24
         assert (off <= tol).all(), (float((off / tol).max()), np.argwhere(off > tol)[:5])
     assert np.array_equal(got[..., R:], x.double().cpu().numpy()[0, ..., R:])
+
+
+@pytest.mark.parametrize("R,D", [(64, 64), (24, 64)])
+def test_starts_whose_tokens_pass_32_bits(R, D):
+    """start + s is not cut to 32 bits: the tokens behind position 2^31 - 1 go on turning forwards."""
+    q, k = inputs(2, 3, 40, D, torch.float32, 25), inputs(2, 1, 40, D, torch.float32, 26)
+    f, _ = pasa().rope_frequencies(R)
+    for start in (2 ** 31 - 7, torch.tensor([2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device="cuda")):
+        oq, ok = torch.empty_like(q), torch.empty_like(k)
+        pasa().rope(q, k, f, start=start, out_q=oq, out_k=ok)
+        first = start.long()[:, None] if isinstance(start, torch.Tensor) else start
+        pos = (first + torch.arange(40, device="cuda")).expand(2, 40)
+        close(oq, q, pos, f)
+        close(ok, k, pos, f)
