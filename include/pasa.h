@@ -549,7 +549,8 @@ int pasa_attn_fwd_decode_step_kv4(const void* q, const void* k, const void* v, v
  *   shift    the cache's; the nodes' keys are taken as they are (q . shift, in fp32, is their distance from cached ones)
  *   workspace  device, 256-byte aligned, at least pasa_attn_fwd_tree_kv4_workspace_bytes(...) bytes (may be NULL
  *            where that is 0), written before it is read, used on `stream` only
- * A node's key or value that is not finite may spoil all nodes of its sequence and kv head. o, lse and the workspace share no
+ * A node whose query holds a NaN has an output and an LSE of NaN, others are not touched by it. A node's key or value that is
+ * not finite may spoil all nodes of its sequence and kv head. o, lse and the workspace share no
  * memory with one another or with what is read (PASA_ERR_SHAPE).
  */
 size_t pasa_attn_fwd_tree_kv4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D);

@@ -724,12 +724,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
         reg_fence<16>(w16);
         const float2 other = make_float2(__uint_as_float(w16[0]), __uint_as_float(w16[1]));
         float m_run = fmaxf(m_w, other.y);   // what O is scaled to: the last block's
-        float l_run = m_run == -INFINITY ? 0.0f : l_w * ex2_approx(m_w - m_run) + other.x * ex2_approx(other.y - m_run);
+        // without a maximum both sums are 0, or NaN for a NaN query
+        float l_run = m_run == -INFINITY ? l_w + other.x : l_w * ex2_approx(m_w - m_run) + other.x * ex2_approx(other.y - m_run);
         if (!live) m_run = -INFINITY, l_run = 0.0f;
         const bool mine = row < p.rows;
         const uint32_t tMine = tO + set * kCols;
         if (seg.whole()) {
-          const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+          const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
           __half* to = p.o + (bh * p.rows + row) * D + set * kCols;
 #pragma unroll
           for (int c = 0; c < kCols / 16; ++c) {
@@ -752,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tree_kernel(const __grid_cons
           if (tid == 0 && p.ctas > 0) p.parts[seg.b * seg.per_b() + seg.in_b] = make_int2(0, 0);
           if (mine && set == 0 && p.lse)
             p.lse[bh * p.rows + row] =
-                l_run > 0.0f ? (m_run + log2f(l_run)) * 0.69314718055994531f + offset * p.scale : -INFINITY;
+                l_run == 0.0f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f + offset * p.scale;
         } else {
           const long long slot = 2ll * blockIdx.x + (seg.first ? 0 : 1);
           float4* to = reinterpret_cast<float4*>(p.part_o) + (slot * (D / 4) + set * (kCols / 4)) * kRows + r;
@@ -852,7 +853,11 @@ __global__ void __launch_bounds__(256) kv4_tree_merge_kernel(const __grid_consta
       float top = mm;
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, ml[i].x);
-      if (top == -INFINITY) continue;   // parts in which the row sees nothing
+      if (top == -INFINITY) {   // parts in which the row sees nothing, or of a NaN query, whose sums are NaN
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) ll += ml[i].y;
+        continue;
+      }
       const float f0 = ex2_approx(mm - top);
       ll *= f0, x.x *= f0, x.y *= f0, x.z *= f0, x.w *= f0;
       mm = top;
@@ -864,11 +869,11 @@ __global__ void __launch_bounds__(256) kv4_tree_merge_kernel(const __grid_consta
       }
     }
   }
-  const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+  const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
   *reinterpret_cast<uint2*>(p.o + (bh * p.rows + row) * D + ch) = make_uint2(pack_half2(x.x * inv, x.y * inv), pack_half2(x.z * inv, x.w * inv));
   if (ch == 0 && p.lse) {
     float off = 0.0f;
-    if (p.shift && ll > 0.0f) {
+    if (p.shift && ll != 0.0f) {
       const uint4* q4 = reinterpret_cast<const uint4*>(p.q + (bh * p.rows + row) * D);
       const uint4* m4 = reinterpret_cast<const uint4*>(p.shift + bh * D);
 #pragma unroll 4
@@ -882,7 +887,7 @@ __global__ void __launch_bounds__(256) kv4_tree_merge_kernel(const __grid_consta
         }
       }
     }
-    p.lse[bh * p.rows + row] = ll > 0.0f ? (mm + log2f(ll)) * 0.69314718055994531f + off * p.scale : -INFINITY;
+    p.lse[bh * p.rows + row] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f + off * p.scale;
   }
 }
 

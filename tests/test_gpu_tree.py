@@ -441,3 +441,19 @@ def test_probabilities_are_rounded_once(D, below):
     o, lse, bo, bl = c.reference(1.0)
     bo = bo + (np.abs(c.held[1]).sum(2)[:, :, None] * 2.0 ** -25).repeat(g, 1)
     check(c.run(scale=1.0), (o, lse, bo, bl))
+
+
+@pytest.mark.parametrize("B,n,Sk,D", [(2, 5, 300, 128), (2, 5, 9000, 64), (2, 5, 9000, 128), (80, 3, 900, 64)])
+def test_a_nan_query_stays_in_its_row(B, n, Sk, D):
+    """As in the decode on this cache: an output and an LSE of NaN, not those of a row without keys, and the other rows as they were.
+    A CTA to a segment, segments that CTAs share, and more segments than CTAs."""
+    c = Case(790, B, 4, 2, n, Sk, Sk, D)
+    want, lse = c.run()
+    assert want.isfinite().all() and lse.isfinite().all()
+    bad = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    bad[B - 1, 3, 0] = bad[0, 0, n - 1] = True
+    c.dev[0] = c.dev[0].clone()
+    c.dev[0][B - 1, 3, 0, 5] = c.dev[0][0, 0, n - 1, D - 1] = float("nan")
+    o, other = c.run()
+    assert o[bad].isnan().all() and other[bad].isnan().all()
+    assert torch.equal(o[~bad], want[~bad]) and torch.equal(other[~bad], lse[~bad])
