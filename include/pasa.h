@@ -635,7 +635,8 @@ int pasa_rope_frequencies(double* inv_freq, float* mscale, int rotary_dim, doubl
  * q_out may be q itself (same strides and type), and k_out k; otherwise outputs share no memory with inputs,
  * with one another or within themselves (PASA_ERR_SHAPE; views side by side in the rows of one
  * buffer do not count as sharing). D is even and at most 256, rotary_dim even and at most D; B * S and Hq + Hkv fit 31
- * bits and, where rows are not fast, the pairs of a token (and its channels behind them) 32 bits, else PASA_ERR_SHAPE. An infinity or NaN spoils its own pair only.
+ * bits and, where rows are not fast, the pairs of a token (and its channels behind them) 32 bits, else PASA_ERR_SHAPE. An
+ * infinity or NaN spoils its own pair only.
  */
 int pasa_rope(const void* q, void* q_out, const long long* q_strides, int Hq, const void* k, void* k_out,
               const long long* k_strides, int Hkv, const double* inv_freq, const int* positions, const int* starts,
@@ -663,7 +664,8 @@ int pasa_rope(const void* q, void* q_out, const long long* q_strides, int Hq, co
  *   workspace  device, 256-byte aligned, at least pasa_attn_fwd_packed_workspace_bytes(...) bytes (0 for
  *              invalid sizes), written before it is read, used on `stream` only
  * o may be q itself (same strides); otherwise o, lse and the workspace share no memory with one another or with what is read
- * (PASA_ERR_SHAPE). A key or value that is not finite spoils the queries of its own sequence in the tiles that
+ * (PASA_ERR_SHAPE). A query that holds a NaN and has a key gets an output and an LSE of NaN, others are not touched by it. A
+ * key or value that is not finite spoils the queries of its own sequence in the tiles that
  * read its block, also those whose mask hides it. Calls with few query rows divide a long sequence's keys among CTAs, by
  * the lengths of all sequences: the last bits of a sequence of more than 1920 keys may depend on its batch.
  * (Tq + N) * Hq and (Tk / 128 + 1 + N) * Hkv fit an int, else PASA_ERR_SHAPE.

@@ -757,12 +757,13 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
       named_bar_sync(1, 128 * SETS);
       const float2 other = s.sums[set ^ (SETS - 1)][r];
       const float m_f = fmaxf(m_run, other.y);   // what O is scaled to: the last block's
-      l_run = m_f == -INFINITY ? 0.0f : l_run * ex2_approx(m_run - m_f) + other.x * ex2_approx(other.y - m_f);
+      // without a maximum both sums are 0, or NaN for a NaN query
+      l_run = m_f == -INFINITY ? l_run + other.x : l_run * ex2_approx(m_run - m_f) + other.x * ex2_approx(other.y - m_f);
       m_run = m_f;
     }
     const int2 piece = PIECES ? s.piece : make_int2(1, 0);
     const bool part = piece.x > 1;
-    const float inv_l = part ? 1.0f : (l_run > 0.0f) ? 1.0f / l_run : 0.0f;
+    const float inv_l = part ? 1.0f : l_run == 0.0f ? 0.0f : 1.0f / l_run;
     const long long at = static_cast<long long>(piece.y) * groups + group;   // of the partial results
     uint8_t* stage = s.q;
     constexpr int kCols = D / SETS;   // of O, for a set
@@ -818,7 +819,7 @@ packed_fwd_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constan
       }
     }
     if (p.lse != nullptr && live && set == 0 && !part) {
-      const float lse = (l_run > 0.0f) ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+      const float lse = l_run == 0.0f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
       p.lse[static_cast<long long>(group * p.hg + r % p.hg) * p.Tq + t.q0 + token] = lse;
     }
   }
@@ -865,7 +866,11 @@ __global__ void __launch_bounds__(kMergeThreads, 4) packed_merge_kernel(const __
       float top = m_run;
 #pragma unroll
       for (int e = 0; e < kAtOnce; ++e) top = fmaxf(top, ml[e].x);
-      if (top == -INFINITY) continue;   // pieces of which the row sees nothing
+      if (top == -INFINITY) {   // pieces of which the row sees nothing, or of a NaN query, whose sums are NaN
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) l_run += ml[e].y;
+        continue;
+      }
       const float f0 = ex2_approx(m_run - top);
       l_run *= f0, x.x *= f0, x.y *= f0, x.z *= f0, x.w *= f0;
       m_run = top;
@@ -876,12 +881,12 @@ __global__ void __launch_bounds__(kMergeThreads, 4) packed_merge_kernel(const __
         x.x = fmaf(f, v[e].x, x.x), x.y = fmaf(f, v[e].y, x.y), x.z = fmaf(f, v[e].z, x.z), x.w = fmaf(f, v[e].w, x.w);
       }
     }
-    const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+    const float inv = l_run == 0.0f ? 0.0f : 1.0f / l_run;
     const int head = group * p.hg + r % p.hg;
     *reinterpret_cast<uint2*>(p.o + (t.q0 + token) * p.o_row + head * p.o_head + ch) =
         make_uint2(pack_half2(x.x * inv, x.y * inv), pack_half2(x.z * inv, x.w * inv));
     if (ch == 0 && p.lse)
-      p.lse[static_cast<long long>(head) * p.Tq + t.q0 + token] = l_run > 0.0f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+      p.lse[static_cast<long long>(head) * p.Tq + t.q0 + token] = l_run == 0.0f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
   }
 }
 

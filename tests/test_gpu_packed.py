@@ -414,3 +414,21 @@ def test_offsets_that_do_not_grow_stay_inside_where_keys_are_divided(D):
                 pasa().check_device_error()
             assert (room[:100] == 7).all() and (room[100 + Tq:] == 7).all() and (lse[0] == 7).all() and (lse[5] == 7).all(), (a, b)
             assert (ws[size:] == 0xFF).all(), (a, b)
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2, 3])
+@pytest.mark.parametrize("lens_q,lens_k", [([70, 40], [70, 300]), ([9, 64], [200, 9000])])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_nan_query_stays_in_its_row(D, lens_q, lens_k, mode):
+    """An output and an LSE of NaN, not those of a query without keys, and the other rows as they were; with whole tiles, and where
+    CTAs share the keys."""
+    q, k, v, cq, ck = make(560 + D, lens_q, lens_k, 4, 2, D, bias=False, tail=0)
+    want, lse = run(q, k, v, cq, ck, mode=mode)
+    assert want.isfinite().all() and lse.isfinite().all()
+    bad = torch.zeros(want.shape[:2], dtype=torch.bool, device="cuda")
+    for t, h, ch in ((3, 0, 0), (len(q) - 1, 3, D - 1), (lens_q[0], 2, 7)):
+        q[t, h, ch] = np.nan
+        bad[t, h] = True
+    o, other = run(q, k, v, cq, ck, mode=mode)
+    assert o[bad].isnan().all() and other.T[bad].isnan().all()
+    assert torch.equal(o[~bad], want[~bad]) and torch.equal(other.T[~bad], lse.T[~bad])
