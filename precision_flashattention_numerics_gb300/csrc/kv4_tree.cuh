@@ -17,9 +17,9 @@
 // A operand in TMEM. Scores, maxima, sums and O are fp32, P is rounded to fp16 once (2^-11 of a probability; 2^-24 of
 // the row's sum where it is subnormal): what scales it afterwards, when the maximum moves, are powers of two, as maxima are
 // whole numbers. (Maxima as they come, with factors in fp16, rounded the probabilities of a row's first blocks up to three times, and
-// O apart from the sum. Output errors, relative RMS, of which its own rounding is 2.0e-4: 300 keys 3.31e-4, so 2.90e-4. Where one key
-// has nearly all of a row's weight its probability was 1, which fp16 holds, and is no longer: 61 nodes, uneven, D = 64, 2.12e-4, so
-// 2.86e-4.)
+// O apart from the sum. Output errors, relative RMS, of which its own rounding is 2.0e-4: 300 keys 3.31e-4, so 2.90e-4; the largest of
+// 28 trees 3.9e-4, so 3.0e-4, or 3.5e-4 with maxima as they come and factors in fp32. Where one key has nearly all of a row's weight its
+// probability was 1, which fp16 holds, and is no longer: 61 nodes, uneven, D = 64, 2.12e-4, so 2.86e-4.)
 // P overwrites the scores it was made of, 32 columns of S giving 16 of P, so that a row needs 32 scores in registers at a time.
 // TMEM holds three S and O: with two S, both sets would wait for PV and QK of their next block before they go on.
 // Registers: a launch of 896 threads has 72 each, moved between the roles by setmaxnreg: 2 x 104 + 40 + 4 x 64 <= 7 x 72.
@@ -36,7 +36,7 @@
 // The nodes' keys are taken as they are, cached ones lack the shift: the node block's scores lose q . shift in fp32. (Keys
 // rounded to fp16 after the shift is taken off moved the LSE of rows that see few keys by up to 4e-5.)
 //
-// Measured (GPU time per call): 16 nodes x 7 heads x 8 x 32768 keys 84.7 us, of which 79 here (issue 56%, tensor pipe 40%: the roles
+// Measured (GPU time per call): 16 nodes x 7 heads x 8 x 32768 keys 85.3 us, of which 79.5 here (issue 56%, tensor pipe 40%: the roles
 // wait for one another); 8 nodes on 300 keys 14.4 us; 61 nodes, 6 uneven sequences, D = 64 22.6 us. With 16 rows to a tile on the decode
 // kernel the first would take about 250 us.
 #pragma once

@@ -23,7 +23,7 @@
 // long prompt with few heads), its blocks are divided among several CTAs, which leave partial results (O, max, sum)
 // that packed_merge_kernel joins. piece_blocks() decides from the lengths, on the device. Measured with and without (mode 1,
 // D = 128): 64 queries on 100000 keys, 32 heads on 8, 173 against 700 us; 128 on 20000, 1 on 8000 and 1 on 300, 28 on 4, 76
-// against 186; a prompt of 16384, one head, 92 against 109. What is not divided pays the launch that finds nothing to join: 107.7
+// against 186; a prompt of 16384, one head, 92 against 109. What is not divided pays the launch that finds nothing to join: 107
 // against 104.5 us for four chunks. Kernels with and without PIECES are apart, as the little that it adds cost every
 // call 2 us.
 //
@@ -32,7 +32,9 @@
 // probability of 0 does not make an infinity or NaN harmless.
 //
 // Bound by a block's chain of softmax and MMAs, as attn_fwd_kernel and attn_fwd_2set_kernel are: 32K tokens in 8 prompts, 28 heads,
-// D = 128 1.94 ms, 1370 TFLOP/s (0.72 of the measured peak); D = 64, 4 prompts of up to 9216, 5 heads 102.6 us, 670 TFLOP/s; 20
+// D = 128 1.94 ms, 1369 TFLOP/s (0.72 of the measured peak) in a graph that is replayed now and then, 2.06 ms, 1290 TFLOP/s (0.68) in
+// calls one after the other, where power bounds the clock; D = 64, 4 prompts of up to 9216, 5 heads 102.7 us, 670 TFLOP/s, with no pipe
+// full (exponentials 33%, tensor 32%, issue 44%: the chain's latency and the CTAs' starts and ends); 20
 // prompts of up to 200 tokens 24.6 us (the latency of 2.2 waves of CTAs of 5 us each).
 //
 // cu_q and cu_k are clamped to their tensors and every number from them to its buffer: offsets that do not
